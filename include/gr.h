@@ -354,6 +354,129 @@ int gr_write_then_read_fp8(const gr_shape* shape, uint8_t* codes, uint8_t* scale
                            const void* y, const float* s_prev, const gr_params* next, void* x,
                            float* s_next, void* stream);
 
+/* ---- the parts of a decoder around the Gated Residual -------------------------------------------
+ * The state a stack starts from, the linear-attention token mixer (a sublayer F between a read and
+ * the next write), the norm at its end, and their gradients. Conventions as above: DEVICE pointers,
+ * caller's stream, validation before any launch, no allocation. None of these calls uses atomics on
+ * its outputs: two runs on the same inputs give the same bits. */
+
+/* Token embedding into a state. n_branch 4 (R [N][4][D]) or 1 (a plain stream [N][D]). */
+typedef struct gr_embedding {
+    int64_t n_tokens;    /* N >= 0                                                          */
+    int64_t n_vocab;     /* V: rows of the table, 1 .. 2^31 - 1                             */
+    int32_t d_model;     /* D: a multiple of 8 in [8, GR_MAX_D]                             */
+    int32_t n_branch;    /* 4 or 1                                                          */
+    int32_t table_dtype; /* GR_F32 or GR_BF16 (not used by the gradient)                    */
+    int32_t state_dtype; /* GR_F32 or GR_BF16 (not used by the gradient, whose dR is fp32)  */
+    int32_t id_bits;     /* 32 or 64: ids are int32_t or int64_t                            */
+    float scale;
+} gr_embedding;
+
+/* R[t][i][:] = scale · table[ids[t]][:] for every branch i ("【论文解读】 Qwen3.8 Flash Next", §二.6:
+ * R_c^(0) is the token's embedding in every branch), formed in fp32 and rounded once. table [V][D].
+ * An id outside [0, V) gives a zero row. ids need only their natural alignment. */
+int gr_embed(const gr_embedding* e, const void* table, const void* ids, void* R, void* stream);
+
+/* Bytes of device workspace gr_embed_backward needs (host only): the sorted ids and positions,
+ * and partial rows. */
+int gr_embed_backward_workspace_size(const gr_embedding* e, size_t* bytes);
+
+/* dtable[v][:] = scale · Σ_{t: ids[t] = v} Σ_i dR[t][i][:], fp32, summed in the order of t. With
+ * accumulate == 0 all V rows are overwritten (rows no id names are zero, also when N == 0); else
+ * the sums are added to dtable. Ids outside [0, V) are left out. dR [N][n_branch][D] fp32.
+ * `workspace` 256-byte aligned, clear of the other buffers. */
+int gr_embed_backward(const gr_embedding* e, const float* dR, const void* ids, float* dtable,
+                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm over rows x [N][G][D]. n_group 1 (a plain stream) or 4 (every branch of a state with its
+ * own gain). */
+typedef struct gr_norm {
+    int64_t n_tokens;    /* N >= 0                                     */
+    int32_t d_model;     /* D: a multiple of 8 in [8, GR_MAX_D]        */
+    int32_t n_group;     /* G: 1 or 4                                  */
+    int32_t dtype;       /* of x and y: GR_F32 or GR_BF16              */
+    float eps;           /* >= 0                                       */
+} gr_norm;
+
+/* y = (x − mean) · rstd · weight + bias, rstd = 1/√(mean (x − mean)² + eps); weight [G][D] fp32, bias
+ * [G][D] fp32 or NULL. mean and rstd [N][G] fp32 are written unless NULL. y may be x itself. */
+int gr_layer_norm(const gr_norm* n, const void* x, const float* weight, const float* bias, void* y,
+                  float* mean, float* rstd, void* stream);
+
+/* Bytes of device workspace gr_layer_norm_backward needs (host only). */
+int gr_layer_norm_backward_workspace_size(const gr_norm* n, size_t* bytes);
+
+/* The gradient, given dy [N][G][D] fp32, x and the forward's mean and rstd: dx [N][G][D] fp32 (may be
+ * dy itself), dweight [G][D] and, unless NULL, dbias [G][D] fp32, summed over the N tokens (all
+ * overwritten; zeros when N == 0). `workspace` 256-byte aligned, clear of the other buffers. */
+int gr_layer_norm_backward(const gr_norm* n, const float* dy, const void* x, const float* weight,
+                           const float* mean, const float* rstd, float* dx, float* dweight,
+                           float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Linear attention with a decay for each head. Per sequence and head h, λ = exp(log_decay[h]),
+ * log_decay[h] <= 0 (−∞: no memory):
+ *     S_t = λ S_{t−1} + k_t v_tᵀ  (d_key × d_value),    o_t = scale · S_tᵀ q_t
+ * The tokens of n_seqs sequences are packed: sequence b has the rows seq_starts[b] ..
+ * seq_starts[b+1] − 1 (int32 [n_seqs + 1], ascending from 0 to n_tokens; empty sequences are allowed;
+ * entries outside [0, n_tokens] are clamped, and rows that no sequence holds are left as they are).
+ * seq_starts NULL with n_seqs == 1: one sequence of all rows. */
+typedef struct gr_mixer {
+    int64_t n_tokens;    /* 0 .. 2^31 − 1                              */
+    int32_t n_seqs;      /* >= 0                                       */
+    int32_t n_heads;     /* >= 1; n_seqs · n_heads < 2^31              */
+    int32_t d_key;       /* multiples of 8 in [8, GR_MAX_HEAD]         */
+    int32_t d_value;
+    int32_t dtype;       /* of q, k, v, o: GR_F32 or GR_BF16           */
+    float scale;
+} gr_mixer;
+#define GR_MAX_HEAD 256
+
+/* Rows [n_tokens][n_heads][d] at any strides (in elements): views of one projection's output, or
+ * head-major tensors. The channels are contiguous; data and both strides are multiples of 16
+ * bytes, each stride at least d (of a dimension longer than one). An output's rows must not
+ * overlap, but may lie between an input's or another output's rows of the same token stride. */
+typedef struct gr_rows {
+    void* data;
+    int64_t token_stride, head_stride;
+} gr_rows;
+
+/* Which kernels a prompt or its gradient takes: "mixer_tc" (tcgen05 tensor cores: bf16, d_key and
+ * d_value 64 or 128), "mixer_simt" (CUDA cores, everything else) or "invalid". Host only. */
+const char* gr_mixer_path(const gr_mixer* m);
+
+/* Bytes of device workspace the prompt call (or, gradient != 0, its gradient) needs; may be 0. */
+int gr_linear_attention_workspace_size(const gr_mixer* m, int gradient, size_t* bytes);
+
+/* Prompts: q, k [.., d_key], v, o [.., d_value]; state_in [n_seqs][n_heads][d_key][d_value] fp32 is S
+ * before each sequence's first token (NULL: zero), state_out, if not NULL, S after its last (the
+ * same buffer is allowed). On "mixer_tc" the scores and the state are rounded to bf16 where they
+ * enter a product; the state itself is held and updated in fp32 (from bf16 triples of the decayed
+ * values, so its error is fp32's). A value that is not finite makes the outputs from its token on
+ * not finite, and no earlier ones. */
+int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, const gr_rows* v,
+                        const float* log_decay, const int32_t* seq_starts, const float* state_in,
+                        const gr_rows* o, float* state_out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* One token a request (n_tokens requests; n_seqs is not used): request n's state is
+ * state[slots[n]] (slots int32 [n_tokens], or NULL: state[n]) of the n_slots states
+ * [n_heads][d_key][d_value] fp32, updated in place, then read. A slot outside [0, n_slots) leaves the
+ * states alone and gives o = 0. Two requests must not name the same slot. */
+int gr_linear_attention_step(const gr_mixer* m, const gr_rows* q, const gr_rows* k,
+                             const gr_rows* v, const float* log_decay, float* state,
+                             int64_t n_slots, const int32_t* slots, const gr_rows* o, void* stream);
+
+/* The gradient of gr_linear_attention: given dO (as o) and dstate_out (the gradient of state_out, NULL:
+ * zero), writes dq, dk, dv in the call's dtype and, if not NULL, dstate_in (the gradient of
+ * state_in; the same buffer as dstate_out is allowed). log_decay is a constant of the model: no
+ * gradient. */
+int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_rows* q,
+                                 const gr_rows* k, const gr_rows* v, const float* log_decay,
+                                 const int32_t* seq_starts, const float* state_in,
+                                 const float* dstate_out, const gr_rows* dq, const gr_rows* dk,
+                                 const gr_rows* dv, float* dstate_in, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

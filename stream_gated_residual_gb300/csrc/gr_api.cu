@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "gr_internal.h"
+#include "gr_mixer.h"
 
 namespace gr {
 
@@ -177,6 +178,8 @@ int run_step(const gr_shape* s, void* R, const void* y, const float* s_prev,
 
 }  // namespace
 
+int usable_device() { return check_device(); }
+
 int sm_count() {
     const int d = current_device();
     if (d < 0) return 1;
@@ -267,7 +270,7 @@ const char* gr_status_string(int status) {
     switch (status) {
         case GR_OK: return "ok";
         case GR_E_NULL: return "a required pointer is NULL";
-        case GR_E_SHAPE: return "bad shape (n_tokens < 0, d_model not a multiple of 8 in [8, 12288], or n_branch != 4)";
+        case GR_E_SHAPE: return "bad shape (n_tokens < 0, d_model not a multiple of 8 in [8, 12288], n_branch != 4, or a count, head size or stride outside the call's limits)";
         case GR_E_DTYPE: return "unknown state dtype";
         case GR_E_ALIGN: return "a pointer is not aligned as the call requires";
         case GR_E_RANK: return "rank outside [1, 64]";
@@ -636,8 +639,9 @@ int gr_device_status(int clear) {
     if (st) return st;
     if (cudaDeviceSynchronize() != cudaSuccess) return GR_E_CUDA;
     const int v = fused_status(clear != 0), w = tiled_status(clear != 0);
-    if (v < 0 || w < 0) return GR_E_CUDA;
-    return (v | w) ? GR_E_TIMEOUT : GR_OK;
+    const int m = mixer_status(clear != 0);
+    if (v < 0 || w < 0 || m < 0) return GR_E_CUDA;
+    return (v | w | m) ? GR_E_TIMEOUT : GR_OK;
 }
 
 int gr_selftest_bounded_wait(int64_t limit_cycles, void* stream) {

@@ -1,0 +1,456 @@
+// The state a stack starts from and the gradient of the table it comes from.
+//   "【论文解读】 Qwen3.8 Flash Next" (wkq9411.github.io), §二.6 starts every branch at the token's
+//   embedding: R_i^(0)[t] = scale · E[id_t], i = 0..n_b-1 (n_b = 4, or 1 for a plain stream).
+//   Its gradient: dE[v] = scale · Σ_{t: id_t = v} Σ_i dR_i[t].
+// An id outside [0, V) reads no row (its state is zero) and has no gradient.
+//
+// The gradient is summed by sorted tokens, so no atomics touch it and two runs give the same bits:
+//   1. sort_fill_kernel   one CTA a tile of <= 16384 tokens sorts (id, position) by id, stably, in
+//                         shared memory; the other CTAs zero dE meanwhile (the sort hides there).
+//   2. run_sum_kernel     pieces of consecutive sorted positions × 512 channels: the rows of a run
+//                         (equal ids) are summed in registers in ascending t. A run inside the piece
+//                         goes to dE, one that crosses the piece's ends leaves a partial row.
+//   3. run_join_kernel    the piece a crossing run starts in adds up the run's partial rows in order.
+// Tiles after the first add to dE, one after another.
+#include <math.h>
+
+#include "gr_internal.h"
+#include "gr_ptx.cuh"
+
+namespace gr {
+namespace {
+
+// ---- lookup ---------------------------------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <> __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+
+template <typename T> struct Vec8;
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ explicit Vec8(const float (&v)[8])
+        : a(make_float4(v[0], v[1], v[2], v[3])), b(make_float4(v[4], v[5], v[6], v[7])) {}
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+};
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ explicit Vec8(const float (&v)[8])
+        : u(make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]),
+                       pack_bf2(v[6], v[7]))) {}
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        *reinterpret_cast<uint4*>(p) = u;
+    }
+};
+
+// A warp a token, 8 channels a lane and step: one 16-byte (bf16) or 32-byte (fp32) read of the
+// row, scaled in fp32 and rounded once, then one store a branch.
+template <typename TI, typename TE, typename TR, int NB>
+__global__ void __launch_bounds__(256)
+embed_kernel(int64_t N, int64_t V, int D, float scale, const TI* __restrict__ ids,
+             const TE* __restrict__ E, TR* __restrict__ R, int split) {
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t t = unit / split;
+    const int part = int(unit - t * split);
+    if (t >= N) return;
+    const int64_t id = int64_t(ids[t]);
+    const bool in = id >= 0 && id < V;
+    const TE* row = E + (in ? id : 0) * D;
+    TR* out = R + t * NB * int64_t(D);
+#pragma unroll 2
+    for (int c = (part * 32 + lane) * 8; c < D; c += split * 256) {
+        float v[8] = {};
+        if (in) {
+            load8(row + c, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= scale;
+        }
+        const Vec8<TR> o(v);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) o.store(out + int64_t(i) * D + c);
+    }
+}
+
+template <typename TI, typename TE, typename TR>
+void embed_nb(int64_t N, int64_t V, int D, int nb, float scale, const void* ids, const void* E,
+              void* R, cudaStream_t st) {
+    // warps a token: enough of them that a few tokens still spread over the SMs
+    int split = 1;
+    while (split * 256 < D && N * split < int64_t(sm_count()) * 32) split *= 2;
+    const int64_t blocks = (N * split + 7) / 8;
+    const TI* i = static_cast<const TI*>(ids);
+    const TE* e = static_cast<const TE*>(E);
+    TR* r = static_cast<TR*>(R);
+    if (nb == 1)
+        embed_kernel<TI, TE, TR, 1><<<unsigned(blocks), 256, 0, st>>>(N, V, D, scale, i, e, r, split);
+    else
+        embed_kernel<TI, TE, TR, 4><<<unsigned(blocks), 256, 0, st>>>(N, V, D, scale, i, e, r, split);
+}
+
+template <typename TI>
+void embed_types(int64_t N, int64_t V, int D, int nb, int table_dtype, int state_dtype,
+                 float scale, const void* ids, const void* E, void* R, cudaStream_t st) {
+    using B = __nv_bfloat16;
+    if (table_dtype == GR_F32 && state_dtype == GR_F32)
+        embed_nb<TI, float, float>(N, V, D, nb, scale, ids, E, R, st);
+    else if (table_dtype == GR_F32)
+        embed_nb<TI, float, B>(N, V, D, nb, scale, ids, E, R, st);
+    else if (state_dtype == GR_F32)
+        embed_nb<TI, B, float>(N, V, D, nb, scale, ids, E, R, st);
+    else
+        embed_nb<TI, B, B>(N, V, D, nb, scale, ids, E, R, st);
+}
+
+// ---- the gradient's sort ------------------------------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortItems = 16;                          // a thread's items
+constexpr int kSortTile = kSortThreads * kSortItems;    // 16384: tokens of one tile
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 256;
+// positions + keys, the warps' digit counts, the scan's warp sums
+constexpr size_t kSortSmem = size_t(kSortTile) * 6 + size_t(kDigits) * kSortWarps * 2 + 128;
+
+// Stable radix sort of a tile's (id, position), 8 bits a pass, least significant first. Warp w
+// owns the items [w·32·items, (w+1)·32·items) in rounds of 32, so a digit's items keep their order:
+// rank = the warp's count of the digit so far + the equal lanes below (match), and the base comes
+// from a scan of the counts in (digit, warp) order. Ids outside [0, V) take the key V.
+template <typename TI>
+__device__ void sort_tile(const TI* __restrict__ ids, int64_t V, int n, int passes,
+                          uint32_t* __restrict__ out_id, uint32_t* __restrict__ out_pos, char* smem) {
+    uint32_t* skey = reinterpret_cast<uint32_t*>(smem);
+    uint16_t* spos = reinterpret_cast<uint16_t*>(smem + size_t(kSortTile) * 4);
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + size_t(kSortTile) * 6);  // [digit][warp]
+    uint32_t* wsum = reinterpret_cast<uint32_t*>(smem + size_t(kSortTile) * 6 +
+                                                 size_t(kDigits) * kSortWarps * 2);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    // items a warp holds: as few rounds as cover n (the ranges stay contiguous)
+    const int rounds = (n + kSortThreads - 1) / kSortThreads;
+    uint32_t key[kSortItems];
+    uint16_t pos[kSortItems];
+    uint16_t rank[kSortItems];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+        const int i = (w * rounds + j) * 32 + lane;
+        key[j] = 0xffffffffu;      // past the tile: sorts behind every key and is not written
+        pos[j] = uint16_t(i);
+        if (j < rounds && i < n) {
+            const int64_t id = int64_t(ids[i]);
+            key[j] = uint32_t(id >= 0 && id < V ? id : V);
+        }
+    }
+    for (int p = 0; p < passes; ++p) {
+        for (int i = tid; i < kDigits * kSortWarps / 2; i += kSortThreads)
+            reinterpret_cast<uint32_t*>(cnt)[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            if (j < rounds) {
+                const uint32_t d = (key[j] >> (8 * p)) & 255u;
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                const uint32_t below = __popc(same & ((1u << lane) - 1u));
+                uint16_t* c = cnt + d * kSortWarps + w;
+                const uint32_t base = *c;
+                rank[j] = uint16_t(base + below);
+                __syncwarp();
+                if (below == 0) *c = uint16_t(base + __popc(same));
+                __syncwarp();
+            }
+        }
+        __syncthreads();
+        // exclusive scan of the 8192 counts in (digit, warp) order, 8 a thread
+        uint4* mine = reinterpret_cast<uint4*>(cnt) + tid;
+        const uint4 u = *mine;
+        const uint32_t pk[4] = {u.x, u.y, u.z, u.w};
+        uint32_t v[8], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = sum;
+            sum += (pk[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+        }
+        uint32_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) wsum[w] = inc;
+        __syncthreads();
+        if (w == 0) {
+            uint32_t x = wsum[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            wsum[lane] = x;
+        }
+        __syncthreads();
+        const uint32_t base = (w ? wsum[w - 1] : 0) + inc - sum;
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            q[k] = ((base + v[2 * k]) & 0xffffu) | ((base + v[2 * k + 1]) << 16);
+        *mine = make_uint4(q[0], q[1], q[2], q[3]);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            if (j < rounds) {
+                const uint32_t d = (key[j] >> (8 * p)) & 255u;
+                const uint32_t to = uint32_t(cnt[d * kSortWarps + w]) + rank[j];
+                skey[to] = key[j];
+                spos[to] = pos[j];
+            }
+        }
+        __syncthreads();
+        if (p + 1 < passes) {
+#pragma unroll
+            for (int j = 0; j < kSortItems; ++j) {
+                if (j < rounds) {
+                    const int i = (w * rounds + j) * 32 + lane;
+                    key[j] = skey[i];
+                    pos[j] = spos[i];
+                }
+            }
+            __syncthreads();
+        }
+    }
+    for (int i = tid; i < n; i += kSortThreads) {
+        out_id[i] = skey[i];
+        out_pos[i] = spos[i];
+    }
+}
+
+template <typename TI>
+__global__ void __launch_bounds__(kSortThreads, 1)
+sort_fill_kernel(const TI* __restrict__ ids, int64_t N, int64_t V, int passes,
+                 uint32_t* __restrict__ sorted_id, uint32_t* __restrict__ sorted_pos, int tiles,
+                 float4* __restrict__ fill, int64_t n4) {
+    extern __shared__ __align__(16) char smem[];
+    dep_launch_dependents();
+    if (int(blockIdx.x) < tiles) {
+        const int64_t t0 = int64_t(blockIdx.x) * kSortTile;
+        const int n = int(N - t0 < kSortTile ? N - t0 : kSortTile);
+        sort_tile(ids + t0, V, n, passes, sorted_id + t0, sorted_pos + t0, smem);
+    } else if (fill) {
+        const int64_t step = int64_t(gridDim.x - tiles) * kSortThreads;
+        for (int64_t i = int64_t(blockIdx.x - tiles) * kSortThreads + threadIdx.x; i < n4; i += step)
+            fill[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+}
+
+// ---- the gradient's sums --------------------------------------------------------------------------
+
+constexpr int kSumThreads = 128;   // × 4 channels
+constexpr int kBatch = 4;          // rows whose loads are in flight together
+
+template <int NB>
+__device__ __forceinline__ float4 row_sum(const float* __restrict__ dR, int64_t t, int D, int c) {
+    const float* p = dR + t * NB * int64_t(D) + c;
+    float4 s = __ldcs(reinterpret_cast<const float4*>(p));
+#pragma unroll
+    for (int i = 1; i < NB; ++i) {
+        const float4 b = __ldcs(reinterpret_cast<const float4*>(p + int64_t(i) * D));
+        s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+    }
+    return s;
+}
+
+__device__ __forceinline__ void flush(float* __restrict__ dst, float4 a, float scale, bool add) {
+    float4* p = reinterpret_cast<float4*>(dst);
+    a.x *= scale, a.y *= scale, a.z *= scale, a.w *= scale;
+    if (add) {
+        const float4 b = *p;
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    *p = a;
+}
+
+// Partial rows: piece p's row 2p is its share of a run that began in an earlier piece, row 2p+1 of
+// a run that begins in it and goes on (a piece inside one run only has row 2p).
+template <int NB>
+__global__ void __launch_bounds__(kSumThreads)
+run_sum_kernel(const float* __restrict__ dR, const uint32_t* __restrict__ sid,
+               const uint32_t* __restrict__ spos, int n, int64_t V, int D, int piece, float scale,
+               bool add, float* __restrict__ dE, float* __restrict__ part) {
+    dep_wait();
+    dep_launch_dependents();
+    const int i0 = blockIdx.x * piece, i1 = min(i0 + piece, n);
+    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+    if (c >= D) return;
+    uint32_t cur = sid[i0];
+    bool from_before = i0 > 0 && sid[i0 - 1] == cur;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = i0; i < i1; i += kBatch) {
+        float4 x[kBatch];
+        uint32_t id[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            id[k] = i + k < i1 ? sid[i + k] : 0xffffffffu;
+            x[k] = id[k] < V ? row_sum<NB>(dR, spos[i + k], D, c)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (i + k >= i1) break;
+            if (id[k] != cur) {
+                if (cur < V) {
+                    if (from_before)
+                        *reinterpret_cast<float4*>(part + int64_t(2 * blockIdx.x) * D + c) = acc;
+                    else
+                        flush(dE + int64_t(cur) * D + c, acc, scale, add);
+                }
+                cur = id[k];
+                from_before = false;
+                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            acc.x += x[k].x, acc.y += x[k].y, acc.z += x[k].z, acc.w += x[k].w;
+        }
+    }
+    if (cur < V) {
+        const bool goes_on = i1 < n && sid[i1] == cur;
+        if (from_before || goes_on)
+            *reinterpret_cast<float4*>(part + int64_t(2 * blockIdx.x + (from_before ? 0 : 1)) * D + c) =
+                acc;
+        else
+            flush(dE + int64_t(cur) * D + c, acc, scale, add);
+    }
+}
+
+__global__ void __launch_bounds__(kSumThreads)
+run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int piece, float scale,
+                bool add, float* __restrict__ dE, const float* __restrict__ part) {
+    dep_wait();
+    const int p = blockIdx.x, i1 = (p + 1) * piece;
+    if (i1 >= n) return;
+    const uint32_t id = sid[i1];
+    // the run that crosses this piece's end has to begin inside it
+    if (id >= V || sid[i1 - 1] != id || (p > 0 && sid[p * piece] == id && sid[p * piece - 1] == id))
+        return;
+    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+    // the run's end by bisection: the first sorted index > i1 whose id differs
+    int lo = i1 + 1, hi = n;
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (sid[m] == id) lo = m + 1;
+        else hi = m;
+    }
+    const int last = (lo - 1) / piece;   // the last piece with a share of the run
+    if (c >= D) return;
+    float4 acc = *reinterpret_cast<const float4*>(part + int64_t(2 * p + 1) * D + c);
+#pragma unroll 8
+    for (int q = p + 1; q <= last; ++q) {
+        const float4 b = *reinterpret_cast<const float4*>(part + int64_t(2 * q) * D + c);
+        acc.x += b.x, acc.y += b.y, acc.z += b.z, acc.w += b.w;
+    }
+    flush(dE + int64_t(id) * D + c, acc, scale, add);
+}
+
+// Sorted positions a CTA of the sums takes: 32 for large tiles (few partial rows), fewer where the
+// pieces would not fill the SMs.
+int piece_of(int64_t n, int D) {
+    const int64_t cols = (D + kSumThreads * 4 - 1) / (kSumThreads * 4);
+    int piece = 32;
+    while (piece > 4 && (n + piece - 1) / piece * cols < int64_t(sm_count()) * 4) piece /= 2;
+    return piece;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <typename TI>
+cudaError_t sort_fill(int64_t N, int64_t V, const void* ids, uint32_t* sid, uint32_t* spos,
+                      float* fill, int64_t fill_n, cudaStream_t st) {
+    int passes = 1;
+    while (passes < 4 && (uint64_t(V) >> (8 * passes)) != 0) ++passes;
+    const int tiles = int((N + kSortTile - 1) / kSortTile);
+    const int64_t n4 = fill_n / 4;
+    int64_t fillers = fill ? (n4 + kSortThreads * 4 - 1) / (kSortThreads * 4) : 0;
+    const int64_t most = int64_t(sm_count()) * 4;
+    fillers = fillers < most ? fillers : most;
+    auto kern = sort_fill_kernel<TI>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(kSortSmem));
+    if (e != cudaSuccess) return e;
+    kern<<<unsigned(tiles + fillers), kSortThreads, kSortSmem, st>>>(
+        static_cast<const TI*>(ids), N, V, passes, sid, spos, tiles, reinterpret_cast<float4*>(fill),
+        n4);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_embed(int64_t N, int64_t V, int D, int nb, int table_dtype, int state_dtype,
+                         int id_bits, float scale, const void* ids, const void* table, void* R,
+                         cudaStream_t st) {
+    if (id_bits == 32)
+        embed_types<int32_t>(N, V, D, nb, table_dtype, state_dtype, scale, ids, table, R, st);
+    else
+        embed_types<int64_t>(N, V, D, nb, table_dtype, state_dtype, scale, ids, table, R, st);
+    return cudaGetLastError();
+}
+
+// The sorted ids and positions [N] each, then two partial rows [D] a piece of the largest tile.
+size_t embed_backward_workspace(int64_t N, int D) {
+    const int64_t tile = N < kSortTile ? N : kSortTile;
+    // piece_of() gives at least 4 positions a piece
+    const int64_t pieces = (tile + 3) / 4;
+    return 2 * align256(size_t(N) * 4) + align256(size_t(2 * pieces) * D * 4);
+}
+
+cudaError_t launch_embed_backward(int64_t N, int64_t V, int D, int nb, int id_bits, float scale,
+                                  const float* dR, const void* ids, float* dE, bool accumulate,
+                                  void* workspace, cudaStream_t st) {
+    char* ws = static_cast<char*>(workspace);
+    uint32_t* sid = reinterpret_cast<uint32_t*>(ws);
+    uint32_t* spos = reinterpret_cast<uint32_t*>(ws + align256(size_t(N) * 4));
+    float* part = reinterpret_cast<float*>(ws + 2 * align256(size_t(N) * 4));
+    float* fill = accumulate ? nullptr : dE;
+    cudaError_t e = id_bits == 32 ? sort_fill<int32_t>(N, V, ids, sid, spos, fill, V * D, st)
+                                  : sort_fill<int64_t>(N, V, ids, sid, spos, fill, V * D, st);
+    for (int64_t t0 = 0; e == cudaSuccess && t0 < N; t0 += kSortTile) {
+        const int n = int(N - t0 < kSortTile ? N - t0 : kSortTile);
+        const int piece = piece_of(n, D);
+        const dim3 grid((n + piece - 1) / piece, (D + kSumThreads * 4 - 1) / (kSumThreads * 4));
+        const float* rows = dR + t0 * nb * int64_t(D);
+        const bool add = accumulate || t0 > 0;
+        e = launch_after(nb == 1 ? run_sum_kernel<1> : run_sum_kernel<4>, grid, kSumThreads, 0, st,
+                         rows, sid + t0, spos + t0, n, V, D, piece, scale, add, dE, part);
+        if (e == cudaSuccess)
+            e = launch_after(run_join_kernel, grid, kSumThreads, 0, st, sid + t0, n, V, D, piece,
+                             scale, add, dE, part);
+    }
+    return e;
+}
+
+}  // namespace gr

@@ -181,6 +181,28 @@ cudaError_t launch_wait_selftest(long long limit_cycles, cudaStream_t st);
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// GR_OK, or GR_E_DEVICE when the current device cannot run this build.
+int usable_device();
+
+// Token embedding into a state and its gradient (gr_embed.cu).
+cudaError_t launch_embed(int64_t N, int64_t V, int D, int nb, int table_dtype, int state_dtype,
+                         int id_bits, float scale, const void* ids, const void* table, void* R,
+                         cudaStream_t st);
+size_t embed_backward_workspace(int64_t N, int D);
+cudaError_t launch_embed_backward(int64_t N, int64_t V, int D, int nb, int id_bits, float scale,
+                                  const float* dR, const void* ids, float* dE, bool accumulate,
+                                  void* workspace, cudaStream_t st);
+
+// Layer norm of [N][G][D] rows and its gradient (gr_norm.cu); db may be null.
+cudaError_t launch_layer_norm(int64_t N, int D, int G, int dtype, float eps, const void* x,
+                              const float* w, const float* b, void* y, float* mean, float* rstd,
+                              cudaStream_t st);
+size_t layer_norm_backward_workspace(int64_t N, int D, int G);
+cudaError_t launch_layer_norm_backward(int64_t N, int D, int G, int dtype, const float* dy,
+                                       const void* x, const float* w, const float* mean,
+                                       const float* rstd, float* dx, float* dw, float* db,
+                                       void* workspace, cudaStream_t st);
+
 // ---- device helpers ------------------------------------------------------------------------
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -43,6 +43,29 @@ class ParamsStruct(ctypes.Structure):
                 ("state_dtype", ctypes.c_int32), ("tag", ctypes.c_uint64)]
 
 
+class EmbeddingStruct(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_vocab", ctypes.c_int64),
+                ("d_model", ctypes.c_int32), ("n_branch", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("id_bits", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NormStruct(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("d_model", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class MixerStruct(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("d_key", ctypes.c_int32),
+                ("d_value", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RowsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _LIB = None
 
 
@@ -61,6 +84,8 @@ def load() -> ctypes.CDLL:
     L = ctypes.CDLL(_build.LIB)
     P, S, V = ctypes.POINTER(ParamsStruct), ctypes.POINTER(Shape), ctypes.c_void_p
     sz = ctypes.POINTER(ctypes.c_size_t)
+    E, LN, M, RW = (ctypes.POINTER(t) for t in (EmbeddingStruct, NormStruct, MixerStruct,
+                                                RowsStruct))
     sig = {
         "gr_api_version": ([], ctypes.c_int),
         "gr_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -90,6 +115,20 @@ def load() -> ctypes.CDLL:
         "gr_read_fp8": ([S, V, V, P, V, V, V], ctypes.c_int),
         "gr_write_fp8": ([S, V, V, V, V, V], ctypes.c_int),
         "gr_write_then_read_fp8": ([S, V, V, V, V, P, V, V, V], ctypes.c_int),
+        "gr_embed": ([E, V, V, V, V], ctypes.c_int),
+        "gr_embed_backward_workspace_size": ([E, sz], ctypes.c_int),
+        "gr_embed_backward": ([E, V, V, V, ctypes.c_int, V, ctypes.c_size_t, V], ctypes.c_int),
+        "gr_layer_norm": ([LN] + [V] * 7, ctypes.c_int),
+        "gr_layer_norm_backward_workspace_size": ([LN, sz], ctypes.c_int),
+        "gr_layer_norm_backward": ([LN] + [V] * 9 + [ctypes.c_size_t, V], ctypes.c_int),
+        "gr_mixer_path": ([M], ctypes.c_char_p),
+        "gr_linear_attention_workspace_size": ([M, ctypes.c_int, sz], ctypes.c_int),
+        "gr_linear_attention": ([M, RW, RW, RW, V, V, V, RW, V, V, ctypes.c_size_t, V],
+                                ctypes.c_int),
+        "gr_linear_attention_step": ([M, RW, RW, RW, V, V, ctypes.c_int64, V, RW, V],
+                                     ctypes.c_int),
+        "gr_linear_attention_backward": ([M, RW, RW, RW, RW, V, V, V, V, RW, RW, RW, V, V,
+                                          ctypes.c_size_t, V], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -539,3 +578,285 @@ def write_then_read_fp8(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tens
                                          _stream(stream)), "gr_write_then_read_fp8")
     return x, s_next
 
+
+# ---- the parts of a decoder around the Gated Residual: embedding, layer norm, linear attention ----
+
+def _aligned_ws(nbytes: int, device) -> torch.Tensor | None:
+    """A fresh 256-byte aligned device buffer of nbytes (torch's allocations start at multiples of
+    512 bytes), or None for 0."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _ws(need: int, workspace: torch.Tensor | None, device, stream):
+    """The call's workspace: the caller's, else a fresh one that `stream` is recorded on."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+    buf = _aligned_ws(need, device)
+    if buf is not None and stream is not None:
+        buf.record_stream(stream)
+    return _ptr(buf), need, buf
+
+
+def _f32(t: torch.Tensor | None, name: str, shape=None) -> None:
+    if t is None:
+        return
+    _dev(t, name)
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _ids(ids: torch.Tensor) -> int:
+    _dev(ids, "ids")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    return 32 if ids.dtype == torch.int32 else 64
+
+
+def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: int = 4,
+          dtype: torch.dtype | None = None, out: torch.Tensor | None = None, stream=None):
+    """gr_embed: the state a stack starts from, R[t, i] = scale * table[ids[t]] in every branch:
+    [N, 4, D], or [N, D] with branches=1; N = ids.numel(), dtype the table's unless given. An id
+    outside the table gives a zero row."""
+    _dev(table, "table")
+    dtype = table.dtype if dtype is None else dtype
+    if table.dtype not in _DTYPES or dtype not in _DTYPES or table.dim() != 2:
+        raise ValueError("table must be a float32 or bfloat16 tensor [V, D] and dtype one of these")
+    bits = _ids(ids)
+    (V, D), N = table.shape, ids.numel()
+    shape = (N, D) if branches == 1 else (N, branches, D)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=table.device)
+    else:
+        _dev(out, "out")
+        if tuple(out.shape) != shape or out.dtype != dtype:
+            raise ValueError(f"out must be {dtype} of shape {list(shape)}")
+    e = EmbeddingStruct(N, V, D, branches, _DTYPES[table.dtype], _DTYPES[dtype], bits, scale)
+    _check(load().gr_embed(ctypes.byref(e), _ptr(table), _ptr(ids), _ptr(out), _stream(stream)),
+           "gr_embed")
+    return out
+
+
+def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: float = 1.0,
+                   dtable: torch.Tensor | None = None, accumulate: bool = False,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gr_embed_backward: the table's gradient [n_vocab, D] fp32 from dR [N, 4, D] or [N, D] fp32;
+    rows of equal ids are summed in token order. accumulate=True adds to the given dtable."""
+    _f32(dR, "dR")
+    bits = _ids(ids)
+    if dR.dim() not in (2, 3) or dR.shape[0] != ids.numel():
+        raise ValueError("dR must be [N, 4, D] or [N, D] with N = ids.numel()")
+    if accumulate and dtable is None:
+        raise ValueError("accumulate needs the dtable to add to")
+    N, D = dR.shape[0], dR.shape[-1]
+    if dtable is None:
+        dtable = torch.empty((n_vocab, D), dtype=torch.float32, device=dR.device)
+    else:
+        _f32(dtable, "dtable", (n_vocab, D))
+    e = EmbeddingStruct(N, n_vocab, D, 1 if dR.dim() == 2 else dR.shape[1], GR_F32, GR_F32, bits,
+                        scale)
+    need = ctypes.c_size_t(0)
+    L = load()
+    _check(L.gr_embed_backward_workspace_size(ctypes.byref(e), ctypes.byref(need)),
+           "gr_embed_backward_workspace_size")
+    wp, wn, _keep = _ws(need.value, workspace, dR.device, stream)
+    _check(L.gr_embed_backward(ctypes.byref(e), _ptr(dR), _ptr(ids), _ptr(dtable),
+                               1 if accumulate else 0, wp, wn, _stream(stream)),
+           "gr_embed_backward")
+    return dtable
+
+
+def _norm_desc(x: torch.Tensor, weight: torch.Tensor, eps: float):
+    _dev(x, "x")
+    if x.dtype not in _DTYPES or x.dim() not in (2, 3):
+        raise ValueError("x must be a float32 or bfloat16 tensor [N, D] or [N, 4, D]")
+    N, G, D = x.shape[0], 1 if x.dim() == 2 else x.shape[1], x.shape[-1]
+    _f32(weight, "weight", x.shape[1:])
+    return NormStruct(N, D, G, _DTYPES[x.dtype], eps)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+               eps: float = 1e-5, y: torch.Tensor | None = None, stats: bool = False, stream=None):
+    """gr_layer_norm over the last axis of x [N, D] (weight, bias [D]) or of every branch of
+    x [N, 4, D] (weight, bias [4, D]); weight and bias fp32. Returns y, or (y, mean, rstd) with
+    stats=True (fp32, what the gradient needs). y may be x."""
+    n = _norm_desc(x, weight, eps)
+    _f32(bias, "bias", x.shape[1:])
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _dev(y, "y")
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError("y must match x")
+    mean = rstd = None
+    if stats:
+        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
+    _check(load().gr_layer_norm(ctypes.byref(n), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                _ptr(mean), _ptr(rstd), _stream(stream)), "gr_layer_norm")
+    return (y, mean, rstd) if stats else y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                        mean: torch.Tensor, rstd: torch.Tensor, bias: bool = True,
+                        dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None):
+    """gr_layer_norm_backward: (dx like x but fp32, dweight, dbias or None) from dy (fp32, x's shape)
+    and the forward's mean and rstd. dx may be dy."""
+    n = _norm_desc(x, weight, 0.0)
+    _f32(dy, "dy", x.shape)
+    _f32(mean, "mean", x.shape[:-1])
+    _f32(rstd, "rstd", x.shape[:-1])
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _f32(dx, "dx", x.shape)
+    dweight = torch.empty_like(weight)
+    dbias = torch.empty_like(weight) if bias else None
+    need = ctypes.c_size_t(0)
+    L = load()
+    _check(L.gr_layer_norm_backward_workspace_size(ctypes.byref(n), ctypes.byref(need)),
+           "gr_layer_norm_backward_workspace_size")
+    wp, wn, _keep = _ws(need.value, workspace, x.device, stream)
+    _check(L.gr_layer_norm_backward(ctypes.byref(n), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean),
+                                    _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), wp, wn,
+                                    _stream(stream)), "gr_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+def _rows(t: torch.Tensor, name: str, N: int, H: int, d: int, dtype: torch.dtype) -> RowsStruct:
+    """A [N, H, d] tensor with contiguous channels at any token and head stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (N, H, d) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {[N, H, d]}, got {t.dtype} of "
+                         f"{list(t.shape)}")
+    ts, hs, cs = t.stride()
+    if cs != 1 and t.numel():
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return RowsStruct(t.data_ptr(), ts, hs)
+
+
+def _mixer_desc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                scale: float | None, n_seqs: int):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must have shape [N, H, d]")
+    N, H, dk = q.shape
+    dv = v.shape[2]
+    if q.dtype not in _DTYPES:
+        raise ValueError("q, k, v must be float32 or bfloat16")
+    rows = [_rows(t, n, N, H, d, q.dtype) for t, n, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
+    _f32(log_decay, "log_decay", (H,))
+    m = MixerStruct(N, n_seqs, H, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else scale)
+    return m, rows
+
+
+def _seqs(seq_starts: torch.Tensor | None) -> int:
+    if seq_starts is None:
+        return 1
+    _dev(seq_starts, "seq_starts")
+    if seq_starts.dtype != torch.int32 or seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must be int32 [n_seqs + 1]")
+    return seq_starts.numel() - 1
+
+
+def _mixer_ws(m: MixerStruct, gradient: int, workspace, device, stream):
+    need = ctypes.c_size_t(0)
+    _check(load().gr_linear_attention_workspace_size(ctypes.byref(m), gradient, ctypes.byref(need)),
+           "gr_linear_attention_workspace_size")
+    return _ws(need.value, workspace, device, stream)
+
+
+def mixer_path(n_tokens: int, n_heads: int, d_key: int, d_value: int, dtype: torch.dtype) -> str:
+    """Which kernels a linear-attention prompt of this shape runs: "mixer_tc" or "mixer_simt"."""
+    m = MixerStruct(n_tokens, 1, n_heads, d_key, d_value, _DTYPES.get(dtype, -1), 1.0)
+    return load().gr_mixer_path(ctypes.byref(m)).decode()
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                     scale: float | None = None, seq_starts: torch.Tensor | None = None,
+                     state: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                     state_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """gr_linear_attention: q, k [N, H, dk], v [N, H, dv] (strided views allowed) of the packed
+    sequences seq_starts (int32 [B + 1]; None: one sequence), log_decay [H] fp32 <= 0, scale
+    dk ** -0.5 unless given, state [B, H, dk, dv] fp32 before each sequence or None. Returns
+    (o [N, H, dv], state_out [B, H, dk, dv] fp32 after each sequence). state_out may be state."""
+    B = _seqs(seq_starts)
+    m, rows = _mixer_desc(q, k, v, log_decay, scale, B)
+    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
+    _f32(state, "state", (B, H, dk, dv))
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    if state_out is None:
+        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    else:
+        _f32(state_out, "state_out", (B, H, dk, dv))
+    orow = _rows(o, "o", N, H, dv, q.dtype)
+    wp, wn, _keep = _mixer_ws(m, 0, workspace, q.device, stream)
+    r = [ctypes.byref(x) for x in rows]
+    _check(load().gr_linear_attention(ctypes.byref(m), *r, _ptr(log_decay), _ptr(seq_starts),
+                                      _ptr(state), ctypes.byref(orow), _ptr(state_out), wp, wn,
+                                      _stream(stream)), "gr_linear_attention")
+    return o, state_out
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          log_decay: torch.Tensor, state: torch.Tensor,
+                          scale: float | None = None, slots: torch.Tensor | None = None,
+                          o: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gr_linear_attention_step: one token of each of N requests. state [slots, H, dk, dv] fp32 is
+    updated in place; request n uses state[slots[n]] (int32; None: state[n]). Returns o [N, H, dv];
+    a slot outside the states leaves them alone and gives o = 0."""
+    m, rows = _mixer_desc(q, k, v, log_decay, scale, 0)
+    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+        raise ValueError(f"state must be [slots, {H}, {dk}, {dv}]")
+    _f32(state, "state")
+    if slots is not None:
+        _dev(slots, "slots")
+        if slots.dtype != torch.int32 or tuple(slots.shape) != (N,):
+            raise ValueError("slots must be int32 [N]")
+    elif state.shape[0] < N:
+        raise ValueError("state must hold a slot for every request")
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    orow = _rows(o, "o", N, H, dv, q.dtype)
+    r = [ctypes.byref(x) for x in rows]
+    _check(load().gr_linear_attention_step(ctypes.byref(m), *r, _ptr(log_decay), _ptr(state),
+                                           state.shape[0], _ptr(slots), ctypes.byref(orow),
+                                           _stream(stream)), "gr_linear_attention_step")
+    return o
+
+
+def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              log_decay: torch.Tensor, scale: float | None = None,
+                              seq_starts: torch.Tensor | None = None,
+                              state: torch.Tensor | None = None,
+                              dstate: torch.Tensor | None = None, out=None,
+                              workspace: torch.Tensor | None = None, stream=None):
+    """gr_linear_attention_backward: (dq, dk, dv, dstate_in) from do [N, H, dv] and, optionally, the
+    gradient dstate [B, H, dk, dv] of state_out. dq, dk, dv come in q's dtype (out: a triple to write,
+    strided views allowed); dstate_in is None unless dstate or state is given."""
+    B = _seqs(seq_starts)
+    m, rows = _mixer_desc(q, k, v, log_decay, scale, B)
+    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
+    _f32(state, "state", (B, H, dk, dv))
+    _f32(dstate, "dstate", (B, H, dk, dv))
+    dorow = _rows(do, "do", N, H, dv, q.dtype)
+    if out is None:
+        out = [torch.empty((N, H, d), dtype=q.dtype, device=q.device) for d in (dk, dk, dv)]
+    outs = [_rows(t, n, N, H, d, q.dtype)
+            for t, n, d in zip(out, ("dq", "dk", "dv"), (dk, dk, dv))]
+    dstate_in = None
+    if state is not None or dstate is not None:
+        dstate_in = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    wp, wn, _keep = _mixer_ws(m, 1, workspace, q.device, stream)
+    r = [ctypes.byref(x) for x in (dorow, *rows)]
+    w = [ctypes.byref(x) for x in outs]
+    _check(load().gr_linear_attention_backward(ctypes.byref(m), *r, _ptr(log_decay),
+                                               _ptr(seq_starts), _ptr(state), _ptr(dstate), *w,
+                                               _ptr(dstate_in), wp, wn, _stream(stream)),
+           "gr_linear_attention_backward")
+    return (*out, dstate_in)
