@@ -100,7 +100,7 @@ struct Rows {
 };
 
 bool tc_shape(const gr_mixer* m) {
-    return kMixTc && m->dtype == GR_BF16 && (m->d_key == 64 || m->d_key == 128) &&
+    return m->dtype == GR_BF16 && (m->d_key == 64 || m->d_key == 128) &&
            (m->d_value == 64 || m->d_value == 128);
 }
 

@@ -53,8 +53,8 @@ __device__ __forceinline__ float decay_pow(float log_decay, int64_t n) {
 // CUDA-core form: every type, head size and length (gr_mixer.cu).
 cudaError_t launch_mix_simt(const MixArgs& p, cudaStream_t st);
 
-// Tensor-core form (gr_mixer_tc.cu): bf16, da and dc 64 or 128. Not built yet.
-constexpr bool kMixTc = false;
+// Tensor-core form (gr_mixer_tc.cu): bf16, da and dc 64 or 128. The workspace holds
+// the segments' states where a prompt is cut.
 bool mix_tc_supported(const MixArgs& p);
 size_t mix_tc_workspace(int64_t n_tokens, int n_seqs, int n_heads, int da, int dc);
 cudaError_t launch_mix_tc(const MixArgs& p, void* workspace, cudaStream_t st);

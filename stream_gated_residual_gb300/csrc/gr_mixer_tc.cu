@@ -1,7 +1,891 @@
+// Linear attention with a decay for each head on the 5th-generation tensor cores (tcgen05,
+// accumulators in tensor memory, operands staged by TMA): bf16 rows, head sizes 64 and 128. The
+// masked, decayed product of gr_mixer.h, in chunks of 128 tokens; a prompt and each of its three
+// gradients is one pass of it.
+//
+// A chunk's rows i = 0..127 (λ the head's decay, M the state before the chunk):
+//     P_ij  = intra λ^{i−j} (a_i·b_j) for j <= i                 MMA 1, then WG A (mask, decay, bf16)
+//     out_i = Σ_j P_ij c_j + inter λ^{i+1} (Mᵀ a_i)              MMA 4 and MMA 2, then WG A
+//     M'    = λ^len M + Σ_j b_j (upd λ^{len−1−j} c_j)ᵀ           MMA 3 (WG B scales c), then WG B
+// (backwards in time the exponents run the other way.)
+//
+// The state M stays in registers, in fp32, for all chunks of a segment. Its update is a product of
+// bf16 operands, so the decayed values are split into three bf16 terms (24 bits together): the
+// state's error is that of fp32. P and the copy of M that the outputs read are rounded to bf16
+// once, 2^-9 of relative error each in the mean, as the output's own rounding.
+//
+// One CTA an SM (its shared memory and all 512 columns of tensor memory); bytes bound it: a chunk
+// moves 128 KB at head size 128 and takes 21 Mflop on the tensor cores, a quarter of the time its
+// bytes take. Prompts with too few heads and sequences to fill the SMs are cut into segments: a first
+// launch forms each segment's own sum, a scan turns the sums into the states the segments start
+// from, and the pass runs on all segments at once.
+//
+// Warps: 0 TMA producer, 1 MMA issuer (owns the tensor memory), 4-7 WG A (scores and outputs),
+// 8-11 WG B (decayed values and state). Every mbarrier wait is bounded; when one runs out the
+// status bit is set, all roles leave their loops, and copies and MMAs in flight are waited for.
+#include <math.h>
+#include <string.h>
+
+#include "gr_internal.h"
 #include "gr_mixer.h"
+#include "gr_ptx.cuh"
+#include "gr_tc.cuh"
+
 namespace gr {
-bool mix_tc_supported(const MixArgs&) { return false; }
-size_t mix_tc_workspace(int64_t, int, int, int, int) { return 0; }
-cudaError_t launch_mix_tc(const MixArgs&, void*, cudaStream_t) { return cudaErrorNotSupported; }
-int mixer_status(bool) { return 0; }
+namespace {
+
+constexpr int kChunk = 128;
+constexpr int kBox = kChunk * 128;        // 128 rows of 64 bf16 channels
+constexpr int kThreads = 384;
+constexpr int kSub = 16;                  // tokens of one step of the state's MMA
+constexpr int kSms = 152;                 // segments are planned for this many CTAs
+
+// Tensor-memory columns: scores (then P in place), Σ P c, Mᵀ a, the state's update.
+constexpr uint32_t kColS = 0, kColO = 128, kColE = 256, kColU = 384;
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzled layout: 64 elements
+// of M or N in each 128-byte row, a row for each k. Leading byte offset: between blocks of 64
+// elements of M or N; stride byte offset: between groups of 8 k (1024, one swizzle atom).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFFu);
+    d |= uint64_t((block_bytes >> 4) & 0x3FFFu) << 16;
+    d |= uint64_t((1024u >> 4) & 0x3FFFu) << 32;
+    d |= uint64_t(1u) << 46;
+    d |= uint64_t(2u) << 61;
+    return d;
+}
+constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;   // A, B given MN-major
+
+template <int DA, int DC> struct Smem {
+    static constexpr int kA = DA / 64 * kBox, kB = kA, kC = DC / 64 * kBox;
+    static constexpr int kTerm = DC / 64 * kSub * 128;   // one bf16 term of a step's values
+    static constexpr int kV = 3 * kTerm;
+    static constexpr int kM = DC / 64 * DA * 128;
+    static constexpr int b = kA, c = b + 2 * kB, v = c + 2 * kC, m = v + 2 * kV, aux = m + kM;
+    static constexpr int kAux = 2048;
+    // a head size of 64 still runs MMAs over 128 rows of b: the second 64-channel block it names
+    // is the 16 KB behind the tile, whatever they hold, and its result rows are not used
+    static constexpr int total = aux + kAux + 1024;
+};
+
+struct Aux {
+    uint64_t a_full, a_empty, b_full[2], b_empty[2], c_full[2], c_empty[2];
+    uint64_t s_full, p_ready, o_full, o_free, v_ready[2], v_free[2], u_full, u_free, m_ready, m_free,
+        c_seen, c_clean[2], done;
+    uint32_t tmem;
+    int dead;
+    int seq, seg;
+    float pw[kChunk + 4];      // λ^0 .. λ^128
+    float rev[32];             // λ^31 .. λ^0
+    int bad[2];                // n + 1 when chunk n's values are not all finite (by n & 1)
+    int first[2][128];         // by column: the first such row, in the order of time
+};
+static_assert(sizeof(Aux) <= 2048, "aux");
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    const uint32_t a = smem_u32(bar);
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (ok) return true;
+        if (*dead) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            *dead = 1;
+            atomicOr(&g_wait_status, 1u);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+// The same for a whole warp: the answer is the same in all lanes, which have come together again.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    return __all_sync(0xffffffffu, wait(bar, parity, dead));
+}
+
+// 32 bytes at once: a thread's own row is written in whole sectors.
+__device__ __forceinline__ void st_row32(void* p, const uint32_t (&u)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ bool not_finite(uint32_t u) {
+    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+
+// A bf16 pair times w as three bf16 pairs: each takes what the ones before left of the fp32 product.
+__device__ __forceinline__ void split3(uint32_t u, float w, uint32_t& t0, uint32_t& t1,
+                                       uint32_t& t2) {
+    float x = lo_f(u) * w, y = hi_f(u) * w;
+    t0 = pack_bf2(x, y);
+    x -= lo_f(t0), y -= hi_f(t0);
+    t1 = pack_bf2(x, y);
+    x -= lo_f(t1), y -= hi_f(t1);
+    t2 = pack_bf2(x, y);
+}
+
+// Where a CTA works: segment `seg` (in the order of time it is processed) of sequence `seq`. Every
+// sequence has at least one segment, so that an empty one passes its state on.
+struct Segments {
+    int per_seg;   // chunks of a segment
+    __device__ __forceinline__ int count(int64_t begin, int64_t end) const {
+        const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
+        const int64_t n = (chunks + per_seg - 1) / per_seg;
+        return n > 0 ? int(n) : 1;
+    }
+};
+
+// The whole warp finds the sequence that holds segment `want`, 32 sequences at a time.
+__device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& sg, int want, int& seq,
+                                             int& seg) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        int n = 0;
+        if (b < p.n_seqs) {
+            int64_t x, y;
+            mix_span(p, b, x, y);
+            n = sg.count(x, y);
+        }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const bool mine = n > 0 && want >= before + inc - n && want < before + inc;
+        const unsigned hit = __ballot_sync(0xffffffffu, mine);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            seq = b0 + l;
+            seg = want - before - (__shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, n, l));
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
+}
+
+// kSum: only the segment's own sum (no outputs), written to slot `unit`; else the pass, which reads
+// its first state from slot unit − H (the segment before) or from m_in.
+template <int DA, int DC, bool kSum>
+__global__ void __launch_bounds__(kThreads, 1)
+mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmC, const MixArgs p, const Segments sg,
+              float* __restrict__ slots, const float* __restrict__ firsts, int split) {
+    using S = Smem<DA, DC>;
+    extern __shared__ __align__(1024) char raw[];
+    char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);   // the swizzle's atoms
+    Aux& x = *reinterpret_cast<Aux*>(sm + S::aux);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x, h = unit % p.n_heads;
+    const float g = p.log_decay[h];
+
+    if (warp == 0) {
+        int seq = 0, seg = 0;
+        const bool found = find_segment(p, sg, unit / p.n_heads, seq, seg);
+        if (lane == 0) {
+            x.seq = found ? seq : -1;
+            x.seg = seg;
+            x.dead = 0;
+            x.bad[0] = x.bad[1] = 0;
+            mbar_init(&x.a_full, 1), mbar_init(&x.a_empty, 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&x.b_full[i], 1), mbar_init(&x.b_empty[i], 1);
+                mbar_init(&x.c_full[i], 1), mbar_init(&x.c_empty[i], 1);
+                mbar_init(&x.v_ready[i], 4), mbar_init(&x.v_free[i], 1);
+            }
+            mbar_init(&x.s_full, 1), mbar_init(&x.p_ready, 4), mbar_init(&x.o_full, 2);
+            mbar_init(&x.o_free, 4), mbar_init(&x.u_full, 1), mbar_init(&x.u_free, 4);
+            mbar_init(&x.m_ready, 4), mbar_init(&x.m_free, 1), mbar_init(&x.c_seen, 4);
+            mbar_init(&x.c_clean[0], 4), mbar_init(&x.c_clean[1], 4);
+            mbar_init(&x.done, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == 1) {
+        tmem_alloc(&x.tmem, 512);
+        tmem_relinquish();
+    } else {
+        for (int i = tid - 64; i <= kChunk; i += kThreads - 64) x.pw[i] = decay_pow(g, i);
+        for (int i = tid - 64; i < 32; i += kThreads - 64) x.rev[i] = decay_pow(g, 31 - i);
+    }
+    __syncthreads();
+    if (kSum) dep_launch_dependents();
+    tc_fence_after();
+    const uint32_t tm = x.tmem;
+    const int seq = x.seq, seg = x.seg;
+    int64_t begin = 0, end = 0;
+    if (seq >= 0) mix_span(p, seq, begin, end);
+    const int64_t all = (end - begin + kChunk - 1) / kChunk;   // the sequence's chunks
+    const int64_t n0 = int64_t(seg) * sg.per_seg;              // the segment's first, in time
+    const bool last_seg = n0 + sg.per_seg >= all;
+    int chunks = int(min(int64_t(sg.per_seg), all - n0));
+    if (seq < 0 || chunks < 0 || (kSum && last_seg)) chunks = 0;
+    const bool idle = seq < 0 || (kSum && last_seg);
+    const bool rev = p.reverse;
+    // the chunk at step n of this segment: its first row, its rows, and whether the state enters
+    // its last token undecayed
+    auto row_of = [&](int n) { return begin + (rev ? all - 1 - (n0 + n) : n0 + n) * kChunk; };
+    auto len_of = [&](int64_t row) { return int(min(int64_t(kChunk), end - row)); };
+    const bool from_slot = seg > 0;
+    const bool has_in = !kSum && (from_slot || p.m_in != nullptr);
+    // whether the state after step n is still read (by the next chunk, or as a result)
+    const bool wants_last = kSum || (last_seg && p.m_out != nullptr);
+
+    if (warp < 4) {
+        reg_dec<72>();
+        if (warp == 0 && lane == 0) {
+            // ---- producer -----------------------------------------------------------------------
+            int n = 0;
+            for (; n < chunks; ++n) {
+                const int row = int(row_of(n));
+                const int st = n & 1;
+                const uint32_t use2 = uint32_t(n >> 1) & 1u;
+                if (n >= 2 && !wait(&x.b_empty[st], use2 ^ 1u, &x.dead)) break;
+                mbar_expect_tx(&x.b_full[st], S::kB);
+#pragma unroll
+                for (int k = 0; k < DA / 64; ++k)
+                    tma_load_3d(sm + S::b + st * S::kB + k * kBox, &tmB, k * 64, h, row, &x.b_full[st]);
+                if (!kSum) {
+                    if (n >= 1 && !wait(&x.a_empty, uint32_t(n - 1) & 1u, &x.dead)) {
+                        ++n;
+                        break;
+                    }
+                    mbar_expect_tx(&x.a_full, S::kA);
+#pragma unroll
+                    for (int k = 0; k < DA / 64; ++k)
+                        tma_load_3d(sm + k * kBox, &tmA, k * 64, h, row, &x.a_full);
+                }
+                if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) {
+                    ++n;
+                    break;
+                }
+                mbar_expect_tx(&x.c_full[st], S::kC);
+#pragma unroll
+                for (int k = 0; k < DC / 64; ++k)
+                    tma_load_3d(sm + S::c + st * S::kC + k * kBox, &tmC, k * 64, h, row, &x.c_full[st]);
+            }
+            if (x.dead) {
+                // nobody consumes any more: let every copy land before the memory is given up
+                const long long t0 = clock64();
+                while (clock64() - t0 < kWaitLimit / 100) {
+                }
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ---- MMA issuer ---------------------------------------------------------------------
+            const uint32_t base = smem_u32(sm);
+            const uint32_t a0 = base, m0 = base + S::m;
+            constexpr uint32_t iS = idesc_bf16_f32(128, 128);
+            constexpr uint32_t iE = idesc_bf16_f32(128, DC) | kMnB;
+            constexpr uint32_t iU = idesc_bf16_f32(128, DC) | kMnA | kMnB;
+            uint32_t v_use = 0;    // steps of the state's MMA so far
+            uint32_t u_n = 0, e_n = 0;
+            for (int n = 0; n < chunks; ++n) {
+                const int st = n & 1;
+                const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
+                const uint32_t b0 = base + S::b + st * S::kB, c0 = base + S::c + st * S::kC;
+                const bool read_m = !kSum && (n > 0 || has_in);
+                const bool need_u = n + 1 < chunks || wants_last;
+                if (!wait(&x.b_full[st], par2, &x.dead)) break;
+                if (!kSum) {
+                    if (!wait(&x.a_full, par, &x.dead)) break;
+                    // the scores take the place of the last chunk's P
+                    if (n > 0 && !wait(&x.o_full, par ^ 1u, &x.dead)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < DA / 16; ++k) {
+                        const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
+                        tc_mma(tm + kColS, sdesc_sw128(a0 + off), sdesc_sw128(b0 + off), iS, k > 0);
+                    }
+                    tc_commit(&x.s_full);
+                    if (read_m) {
+                        if (!wait(&x.m_ready, e_n & 1u, &x.dead)) break;
+                        // the last chunk's outputs have been read
+                        if (n > 0 && !wait(&x.o_free, par ^ 1u, &x.dead)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < DA / 16; ++k) {
+                            const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
+                            tc_mma(tm + kColE, sdesc_sw128(a0 + off), sdesc_mn(m0 + k * 2048, DA * 128),
+                                   iE, k > 0);
+                        }
+                        tc_commit(&x.m_free);
+                        ++e_n;
+                    }
+                    tc_commit(&x.a_empty);
+                }
+                if (need_u) {
+                    if (u_n > 0 && !wait(&x.u_free, (u_n - 1) & 1u, &x.dead)) break;
+                    bool ok = true;
+                    for (int s = 0; s < kChunk / kSub; ++s, ++v_use) {
+                        const uint32_t buf = v_use & 1u;
+                        if (!(ok = wait(&x.v_ready[buf], (v_use >> 1) & 1u, &x.dead))) break;
+                        tc_fence_after();
+                        const uint64_t ad = sdesc_mn(b0 + s * 2048, kBox);
+                        const uint32_t v0 = base + S::v + buf * S::kV;
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            tc_mma(tm + kColU, ad, sdesc_mn(v0 + t * S::kTerm, kSub * 128), iU,
+                                   s > 0 || t > 0);
+                        tc_commit(&x.v_free[buf]);
+                    }
+                    if (!ok) break;
+                    tc_commit(&x.u_full);
+                    ++u_n;
+                }
+                tc_commit(&x.b_empty[st]);
+                if (!kSum) {
+                    if (!wait(&x.c_clean[st], par2, &x.dead)) break;
+                    // hands on what c_clean told (x.bad, x.first) with the outputs
+                    mbar_arrive(&x.o_full);
+                    if (n > 0 && !wait(&x.o_free, par ^ 1u, &x.dead)) break;
+                    if (!wait(&x.p_ready, par, &x.dead)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        tc_mma_ts(tm + kColO, tm + kColS + k * 8, sdesc_mn(c0 + k * 2048, kBox), iE, k > 0);
+                    tc_commit(&x.o_full);
+                }
+                tc_commit(&x.c_empty[st]);
+            }
+            tc_commit(&x.done);
+            int never = 0;
+            wait(&x.done, 0, &never);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        reg_dec<160>();
+        if (!kSum) {
+            // ---- WG A: scores to P, outputs ---------------------------------------------------------
+            const int wq = warp - 4, i = wq * 32 + lane;
+            const uint32_t tl = tm + (uint32_t(wq * 32) << 16);
+            char* out0 = static_cast<char*>(p.out.p) + int64_t(h) * p.out.hs * 2;
+            const bool wide = ((reinterpret_cast<uintptr_t>(out0) | uintptr_t(p.out.ts * 2)) & 31u) == 0;
+            for (int n = 0; n < chunks; ++n) {
+                const uint32_t par = uint32_t(n) & 1u;
+                const int64_t row = row_of(n);
+                const int len = len_of(row);
+                const int late = rev && seg == 0 && n == 0 ? 1 : 0;
+                const bool read_m = n > 0 || has_in;
+                if (!wait_warp(&x.s_full, par, &x.dead)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int jb = 0; jb < 4; ++jb) {
+                    uint32_t r[32], q[16];
+                    const bool off = rev ? jb > wq : jb < wq;
+                    if (off || jb == wq) {
+                        tmem_ld32(tl + kColS + jb * 32, r);
+                        tmem_wait32(r);
+                    }
+                    if (off) {
+                        // λ^|i−j| as the row's distance to the block times the column's within it
+                        const float rw = p.intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
+                        const float* cw = rev ? x.pw : x.rev;
+                        const int live = len - jb * 32;      // columns that hold the chunk's rows
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float u = __uint_as_float(r[j]) * (rw * cw[j]);
+                            float v = __uint_as_float(r[j + 1]) * (rw * cw[j + 1]);
+                            if (j >= live) u = 0.0f;
+                            if (j + 1 >= live) v = 0.0f;
+                            q[j >> 1] = pack_bf2(u, v);
+                        }
+                    } else if (jb == wq) {
+                        const int live = len - jb * 32;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const int d0 = rev ? j - lane : lane - j, d1 = rev ? d0 + 1 : d0 - 1;
+                            float u = __uint_as_float(r[j]) * (p.intra * x.pw[max(d0, 0)]);
+                            float v = __uint_as_float(r[j + 1]) * (p.intra * x.pw[max(d1, 0)]);
+                            if (d0 < 0 || j >= live) u = 0.0f;
+                            if (d1 < 0 || j + 1 >= live) v = 0.0f;
+                            q[j >> 1] = pack_bf2(u, v);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) q[j] = 0;
+                    }
+                    // P's columns lie below the scores that are still to be read
+                    tmem_st16(tl + kColS + jb * 16, q);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.p_ready);
+                if (!wait_warp(&x.o_full, par, &x.dead)) break;
+                tc_fence_after();
+                const bool bad = x.bad[par] == n + 1;
+                const bool live = i < len;
+                const float ew = live ? p.inter * x.pw[rev ? len - i - late : i + 1] : 0.0f;
+                char* dst = out0 + (row + i) * p.out.ts * 2;
+                const int ti = rev ? kChunk - 1 - i : i;
+#pragma unroll 1
+                for (int e = 0; e < DC; e += 32) {
+                    uint32_t o[32], m[32];
+                    tmem_ld32(tl + kColO + e, o);
+                    if (read_m) {
+                        tmem_ld32(tl + kColE + e, m);
+                        tmem_wait32(o);
+                        tmem_wait32(m);
+                    } else {
+                        tmem_wait32(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) m[k] = 0;
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (ti >= x.first[par][e + k]) o[k] = 0x7fffffffu;
+                    }
+                    if (e + 32 == DC) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&x.o_free);
+                    }
+                    if (live) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            u[k] = pack_bf2(
+                                fmaf(ew, __uint_as_float(m[2 * k]), __uint_as_float(o[2 * k])),
+                                fmaf(ew, __uint_as_float(m[2 * k + 1]), __uint_as_float(o[2 * k + 1])));
+                        if (wide) {
+                            const uint32_t u0[8] = {u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]};
+                            const uint32_t u1[8] = {u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]};
+                            st_row32(dst + e * 2, u0);
+                            st_row32(dst + e * 2 + 32, u1);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4*>(dst + e * 2 + 16 * k) =
+                                    make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        reg_inc<240>();
+        // ---- WG B: decayed values, the state ---------------------------------------------------------
+        const int wq = warp - 8, t = tid - 256, d = t;
+        const uint32_t tl = tm + (uint32_t(wq * 32) << 16);
+        const bool owns = d < DA;            // thread d holds the state's row d
+        float M[DC];
+#pragma unroll
+        for (int e = 0; e < DC; ++e) M[e] = 0.0f;
+        const int64_t one = int64_t(DA) * DC;
+        if (!kSum && split) dep_wait();
+        if (has_in && owns && !idle) {
+            const bool copied = firsts && !last_seg;
+            if (from_slot || copied) {
+                const float* from = from_slot ? slots + int64_t(unit - p.n_heads) * one
+                                              : firsts + (int64_t(seq) * p.n_heads + h) * one;
+                const float4* s = reinterpret_cast<const float4*>(from + int64_t(d) * DC);
+#pragma unroll
+                for (int e = 0; e < DC / 4; ++e) {
+                    const float4 v = __ldcg(s + e);
+                    M[4 * e] = v.x, M[4 * e + 1] = v.y, M[4 * e + 2] = v.z, M[4 * e + 3] = v.w;
+                }
+            } else {
+                const float* s = p.m_in + (int64_t(seq) * p.n_heads + h) * one + int64_t(d) * p.mr;
+#pragma unroll
+                for (int e = 0; e < DC; ++e) M[e] = s[int64_t(e) * p.mc];
+            }
+        }
+        // the state as the MMA reads it: row d of 64-column boxes, bf16
+        auto publish = [&]() {
+            if (owns) {
+#pragma unroll
+                for (int k = 0; k < DC / 8; ++k) {
+                    const uint4 u = make_uint4(pack_bf2(M[8 * k], M[8 * k + 1]),
+                                               pack_bf2(M[8 * k + 2], M[8 * k + 3]),
+                                               pack_bf2(M[8 * k + 4], M[8 * k + 5]),
+                                               pack_bf2(M[8 * k + 6], M[8 * k + 7]));
+                    *reinterpret_cast<uint4*>(sm + S::m + (k >> 3) * (DA * 128) + swz(d, k & 7)) = u;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.m_ready);
+        };
+        if (has_in && chunks > 0) publish();
+        uint32_t v_use = 0, u_n = 0, published = has_in ? 1u : 0u;
+        const int vr = t >> 3, vc = t & 7;   // this thread's row of a step and 16-byte column
+        int n = 0;
+        for (; n < chunks; ++n) {
+            const int st = n & 1;
+            const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
+            const int len = len_of(row_of(n));
+            const int late = rev && seg == 0 && n == 0 ? 1 : 0;
+            const bool need_u = n + 1 < chunks || wants_last;
+            char* ct = sm + S::c + st * S::kC;
+            char* bt = sm + S::b + st * S::kB;
+            if (!wait_warp(&x.c_full[st], par2, &x.dead)) break;
+            if (len < kChunk && !wait_warp(&x.b_full[st], par2, &x.dead)) break;
+            bool odd = false, ok = true, bad = false;
+            for (int s = 0; s < kChunk / kSub; ++s) {
+                const int r = s * kSub + vr;
+                if (r >= len) {
+                    // rows past the sequence's end may hold anything: they become zero
+#pragma unroll
+                    for (int k = 0; k < DC / 64; ++k)
+                        *reinterpret_cast<uint4*>(ct + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < DA / 64; ++k)
+                        *reinterpret_cast<uint4*>(bt + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
+                }
+                uint4 u[DC / 64];
+#pragma unroll
+                for (int k = 0; k < DC / 64; ++k) {
+                    u[k] = *reinterpret_cast<const uint4*>(ct + k * kBox + swz(r, vc));
+                    odd |= not_finite(u[k].x) | not_finite(u[k].y) | not_finite(u[k].z) |
+                           not_finite(u[k].w);
+                }
+                if (s == kChunk / kSub - 1) {
+                    // all values seen: a chunk with one that is not finite takes the slow way before
+                    // its product is formed (0 times such a value would reach earlier rows)
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (!kSum) {
+                        if (lane == 0) {
+                            if (odd) x.bad[par] = n + 1;
+                            mbar_arrive(&x.c_seen);
+                        }
+                        if (!(ok = wait_warp(&x.c_seen, par, &x.dead))) break;
+                        bad = x.bad[par] == n + 1;
+                    }
+                    if (bad) {
+                        for (int e = t; e < DC; e += 128) {
+                            int f = kChunk;
+                            for (int j = 0; j < len; ++j) {
+                                unsigned short* q = reinterpret_cast<unsigned short*>(
+                                                        ct + (e >> 6) * kBox + swz(j, (e >> 3) & 7)) +
+                                                    (e & 7);
+                                if ((*q & 0x7f80u) != 0x7f80u) continue;
+                                f = min(f, rev ? kChunk - 1 - j : j);
+                                *q = 0;   // the product is formed without it
+                            }
+                            x.first[par][e] = f;
+                        }
+                    }
+                }
+                if (need_u) {
+                    const uint32_t buf = v_use & 1u;
+                    if (v_use >= 2 && !(ok = wait_warp(&x.v_free[buf], ((v_use >> 1) & 1u) ^ 1u, &x.dead)))
+                        break;
+                    const float w = p.upd * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
+                    char* v0 = sm + S::v + buf * S::kV;
+#pragma unroll
+                    for (int k = 0; k < DC / 64; ++k) {
+                        uint4 a, b, c;
+                        split3(u[k].x, w, a.x, b.x, c.x);
+                        split3(u[k].y, w, a.y, b.y, c.y);
+                        split3(u[k].z, w, a.z, b.z, c.z);
+                        split3(u[k].w, w, a.w, b.w, c.w);
+                        char* q = v0 + k * (kSub * 128) + swz(vr, vc);
+                        *reinterpret_cast<uint4*>(q) = a;
+                        *reinterpret_cast<uint4*>(q + S::kTerm) = b;
+                        *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x.v_ready[buf]);
+                    ++v_use;
+                }
+            }
+            if (!ok) break;
+            if (!kSum) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.c_clean[st]);
+            }
+            if (need_u) {
+                const float keep = x.pw[len - late];
+                if (!wait_warp(&x.u_full, u_n & 1u, &x.dead)) break;
+                ++u_n;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < DC; e += 32) {
+                    uint32_t u[32];
+                    tmem_ld32(tl + kColU + e, u);
+                    tmem_wait32(u);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) M[e + k] = fmaf(keep, M[e + k], __uint_as_float(u[k]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.u_free);
+                if (!kSum && n + 1 < chunks) {
+                    if (published > 0 && !wait_warp(&x.m_free, (published - 1) & 1u, &x.dead)) break;
+                    publish();
+                    ++published;
+                }
+            }
+        }
+        if (n == chunks && owns && !idle) {
+            if (kSum) {
+                float* s = slots + int64_t(unit) * one + int64_t(d) * DC;
+#pragma unroll
+                for (int e = 0; e < DC; e += 8) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(M[e + k]);
+                    st_row32(s + e, u);
+                }
+            } else if (last_seg && p.m_out) {
+                // backwards, λ once more takes the gradient to the state before the first token
+                const float w = rev && end > begin ? x.pw[1] : 1.0f;
+                float* s = p.m_out + (int64_t(seq) * p.n_heads + h) * one + int64_t(d) * p.mr;
+                if (p.mc == 1) {
+#pragma unroll
+                    for (int e = 0; e < DC; e += 4)
+                        *reinterpret_cast<float4*>(s + e) =
+                            make_float4(w * M[e], w * M[e + 1], w * M[e + 2], w * M[e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DC; ++e) s[int64_t(e) * p.mc] = w * M[e];
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// The segments' sums to the states after them, in place: slot s <- λ^len_s (state before s) + slot s.
+// One thread four elements of a (sequence, head); the last segment's slot is not used. `firsts`, when
+// m_out is m_in itself, takes a copy of m_in for the first segments of sequences of several: their
+// last segment may be done before the first one starts.
+__global__ void __launch_bounds__(256)
+mix_scan_kernel(const MixArgs p, const Segments sg, float* __restrict__ slots,
+                float* __restrict__ firsts) {
+    dep_wait();
+    dep_launch_dependents();
+    const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
+    const int one = p.da * p.dc;
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    int64_t begin, end;
+    mix_span(p, b, begin, end);
+    const int n = sg.count(begin, end);
+    if (n < 2 || at >= one) return;
+    __shared__ int first;
+    // the segments of the sequences before this one
+    if (threadIdx.x < 32) {
+        int sum = 0;
+        for (int k = threadIdx.x; k < b; k += 32) {
+            int64_t x, y;
+            mix_span(p, k, x, y);
+            sum += sg.count(x, y);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) first = sum;
+    }
+    __syncthreads();
+    const float g = p.log_decay[h];
+    float m[4] = {};
+    if (p.m_in) {
+        const float* s = p.m_in + (int64_t(b) * p.n_heads + h) * one;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = (at + k) / p.dc, j = (at + k) - i * p.dc;
+            m[k] = s[int64_t(i) * p.mr + int64_t(j) * p.mc];
+        }
+    }
+    if (firsts)
+        *reinterpret_cast<float4*>(firsts + (int64_t(b) * p.n_heads + h) * one + at) =
+            make_float4(m[0], m[1], m[2], m[3]);
+    const int64_t full = int64_t(sg.per_seg) * kChunk;
+    // backwards the first segment holds the sequence's partial chunk, and its state enters undecayed
+    const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
+    const int64_t len0 = p.reverse ? full - (chunks * kChunk - (end - begin)) - 1 : full;
+    const float l0 = decay_pow(g, len0), lf = decay_pow(g, full);
+    const int64_t step = int64_t(p.n_heads) * one;
+    float* s = slots + (int64_t(first) * p.n_heads + h) * one + at;
+    constexpr int kU = 4;
+    for (int i = 0; i < n - 1; i += kU) {
+        float4 v[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+            if (i + k < n - 1) v[k] = __ldcg(reinterpret_cast<const float4*>(s + (i + k) * step));
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+            if (i + k < n - 1) {
+                const float w = i + k == 0 ? l0 : lf;
+                m[0] = fmaf(w, m[0], v[k].x), m[1] = fmaf(w, m[1], v[k].y);
+                m[2] = fmaf(w, m[2], v[k].z), m[3] = fmaf(w, m[3], v[k].w);
+                *reinterpret_cast<float4*>(s + (i + k) * step) = make_float4(m[0], m[1], m[2], m[3]);
+            }
+    }
+}
+
+// Chunks a segment: sequences of the mean length, cut so that the estimated time is least. A unit (a
+// segment of a head) takes its chunks one after another, one unit an SM at a time; cutting a sequence
+// costs a second pass over b and c of all but its last segment, and two launches.
+int plan_segments(int64_t N, int n_seqs, int H) {
+    const int64_t mean = (N + n_seqs - 1) / n_seqs;
+    const int64_t chunks = (mean + kChunk - 1) / kChunk;
+    if (chunks <= 1) return 1;
+    const int64_t rows = int64_t(n_seqs) * H;
+    int64_t most = (6 * kSms + rows - 1) / rows;
+    most = most < chunks ? most : chunks;
+    int64_t best = chunks;
+    double least = 1e300;
+    for (int64_t n = 1; n <= most; ++n) {
+        const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
+        const int64_t waves = (rows * segs + kSms - 1) / kSms;
+        const int64_t waves1 = (rows * (segs - 1) + kSms - 1) / kSms;
+        // in units of a chunk's time (about 3 us): 1.5 a unit to start and drain; sums half a chunk
+        double t = waves * (per + 1.5);
+        if (segs > 1) t += waves1 * (0.5 * per + 1.5) + 2.0;
+        if (t < least) least = t, best = per;
+    }
+    return int(best);
+}
+
+int64_t most_units(int64_t N, int n_seqs, int H, int per_seg) {
+    return (N / (int64_t(per_seg) * kChunk) + n_seqs) * H;
+}
+
+bool map_rows(CUtensorMap* m, const MixRows& r, int64_t N, int H, int d) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(H), cuuint64_t(N)};
+    const cuuint64_t strides[2] = {cuuint64_t(r.hs) * 2, cuuint64_t(r.ts) * 2};
+    const cuuint32_t box[3] = {64, 1, kChunk};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   bool after, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <int DA, int DC>
+cudaError_t run(const MixArgs& p, float* slots, cudaStream_t st) {
+    CUtensorMap ma, mb, mc;
+    if (!map_rows(&ma, p.a, p.n_tokens, p.n_heads, DA) || !map_rows(&mb, p.b, p.n_tokens, p.n_heads, DA) ||
+        !map_rows(&mc, p.c, p.n_tokens, p.n_heads, DC))
+        return cudaErrorInvalidValue;
+    const Segments sg{plan_segments(p.n_tokens, p.n_seqs, p.n_heads)};
+    const dim3 grid(unsigned(most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg)));
+    constexpr int smem = Smem<DA, DC>::total;
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // no sequence is longer than all tokens
+    const bool split = p.n_tokens > int64_t(sg.per_seg) * kChunk;
+    float* firsts =
+        split && p.m_in && p.m_in == p.m_out
+            ? slots + most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg) * int64_t(DA * DC)
+            : nullptr;
+    if (e == cudaSuccess && split) {
+        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = launch(mix_tc_kernel<DA, DC, true>, grid, kThreads, smem, st, false, ma, mb, mc, p, sg,
+                       slots, static_cast<const float*>(nullptr), 1);
+        if (e == cudaSuccess)
+            e = launch(mix_scan_kernel, dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024), 256, 0,
+                       st, true, p, sg, slots, firsts);
+    }
+    if (e == cudaSuccess)
+        e = launch(mix_tc_kernel<DA, DC, false>, grid, kThreads, smem, st, split, ma, mb, mc, p, sg,
+                   slots, static_cast<const float*>(firsts), split ? 1 : 0);
+    return e;
+}
+
+}  // namespace
+
+bool mix_tc_supported(const MixArgs& p) {
+    const int64_t most = int64_t(1) << 38;   // a tensor map's strides are below 2^40 bytes
+    for (const MixRows* r : {&p.a, &p.b, &p.c})
+        if (r->ts > most || r->hs > most) return false;
+    return p.dtype == GR_BF16 && (p.da == 64 || p.da == 128) && (p.dc == 64 || p.dc == 128) &&
+           p.n_tokens > 0 && p.n_seqs > 0 &&
+           most_units(p.n_tokens, p.n_seqs, p.n_heads,
+                      plan_segments(p.n_tokens, p.n_seqs, p.n_heads)) <= 0x7fffffff;
+}
+
+size_t mix_tc_workspace(int64_t N, int n_seqs, int H, int da, int dc) {
+    if (N == 0 || n_seqs == 0) return 0;
+    const int per = plan_segments(N, n_seqs, H);
+    if (N <= int64_t(per) * kChunk) return 0;
+    return align256(size_t(most_units(N, n_seqs, H, per) + int64_t(n_seqs) * H) * da * dc * 4);
+}
+
+cudaError_t launch_mix_tc(const MixArgs& p, void* workspace, cudaStream_t st) {
+    float* slots = static_cast<float*>(workspace);
+    if (p.da == 128) return p.dc == 128 ? run<128, 128>(p, slots, st) : run<128, 64>(p, slots, st);
+    return p.dc == 128 ? run<64, 128>(p, slots, st) : run<64, 64>(p, slots, st);
+}
+
+int mixer_status(bool clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_status, sizeof(v)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbol(g_wait_status, &z, sizeof(z)) != cudaSuccess) return -1;
+    }
+    return int(v);
+}
+
 }  // namespace gr

@@ -146,6 +146,7 @@ def test_mixer_shapes(lib, kw, code):
 
 def test_mixer_paths(lib):
     path = lambda **kw: lib.gr_mixer_path(byref(mixer(**kw)))  # noqa: E731
+    assert path() == path(dk=128, dv=64) == path(dk=128, dv=128) == b"mixer_tc"
     assert path(dk=72) == path(dt=0) == path(dk=256) == b"mixer_simt"
 
 
