@@ -6,7 +6,7 @@
 // A chunk's rows i = 0..127 (λ the head's decay, M the state before the chunk):
 //     P_ij  = intra λ^{i−j} (a_i·b_j) for j <= i                 MMA 1, then WG A (mask, decay, bf16)
 //     out_i = Σ_j P_ij c_j + inter λ^{i+1} (Mᵀ a_i)              MMA 4 and MMA 2, then WG A
-//     M'    = λ^len M + Σ_j b_j (upd λ^{len−1−j} c_j)ᵀ           MMA 3 (WG B scales c), then WG B
+//     M'    = λ^len M + Σ_j b_j (upd λ^{len−1−j} c_j)ᵀ           MMA 3 (WG V0, V1 scale c), then WG M
 // (backwards in time the exponents run the other way.)
 //
 // The state M stays in registers, in fp32, for all chunks of a segment. Its update is a product of
@@ -20,8 +20,9 @@
 // launch forms each segment's own sum, a scan turns the sums into the states the segments start
 // from, and the pass runs on all segments at once.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (owns the tensor memory), 4-7 WG A (scores and outputs),
-// 8-11 WG B (decayed values and state). Every mbarrier wait is bounded; when one runs out the
+// Warps: 0 TMA producer, 1 issuer of the scores' and outputs' MMAs (owns the tensor memory), 2 issuer
+// of the state's MMAs, 4-7 WG A (scores and outputs), 8-15 WG V0 and V1 (decayed values, in turn),
+// 16-19 WG M (the state). The state's chain and the outputs' meet only where MMA 2 reads M. Every mbarrier wait is bounded; when one runs out the
 // status bit is set, all roles leave their loops, and copies and MMAs in flight are waited for.
 #include <math.h>
 #include <string.h>
@@ -36,7 +37,7 @@ namespace {
 
 constexpr int kChunk = 128;
 constexpr int kBox = kChunk * 128;        // 128 rows of 64 bf16 channels
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kSub = 16;                  // tokens of one step of the state's MMA
 constexpr int kSms = 152;                 // segments are planned for this many CTAs
 
@@ -63,7 +64,7 @@ template <int DA, int DC> struct Smem {
     static constexpr int kV = 3 * kTerm;
     static constexpr int kM = DC / 64 * DA * 128;
     static constexpr int b = kA, c = b + 2 * kB, v = c + 2 * kC, m = v + 2 * kV, aux = m + kM;
-    static constexpr int kAux = 2048;
+    static constexpr int kAux = 7168;
     // a head size of 64 still runs MMAs over 128 rows of b: the second 64-channel block it names
     // is the 16 KB behind the tile, whatever they hold, and its result rows are not used
     static constexpr int total = aux + kAux + 1024;
@@ -76,17 +77,22 @@ struct Aux {
     uint32_t tmem;
     int dead;
     int seq, seg;
-    float pw[kChunk + 4];      // λ^0 .. λ^128
-    float rev[32];             // λ^31 .. λ^0
-    int bad[2];                // n + 1 when chunk n's values are not all finite (by n & 1)
-    int first[2][128];         // by column: the first such row, in the order of time
+    alignas(16) float pw[kChunk + 4];   // λ^0 .. λ^128
+    alignas(16) float rev[32];          // λ^31 .. λ^0
+    // a block of 32 rows and columns on the diagonal: intra λ^|i−j| (rows 16 bytes off a multiple of
+    // 128, so that the lanes' 16-byte reads of one column group meet no bank twice)
+    alignas(16) float diag[32][36];
+    // By n & 3, which no other chunk writes before chunk n's outputs are out (WG V at chunk n + 3 has
+    // seen PV of n + 1 done, and that waits for the outputs of n):
+    int bad[4];                // n + 1 when chunk n's values are not all finite
+    uint8_t first[4][128];     // by column: the first such row, in the order of time
 };
-static_assert(sizeof(Aux) <= 2048, "aux");
+static_assert(sizeof(Aux) <= 7168, "aux");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
     const uint32_t a = smem_u32(bar);
-    const long long t0 = clock64();
-    for (;;) {
+    long long t0 = 0;
+    for (int k = 0;; ++k) {
         uint32_t ok;
         asm volatile(
             "{\n .reg .pred p;\n"
@@ -97,6 +103,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
             : "memory");
         if (ok) return true;
         if (*dead) return false;
+        if (k == 0) t0 = clock64();
         if (clock64() - t0 > kWaitLimit) {
             *dead = 1;
             atomicOr(&g_wait_status, 1u);
@@ -140,27 +147,42 @@ __device__ __forceinline__ void st_row32(void* p, const uint32_t (&u)[8]) {
                  "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
 }
+// One lane of the (whole) warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
+}
 template <int N> __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 template <int N> __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ bool not_finite(uint32_t u) {
-    return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+// The larger magnitudes of two bf16 pairs, half by half: 0x7f80 or more where one is not finite.
+__device__ __forceinline__ uint32_t most_of(uint32_t m, uint32_t u) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(u & 0x7fff7fffu));
+    return r;
+}
+__device__ __forceinline__ bool not_finite(uint32_t m) {
+    return (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
+}
+__device__ __forceinline__ uint32_t upper_halves(uint64_t v) {
+    return __byte_perm(uint32_t(v), uint32_t(v >> 32), 0x7632);
 }
 
-// A bf16 pair times w as three bf16 pairs: each takes what the ones before left of the fp32 product.
-__device__ __forceinline__ void split3(uint32_t u, float w, uint32_t& t0, uint32_t& t1,
+// A bf16 pair times w as three bf16 pairs: 8 bits of the fp32 product's 24 each, cut off, so that
+// they sum to the product exactly.
+__device__ __forceinline__ void split3(uint32_t u, uint64_t w2, uint32_t& t0, uint32_t& t1,
                                        uint32_t& t2) {
-    float x = lo_f(u) * w, y = hi_f(u) * w;
-    t0 = pack_bf2(x, y);
-    x -= lo_f(t0), y -= hi_f(t0);
-    t1 = pack_bf2(x, y);
-    x -= lo_f(t1), y -= hi_f(t1);
-    t2 = pack_bf2(x, y);
+    const uint64_t keep = 0xffff0000ffff0000ull, minus = f2(-1.0f, -1.0f);
+    uint64_t v = mul2(bf2_to_f2(u), w2);
+    t0 = upper_halves(v);
+    v = fma2(v & keep, minus, v);
+    t1 = upper_halves(v);
+    v = fma2(v & keep, minus, v);
+    t2 = upper_halves(v);
 }
 
 // Where a CTA works: segment `seg` (in the order of time it is processed) of sequence `seq`. Every
@@ -228,19 +250,19 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             x.seq = found ? seq : -1;
             x.seg = seg;
             x.dead = 0;
-            x.bad[0] = x.bad[1] = 0;
+            x.bad[0] = x.bad[1] = x.bad[2] = x.bad[3] = 0;
             mbar_init(&x.a_full, 1), mbar_init(&x.a_empty, 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&x.b_full[i], 1), mbar_init(&x.b_empty[i], 1);
+                mbar_init(&x.b_full[i], 1), mbar_init(&x.b_empty[i], kSum ? 1 : 2);
                 mbar_init(&x.c_full[i], 1), mbar_init(&x.c_empty[i], 1);
                 mbar_init(&x.v_ready[i], 4), mbar_init(&x.v_free[i], 1);
             }
             mbar_init(&x.s_full, 1), mbar_init(&x.p_ready, 4), mbar_init(&x.o_full, 2);
             mbar_init(&x.o_free, 4), mbar_init(&x.u_full, 1), mbar_init(&x.u_free, 4);
-            mbar_init(&x.m_ready, 4), mbar_init(&x.m_free, 1), mbar_init(&x.c_seen, 4);
-            mbar_init(&x.c_clean[0], 4), mbar_init(&x.c_clean[1], 4);
-            mbar_init(&x.done, 1);
+            mbar_init(&x.m_ready, 4), mbar_init(&x.m_free, 1), mbar_init(&x.c_seen, 8);
+            mbar_init(&x.c_clean[0], 8), mbar_init(&x.c_clean[1], 8);
+            mbar_init(&x.done, 2);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     } else if (warp == 1) {
@@ -249,11 +271,15 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     } else {
         for (int i = tid - 64; i <= kChunk; i += kThreads - 64) x.pw[i] = decay_pow(g, i);
         for (int i = tid - 64; i < 32; i += kThreads - 64) x.rev[i] = decay_pow(g, 31 - i);
+        for (int i = tid - 64; i < 1024; i += kThreads - 64) {
+            const int d = (i >> 5) - (i & 31);
+            x.diag[i >> 5][i & 31] = p.intra * decay_pow(g, d < 0 ? -d : d);
+        }
     }
     __syncthreads();
     if (kSum) dep_launch_dependents();
     tc_fence_after();
-    const uint32_t tm = x.tmem;
+    const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
     const int seq = x.seq, seg = x.seg;
     int64_t begin = 0, end = 0;
     if (seq >= 0) mix_span(p, seq, begin, end);
@@ -274,7 +300,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const bool wants_last = kSum || (last_seg && p.m_out != nullptr);
 
     if (warp < 4) {
-        reg_dec<72>();
+        reg_dec<56>();
         if (warp == 0 && lane == 0) {
             // ---- producer -----------------------------------------------------------------------
             int n = 0;
@@ -312,38 +338,40 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 while (clock64() - t0 < kWaitLimit / 100) {
                 }
             }
-        } else if (warp == 1 && lane == 0) {
-            // ---- MMA issuer ---------------------------------------------------------------------
+        } else if (warp == 1) {
+            // ---- scores and outputs -------------------------------------------------------------
+            // The whole warp runs the loop and one lane issues: descriptors and addresses stay in
+            // uniform registers (issued from a branch of one lane, an MMA took about 120 cycles)
+            const bool leader = elect_one();
             const uint32_t base = smem_u32(sm);
             const uint32_t a0 = base, m0 = base + S::m;
             constexpr uint32_t iS = idesc_bf16_f32(128, 128);
             constexpr uint32_t iE = idesc_bf16_f32(128, DC) | kMnB;
-            constexpr uint32_t iU = idesc_bf16_f32(128, DC) | kMnA | kMnB;
-            uint32_t v_use = 0;    // steps of the state's MMA so far
-            uint32_t u_n = 0, e_n = 0;
-            for (int n = 0; n < chunks; ++n) {
+            uint32_t e_n = 0;
+            for (int n = 0; !kSum && n < chunks; ++n) {
                 const int st = n & 1;
                 const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
                 const uint32_t b0 = base + S::b + st * S::kB, c0 = base + S::c + st * S::kC;
-                const bool read_m = !kSum && (n > 0 || has_in);
-                const bool need_u = n + 1 < chunks || wants_last;
-                if (!wait(&x.b_full[st], par2, &x.dead)) break;
-                if (!kSum) {
-                    if (!wait(&x.a_full, par, &x.dead)) break;
-                    // the scores take the place of the last chunk's P
-                    if (n > 0 && !wait(&x.o_full, par ^ 1u, &x.dead)) break;
-                    tc_fence_after();
+                if (!wait_warp(&x.b_full[st], par2, &x.dead)) break;
+                if (!wait_warp(&x.a_full, par, &x.dead)) break;
+                // the scores take the place of the last chunk's P
+                if (n > 0 && !wait_warp(&x.o_full, par ^ 1u, &x.dead)) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < DA / 16; ++k) {
                         const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
                         tc_mma(tm + kColS, sdesc_sw128(a0 + off), sdesc_sw128(b0 + off), iS, k > 0);
                     }
                     tc_commit(&x.s_full);
-                    if (read_m) {
-                        if (!wait(&x.m_ready, e_n & 1u, &x.dead)) break;
-                        // the last chunk's outputs have been read
-                        if (n > 0 && !wait(&x.o_free, par ^ 1u, &x.dead)) break;
-                        tc_fence_after();
+                    tc_commit(&x.b_empty[st]);
+                }
+                if (n > 0 || has_in) {
+                    if (!wait_warp(&x.m_ready, e_n & 1u, &x.dead)) break;
+                    // the last chunk's outputs have been read
+                    if (n > 0 && !wait_warp(&x.o_free, par ^ 1u, &x.dead)) break;
+                    tc_fence_after();
+                    if (leader) {
 #pragma unroll
                         for (int k = 0; k < DA / 16; ++k) {
                             const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
@@ -351,51 +379,72 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                    iE, k > 0);
                         }
                         tc_commit(&x.m_free);
-                        ++e_n;
                     }
-                    tc_commit(&x.a_empty);
+                    ++e_n;
                 }
-                if (need_u) {
-                    if (u_n > 0 && !wait(&x.u_free, (u_n - 1) & 1u, &x.dead)) break;
-                    bool ok = true;
-                    for (int s = 0; s < kChunk / kSub; ++s, ++v_use) {
-                        const uint32_t buf = v_use & 1u;
-                        if (!(ok = wait(&x.v_ready[buf], (v_use >> 1) & 1u, &x.dead))) break;
-                        tc_fence_after();
-                        const uint64_t ad = sdesc_mn(b0 + s * 2048, kBox);
-                        const uint32_t v0 = base + S::v + buf * S::kV;
-#pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            tc_mma(tm + kColU, ad, sdesc_mn(v0 + t * S::kTerm, kSub * 128), iU,
-                                   s > 0 || t > 0);
-                        tc_commit(&x.v_free[buf]);
-                    }
-                    if (!ok) break;
-                    tc_commit(&x.u_full);
-                    ++u_n;
-                }
-                tc_commit(&x.b_empty[st]);
-                if (!kSum) {
-                    if (!wait(&x.c_clean[st], par2, &x.dead)) break;
-                    // hands on what c_clean told (x.bad, x.first) with the outputs
-                    mbar_arrive(&x.o_full);
-                    if (n > 0 && !wait(&x.o_free, par ^ 1u, &x.dead)) break;
-                    if (!wait(&x.p_ready, par, &x.dead)) break;
-                    tc_fence_after();
+                if (leader) tc_commit(&x.a_empty);
+                if (!wait_warp(&x.c_clean[st], par2, &x.dead)) break;
+                // hands on what c_clean told (x.bad, x.first) with the outputs
+                if (leader) mbar_arrive(&x.o_full);
+                if (n > 0 && !wait_warp(&x.o_free, par ^ 1u, &x.dead)) break;
+                if (!wait_warp(&x.p_ready, par, &x.dead)) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k)
                         tc_mma_ts(tm + kColO, tm + kColS + k * 8, sdesc_mn(c0 + k * 2048, kBox), iE, k > 0);
                     tc_commit(&x.o_full);
+                    tc_commit(&x.c_empty[st]);
                 }
-                tc_commit(&x.c_empty[st]);
             }
-            tc_commit(&x.done);
+            if (leader) tc_commit(&x.done);
             int never = 0;
-            wait(&x.done, 0, &never);
+            wait_warp(&x.done, 0, &never);
+        } else if (warp == 2) {
+            // ---- the state's update -------------------------------------------------------------
+            const bool leader = elect_one();
+            const uint32_t base = smem_u32(sm);
+            constexpr uint32_t iU = idesc_bf16_f32(128, DC) | kMnA | kMnB;
+            uint32_t v_use = 0;    // rounds of the two buffers so far
+            for (int n = 0; n < chunks; ++n) {
+                const int st = n & 1;
+                const uint32_t b0 = base + S::b + st * S::kB;
+                if (!wait_warp(&x.b_full[st], uint32_t(n >> 1) & 1u, &x.dead)) break;
+                if (n + 1 < chunks || wants_last) {
+                    if (n > 0 && !wait_warp(&x.u_free, uint32_t(n - 1) & 1u, &x.dead)) break;
+                    bool ok = true;
+                    for (int s = 0; ok && s < kChunk / kSub; s += 2, ++v_use) {
+#pragma unroll
+                        for (int buf = 0; buf < 2; ++buf) {
+                            if (!(ok = wait_warp(&x.v_ready[buf], v_use & 1u, &x.dead))) break;
+                            tc_fence_after();
+                            if (leader) {
+                                const uint64_t ad = sdesc_mn(b0 + (s + buf) * 2048, kBox);
+#pragma unroll
+                                for (int t = 0; t < 3; ++t)
+                                    tc_mma(tm + kColU, ad,
+                                           sdesc_mn(base + S::v + buf * S::kV + t * S::kTerm, kSub * 128),
+                                           iU, s > 0 || buf > 0 || t > 0);
+                                tc_commit(&x.v_free[buf]);
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (leader) tc_commit(&x.u_full);
+                }
+                if (leader) {
+                    tc_commit(&x.b_empty[st]);
+                    if (kSum) tc_commit(&x.c_empty[st]);
+                }
+            }
+            if (leader) tc_commit(&x.done);
+            int never = 0;
+            wait_warp(&x.done, 0, &never);
         }
         __syncwarp();
     } else if (warp < 8) {
-        reg_dec<160>();
+        // 56 + 120 + 2 · 56 + 192 registers a thread: the launch's 5 · 96
+        reg_inc<120>();
         if (!kSum) {
             // ---- WG A: scores to P, outputs ---------------------------------------------------------
             const int wq = warp - 4, i = wq * 32 + lane;
@@ -414,37 +463,52 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 for (int jb = 0; jb < 4; ++jb) {
                     uint32_t r[32], q[16];
                     const bool off = rev ? jb > wq : jb < wq;
-                    if (off || jb == wq) {
-                        tmem_ld32(tl + kColS + jb * 32, r);
-                        tmem_wait32(r);
-                    }
+                    if (off || jb == wq) tmem_ld32(tl + kColS + jb * 32, r);
                     if (off) {
                         // λ^|i−j| as the row's distance to the block times the column's within it
                         const float rw = p.intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
-                        const float* cw = rev ? x.pw : x.rev;
-                        const int live = len - jb * 32;      // columns that hold the chunk's rows
+                        const float4* cw = reinterpret_cast<const float4*>(rev ? x.pw : x.rev);
+                        const uint64_t rw2 = f2(rw, rw);
+                        tmem_wait32(r);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float u = __uint_as_float(r[j]) * (rw * cw[j]);
-                            float v = __uint_as_float(r[j + 1]) * (rw * cw[j + 1]);
-                            if (j >= live) u = 0.0f;
-                            if (j + 1 >= live) v = 0.0f;
-                            q[j >> 1] = pack_bf2(u, v);
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 c = cw[j];
+                            const uint64_t u = f2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+                            const uint64_t v =
+                                f2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+                            q[2 * j] = f2_to_bf2(mul2(u, mul2(f2(c.x, c.y), rw2)));
+                            q[2 * j + 1] = f2_to_bf2(mul2(v, mul2(f2(c.z, c.w), rw2)));
                         }
                     } else if (jb == wq) {
-                        const int live = len - jb * 32;
+                        const float4* cw = reinterpret_cast<const float4*>(x.diag[lane]);
+                        tmem_wait32(r);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const int d0 = rev ? j - lane : lane - j, d1 = rev ? d0 + 1 : d0 - 1;
-                            float u = __uint_as_float(r[j]) * (p.intra * x.pw[max(d0, 0)]);
-                            float v = __uint_as_float(r[j + 1]) * (p.intra * x.pw[max(d1, 0)]);
-                            if (d0 < 0 || j >= live) u = 0.0f;
-                            if (d1 < 0 || j + 1 >= live) v = 0.0f;
-                            q[j >> 1] = pack_bf2(u, v);
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 c = cw[j];
+                            const uint64_t u = f2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+                            const uint64_t v =
+                                f2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+                            q[2 * j] = f2_to_bf2(mul2(u, f2(c.x, c.y)));
+                            q[2 * j + 1] = f2_to_bf2(mul2(v, f2(c.z, c.w)));
+                        }
+                        // the columns of later (backwards: earlier) rows are cut off, whatever they hold
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (rev ? 2 * j < lane : 2 * j + 1 > lane) q[j] &= rev ? 0xffff0000u : 0xffffu;
+                            if (rev ? 2 * j + 1 < lane : 2 * j > lane) q[j] = 0;
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) q[j] = 0;
+                    }
+                    if (rev && len < kChunk) {
+                        // and those past the sequence's end (forwards no valid row reaches them)
+                        const int live = len - jb * 32;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (2 * j + 1 >= live) q[j] &= 0xffffu;
+                            if (2 * j >= live) q[j] = 0;
+                        }
                     }
                     // P's columns lie below the scores that are still to be read
                     tmem_st16(tl + kColS + jb * 16, q);
@@ -455,60 +519,154 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 if (lane == 0) mbar_arrive(&x.p_ready);
                 if (!wait_warp(&x.o_full, par, &x.dead)) break;
                 tc_fence_after();
-                const bool bad = x.bad[par] == n + 1;
+                const bool bad = x.bad[n & 3] == n + 1;
                 const bool live = i < len;
                 const float ew = live ? p.inter * x.pw[rev ? len - i - late : i + 1] : 0.0f;
+                const uint64_t ew2 = f2(ew, ew);
                 char* dst = out0 + (row + i) * p.out.ts * 2;
                 const int ti = rev ? kChunk - 1 - i : i;
+                // 16 columns at a time, the next ones on their way
+                uint32_t o[2][16], m[2][16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) m[0][k] = m[1][k] = 0;
+                auto fetch = [&](int e, int k2) {
+                    tmem_ld16_nowait(tl + kColO + e, o[k2]);
+                    if (read_m) tmem_ld16_nowait(tl + kColE + e, m[k2]);
+                };
+                fetch(0, 0);
 #pragma unroll 1
-                for (int e = 0; e < DC; e += 32) {
-                    uint32_t o[32], m[32];
-                    tmem_ld32(tl + kColO + e, o);
-                    if (read_m) {
-                        tmem_ld32(tl + kColE + e, m);
-                        tmem_wait32(o);
-                        tmem_wait32(m);
-                    } else {
-                        tmem_wait32(o);
+                for (int e0 = 0; e0 < DC; e0 += 32) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) m[k] = 0;
-                    }
-                    if (bad) {
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        const int e = e0 + 16 * k2;
+                        tmem_wait_ld(o[k2]);
+                        if (read_m) tmem_wait_ld(m[k2]);
+                        if (e + 16 < DC) fetch(e + 16, k2 ^ 1);
+                        if (bad) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (ti >= x.first[par][e + k]) o[k] = 0x7fffffffu;
-                    }
-                    if (e + 32 == DC) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&x.o_free);
-                    }
-                    if (live) {
-                        uint32_t u[16];
+                            for (int k = 0; k < 16; ++k)
+                                if (ti >= int(x.first[n & 3][e + k])) o[k2][k] = 0x7fffffffu;
+                        }
+                        if (k2 == 1 && e + 16 == DC) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&x.o_free);
+                        }
+                        if (live) {
+                            uint32_t u[8];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            u[k] = pack_bf2(
-                                fmaf(ew, __uint_as_float(m[2 * k]), __uint_as_float(o[2 * k])),
-                                fmaf(ew, __uint_as_float(m[2 * k + 1]), __uint_as_float(o[2 * k + 1])));
-                        if (wide) {
-                            const uint32_t u0[8] = {u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]};
-                            const uint32_t u1[8] = {u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]};
-                            st_row32(dst + e * 2, u0);
-                            st_row32(dst + e * 2 + 32, u1);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<uint4*>(dst + e * 2 + 16 * k) =
-                                    make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+                            for (int k = 0; k < 8; ++k)
+                                u[k] = f2_to_bf2(fma2(
+                                    ew2,
+                                    f2(__uint_as_float(m[k2][2 * k]), __uint_as_float(m[k2][2 * k + 1])),
+                                    f2(__uint_as_float(o[k2][2 * k]), __uint_as_float(o[k2][2 * k + 1]))));
+                            if (wide) {
+                                st_row32(dst + e * 2, u);
+                            } else {
+                                reinterpret_cast<uint4*>(dst + e * 2)[0] =
+                                    make_uint4(u[0], u[1], u[2], u[3]);
+                                reinterpret_cast<uint4*>(dst + e * 2)[1] =
+                                    make_uint4(u[4], u[5], u[6], u[7]);
+                            }
                         }
                     }
                 }
             }
         }
+    } else if (warp < 16) {
+        reg_dec<56>();
+        // ---- WG V0, V1: decayed values; V0 takes the even steps, V1 the odd ones, each with a buffer ----
+        const int buf = warp >= 12, t = (tid - 256) & 127;
+        const int vr = t >> 3, vc = t & 7;   // its row of a step and 16-byte column
+        char* vt = sm + S::v + buf * S::kV + swz(vr, vc);
+        uint32_t v_use = 0;
+        for (int n = 0; n < chunks; ++n) {
+            const int st = n & 1;
+            const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
+            const int len = len_of(row_of(n));
+            const bool need_u = n + 1 < chunks || wants_last;
+            char* ct = sm + S::c + st * S::kC;
+            char* bt = sm + S::b + st * S::kB;
+            if (!wait_warp(&x.c_full[st], par2, &x.dead)) break;
+            if (len < kChunk && !wait_warp(&x.b_full[st], par2, &x.dead)) break;
+            bool ok = true;
+            uint32_t most = 0;
+#pragma unroll 1
+            for (int s = buf; s < kChunk / kSub; s += 2) {
+                const int r = s * kSub + vr;
+                if (r >= len) {
+                    // rows past the sequence's end may hold anything: they become zero
+#pragma unroll
+                    for (int k = 0; k < DC / 64; ++k)
+                        *reinterpret_cast<uint4*>(ct + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < DA / 64; ++k)
+                        *reinterpret_cast<uint4*>(bt + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
+                }
+                uint4 u[DC / 64];
+#pragma unroll
+                for (int k = 0; k < DC / 64; ++k) {
+                    u[k] = *reinterpret_cast<const uint4*>(ct + k * kBox + swz(r, vc));
+                    if (!kSum)
+                        most = most_of(most_of(most_of(most_of(most, u[k].x), u[k].y), u[k].z), u[k].w);
+                }
+                if (!kSum && s >= kChunk / kSub - 2) {
+                    // all values seen: a chunk with one that is not finite takes the slow way before
+                    // its product is formed (0 times such a value would reach earlier rows)
+                    const bool odd = __any_sync(0xffffffffu, not_finite(most));
+                    if (lane == 0) {
+                        if (odd) x.bad[n & 3] = n + 1;
+                        mbar_arrive(&x.c_seen);
+                    }
+                    if (!(ok = wait_warp(&x.c_seen, par, &x.dead))) break;
+                    if (buf == 0 && x.bad[n & 3] == n + 1) {
+                        for (int e = t; e < DC; e += 128) {
+                            int f = kChunk;
+                            for (int j = 0; j < len; ++j) {
+                                unsigned short* q = reinterpret_cast<unsigned short*>(
+                                                        ct + (e >> 6) * kBox + swz(j, (e >> 3) & 7)) +
+                                                    (e & 7);
+                                if ((*q & 0x7f80u) != 0x7f80u) continue;
+                                f = min(f, rev ? kChunk - 1 - j : j);
+                                *q = 0;   // the product is formed without it
+                            }
+                            x.first[n & 3][e] = uint8_t(f);
+                        }
+                    }
+                }
+                if (need_u) {
+                    const float w = p.upd * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
+                    const uint64_t w2 = f2(w, w);
+                    if (v_use >= 1 && !(ok = wait_warp(&x.v_free[buf], (v_use - 1) & 1u, &x.dead))) break;
+#pragma unroll
+                    for (int k = 0; k < DC / 64; ++k) {
+                        uint4 a, b, c;
+                        split3(u[k].x, w2, a.x, b.x, c.x);
+                        split3(u[k].y, w2, a.y, b.y, c.y);
+                        split3(u[k].z, w2, a.z, b.z, c.z);
+                        split3(u[k].w, w2, a.w, b.w, c.w);
+                        char* q = vt + k * (kSub * 128);
+                        *reinterpret_cast<uint4*>(q) = a;
+                        *reinterpret_cast<uint4*>(q + S::kTerm) = b;
+                        *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x.v_ready[buf]);
+                    ++v_use;
+                }
+            }
+            if (!ok) break;
+            if (!kSum) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.c_clean[st]);
+            }
+        }
     } else {
-        reg_inc<240>();
-        // ---- WG B: decayed values, the state ---------------------------------------------------------
-        const int wq = warp - 8, t = tid - 256, d = t;
+        reg_inc<192>();
+        // ---- WG M: the state ------------------------------------------------------------------------
+        const int wq = warp - 16, d = tid - 512;
         const uint32_t tl = tm + (uint32_t(wq * 32) << 16);
         const bool owns = d < DA;            // thread d holds the state's row d
         float M[DC];
@@ -550,116 +708,33 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             if (lane == 0) mbar_arrive(&x.m_ready);
         };
         if (has_in && chunks > 0) publish();
-        uint32_t v_use = 0, u_n = 0, published = has_in ? 1u : 0u;
-        const int vr = t >> 3, vc = t & 7;   // this thread's row of a step and 16-byte column
+        uint32_t published = has_in ? 1u : 0u;
         int n = 0;
-        for (; n < chunks; ++n) {
-            const int st = n & 1;
-            const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
+        for (; n < chunks && (n + 1 < chunks || wants_last); ++n) {
             const int len = len_of(row_of(n));
             const int late = rev && seg == 0 && n == 0 ? 1 : 0;
-            const bool need_u = n + 1 < chunks || wants_last;
-            char* ct = sm + S::c + st * S::kC;
-            char* bt = sm + S::b + st * S::kB;
-            if (!wait_warp(&x.c_full[st], par2, &x.dead)) break;
-            if (len < kChunk && !wait_warp(&x.b_full[st], par2, &x.dead)) break;
-            bool odd = false, ok = true, bad = false;
-            for (int s = 0; s < kChunk / kSub; ++s) {
-                const int r = s * kSub + vr;
-                if (r >= len) {
-                    // rows past the sequence's end may hold anything: they become zero
+            const float keep = x.pw[len - late];
+            if (!wait_warp(&x.u_full, uint32_t(n) & 1u, &x.dead)) break;
+            tc_fence_after();
+            const uint64_t keep2 = f2(keep, keep);
 #pragma unroll
-                    for (int k = 0; k < DC / 64; ++k)
-                        *reinterpret_cast<uint4*>(ct + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < DC; e += 16) {
+                uint32_t u[16];
+                tmem_ld16_nowait(tl + kColU + e, u);
+                tmem_wait_ld(u);
 #pragma unroll
-                    for (int k = 0; k < DA / 64; ++k)
-                        *reinterpret_cast<uint4*>(bt + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
-                }
-                uint4 u[DC / 64];
-#pragma unroll
-                for (int k = 0; k < DC / 64; ++k) {
-                    u[k] = *reinterpret_cast<const uint4*>(ct + k * kBox + swz(r, vc));
-                    odd |= not_finite(u[k].x) | not_finite(u[k].y) | not_finite(u[k].z) |
-                           not_finite(u[k].w);
-                }
-                if (s == kChunk / kSub - 1) {
-                    // all values seen: a chunk with one that is not finite takes the slow way before
-                    // its product is formed (0 times such a value would reach earlier rows)
-                    odd = __any_sync(0xffffffffu, odd);
-                    if (!kSum) {
-                        if (lane == 0) {
-                            if (odd) x.bad[par] = n + 1;
-                            mbar_arrive(&x.c_seen);
-                        }
-                        if (!(ok = wait_warp(&x.c_seen, par, &x.dead))) break;
-                        bad = x.bad[par] == n + 1;
-                    }
-                    if (bad) {
-                        for (int e = t; e < DC; e += 128) {
-                            int f = kChunk;
-                            for (int j = 0; j < len; ++j) {
-                                unsigned short* q = reinterpret_cast<unsigned short*>(
-                                                        ct + (e >> 6) * kBox + swz(j, (e >> 3) & 7)) +
-                                                    (e & 7);
-                                if ((*q & 0x7f80u) != 0x7f80u) continue;
-                                f = min(f, rev ? kChunk - 1 - j : j);
-                                *q = 0;   // the product is formed without it
-                            }
-                            x.first[par][e] = f;
-                        }
-                    }
-                }
-                if (need_u) {
-                    const uint32_t buf = v_use & 1u;
-                    if (v_use >= 2 && !(ok = wait_warp(&x.v_free[buf], ((v_use >> 1) & 1u) ^ 1u, &x.dead)))
-                        break;
-                    const float w = p.upd * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
-                    char* v0 = sm + S::v + buf * S::kV;
-#pragma unroll
-                    for (int k = 0; k < DC / 64; ++k) {
-                        uint4 a, b, c;
-                        split3(u[k].x, w, a.x, b.x, c.x);
-                        split3(u[k].y, w, a.y, b.y, c.y);
-                        split3(u[k].z, w, a.z, b.z, c.z);
-                        split3(u[k].w, w, a.w, b.w, c.w);
-                        char* q = v0 + k * (kSub * 128) + swz(vr, vc);
-                        *reinterpret_cast<uint4*>(q) = a;
-                        *reinterpret_cast<uint4*>(q + S::kTerm) = b;
-                        *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&x.v_ready[buf]);
-                    ++v_use;
-                }
+                for (int k = 0; k < 16; k += 2)
+                    unf2(fma2(keep2, f2(M[e + k], M[e + k + 1]),
+                              f2(__uint_as_float(u[k]), __uint_as_float(u[k + 1]))),
+                         M[e + k], M[e + k + 1]);
             }
-            if (!ok) break;
-            if (!kSum) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&x.c_clean[st]);
-            }
-            if (need_u) {
-                const float keep = x.pw[len - late];
-                if (!wait_warp(&x.u_full, u_n & 1u, &x.dead)) break;
-                ++u_n;
-                tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < DC; e += 32) {
-                    uint32_t u[32];
-                    tmem_ld32(tl + kColU + e, u);
-                    tmem_wait32(u);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) M[e + k] = fmaf(keep, M[e + k], __uint_as_float(u[k]));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&x.u_free);
-                if (!kSum && n + 1 < chunks) {
-                    if (published > 0 && !wait_warp(&x.m_free, (published - 1) & 1u, &x.dead)) break;
-                    publish();
-                    ++published;
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.u_free);
+            if (!kSum && n + 1 < chunks) {
+                if (published > 0 && !wait_warp(&x.m_free, (published - 1) & 1u, &x.dead)) break;
+                publish();
+                ++published;
             }
         }
         if (n == chunks && owns && !idle) {
