@@ -298,6 +298,9 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const bool has_in = !kSum && (from_slot || p.m_in != nullptr);
     // whether the state after step n is still read (by the next chunk, or as a result)
     const bool wants_last = kSum || (last_seg && p.m_out != nullptr);
+    // terms of the decayed values: three where the state is a result; where only outputs read it, through
+    // a rounding to bf16, two (relative error 2^-17) leave that rounding as it is
+    const int terms = p.m_out ? 3 : 2;
 
     if (warp < 4) {
         reg_dec<56>();
@@ -313,6 +316,14 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
                 for (int k = 0; k < DA / 64; ++k)
                     tma_load_3d(sm + S::b + st * S::kB + k * kBox, &tmB, k * 64, h, row, &x.b_full[st]);
+                if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) {
+                    ++n;
+                    break;
+                }
+                mbar_expect_tx(&x.c_full[st], S::kC);
+#pragma unroll
+                for (int k = 0; k < DC / 64; ++k)
+                    tma_load_3d(sm + S::c + st * S::kC + k * kBox, &tmC, k * 64, h, row, &x.c_full[st]);
                 if (!kSum) {
                     if (n >= 1 && !wait(&x.a_empty, uint32_t(n - 1) & 1u, &x.dead)) {
                         ++n;
@@ -323,14 +334,6 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     for (int k = 0; k < DA / 64; ++k)
                         tma_load_3d(sm + k * kBox, &tmA, k * 64, h, row, &x.a_full);
                 }
-                if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) {
-                    ++n;
-                    break;
-                }
-                mbar_expect_tx(&x.c_full[st], S::kC);
-#pragma unroll
-                for (int k = 0; k < DC / 64; ++k)
-                    tma_load_3d(sm + S::c + st * S::kC + k * kBox, &tmC, k * 64, h, row, &x.c_full[st]);
             }
             if (x.dead) {
                 // nobody consumes any more: let every copy land before the memory is given up
@@ -422,9 +425,11 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                 const uint64_t ad = sdesc_mn(b0 + (s + buf) * 2048, kBox);
 #pragma unroll
                                 for (int t = 0; t < 3; ++t)
-                                    tc_mma(tm + kColU, ad,
-                                           sdesc_mn(base + S::v + buf * S::kV + t * S::kTerm, kSub * 128),
-                                           iU, s > 0 || buf > 0 || t > 0);
+                                    if (t < terms)
+                                        tc_mma(tm + kColU, ad,
+                                               sdesc_mn(base + S::v + buf * S::kV + t * S::kTerm,
+                                                        kSub * 128),
+                                               iU, s > 0 || buf > 0 || t > 0);
                                 tc_commit(&x.v_free[buf]);
                             }
                         }
@@ -635,20 +640,24 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     }
                 }
                 if (need_u) {
+                    // split before the wait for the buffer, so that only stores lie between the MMAs
                     const float w = p.upd * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
                     const uint64_t w2 = f2(w, w);
+                    uint4 a[DC / 64], b[DC / 64], c[DC / 64];
+#pragma unroll
+                    for (int k = 0; k < DC / 64; ++k) {
+                        split3(u[k].x, w2, a[k].x, b[k].x, c[k].x);
+                        split3(u[k].y, w2, a[k].y, b[k].y, c[k].y);
+                        split3(u[k].z, w2, a[k].z, b[k].z, c[k].z);
+                        split3(u[k].w, w2, a[k].w, b[k].w, c[k].w);
+                    }
                     if (v_use >= 1 && !(ok = wait_warp(&x.v_free[buf], (v_use - 1) & 1u, &x.dead))) break;
 #pragma unroll
                     for (int k = 0; k < DC / 64; ++k) {
-                        uint4 a, b, c;
-                        split3(u[k].x, w2, a.x, b.x, c.x);
-                        split3(u[k].y, w2, a.y, b.y, c.y);
-                        split3(u[k].z, w2, a.z, b.z, c.z);
-                        split3(u[k].w, w2, a.w, b.w, c.w);
                         char* q = vt + k * (kSub * 128);
-                        *reinterpret_cast<uint4*>(q) = a;
-                        *reinterpret_cast<uint4*>(q + S::kTerm) = b;
-                        *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c;
+                        *reinterpret_cast<uint4*>(q) = a[k];
+                        *reinterpret_cast<uint4*>(q + S::kTerm) = b[k];
+                        if (terms > 2) *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c[k];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
