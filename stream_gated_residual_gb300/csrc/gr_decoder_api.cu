@@ -306,8 +306,8 @@ int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, c
     MixArgs p = mix_args(m, in[0], in[1], in[2], out, log_decay, seq_starts);
     p.m_in = state_in;
     p.m_out = state_out;
-    p.intra = p.inter = m->scale;
-    p.upd = 1.0f;
+    p.weight = 1.0f;
+    p.outer = m->scale;
     return run_mix(p, workspace, static_cast<cudaStream_t>(stream));
 }
 
@@ -390,24 +390,24 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
     MixArgs p = mix_args(m, in[0], in[3], in[2], out[0], log_decay, seq_starts);
     p.m_in = state_in;
     p.mr = 1, p.mc = m->d_value;
-    p.intra = p.inter = m->scale;
-    p.upd = 1.0f;
+    p.weight = 1.0f;
+    p.outer = m->scale;
     if ((st = run_mix(p, workspace, s))) return st;
     // dk_t = G_t v_t: backwards over (v, dO, q), G transposed
     p = mix_args(m, in[3], in[0], in[1], out[1], log_decay, seq_starts);
     p.m_in = dstate_out;
     p.mr = 1, p.mc = m->d_value;
     p.reverse = true;
-    p.intra = p.upd = m->scale;
-    p.inter = 1.0f;
+    p.weight = m->scale;
+    p.outer = 1.0f;
     if ((st = run_mix(p, workspace, s))) return st;
     // dv_t = G_tᵀ k_t: backwards over (k, q, dO); its G goes on to the incoming state
     p = mix_args(m, in[2], in[1], in[0], out[2], log_decay, seq_starts);
     p.m_in = dstate_out;
     p.m_out = dstate_in;
     p.reverse = true;
-    p.intra = p.upd = m->scale;
-    p.inter = 1.0f;
+    p.weight = m->scale;
+    p.outer = 1.0f;
     return run_mix(p, workspace, s);
 }
 

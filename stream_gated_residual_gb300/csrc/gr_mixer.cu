@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(const MixArgs p) {
                 for (int y = 0; y < 2; ++y) {
                     const int i = 2 * ti + x, j = tj + 16 * y;
                     const int gap = p.reverse ? j - i : i - j;
-                    P[i * (kC + 1) + j] = gap >= 0 ? s[x][y] * (pw[gap] * p.intra) : 0.0f;
+                    P[i * (kC + 1) + j] = gap >= 0 ? s[x][y] * (pw[gap] * p.weight) : 0.0f;
                 }
         }
         __syncthreads();
@@ -124,10 +124,10 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(const MixArgs p) {
             for (int x = 0; x < 2; ++x) {
                 const int i = i0 + x;
                 if (i < len && e < cols) {
-                    const float w = p.inter * pw[p.reverse ? len - i - late : i + 1];
+                    const float w = pw[p.reverse ? len - i - late : i + 1];
                     T* dst = static_cast<T*>(p.out.p) + (row0 + i) * p.out.ts + h * p.out.hs + e0 + e;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) dst[k] = from_f32<T>(fmaf(w, m[x][k], o[x][k]));
+                    for (int k = 0; k < 4; ++k) dst[k] = from_f32<T>(p.outer * fmaf(w, m[x][k], o[x][k]));
                 }
             }
         }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(const MixArgs p) {
                     m[k][3] = keep * s.w;
                 }
                 for (int j = 0; j < len; ++j) {
-                    const float w = p.upd * pw[p.reverse ? j : len - 1 - j];
+                    const float w = p.weight * pw[p.reverse ? j : len - 1 - j];
                     const float4 c = *reinterpret_cast<const float4*>(C + j * kCs + e);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {

@@ -14,8 +14,8 @@ struct MixRows {
 };
 
 // For every sequence (rows starts[b] .. starts[b+1]) and head, with λ = exp(log_decay[h]):
-//   forwards   M_t = λ M_{t−1} + upd·b_t c_tᵀ,  out_t = inter/upd-weighted:
-//              out_t = intra Σ_{s<=t} λ^{t−s} (a_t·b_s) c_s + inter λ^{t+1} M_inᵀ a_t
+//   forwards   M_t = λ M_{t−1} + weight b_t c_tᵀ,   out_t = outer M_tᵀ a_t
+//              = outer [ weight Σ_{s<=t} λ^{t−s} (a_t·b_s) c_s + λ^{t+1} M_inᵀ a_t ]
 //   backwards  the same with the order of the tokens reversed (s >= t), except that M_in enters the
 //              last token undecayed (it is the gradient of the state after that token):
 //              the exponent of its decay is T − 1 − t
@@ -31,7 +31,7 @@ struct MixArgs {
     const float* m_in;
     float* m_out;
     int mr, mc;
-    float intra, inter, upd;
+    float weight, outer;
     bool reverse;
 };
 

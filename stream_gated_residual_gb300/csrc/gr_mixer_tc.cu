@@ -4,9 +4,9 @@
 // gradients is one pass of it.
 //
 // A chunk's rows i = 0..127 (λ the head's decay, M the state before the chunk):
-//     P_ij  = intra λ^{i−j} (a_i·b_j) for j <= i                 MMA 1, then WG A (mask, decay, bf16)
-//     out_i = Σ_j P_ij c_j + inter λ^{i+1} (Mᵀ a_i)              MMA 4 and MMA 2, then WG A
-//     M'    = λ^len M + Σ_j b_j (upd λ^{len−1−j} c_j)ᵀ           MMA 3 (WG V0, V1 scale c), then WG M
+//     P_ij  = outer weight λ^{i−j} (a_i·b_j) for j <= i                 MMA 1, then WG A (mask, decay, bf16)
+//     out_i = Σ_j P_ij c_j + outer λ^{i+1} (Mᵀ a_i)              MMA 4 and MMA 2, then WG A
+//     M'    = λ^len M + Σ_j b_j (weight λ^{len−1−j} c_j)ᵀ           MMA 3 (WG V0, V1 scale c), then WG M
 // (backwards in time the exponents run the other way.)
 //
 // The state M stays in registers, in fp32, for all chunks of a segment. Its update is a product of
@@ -79,7 +79,7 @@ struct Aux {
     int seq, seg;
     alignas(16) float pw[kChunk + 4];   // λ^0 .. λ^128
     alignas(16) float rev[32];          // λ^31 .. λ^0
-    // a block of 32 rows and columns on the diagonal: intra λ^|i−j| (rows 16 bytes off a multiple of
+    // a block of 32 rows and columns on the diagonal: outer weight λ^|i−j| (rows 16 bytes off a multiple of
     // 128, so that the lanes' 16-byte reads of one column group meet no bank twice)
     alignas(16) float diag[32][36];
     // By n & 3, which no other chunk writes before chunk n's outputs are out (WG V at chunk n + 3 has
@@ -159,30 +159,28 @@ template <int N> __device__ __forceinline__ void reg_inc() {
 template <int N> __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// The larger magnitudes of two bf16 pairs, half by half: 0x7f80 or more where one is not finite.
-__device__ __forceinline__ uint32_t most_of(uint32_t m, uint32_t u) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(u & 0x7fff7fffu));
-    return r;
-}
-__device__ __forceinline__ bool not_finite(uint32_t m) {
-    return (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
-}
 __device__ __forceinline__ uint32_t upper_halves(uint64_t v) {
     return __byte_perm(uint32_t(v), uint32_t(v >> 32), 0x7632);
 }
 
-// A bf16 pair times w as three bf16 pairs: 8 bits of the fp32 product's 24 each, cut off, so that
-// they sum to the product exactly.
-__device__ __forceinline__ void split3(uint32_t u, uint64_t w2, uint32_t& t0, uint32_t& t1,
-                                       uint32_t& t2) {
+// A bf16 pair times w as three (or two) bf16 pairs: 8 bits of the fp32 product's 24 each, cut off, so
+// that three sum to the product exactly; of two the second is rounded. `seen` turns NaN where the pair
+// is not finite.
+template <int kTerms>
+__device__ __forceinline__ void split_terms(uint32_t u, uint64_t w2, uint32_t& t0, uint32_t& t1, uint32_t& t2,
+                                      uint64_t& seen) {
     const uint64_t keep = 0xffff0000ffff0000ull, minus = f2(-1.0f, -1.0f);
     uint64_t v = mul2(bf2_to_f2(u), w2);
+    seen = fma2(v, 0ull, seen);
     t0 = upper_halves(v);
     v = fma2(v & keep, minus, v);
-    t1 = upper_halves(v);
-    v = fma2(v & keep, minus, v);
-    t2 = upper_halves(v);
+    if (kTerms == 2) {
+        t1 = f2_to_bf2(v);
+    } else {
+        t1 = upper_halves(v);
+        v = fma2(v & keep, minus, v);
+        t2 = upper_halves(v);
+    }
 }
 
 // Where a CTA works: segment `seg` (in the order of time it is processed) of sequence `seq`. Every
@@ -228,9 +226,11 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
     return false;
 }
 
+// kTerms: bf16 terms of the decayed values. Three where the state is a result; where only outputs read
+// it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
 // kSum: only the segment's own sum (no outputs), written to slot `unit`; else the pass, which reads
 // its first state from slot unit − H (the segment before) or from m_in.
-template <int DA, int DC, bool kSum>
+template <int DA, int DC, bool kSum, int kTerms>
 __global__ void __launch_bounds__(kThreads, 1)
 mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const MixArgs p, const Segments sg,
@@ -241,7 +241,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     Aux& x = *reinterpret_cast<Aux*>(sm + S::aux);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = blockIdx.x, h = unit % p.n_heads;
-    const float g = p.log_decay[h];
+    const float g = p.log_decay[h], intra = p.weight * p.outer;
 
     if (warp == 0) {
         int seq = 0, seg = 0;
@@ -273,7 +273,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int i = tid - 64; i < 32; i += kThreads - 64) x.rev[i] = decay_pow(g, 31 - i);
         for (int i = tid - 64; i < 1024; i += kThreads - 64) {
             const int d = (i >> 5) - (i & 31);
-            x.diag[i >> 5][i & 31] = p.intra * decay_pow(g, d < 0 ? -d : d);
+            x.diag[i >> 5][i & 31] = intra * decay_pow(g, d < 0 ? -d : d);
         }
     }
     __syncthreads();
@@ -298,9 +298,6 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const bool has_in = !kSum && (from_slot || p.m_in != nullptr);
     // whether the state after step n is still read (by the next chunk, or as a result)
     const bool wants_last = kSum || (last_seg && p.m_out != nullptr);
-    // terms of the decayed values: three where the state is a result; where only outputs read it, through
-    // a rounding to bf16, two (relative error 2^-17) leave that rounding as it is
-    const int terms = p.m_out ? 3 : 2;
 
     if (warp < 4) {
         reg_dec<56>();
@@ -424,12 +421,10 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             if (leader) {
                                 const uint64_t ad = sdesc_mn(b0 + (s + buf) * 2048, kBox);
 #pragma unroll
-                                for (int t = 0; t < 3; ++t)
-                                    if (t < terms)
-                                        tc_mma(tm + kColU, ad,
-                                               sdesc_mn(base + S::v + buf * S::kV + t * S::kTerm,
-                                                        kSub * 128),
-                                               iU, s > 0 || buf > 0 || t > 0);
+                                for (int t = 0; t < kTerms; ++t)
+                                    tc_mma(tm + kColU, ad,
+                                           sdesc_mn(base + S::v + buf * S::kV + t * S::kTerm, kSub * 128),
+                                           iU, s > 0 || buf > 0 || t > 0);
                                 tc_commit(&x.v_free[buf]);
                             }
                         }
@@ -471,7 +466,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     if (off || jb == wq) tmem_ld32(tl + kColS + jb * 32, r);
                     if (off) {
                         // λ^|i−j| as the row's distance to the block times the column's within it
-                        const float rw = p.intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
+                        const float rw = intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
                         const float4* cw = reinterpret_cast<const float4*>(rev ? x.pw : x.rev);
                         const uint64_t rw2 = f2(rw, rw);
                         tmem_wait32(r);
@@ -526,7 +521,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 tc_fence_after();
                 const bool bad = x.bad[n & 3] == n + 1;
                 const bool live = i < len;
-                const float ew = live ? p.inter * x.pw[rev ? len - i - late : i + 1] : 0.0f;
+                const float ew = live ? p.outer * x.pw[rev ? len - i - late : i + 1] : 0.0f;
                 const uint64_t ew2 = f2(ew, ew);
                 char* dst = out0 + (row + i) * p.out.ts * 2;
                 const int ti = rev ? kChunk - 1 - i : i;
@@ -595,7 +590,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             if (!wait_warp(&x.c_full[st], par2, &x.dead)) break;
             if (len < kChunk && !wait_warp(&x.b_full[st], par2, &x.dead)) break;
             bool ok = true;
-            uint32_t most = 0;
+            uint64_t seen = 0;
 #pragma unroll 1
             for (int s = buf; s < kChunk / kSub; s += 2) {
                 const int r = s * kSub + vr;
@@ -608,56 +603,26 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     for (int k = 0; k < DA / 64; ++k)
                         *reinterpret_cast<uint4*>(bt + k * kBox + swz(r, vc)) = make_uint4(0, 0, 0, 0);
                 }
-                uint4 u[DC / 64];
+                // split before the wait for the buffer, so that only stores lie between the MMAs
+                const float w = p.weight * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
+                const uint64_t w2 = f2(w, w);
+                uint4 a[DC / 64], b[DC / 64], c[DC / 64];
 #pragma unroll
                 for (int k = 0; k < DC / 64; ++k) {
-                    u[k] = *reinterpret_cast<const uint4*>(ct + k * kBox + swz(r, vc));
-                    if (!kSum)
-                        most = most_of(most_of(most_of(most_of(most, u[k].x), u[k].y), u[k].z), u[k].w);
-                }
-                if (!kSum && s >= kChunk / kSub - 2) {
-                    // all values seen: a chunk with one that is not finite takes the slow way before
-                    // its product is formed (0 times such a value would reach earlier rows)
-                    const bool odd = __any_sync(0xffffffffu, not_finite(most));
-                    if (lane == 0) {
-                        if (odd) x.bad[n & 3] = n + 1;
-                        mbar_arrive(&x.c_seen);
-                    }
-                    if (!(ok = wait_warp(&x.c_seen, par, &x.dead))) break;
-                    if (buf == 0 && x.bad[n & 3] == n + 1) {
-                        for (int e = t; e < DC; e += 128) {
-                            int f = kChunk;
-                            for (int j = 0; j < len; ++j) {
-                                unsigned short* q = reinterpret_cast<unsigned short*>(
-                                                        ct + (e >> 6) * kBox + swz(j, (e >> 3) & 7)) +
-                                                    (e & 7);
-                                if ((*q & 0x7f80u) != 0x7f80u) continue;
-                                f = min(f, rev ? kChunk - 1 - j : j);
-                                *q = 0;   // the product is formed without it
-                            }
-                            x.first[n & 3][e] = uint8_t(f);
-                        }
-                    }
+                    const uint4 u = *reinterpret_cast<const uint4*>(ct + k * kBox + swz(r, vc));
+                    split_terms<kTerms>(u.x, w2, a[k].x, b[k].x, c[k].x, seen);
+                    split_terms<kTerms>(u.y, w2, a[k].y, b[k].y, c[k].y, seen);
+                    split_terms<kTerms>(u.z, w2, a[k].z, b[k].z, c[k].z, seen);
+                    split_terms<kTerms>(u.w, w2, a[k].w, b[k].w, c[k].w, seen);
                 }
                 if (need_u) {
-                    // split before the wait for the buffer, so that only stores lie between the MMAs
-                    const float w = p.upd * (r < len ? x.pw[rev ? r : len - 1 - r] : 0.0f);
-                    const uint64_t w2 = f2(w, w);
-                    uint4 a[DC / 64], b[DC / 64], c[DC / 64];
-#pragma unroll
-                    for (int k = 0; k < DC / 64; ++k) {
-                        split3(u[k].x, w2, a[k].x, b[k].x, c[k].x);
-                        split3(u[k].y, w2, a[k].y, b[k].y, c[k].y);
-                        split3(u[k].z, w2, a[k].z, b[k].z, c[k].z);
-                        split3(u[k].w, w2, a[k].w, b[k].w, c[k].w);
-                    }
                     if (v_use >= 1 && !(ok = wait_warp(&x.v_free[buf], (v_use - 1) & 1u, &x.dead))) break;
 #pragma unroll
                     for (int k = 0; k < DC / 64; ++k) {
                         char* q = vt + k * (kSub * 128);
                         *reinterpret_cast<uint4*>(q) = a[k];
                         *reinterpret_cast<uint4*>(q + S::kTerm) = b[k];
-                        if (terms > 2) *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c[k];
+                        if (kTerms > 2) *reinterpret_cast<uint4*>(q + 2 * S::kTerm) = c[k];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -667,6 +632,30 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if (!ok) break;
             if (!kSum) {
+                // all values seen: a chunk with one that is not finite takes the slow way before its
+                // product is formed (0 times such a value would reach earlier rows)
+                float s0, s1;
+                unf2(seen, s0, s1);
+                const bool odd = __any_sync(0xffffffffu, !(s0 == 0.0f && s1 == 0.0f));
+                if (lane == 0) {
+                    if (odd) x.bad[n & 3] = n + 1;
+                    mbar_arrive(&x.c_seen);
+                }
+                if (!wait_warp(&x.c_seen, par, &x.dead)) break;
+                if (buf == 0 && x.bad[n & 3] == n + 1) {
+                    for (int e = t; e < DC; e += 128) {
+                        int f = kChunk;
+                        for (int j = 0; j < len; ++j) {
+                            unsigned short* q = reinterpret_cast<unsigned short*>(
+                                                    ct + (e >> 6) * kBox + swz(j, (e >> 3) & 7)) +
+                                                (e & 7);
+                            if ((*q & 0x7f80u) != 0x7f80u) continue;
+                            f = min(f, rev ? kChunk - 1 - j : j);
+                            *q = 0;   // the product is formed without it
+                        }
+                        x.first[n & 3][e] = uint8_t(f);
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x.c_clean[st]);
@@ -903,7 +892,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-template <int DA, int DC>
+template <int DA, int DC, int kTerms>
 cudaError_t run(const MixArgs& p, float* slots, cudaStream_t st) {
     CUtensorMap ma, mb, mc;
     if (!map_rows(&ma, p.a, p.n_tokens, p.n_heads, DA) || !map_rows(&mb, p.b, p.n_tokens, p.n_heads, DA) ||
@@ -913,7 +902,7 @@ cudaError_t run(const MixArgs& p, float* slots, cudaStream_t st) {
     const dim3 grid(unsigned(most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg)));
     constexpr int smem = Smem<DA, DC>::total;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false>,
+    cudaError_t e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false, kTerms>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     // no sequence is longer than all tokens
     const bool split = p.n_tokens > int64_t(sg.per_seg) * kChunk;
@@ -922,17 +911,17 @@ cudaError_t run(const MixArgs& p, float* slots, cudaStream_t st) {
             ? slots + most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg) * int64_t(DA * DC)
             : nullptr;
     if (e == cudaSuccess && split) {
-        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true>,
+        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true, kTerms>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess)
-            e = launch(mix_tc_kernel<DA, DC, true>, grid, kThreads, smem, st, false, ma, mb, mc, p, sg,
+            e = launch(mix_tc_kernel<DA, DC, true, kTerms>, grid, kThreads, smem, st, false, ma, mb, mc, p, sg,
                        slots, static_cast<const float*>(nullptr), 1);
         if (e == cudaSuccess)
             e = launch(mix_scan_kernel, dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024), 256, 0,
                        st, true, p, sg, slots, firsts);
     }
     if (e == cudaSuccess)
-        e = launch(mix_tc_kernel<DA, DC, false>, grid, kThreads, smem, st, split, ma, mb, mc, p, sg,
+        e = launch(mix_tc_kernel<DA, DC, false, kTerms>, grid, kThreads, smem, st, split, ma, mb, mc, p, sg,
                    slots, static_cast<const float*>(firsts), split ? 1 : 0);
     return e;
 }
@@ -958,8 +947,11 @@ size_t mix_tc_workspace(int64_t N, int n_seqs, int H, int da, int dc) {
 
 cudaError_t launch_mix_tc(const MixArgs& p, void* workspace, cudaStream_t st) {
     float* slots = static_cast<float*>(workspace);
-    if (p.da == 128) return p.dc == 128 ? run<128, 128>(p, slots, st) : run<128, 64>(p, slots, st);
-    return p.dc == 128 ? run<64, 128>(p, slots, st) : run<64, 64>(p, slots, st);
+    const bool state = p.m_out != nullptr;
+    if (p.da == 128 && p.dc == 128) return state ? run<128, 128, 3>(p, slots, st) : run<128, 128, 2>(p, slots, st);
+    if (p.da == 128) return state ? run<128, 64, 3>(p, slots, st) : run<128, 64, 2>(p, slots, st);
+    if (p.dc == 128) return state ? run<64, 128, 3>(p, slots, st) : run<64, 128, 2>(p, slots, st);
+    return state ? run<64, 64, 3>(p, slots, st) : run<64, 64, 2>(p, slots, st);
 }
 
 int mixer_status(bool clear) {
