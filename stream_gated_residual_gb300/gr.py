@@ -9,7 +9,9 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -84,8 +86,8 @@ def load() -> ctypes.CDLL:
     L = ctypes.CDLL(_build.LIB)
     P, S, V = ctypes.POINTER(ParamsStruct), ctypes.POINTER(Shape), ctypes.c_void_p
     sz = ctypes.POINTER(ctypes.c_size_t)
-    E, LN, M, RW = (ctypes.POINTER(t) for t in (EmbeddingStruct, NormStruct, MixerStruct,
-                                                RowsStruct))
+    # the decoder parts take their descriptors as packed bytes (or byref of the structures above)
+    E = LN = M = RW = V
     sig = {
         "gr_api_version": ([], ctypes.c_int),
         "gr_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -580,39 +582,77 @@ def write_then_read_fp8(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tens
 
 
 # ---- the parts of a decoder around the Gated Residual: embedding, layer norm, linear attention ----
+#
+# These calls are also made for a few tokens at a time, where the binding itself is what a call costs.
+# Descriptors are packed bytes, kept by their values; workspace sizes are kept by the descriptor (both are
+# pure functions of the arguments), and pointers go as plain integers.
 
-def _aligned_ws(nbytes: int, device) -> torch.Tensor | None:
-    """A fresh 256-byte aligned device buffer of nbytes (torch's allocations start at multiples of
-    512 bytes), or None for 0."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+_EMBED = struct.Struct("=qqiiiiif")    # gr_embedding
+_NORM = struct.Struct("=qiiif")        # gr_norm
+_MIXER = struct.Struct("=qiiiiif")     # gr_mixer
+_ROWS = struct.Struct("=Qqq")          # gr_rows
+_embed_desc = functools.lru_cache(1024)(_EMBED.pack)
+_norm_desc = functools.lru_cache(1024)(_NORM.pack)
+_mixer_desc = functools.lru_cache(1024)(_MIXER.pack)
 
 
-def _ws(need: int, workspace: torch.Tensor | None, device, stream):
-    """The call's workspace: the caller's, else a fresh one that `stream` is recorded on."""
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """cudaStream_t of `stream`, or of torch's current stream on t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _call(name: str, *args) -> None:
+    status = getattr(_LIB or load(), name)(*args)
+    if status != 0:
+        raise GRError(status, name)
+
+
+@functools.lru_cache(1024)
+def _need(name: str, desc: bytes, *args) -> int:
+    """Bytes of a workspace-size entry (a function of the descriptor alone)."""
+    n = ctypes.c_size_t(0)
+    _call(name, desc, *args, ctypes.byref(n))
+    return n.value
+
+
+def _ws(need: int, workspace: torch.Tensor | None, like: torch.Tensor, stream):
+    """(pointer, bytes, tensor) of the call's workspace: the caller's, else a fresh one (torch's
+    allocations start at multiples of 512 bytes) that `stream` is recorded on."""
     if workspace is not None:
         _dev(workspace, "workspace")
-        return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
-    buf = _aligned_ws(need, device)
-    if buf is not None and stream is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if need == 0:
+        return None, 0, None
+    buf = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if stream is not None:
         buf.record_stream(stream)
-    return _ptr(buf), need, buf
+    return buf.data_ptr(), need, buf
+
+
+def _opt(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _f32(t: torch.Tensor | None, name: str, shape=None) -> None:
     if t is None:
         return
-    _dev(t, name)
+    if not t.is_cuda or not t.is_contiguous():
+        _dev(t, name)
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be float32")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
 def _ids(ids: torch.Tensor) -> int:
     _dev(ids, "ids")
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype == torch.int64:
+        return 64
+    if ids.dtype != torch.int32:
         raise ValueError("ids must be int32 or int64")
-    return 32 if ids.dtype == torch.int32 else 64
+    return 32
 
 
 def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: int = 4,
@@ -631,11 +671,10 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: 
         out = torch.empty(shape, dtype=dtype, device=table.device)
     else:
         _dev(out, "out")
-        if tuple(out.shape) != shape or out.dtype != dtype:
+        if out.shape != shape or out.dtype != dtype:
             raise ValueError(f"out must be {dtype} of shape {list(shape)}")
-    e = EmbeddingStruct(N, V, D, branches, _DTYPES[table.dtype], _DTYPES[dtype], bits, scale)
-    _check(load().gr_embed(ctypes.byref(e), _ptr(table), _ptr(ids), _ptr(out), _stream(stream)),
-           "gr_embed")
+    e = _embed_desc(N, V, D, branches, _DTYPES[table.dtype], _DTYPES[dtype], bits, scale)
+    _call("gr_embed", e, table.data_ptr(), ids.data_ptr(), out.data_ptr(), _raw_stream(stream, table))
     return out
 
 
@@ -646,7 +685,8 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
     rows of equal ids are summed in token order. accumulate=True adds to the given dtable."""
     _f32(dR, "dR")
     bits = _ids(ids)
-    if dR.dim() not in (2, 3) or dR.shape[0] != ids.numel():
+    nd = dR.dim()
+    if nd not in (2, 3) or dR.shape[0] != ids.numel():
         raise ValueError("dR must be [N, 4, D] or [N, D] with N = ids.numel()")
     if accumulate and dtable is None:
         raise ValueError("accumulate needs the dtable to add to")
@@ -655,26 +695,21 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
         dtable = torch.empty((n_vocab, D), dtype=torch.float32, device=dR.device)
     else:
         _f32(dtable, "dtable", (n_vocab, D))
-    e = EmbeddingStruct(N, n_vocab, D, 1 if dR.dim() == 2 else dR.shape[1], GR_F32, GR_F32, bits,
-                        scale)
-    need = ctypes.c_size_t(0)
-    L = load()
-    _check(L.gr_embed_backward_workspace_size(ctypes.byref(e), ctypes.byref(need)),
-           "gr_embed_backward_workspace_size")
-    wp, wn, _keep = _ws(need.value, workspace, dR.device, stream)
-    _check(L.gr_embed_backward(ctypes.byref(e), _ptr(dR), _ptr(ids), _ptr(dtable),
-                               1 if accumulate else 0, wp, wn, _stream(stream)),
-           "gr_embed_backward")
+    e = _embed_desc(N, n_vocab, D, 1 if nd == 2 else dR.shape[1], GR_F32, GR_F32, bits, scale)
+    wp, wn, _keep = _ws(_need("gr_embed_backward_workspace_size", e), workspace, dR, stream)
+    _call("gr_embed_backward", e, dR.data_ptr(), ids.data_ptr(), dtable.data_ptr(),
+          1 if accumulate else 0, wp, wn, _raw_stream(stream, dR))
     return dtable
 
 
-def _norm_desc(x: torch.Tensor, weight: torch.Tensor, eps: float):
-    _dev(x, "x")
+def _norm_rows(x: torch.Tensor, weight: torch.Tensor, eps: float) -> bytes:
+    if not x.is_cuda or not x.is_contiguous():
+        _dev(x, "x")
     if x.dtype not in _DTYPES or x.dim() not in (2, 3):
         raise ValueError("x must be a float32 or bfloat16 tensor [N, D] or [N, 4, D]")
-    N, G, D = x.shape[0], 1 if x.dim() == 2 else x.shape[1], x.shape[-1]
-    _f32(weight, "weight", x.shape[1:])
-    return NormStruct(N, D, G, _DTYPES[x.dtype], eps)
+    shape = x.shape
+    _f32(weight, "weight", shape[1:])
+    return _norm_desc(shape[0], shape[-1], 1 if len(shape) == 2 else shape[1], _DTYPES[x.dtype], eps)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -682,7 +717,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     """gr_layer_norm over the last axis of x [N, D] (weight, bias [D]) or of every branch of
     x [N, 4, D] (weight, bias [4, D]); weight and bias fp32. Returns y, or (y, mean, rstd) with
     stats=True (fp32, what the gradient needs). y may be x."""
-    n = _norm_desc(x, weight, eps)
+    n = _norm_rows(x, weight, eps)
     _f32(bias, "bias", x.shape[1:])
     if y is None:
         y = torch.empty_like(x)
@@ -692,9 +727,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
             raise ValueError("y must match x")
     mean = rstd = None
     if stats:
-        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
-    _check(load().gr_layer_norm(ctypes.byref(n), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                _ptr(mean), _ptr(rstd), _stream(stream)), "gr_layer_norm")
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    _call("gr_layer_norm", n, x.data_ptr(), weight.data_ptr(), _opt(bias), y.data_ptr(), _opt(mean),
+          _opt(rstd), _raw_stream(stream, x))
     return (y, mean, rstd) if stats else y
 
 
@@ -704,52 +740,50 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                         stream=None):
     """gr_layer_norm_backward: (dx like x but fp32, dweight, dbias or None) from dy (fp32, x's shape)
     and the forward's mean and rstd. dx may be dy."""
-    n = _norm_desc(x, weight, 0.0)
-    _f32(dy, "dy", x.shape)
-    _f32(mean, "mean", x.shape[:-1])
-    _f32(rstd, "rstd", x.shape[:-1])
+    n = _norm_rows(x, weight, 0.0)
+    shape = x.shape
+    _f32(dy, "dy", shape)
+    _f32(mean, "mean", shape[:-1])
+    _f32(rstd, "rstd", shape[:-1])
     if dx is None:
         dx = torch.empty_like(dy)
     else:
-        _f32(dx, "dx", x.shape)
+        _f32(dx, "dx", shape)
     dweight = torch.empty_like(weight)
     dbias = torch.empty_like(weight) if bias else None
-    need = ctypes.c_size_t(0)
-    L = load()
-    _check(L.gr_layer_norm_backward_workspace_size(ctypes.byref(n), ctypes.byref(need)),
-           "gr_layer_norm_backward_workspace_size")
-    wp, wn, _keep = _ws(need.value, workspace, x.device, stream)
-    _check(L.gr_layer_norm_backward(ctypes.byref(n), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean),
-                                    _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), wp, wn,
-                                    _stream(stream)), "gr_layer_norm_backward")
+    wp, wn, _keep = _ws(_need("gr_layer_norm_backward_workspace_size", n), workspace, x, stream)
+    _call("gr_layer_norm_backward", n, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _opt(dbias), wp, wn,
+          _raw_stream(stream, x))
     return dx, dweight, dbias
 
 
-def _rows(t: torch.Tensor, name: str, N: int, H: int, d: int, dtype: torch.dtype) -> RowsStruct:
-    """A [N, H, d] tensor with contiguous channels at any token and head stride."""
+def _rows(t: torch.Tensor, name: str, N: int, H: int, d: int, dtype: torch.dtype) -> bytes:
+    """gr_rows of a [N, H, d] tensor with contiguous channels at any token and head stride."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (N, H, d) or t.dtype != dtype:
+    if t.shape != (N, H, d) or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {[N, H, d]}, got {t.dtype} of "
                          f"{list(t.shape)}")
     ts, hs, cs = t.stride()
     if cs != 1 and t.numel():
         raise ValueError(f"the channels of {name} must be contiguous")
-    return RowsStruct(t.data_ptr(), ts, hs)
+    return _ROWS.pack(t.data_ptr(), ts, hs)
 
 
-def _mixer_desc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
-                scale: float | None, n_seqs: int):
+def _mixer(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+           scale: float | None, n_seqs: int):
+    """(N, H, dk, dv, descriptor, rows of q, k and v) of a linear-attention call."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must have shape [N, H, d]")
-    N, H, dk = q.shape
-    dv = v.shape[2]
-    if q.dtype not in _DTYPES:
+    (N, H, dk), dv, dtype = q.shape, v.shape[2], q.dtype
+    if dtype not in _DTYPES:
         raise ValueError("q, k, v must be float32 or bfloat16")
-    rows = [_rows(t, n, N, H, d, q.dtype) for t, n, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
+    rows = (_rows(q, "q", N, H, dk, dtype), _rows(k, "k", N, H, dk, dtype),
+            _rows(v, "v", N, H, dv, dtype))
     _f32(log_decay, "log_decay", (H,))
-    m = MixerStruct(N, n_seqs, H, dk, dv, _DTYPES[q.dtype], dk ** -0.5 if scale is None else scale)
-    return m, rows
+    m = _mixer_desc(N, n_seqs, H, dk, dv, _DTYPES[dtype], dk ** -0.5 if scale is None else scale)
+    return N, H, dk, dv, m, rows
 
 
 def _seqs(seq_starts: torch.Tensor | None) -> int:
@@ -761,17 +795,10 @@ def _seqs(seq_starts: torch.Tensor | None) -> int:
     return seq_starts.numel() - 1
 
 
-def _mixer_ws(m: MixerStruct, gradient: int, workspace, device, stream):
-    need = ctypes.c_size_t(0)
-    _check(load().gr_linear_attention_workspace_size(ctypes.byref(m), gradient, ctypes.byref(need)),
-           "gr_linear_attention_workspace_size")
-    return _ws(need.value, workspace, device, stream)
-
-
 def mixer_path(n_tokens: int, n_heads: int, d_key: int, d_value: int, dtype: torch.dtype) -> str:
     """Which kernels a linear-attention prompt of this shape runs: "mixer_tc" or "mixer_simt"."""
-    m = MixerStruct(n_tokens, 1, n_heads, d_key, d_value, _DTYPES.get(dtype, -1), 1.0)
-    return load().gr_mixer_path(ctypes.byref(m)).decode()
+    m = _mixer_desc(n_tokens, 1, n_heads, d_key, d_value, _DTYPES.get(dtype, -1), 1.0)
+    return load().gr_mixer_path(m).decode()
 
 
 def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -784,8 +811,7 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     dk ** -0.5 unless given, state [B, H, dk, dv] fp32 before each sequence or None. Returns
     (o [N, H, dv], state_out [B, H, dk, dv] fp32 after each sequence). state_out may be state."""
     B = _seqs(seq_starts)
-    m, rows = _mixer_desc(q, k, v, log_decay, scale, B)
-    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
+    N, H, dk, dv, m, rows = _mixer(q, k, v, log_decay, scale, B)
     _f32(state, "state", (B, H, dk, dv))
     if o is None:
         o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
@@ -794,11 +820,9 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     else:
         _f32(state_out, "state_out", (B, H, dk, dv))
     orow = _rows(o, "o", N, H, dv, q.dtype)
-    wp, wn, _keep = _mixer_ws(m, 0, workspace, q.device, stream)
-    r = [ctypes.byref(x) for x in rows]
-    _check(load().gr_linear_attention(ctypes.byref(m), *r, _ptr(log_decay), _ptr(seq_starts),
-                                      _ptr(state), ctypes.byref(orow), _ptr(state_out), wp, wn,
-                                      _stream(stream)), "gr_linear_attention")
+    wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 0), workspace, q, stream)
+    _call("gr_linear_attention", m, *rows, log_decay.data_ptr(), _opt(seq_starts), _opt(state), orow,
+          state_out.data_ptr(), wp, wn, _raw_stream(stream, q))
     return o, state_out
 
 
@@ -809,24 +833,20 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """gr_linear_attention_step: one token of each of N requests. state [slots, H, dk, dv] fp32 is
     updated in place; request n uses state[slots[n]] (int32; None: state[n]). Returns o [N, H, dv];
     a slot outside the states leaves them alone and gives o = 0."""
-    m, rows = _mixer_desc(q, k, v, log_decay, scale, 0)
-    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, dk, dv):
+    N, H, dk, dv, m, rows = _mixer(q, k, v, log_decay, scale, 0)
+    if state.dim() != 4 or state.shape[1:] != (H, dk, dv):
         raise ValueError(f"state must be [slots, {H}, {dk}, {dv}]")
     _f32(state, "state")
     if slots is not None:
         _dev(slots, "slots")
-        if slots.dtype != torch.int32 or tuple(slots.shape) != (N,):
+        if slots.dtype != torch.int32 or slots.shape != (N,):
             raise ValueError("slots must be int32 [N]")
     elif state.shape[0] < N:
         raise ValueError("state must hold a slot for every request")
     if o is None:
         o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-    orow = _rows(o, "o", N, H, dv, q.dtype)
-    r = [ctypes.byref(x) for x in rows]
-    _check(load().gr_linear_attention_step(ctypes.byref(m), *r, _ptr(log_decay), _ptr(state),
-                                           state.shape[0], _ptr(slots), ctypes.byref(orow),
-                                           _stream(stream)), "gr_linear_attention_step")
+    _call("gr_linear_attention_step", m, *rows, log_decay.data_ptr(), state.data_ptr(),
+          state.shape[0], _opt(slots), _rows(o, "o", N, H, dv, q.dtype), _raw_stream(stream, q))
     return o
 
 
@@ -840,8 +860,7 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     gradient dstate [B, H, dk, dv] of state_out. dq, dk, dv come in q's dtype (out: a triple to write,
     strided views allowed); dstate_in is None unless dstate or state is given."""
     B = _seqs(seq_starts)
-    m, rows = _mixer_desc(q, k, v, log_decay, scale, B)
-    N, H, dk, dv = m.n_tokens, m.n_heads, m.d_key, m.d_value
+    N, H, dk, dv, m, rows = _mixer(q, k, v, log_decay, scale, B)
     _f32(state, "state", (B, H, dk, dv))
     _f32(dstate, "dstate", (B, H, dk, dv))
     dorow = _rows(do, "do", N, H, dv, q.dtype)
@@ -852,11 +871,7 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     dstate_in = None
     if state is not None or dstate is not None:
         dstate_in = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
-    wp, wn, _keep = _mixer_ws(m, 1, workspace, q.device, stream)
-    r = [ctypes.byref(x) for x in (dorow, *rows)]
-    w = [ctypes.byref(x) for x in outs]
-    _check(load().gr_linear_attention_backward(ctypes.byref(m), *r, _ptr(log_decay),
-                                               _ptr(seq_starts), _ptr(state), _ptr(dstate), *w,
-                                               _ptr(dstate_in), wp, wn, _stream(stream)),
-           "gr_linear_attention_backward")
+    wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 1), workspace, q, stream)
+    _call("gr_linear_attention_backward", m, dorow, *rows, log_decay.data_ptr(), _opt(seq_starts),
+          _opt(state), _opt(dstate), *outs, _opt(dstate_in), wp, wn, _raw_stream(stream, q))
     return (*out, dstate_in)
