@@ -104,13 +104,28 @@ bool tc_shape(const gr_mixer* m) {
            (m->d_value == 64 || m->d_value == 128);
 }
 
-size_t mixer_workspace(const gr_mixer* m) {
-    return tc_shape(m) ? mix_tc_workspace(m->n_tokens, m->n_seqs, m->n_heads, m->d_key, m->d_value)
-                       : 0;
+// Workspace of a prompt, or of its gradient: all three passes at once where they have the same shape
+// (d_key == d_value), else one after another.
+size_t mixer_workspace(const gr_mixer* m, bool gradient) {
+    if (!tc_shape(m)) return 0;
+    auto of = [&](int passes) {
+        return mix_tc_workspace(m->n_tokens, m->n_seqs, m->n_heads, m->d_key, m->d_value, passes);
+    };
+    const size_t one = of(1), three = gradient && m->d_key == m->d_value ? of(3) : 0;
+    return one > three ? one : three;
 }
 
-int run_mix(const MixArgs& p, void* ws, cudaStream_t st) {
-    return as_status(mix_tc_supported(p) ? launch_mix_tc(p, ws, st) : launch_mix_simt(p, st));
+// Passes over the same rows: three in one launch on the tensor cores, else one after another.
+int run_mix(const MixArgs* p, int passes, void* ws, cudaStream_t st) {
+    bool tc = true;
+    for (int i = 0; i < passes; ++i) tc = tc && mix_tc_supported(p[i]);
+    if (tc && passes == 3) return as_status(launch_mix_tc(p, passes, ws, st));
+    for (int i = 0; i < passes; ++i) {
+        const cudaError_t e =
+            mix_tc_supported(p[i]) ? launch_mix_tc(p + i, 1, ws, st) : launch_mix_simt(p[i], st);
+        if (e != cudaSuccess) return GR_E_CUDA;
+    }
+    return GR_OK;
 }
 
 size_t state_bytes(const gr_mixer* m, int64_t n) {
@@ -118,10 +133,11 @@ size_t state_bytes(const gr_mixer* m, int64_t n) {
 }
 
 // seq_starts and the workspace, as every packed call takes them.
-int check_packed(const gr_mixer* m, const int32_t* starts, void* ws, size_t ws_bytes) {
+int check_packed(const gr_mixer* m, bool gradient, const int32_t* starts, void* ws,
+                 size_t ws_bytes) {
     if (!starts && m->n_seqs != 1) return GR_E_NULL;
     if (!aligned(starts, 4)) return GR_E_ALIGN;
-    const size_t need = mixer_workspace(m);
+    const size_t need = mixer_workspace(m, gradient);
     if (need && (!ws || ws_bytes < need)) return GR_E_SIZE;
     if (need && !aligned(ws, 256)) return GR_E_ALIGN;
     return GR_OK;
@@ -266,11 +282,11 @@ const char* gr_mixer_path(const gr_mixer* m) {
     return tc_shape(m) ? "mixer_tc" : "mixer_simt";
 }
 
-int gr_linear_attention_workspace_size(const gr_mixer* m, int, size_t* bytes) {
+int gr_linear_attention_workspace_size(const gr_mixer* m, int gradient, size_t* bytes) {
     const int st = check_mixer(m);
     if (st) return st;
     if (!bytes) return GR_E_NULL;
-    *bytes = mixer_workspace(m);
+    *bytes = mixer_workspace(m, gradient != 0);
     return GR_OK;
 }
 
@@ -289,10 +305,10 @@ int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, c
     for (const Rows& r : in)
         if ((st = r.check(false))) return st;
     if ((st = out.check(true))) return st;
-    if ((st = check_packed(m, seq_starts, workspace, workspace_bytes))) return st;
+    if ((st = check_packed(m, false, seq_starts, workspace, workspace_bytes))) return st;
     if (!aligned(log_decay, 4) || !aligned(state_in, 16) || !aligned(state_out, 16)) return GR_E_ALIGN;
     const size_t ns = state_bytes(m, m->n_seqs);
-    const Span so{state_out, ns}, si{state_in, ns}, ws{workspace, mixer_workspace(m)};
+    const Span so{state_out, ns}, si{state_in, ns}, ws{workspace, mixer_workspace(m, false)};
     const Span flat[2] = {{log_decay, size_t(H) * 4},
                           {seq_starts, (size_t(m->n_seqs) + 1) * sizeof(int32_t)}};
     for (const Rows& r : in)
@@ -308,7 +324,7 @@ int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, c
     p.m_out = state_out;
     p.weight = 1.0f;
     p.outer = m->scale;
-    return run_mix(p, workspace, static_cast<cudaStream_t>(stream));
+    return run_mix(&p, 1, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int gr_linear_attention_step(const gr_mixer* m, const gr_rows* q, const gr_rows* k,
@@ -359,12 +375,12 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
         if ((st = r.check(false))) return st;
     for (const Rows& r : out)
         if ((st = r.check(true))) return st;
-    if ((st = check_packed(m, seq_starts, workspace, workspace_bytes))) return st;
+    if ((st = check_packed(m, true, seq_starts, workspace, workspace_bytes))) return st;
     if (!aligned(log_decay, 4) || !aligned(state_in, 16) || !aligned(dstate_out, 16) ||
         !aligned(dstate_in, 16))
         return GR_E_ALIGN;
     const size_t ns = state_bytes(m, m->n_seqs);
-    const Span so{dstate_in, ns}, ws{workspace, mixer_workspace(m)};
+    const Span so{dstate_in, ns}, ws{workspace, mixer_workspace(m, true)};
     const Span flat[4] = {{log_decay, size_t(H) * 4},
                           {seq_starts, (size_t(m->n_seqs) + 1) * sizeof(int32_t)},
                           {state_in, ns},
@@ -386,29 +402,31 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
     if (meet(so, ws)) return GR_E_ALIAS;
     if ((st = usable_device())) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MixArgs p[3];
     // dq_t = scale S_t dO_t: forwards over (dO, v, k) with the state transposed
-    MixArgs p = mix_args(m, in[0], in[3], in[2], out[0], log_decay, seq_starts);
-    p.m_in = state_in;
-    p.mr = 1, p.mc = m->d_value;
-    p.weight = 1.0f;
-    p.outer = m->scale;
-    if ((st = run_mix(p, workspace, s))) return st;
+    p[0] = mix_args(m, in[0], in[3], in[2], out[0], log_decay, seq_starts);
+    p[0].m_in = state_in;
+    p[0].mr = 1, p[0].mc = m->d_value;
+    p[0].weight = 1.0f;
+    p[0].outer = m->scale;
     // dk_t = G_t v_t: backwards over (v, dO, q), G transposed
-    p = mix_args(m, in[3], in[0], in[1], out[1], log_decay, seq_starts);
-    p.m_in = dstate_out;
-    p.mr = 1, p.mc = m->d_value;
-    p.reverse = true;
-    p.weight = m->scale;
-    p.outer = 1.0f;
-    if ((st = run_mix(p, workspace, s))) return st;
+    p[1] = mix_args(m, in[3], in[0], in[1], out[1], log_decay, seq_starts);
+    p[1].m_in = dstate_out;
+    p[1].mr = 1, p[1].mc = m->d_value;
+    p[1].reverse = true;
+    p[1].weight = m->scale;
+    p[1].outer = 1.0f;
     // dv_t = G_tᵀ k_t: backwards over (k, q, dO); its G goes on to the incoming state
-    p = mix_args(m, in[2], in[1], in[0], out[2], log_decay, seq_starts);
-    p.m_in = dstate_out;
-    p.m_out = dstate_in;
-    p.reverse = true;
-    p.weight = m->scale;
-    p.outer = 1.0f;
-    return run_mix(p, workspace, s);
+    p[2] = mix_args(m, in[2], in[1], in[0], out[2], log_decay, seq_starts);
+    p[2].m_in = dstate_out;
+    p[2].m_out = dstate_in;
+    p[2].reverse = true;
+    p[2].weight = m->scale;
+    p[2].outer = 1.0f;
+    // dv apart where its shape is another one, or where it writes what dk still reads
+    const int together = m->d_key != m->d_value || (dstate_in && dstate_in == dstate_out) ? 2 : 3;
+    if ((st = run_mix(p, together, workspace, s))) return st;
+    return together == 3 ? GR_OK : run_mix(p + 2, 1, workspace, s);
 }
 
 }  // extern "C"

@@ -53,11 +53,14 @@ __device__ __forceinline__ float decay_pow(float log_decay, int64_t n) {
 // CUDA-core form: every type, head size and length (gr_mixer.cu).
 cudaError_t launch_mix_simt(const MixArgs& p, cudaStream_t st);
 
-// Tensor-core form (gr_mixer_tc.cu): bf16, da and dc 64 or 128. The workspace holds
-// the segments' states where a prompt is cut.
+// Tensor-core form (gr_mixer_tc.cu): bf16, da and dc 64 or 128. One pass, or three over the same packed
+// sequences in one launch (the gradient's dq, dk and dv where da == dc): same da, dc, heads and starts;
+// no pass's m_out may be another one's m_in. The workspace holds the segments' states where prompts
+// are cut.
+constexpr int kMostPasses = 3;
 bool mix_tc_supported(const MixArgs& p);
-size_t mix_tc_workspace(int64_t n_tokens, int n_seqs, int n_heads, int da, int dc);
-cudaError_t launch_mix_tc(const MixArgs& p, void* workspace, cudaStream_t st);
+size_t mix_tc_workspace(int64_t n_tokens, int n_seqs, int n_heads, int da, int dc, int passes);
+cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStream_t st);
 int mixer_status(bool clear);
 
 // One token a request, the fp32 states read and written in place (gr_mixer.cu).

@@ -27,6 +27,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "gr_internal.h"
 #include "gr_mixer.h"
 #include "gr_ptx.cuh"
@@ -230,11 +232,25 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
 // it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
 // kSum: only the segment's own sum (no outputs), written to slot `unit`; else the pass, which reads
 // its first state from slot unit − H (the segment before) or from m_in.
-template <int DA, int DC, bool kSum, int kTerms>
-__global__ void __launch_bounds__(kThreads, 1)
-mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmC, const MixArgs p, const Segments sg,
-              float* __restrict__ slots, const float* __restrict__ firsts, int split) {
+struct Launch {
+    CUtensorMap rows[4];             // the distinct row arguments
+    MixArgs pass[kMostPasses];
+    int a[kMostPasses], b[kMostPasses], c[kMostPasses];   // the passes' maps
+    Segments sg;
+    float* slots;                    // [pass][segment][head] states
+    float* firsts;                   // a copy of m_in, see mix_scan_kernel; else null
+    int64_t units;                   // slots of a pass
+    int split;
+};
+
+template <int DA, int DC, bool kSum, int kTerms, int kPass>
+__device__ __forceinline__ void mix_pass(const Launch& L) {
+    const MixArgs& p = L.pass[kPass];
+    const CUtensorMap &tmA = L.rows[L.a[kPass]], &tmB = L.rows[L.b[kPass]], &tmC = L.rows[L.c[kPass]];
+    const Segments sg = L.sg;
+    float* const slots = L.slots + int64_t(kPass) * L.units * (DA * DC);
+    const float* const firsts = p.m_in && p.m_in == p.m_out ? L.firsts : nullptr;
+    const bool split = L.split != 0;
     using S = Smem<DA, DC>;
     extern __shared__ __align__(1024) char raw[];
     char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);   // the swizzle's atoms
@@ -265,10 +281,41 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             mbar_init(&x.done, 2);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 1) {
+    }
+    __syncthreads();
+    if (kSum) dep_launch_dependents();
+    const int seq = x.seq, seg = x.seg;
+    int64_t begin = 0, end = 0;
+    if (seq >= 0) mix_span(p, seq, begin, end);
+    const int64_t all = (end - begin + kChunk - 1) / kChunk;   // the sequence's chunks
+    const int64_t n0 = int64_t(seg) * sg.per_seg;              // the segment's first, in time
+    const bool last_seg = n0 + sg.per_seg >= all;
+    if (seq < 0 || (kSum && last_seg)) {
+        // nothing to do here (the grid is an upper bound); the pass must not complete before the scan
+        if (!kSum && split && warp == 0) dep_wait();
+        return;
+    }
+    const int chunks = int(min(int64_t(sg.per_seg), all - n0));
+    const bool rev = p.reverse;
+    // the chunk at step n of this segment: its first row, its rows, and whether the state enters
+    // its last token undecayed
+    auto row_of = [&](int n) { return begin + (rev ? all - 1 - (n0 + n) : n0 + n) * kChunk; };
+    auto len_of = [&](int64_t row) { return int(min(int64_t(kChunk), end - row)); };
+    auto load = [&](const CUtensorMap* map, int boxes, int at, uint64_t* bar, int n) {
+        mbar_expect_tx(bar, boxes * kBox);
+        for (int k = 0; k < boxes; ++k)
+            tma_load_3d(sm + at + k * kBox, map, k * 64, h, int(row_of(n)), bar);
+    };
+    if (warp == 0 && lane == 0 && chunks > 0) {
+        // the first chunk is on its way while the tables are made
+        load(&tmB, DA / 64, S::b, &x.b_full[0], 0);
+        load(&tmC, DC / 64, S::c, &x.c_full[0], 0);
+        if (!kSum) load(&tmA, DA / 64, 0, &x.a_full, 0);
+    }
+    if (warp == 1) {
         tmem_alloc(&x.tmem, 512);
         tmem_relinquish();
-    } else {
+    } else if (warp > 1) {
         for (int i = tid - 64; i <= kChunk; i += kThreads - 64) x.pw[i] = decay_pow(g, i);
         for (int i = tid - 64; i < 32; i += kThreads - 64) x.rev[i] = decay_pow(g, 31 - i);
         for (int i = tid - 64; i < 1024; i += kThreads - 64) {
@@ -277,23 +324,8 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         }
     }
     __syncthreads();
-    if (kSum) dep_launch_dependents();
     tc_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
-    const int seq = x.seq, seg = x.seg;
-    int64_t begin = 0, end = 0;
-    if (seq >= 0) mix_span(p, seq, begin, end);
-    const int64_t all = (end - begin + kChunk - 1) / kChunk;   // the sequence's chunks
-    const int64_t n0 = int64_t(seg) * sg.per_seg;              // the segment's first, in time
-    const bool last_seg = n0 + sg.per_seg >= all;
-    int chunks = int(min(int64_t(sg.per_seg), all - n0));
-    if (seq < 0 || chunks < 0 || (kSum && last_seg)) chunks = 0;
-    const bool idle = seq < 0 || (kSum && last_seg);
-    const bool rev = p.reverse;
-    // the chunk at step n of this segment: its first row, its rows, and whether the state enters
-    // its last token undecayed
-    auto row_of = [&](int n) { return begin + (rev ? all - 1 - (n0 + n) : n0 + n) * kChunk; };
-    auto len_of = [&](int64_t row) { return int(min(int64_t(kChunk), end - row)); };
     const bool from_slot = seg > 0;
     const bool has_in = !kSum && (from_slot || p.m_in != nullptr);
     // whether the state after step n is still read (by the next chunk, or as a result)
@@ -303,34 +335,16 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         reg_dec<56>();
         if (warp == 0 && lane == 0) {
             // ---- producer -----------------------------------------------------------------------
-            int n = 0;
-            for (; n < chunks; ++n) {
-                const int row = int(row_of(n));
+            for (int n = 1; n < chunks; ++n) {
                 const int st = n & 1;
                 const uint32_t use2 = uint32_t(n >> 1) & 1u;
                 if (n >= 2 && !wait(&x.b_empty[st], use2 ^ 1u, &x.dead)) break;
-                mbar_expect_tx(&x.b_full[st], S::kB);
-#pragma unroll
-                for (int k = 0; k < DA / 64; ++k)
-                    tma_load_3d(sm + S::b + st * S::kB + k * kBox, &tmB, k * 64, h, row, &x.b_full[st]);
-                if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) {
-                    ++n;
-                    break;
-                }
-                mbar_expect_tx(&x.c_full[st], S::kC);
-#pragma unroll
-                for (int k = 0; k < DC / 64; ++k)
-                    tma_load_3d(sm + S::c + st * S::kC + k * kBox, &tmC, k * 64, h, row, &x.c_full[st]);
-                if (!kSum) {
-                    if (n >= 1 && !wait(&x.a_empty, uint32_t(n - 1) & 1u, &x.dead)) {
-                        ++n;
-                        break;
-                    }
-                    mbar_expect_tx(&x.a_full, S::kA);
-#pragma unroll
-                    for (int k = 0; k < DA / 64; ++k)
-                        tma_load_3d(sm + k * kBox, &tmA, k * 64, h, row, &x.a_full);
-                }
+                load(&tmB, DA / 64, S::b + st * S::kB, &x.b_full[st], n);
+                if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) break;
+                load(&tmC, DC / 64, S::c + st * S::kC, &x.c_full[st], n);
+                if (kSum) continue;
+                if (!wait(&x.a_empty, uint32_t(n - 1) & 1u, &x.dead)) break;
+                load(&tmA, DA / 64, 0, &x.a_full, n);
             }
             if (x.dead) {
                 // nobody consumes any more: let every copy land before the memory is given up
@@ -671,8 +685,11 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
         for (int e = 0; e < DC; ++e) M[e] = 0.0f;
         const int64_t one = int64_t(DA) * DC;
-        if (!kSum && split) dep_wait();
-        if (has_in && owns && !idle) {
+        // the states come from the scan (units that need none wait for it at their end: this launch must
+        // not complete before it)
+        const bool early = !kSum && split && (from_slot || (firsts && !last_seg));
+        if (early) dep_wait();
+        if (has_in && owns) {
             const bool copied = firsts && !last_seg;
             if (from_slot || copied) {
                 const float* from = from_slot ? slots + int64_t(unit - p.n_heads) * one
@@ -735,7 +752,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 ++published;
             }
         }
-        if (n == chunks && owns && !idle) {
+        if (n == chunks && owns) {
             if (kSum) {
                 float* s = slots + int64_t(unit) * one + int64_t(d) * DC;
 #pragma unroll
@@ -761,6 +778,7 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
         }
     }
+    if (!kSum && split && warp == 3) dep_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -769,17 +787,29 @@ mix_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
 }
 
+// blockIdx.y is the pass. Each has its code by itself, so that its arguments stay constants of the launch
+// and branches on them uniform ones (read through an index, a chunk took a quarter longer).
+template <int DA, int DC, bool kSum, int kTerms, int kPasses>
+__global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_constant__ Launch L) {
+    if (kPasses == 1 || blockIdx.y == 0) mix_pass<DA, DC, kSum, kTerms, 0>(L);
+    else if (blockIdx.y == 1) mix_pass<DA, DC, kSum, kTerms, 1>(L);
+    else mix_pass<DA, DC, kSum, kTerms, 2>(L);
+}
+
 // The segments' sums to the states after them, in place: slot s <- λ^len_s (state before s) + slot s.
 // One thread four elements of a (sequence, head); the last segment's slot is not used. `firsts`, when
 // m_out is m_in itself, takes a copy of m_in for the first segments of sequences of several: their
 // last segment may be done before the first one starts.
-__global__ void __launch_bounds__(256)
-mix_scan_kernel(const MixArgs p, const Segments sg, float* __restrict__ slots,
-                float* __restrict__ firsts) {
-    dep_wait();
+__global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ Launch L) {
+    // the pass may start on SMs that are free: all CTAs of the sums are running by now
     dep_launch_dependents();
+    dep_wait();
+    const MixArgs& p = L.pass[blockIdx.z];
+    const Segments sg = L.sg;
+    float* const firsts = p.m_in && p.m_in == p.m_out ? L.firsts : nullptr;
     const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
     const int one = p.da * p.dc;
+    float* const slots = L.slots + int64_t(blockIdx.z) * L.units * one;
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     int64_t begin, end;
     mix_span(p, b, begin, end);
@@ -836,14 +866,23 @@ mix_scan_kernel(const MixArgs p, const Segments sg, float* __restrict__ slots,
     }
 }
 
-// Chunks a segment: sequences of the mean length, cut so that the estimated time is least. A unit (a
-// segment of a head) takes its chunks one after another, one unit an SM at a time; cutting a sequence
-// costs a second pass over b and c of all but its last segment, and two launches.
-int plan_segments(int64_t N, int n_seqs, int H) {
+// Chunks a segment. A unit (a segment of a head) takes its chunks one after another, one unit an SM at a
+// time; cutting a sequence costs a second pass over b and c of all but its last segment, and two
+// launches. The host knows the sequences' number and sum, not their lengths:
+//   - too few of them to fill the SMs (rows < 152): taken as equally long, cut so that the estimated time
+//     is least (32768 tokens, 32 heads of 128: 256 chunks uncut 969 us, in 4 segments 423, in 9 389);
+//   - enough of them: only a sequence longer than an SM's even share of all chunks is cut, which
+//     bounds what a single long one can cost (equal ones are never cut).
+int plan_segments(int64_t N, int n_seqs, int64_t heads) {
+    const int64_t rows = n_seqs * heads;
     const int64_t mean = (N + n_seqs - 1) / n_seqs;
     const int64_t chunks = (mean + kChunk - 1) / kChunk;
+    if (rows >= kSms) {
+        const int64_t total = (N / kChunk + n_seqs) * heads;
+        const int64_t share = (total + kSms - 1) / kSms;
+        return int(share < 1 << 20 ? share : 1 << 20);
+    }
     if (chunks <= 1) return 1;
-    const int64_t rows = int64_t(n_seqs) * H;
     int64_t most = (6 * kSms + rows - 1) / rows;
     most = most < chunks ? most : chunks;
     int64_t best = chunks;
@@ -852,14 +891,15 @@ int plan_segments(int64_t N, int n_seqs, int H) {
         const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
         const int64_t waves = (rows * segs + kSms - 1) / kSms;
         const int64_t waves1 = (rows * (segs - 1) + kSms - 1) / kSms;
-        // in units of a chunk's time (about 3 us): 1.5 a unit to start and drain; sums half a chunk
-        double t = waves * (per + 1.5);
-        if (segs > 1) t += waves1 * (0.5 * per + 1.5) + 2.0;
+        // in units of a chunk's time (about 4 us): 2 a unit to start and drain; sums 0.6 of a chunk
+        double t = waves * (per + 2.0);
+        if (segs > 1) t += waves1 * (0.6 * per + 1.5) + 2.0;
         if (t < least) least = t, best = per;
     }
-    return int(best);
+    return int(best < 1 << 20 ? best : 1 << 20);
 }
 
+// An upper bound of the segments of all sequences, times the heads.
 int64_t most_units(int64_t N, int n_seqs, int H, int per_seg) {
     return (N / (int64_t(per_seg) * kChunk) + n_seqs) * H;
 }
@@ -892,37 +932,59 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-template <int DA, int DC, int kTerms>
-cudaError_t run(const MixArgs& p, float* slots, cudaStream_t st) {
-    CUtensorMap ma, mb, mc;
-    if (!map_rows(&ma, p.a, p.n_tokens, p.n_heads, DA) || !map_rows(&mb, p.b, p.n_tokens, p.n_heads, DA) ||
-        !map_rows(&mc, p.c, p.n_tokens, p.n_heads, DC))
-        return cudaErrorInvalidValue;
-    const Segments sg{plan_segments(p.n_tokens, p.n_seqs, p.n_heads)};
-    const dim3 grid(unsigned(most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg)));
+template <int DA, int DC, int kTerms, int kPasses>
+cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
+    constexpr int passes = kPasses;
+    const MixArgs& p = pass[0];
+    Launch L;
+    memset(&L, 0, sizeof(L));
+    int maps = 0;
+    MixRows seen[4];
+    int width[4];
+    auto map_of = [&](const MixRows& r, int d) {
+        for (int i = 0; i < maps; ++i)
+            if (seen[i].p == r.p && seen[i].ts == r.ts && seen[i].hs == r.hs && width[i] == d) return i;
+        if (maps == 4 || !map_rows(&L.rows[maps], r, p.n_tokens, p.n_heads, d)) return -1;
+        seen[maps] = r;
+        width[maps] = d;
+        return maps++;
+    };
+    for (int i = 0; i < passes; ++i) {
+        L.pass[i] = pass[i];
+        L.a[i] = map_of(pass[i].a, DA);
+        L.b[i] = map_of(pass[i].b, DA);
+        L.c[i] = map_of(pass[i].c, DC);
+        if (L.a[i] < 0 || L.b[i] < 0 || L.c[i] < 0) return cudaErrorInvalidValue;
+    }
+    L.sg.per_seg = plan_segments(p.n_tokens, p.n_seqs, int64_t(p.n_heads) * passes);
+    L.units = most_units(p.n_tokens, p.n_seqs, p.n_heads, L.sg.per_seg);
+    // no sequence is longer than all tokens
+    L.split = p.n_tokens > int64_t(L.sg.per_seg) * kChunk;
+    L.slots = slots;
+    L.firsts = L.split ? slots + passes * L.units * int64_t(DA * DC) : nullptr;
+    const dim3 grid(unsigned(L.units), passes);
     constexpr int smem = Smem<DA, DC>::total;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false, kTerms>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    // no sequence is longer than all tokens
-    const bool split = p.n_tokens > int64_t(sg.per_seg) * kChunk;
-    float* firsts =
-        split && p.m_in && p.m_in == p.m_out
-            ? slots + most_units(p.n_tokens, p.n_seqs, p.n_heads, sg.per_seg) * int64_t(DA * DC)
-            : nullptr;
-    if (e == cudaSuccess && split) {
-        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true, kTerms>,
+    static std::atomic<uint64_t> ready;   // a bit for each device whose kernels have their shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
+        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false, kTerms, kPasses>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess)
-            e = launch(mix_tc_kernel<DA, DC, true, kTerms>, grid, kThreads, smem, st, false, ma, mb, mc, p, sg,
-                       slots, static_cast<const float*>(nullptr), 1);
+            e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true, kTerms, kPasses>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && dev <= 63) ready.fetch_or(uint64_t(1) << dev);
+    }
+    if (e == cudaSuccess && L.split) {
+        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses>, grid, kThreads, smem, st, false, L);
         if (e == cudaSuccess)
-            e = launch(mix_scan_kernel, dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024), 256, 0,
-                       st, true, p, sg, slots, firsts);
+            e = launch(mix_scan_kernel,
+                       dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024, passes), 256, 0, st,
+                       true, L);
     }
     if (e == cudaSuccess)
-        e = launch(mix_tc_kernel<DA, DC, false, kTerms>, grid, kThreads, smem, st, split, ma, mb, mc, p, sg,
-                   slots, static_cast<const float*>(firsts), split ? 1 : 0);
+        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses>, grid, kThreads, smem, st, L.split != 0, L);
     return e;
 }
 
@@ -934,24 +996,34 @@ bool mix_tc_supported(const MixArgs& p) {
         if (r->ts > most || r->hs > most) return false;
     return p.dtype == GR_BF16 && (p.da == 64 || p.da == 128) && (p.dc == 64 || p.dc == 128) &&
            p.n_tokens > 0 && p.n_seqs > 0 &&
-           most_units(p.n_tokens, p.n_seqs, p.n_heads,
-                      plan_segments(p.n_tokens, p.n_seqs, p.n_heads)) <= 0x7fffffff;
+           most_units(p.n_tokens, p.n_seqs, p.n_heads, 1) <= 0x7fffffff;
 }
 
-size_t mix_tc_workspace(int64_t N, int n_seqs, int H, int da, int dc) {
+// The slots of all passes and, for one of them, a copy of its first states.
+size_t mix_tc_workspace(int64_t N, int n_seqs, int H, int da, int dc, int passes) {
     if (N == 0 || n_seqs == 0) return 0;
-    const int per = plan_segments(N, n_seqs, H);
+    const int per = plan_segments(N, n_seqs, int64_t(H) * passes);
     if (N <= int64_t(per) * kChunk) return 0;
-    return align256(size_t(most_units(N, n_seqs, H, per) + int64_t(n_seqs) * H) * da * dc * 4);
+    return align256(size_t(passes * most_units(N, n_seqs, H, per) + int64_t(n_seqs) * H) * da * dc * 4);
 }
 
-cudaError_t launch_mix_tc(const MixArgs& p, void* workspace, cudaStream_t st) {
+cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStream_t st) {
     float* slots = static_cast<float*>(workspace);
-    const bool state = p.m_out != nullptr;
-    if (p.da == 128 && p.dc == 128) return state ? run<128, 128, 3>(p, slots, st) : run<128, 128, 2>(p, slots, st);
-    if (p.da == 128) return state ? run<128, 64, 3>(p, slots, st) : run<128, 64, 2>(p, slots, st);
-    if (p.dc == 128) return state ? run<64, 128, 3>(p, slots, st) : run<64, 128, 2>(p, slots, st);
-    return state ? run<64, 64, 3>(p, slots, st) : run<64, 64, 2>(p, slots, st);
+    bool state = false;
+    for (int i = 0; i < passes; ++i) state = state || p[i].m_out;
+    if (passes == 3 && p->da == p->dc) {
+        if (p->da == 128)
+            return state ? run<128, 128, 3, 3>(p, slots, st) : run<128, 128, 2, 3>(p, slots, st);
+        return state ? run<64, 64, 3, 3>(p, slots, st) : run<64, 64, 2, 3>(p, slots, st);
+    }
+    if (passes != 1) return cudaErrorInvalidValue;
+    const int kind = (p->da == 128 ? 2 : 0) + (p->dc == 128 ? 1 : 0);
+    switch (kind) {
+        case 3: return state ? run<128, 128, 3, 1>(p, slots, st) : run<128, 128, 2, 1>(p, slots, st);
+        case 2: return state ? run<128, 64, 3, 1>(p, slots, st) : run<128, 64, 2, 1>(p, slots, st);
+        case 1: return state ? run<64, 128, 3, 1>(p, slots, st) : run<64, 128, 2, 1>(p, slots, st);
+        default: return state ? run<64, 64, 3, 1>(p, slots, st) : run<64, 64, 2, 1>(p, slots, st);
+    }
 }
 
 int mixer_status(bool clear) {

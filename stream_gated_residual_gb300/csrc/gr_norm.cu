@@ -12,6 +12,8 @@
 // rows, and a second kernel adds those in a fixed order, so two runs give the same bits.
 #include <math.h>
 
+#include <atomic>
+
 #include "gr_internal.h"
 #include "gr_ptx.cuh"
 
@@ -27,6 +29,10 @@ template <> struct Raw8<float> {
     __device__ __forceinline__ void load(const float* p) {
         a = __ldcs(reinterpret_cast<const float4*>(p));
         b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void load_kept(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -114,8 +120,11 @@ norm_kernel(int64_t N, int D, int G, float eps, const T* __restrict__ x,
     const int g = blockIdx.x % G;
     const int64_t first = blockIdx.x / G, step = gridDim.x / G;
     const int c0 = threadIdx.x * 8, c1 = c0 + blockDim.x * 8;
-    Row<T> row;
-    if (first < N) row.load(x + (first * G + g) * int64_t(D), c0, c1, D);
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;   // rows on their way: the same registers either way
+    Row<T> ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (first + k * step < N) ahead[k].load(x + ((first + k * step) * G + g) * int64_t(D), c0, c1, D);
     Raw8<float> wr[2], br[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -123,17 +132,19 @@ norm_kernel(int64_t N, int D, int G, float eps, const T* __restrict__ x,
         wr[k].zero();
         br[k].zero();
         if (c < D) {
-            wr[k].load(w + int64_t(g) * D + c);
-            if (b) br[k].load(b + int64_t(g) * D + c);
+            wr[k].load_kept(w + int64_t(g) * D + c);
+            if (b) br[k].load_kept(b + int64_t(g) * D + c);
         }
     }
     const float inv_d = 1.0f / float(D);
     int turn = 0;
     for (int64_t n = first; n < N; n += step) {
         float v[2][8];
-        row.v[0].get(v[0]);
-        row.v[1].get(v[1]);
-        if (n + step < N) row.load(x + ((n + step) * G + g) * int64_t(D), c0, c1, D);
+        ahead[0].v[0].get(v[0]);
+        ahead[0].v[1].get(v[1]);
+        if (kAhead == 2) ahead[0] = ahead[kAhead - 1];
+        if (n + kAhead * step < N)
+            ahead[kAhead - 1].load(x + ((n + kAhead * step) * G + g) * int64_t(D), c0, c1, D);
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[0][k] + v[1][k];
@@ -202,7 +213,7 @@ norm_backward_kernel(int64_t N, int D, int G, const float* __restrict__ dy,
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         wr[k].zero();
-        if ((k ? c1 : c0) < D) wr[k].load(w + int64_t(g) * D + (k ? c1 : c0));
+        if ((k ? c1 : c0) < D) wr[k].load_kept(w + int64_t(g) * D + (k ? c1 : c0));
     }
     const float inv_d = 1.0f / float(D);
     int turn = 0;
@@ -253,31 +264,38 @@ norm_backward_kernel(int64_t N, int D, int G, const float* __restrict__ dy,
     }
 }
 
-// dw and db: 128 channels a block, its 8 warps take the partial rows in turn (blocks g, g + G, ...)
-// and are added up in warp order.
+// dw and db: 32 channels a block, its 32 groups of 8 threads take the partial rows in turn (blocks g,
+// g + G, ...) and are added up in a fixed tree. (128 channels and 8 groups a block took 12 us for the
+// 304 rows of D = 4096, four times as long: too few loads in flight.)
 __global__ void __launch_bounds__(256)
 norm_reduce_kernel(int blocks, int D, int G, bool bias, const float* __restrict__ part,
                    float* __restrict__ dw, float* __restrict__ db) {
-    __shared__ float4 sums[8][32];
+    __shared__ float4 sums[8][8];
     dep_wait();
-    const int lane = threadIdx.x & 31, wq = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + lane) * 4, g = blockIdx.y, which = blockIdx.z;
+    const int col = threadIdx.x & 7, q = threadIdx.x >> 3;
+    const int c = (blockIdx.x * 8 + col) * 4, g = blockIdx.y, which = blockIdx.z;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < D) {
         const int64_t rows = bias ? 2 : 1;
-#pragma unroll 8
-        for (int k = g + G * wq; k < blocks; k += 8 * G) {
+#pragma unroll 10
+        for (int k = g + G * q; k < blocks; k += 32 * G) {
             const float4 v =
                 *reinterpret_cast<const float4*>(part + (int64_t(k) * rows + which) * D + c);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
     }
-    sums[wq][lane] = s;
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o), s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        s.z += __shfl_xor_sync(0xffffffffu, s.z, o), s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    }
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) < 8) sums[w][col] = s;
     __syncthreads();
-    if (wq == 0 && c < D) {
+    if (threadIdx.x < 8 && c < D) {
 #pragma unroll
         for (int k = 1; k < 8; ++k) {
-            const float4 v = sums[k][lane];
+            const float4 v = sums[k][col];
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
         *reinterpret_cast<float4*>((which ? db : dw) + int64_t(g) * D + c) = s;
@@ -286,12 +304,17 @@ norm_reduce_kernel(int blocks, int D, int G, bool bias, const float* __restrict_
 
 int threads_of(int D) { return ((D + 15) / 16 + 31) / 32 * 32; }
 
-// Persistent grids: a multiple of G blocks, at most what the device holds at once.
-template <typename K> int resident_blocks(K kern, int threads, int G, int64_t N) {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess ||
-        per_sm < 1)
-        per_sm = 1;
+// Persistent grids: a multiple of G blocks, at most what the device holds at once (asked once per
+// kernel and block size; `known` is the kernel's table).
+template <typename K>
+int resident_blocks(K kern, std::atomic<int>* known, int threads, int G, int64_t N) {
+    int per_sm = known[threads / 32].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess ||
+            per_sm < 1)
+            per_sm = 1;
+        known[threads / 32].store(per_sm, std::memory_order_relaxed);
+    }
     int64_t most = int64_t(per_sm) * sm_count() / G;
     if (most < 1) most = 1;
     return int((N < most ? N : most) * G);
@@ -302,7 +325,8 @@ cudaError_t norm_typed(int64_t N, int D, int G, float eps, const void* x, const 
                        const float* b, void* y, float* mean, float* rstd, cudaStream_t st) {
     const int threads = threads_of(D);
     auto kern = threads <= kSmall ? norm_kernel<T, kSmall> : norm_kernel<T, kLarge>;
-    const int blocks = resident_blocks(kern, threads, G, N);
+    static std::atomic<int> known[kLarge / 32 + 1];   // by warps, which also tell the kernel
+    const int blocks = resident_blocks(kern, known, threads, G, N);
     kern<<<blocks, threads, 0, st>>>(N, D, G, eps, static_cast<const T*>(x), w, b,
                                      static_cast<T*>(y), mean, rstd);
     return cudaGetLastError();
@@ -358,7 +382,7 @@ cudaError_t launch_layer_norm_backward(int64_t N, int D, int G, int dtype, const
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((D + 127) / 128, G, bias ? 2 : 1);
+    cfg.gridDim = dim3((D + 31) / 32, G, bias ? 2 : 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
