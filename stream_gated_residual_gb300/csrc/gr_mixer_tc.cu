@@ -230,6 +230,10 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
 
 // kTerms: bf16 terms of the decayed values. Three where the state is a result; where only outputs read
 // it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
+// kFine: for calls of one chunk, P and the state's copy as two bf16 terms each, so that only the output's
+// own rounding is left: over few rows the others do not average out (one row's error was up to 2.6
+// times the output's; over a chunk's rows 1.41 ± 0.05 times), and such a call is bound by latency. The
+// second terms are P's in the columns of its own scores, and the state's in the second stage of b.
 // kSum: only the segment's own sum (no outputs), written to slot `unit`; else the pass, which reads
 // its first state from slot unit − H (the segment before) or from m_in.
 struct Launch {
@@ -243,7 +247,7 @@ struct Launch {
     int split;
 };
 
-template <int DA, int DC, bool kSum, int kTerms, int kPass>
+template <int DA, int DC, bool kSum, int kTerms, int kPass, bool kFine>
 __device__ __forceinline__ void mix_pass(const Launch& L) {
     const MixArgs& p = L.pass[kPass];
     const CUtensorMap &tmA = L.rows[L.a[kPass]], &tmB = L.rows[L.b[kPass]], &tmC = L.rows[L.c[kPass]];
@@ -391,6 +395,9 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                             const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
                             tc_mma(tm + kColE, sdesc_sw128(a0 + off), sdesc_mn(m0 + k * 2048, DA * 128),
                                    iE, k > 0);
+                            if (kFine)
+                                tc_mma(tm + kColE, sdesc_sw128(a0 + off),
+                                       sdesc_mn(base + S::b + S::kB + k * 2048, DA * 128), iE, 1);
                         }
                         tc_commit(&x.m_free);
                     }
@@ -406,7 +413,14 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k)
-                        tc_mma_ts(tm + kColO, tm + kColS + k * 8, sdesc_mn(c0 + k * 2048, kBox), iE, k > 0);
+                        if (kFine) {
+                            const uint32_t at = tm + kColS + (k >> 1) * 32 + (k & 1) * 8;
+                            tc_mma_ts(tm + kColO, at, sdesc_mn(c0 + k * 2048, kBox), iE, k > 0);
+                            tc_mma_ts(tm + kColO, at + 16, sdesc_mn(c0 + k * 2048, kBox), iE, 1);
+                        } else {
+                            tc_mma_ts(tm + kColO, tm + kColS + k * 8, sdesc_mn(c0 + k * 2048, kBox), iE,
+                                      k > 0);
+                        }
                     tc_commit(&x.o_full);
                     tc_commit(&x.c_empty[st]);
                 }
@@ -475,57 +489,58 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                 tc_fence_after();
 #pragma unroll 1
                 for (int jb = 0; jb < 4; ++jb) {
-                    uint32_t r[32], q[16];
+                    uint32_t q[16], q2[16];
                     const bool off = rev ? jb > wq : jb < wq;
-                    if (off || jb == wq) tmem_ld32(tl + kColS + jb * 32, r);
-                    if (off) {
-                        // λ^|i−j| as the row's distance to the block times the column's within it
-                        const float rw = intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
-                        const float4* cw = reinterpret_cast<const float4*>(rev ? x.pw : x.rev);
+                    if (off || jb == wq) {
+                        uint32_t r[32];
+                        tmem_ld32(tl + kColS + jb * 32, r);
+                        // λ^|i−j|: off the diagonal the row's distance to the block times the column's
+                        // within it
+                        const float rw =
+                            !off ? 1.0f : intra * (rev ? x.pw[jb * 32 - i] : x.pw[i - jb * 32 - 31]);
+                        const float4* cw =
+                            reinterpret_cast<const float4*>(!off ? x.diag[lane] : rev ? x.pw : x.rev);
                         const uint64_t rw2 = f2(rw, rw);
                         tmem_wait32(r);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 c = cw[j];
-                            const uint64_t u = f2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+                            const uint64_t u = mul2(f2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                                                    mul2(f2(c.x, c.y), rw2));
                             const uint64_t v =
-                                f2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-                            q[2 * j] = f2_to_bf2(mul2(u, mul2(f2(c.x, c.y), rw2)));
-                            q[2 * j + 1] = f2_to_bf2(mul2(v, mul2(f2(c.z, c.w), rw2)));
+                                mul2(f2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                                     mul2(f2(c.z, c.w), rw2));
+                            q[2 * j] = f2_to_bf2(u), q[2 * j + 1] = f2_to_bf2(v);
+                            if (kFine) {
+                                const uint64_t minus = f2(-1.0f, -1.0f);
+                                q2[2 * j] = f2_to_bf2(fma2(bf2_to_f2(q[2 * j]), minus, u));
+                                q2[2 * j + 1] = f2_to_bf2(fma2(bf2_to_f2(q[2 * j + 1]), minus, v));
+                            }
                         }
-                    } else if (jb == wq) {
-                        const float4* cw = reinterpret_cast<const float4*>(x.diag[lane]);
-                        tmem_wait32(r);
+                        // the columns of later (backwards: earlier) rows are cut off, whatever they hold, and,
+                        // backwards, those past the sequence's end (forwards no valid row reaches them)
+                        const int live = rev ? len - jb * 32 : 32;
+                        if (!off || live < 32) {
+                            const int from = rev && !off ? lane : 0, to = rev || off ? live : lane + 1;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 c = cw[j];
-                            const uint64_t u = f2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
-                            const uint64_t v =
-                                f2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-                            q[2 * j] = f2_to_bf2(mul2(u, f2(c.x, c.y)));
-                            q[2 * j + 1] = f2_to_bf2(mul2(v, f2(c.z, c.w)));
-                        }
-                        // the columns of later (backwards: earlier) rows are cut off, whatever they hold
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (rev ? 2 * j < lane : 2 * j + 1 > lane) q[j] &= rev ? 0xffff0000u : 0xffffu;
-                            if (rev ? 2 * j + 1 < lane : 2 * j > lane) q[j] = 0;
+                            for (int j = 0; j < 16; ++j) {
+                                const uint32_t keep = (2 * j >= from && 2 * j < to ? 0xffffu : 0u) |
+                                                      (2 * j + 1 >= from && 2 * j + 1 < to ? 0xffff0000u : 0u);
+                                q[j] &= keep;
+                                if (kFine) q2[j] &= keep;
+                            }
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) q[j] = 0;
+                        for (int j = 0; j < 16; ++j) q[j] = q2[j] = 0;
                     }
-                    if (rev && len < kChunk) {
-                        // and those past the sequence's end (forwards no valid row reaches them)
-                        const int live = len - jb * 32;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (2 * j + 1 >= live) q[j] &= 0xffffu;
-                            if (2 * j >= live) q[j] = 0;
-                        }
+                    if (kFine) {
+                        tmem_st16(tl + kColS + jb * 32, q);
+                        tmem_st16(tl + kColS + jb * 32 + 16, q2);
+                    } else {
+                        // P's columns lie below the scores that are still to be read
+                        tmem_st16(tl + kColS + jb * 16, q);
                     }
-                    // P's columns lie below the scores that are still to be read
-                    tmem_st16(tl + kColS + jb * 16, q);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -715,7 +730,17 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                                                pack_bf2(M[8 * k + 2], M[8 * k + 3]),
                                                pack_bf2(M[8 * k + 4], M[8 * k + 5]),
                                                pack_bf2(M[8 * k + 6], M[8 * k + 7]));
-                    *reinterpret_cast<uint4*>(sm + S::m + (k >> 3) * (DA * 128) + swz(d, k & 7)) = u;
+                    const int at = (k >> 3) * (DA * 128) + swz(d, k & 7);
+                    *reinterpret_cast<uint4*>(sm + S::m + at) = u;
+                    if (kFine) {
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = f2_to_bf2(fma2(bf2_to_f2(w[j]), f2(-1.0f, -1.0f),
+                                                  f2(M[8 * k + 2 * j], M[8 * k + 2 * j + 1])));
+                        *reinterpret_cast<uint4*>(sm + S::b + S::kB + at) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -789,11 +814,11 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
 
 // blockIdx.y is the pass. Each has its code by itself, so that its arguments stay constants of the launch
 // and branches on them uniform ones (read through an index, a chunk took a quarter longer).
-template <int DA, int DC, bool kSum, int kTerms, int kPasses>
+template <int DA, int DC, bool kSum, int kTerms, int kPasses, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_constant__ Launch L) {
-    if (kPasses == 1 || blockIdx.y == 0) mix_pass<DA, DC, kSum, kTerms, 0>(L);
-    else if (blockIdx.y == 1) mix_pass<DA, DC, kSum, kTerms, 1>(L);
-    else mix_pass<DA, DC, kSum, kTerms, 2>(L);
+    if (kPasses == 1 || blockIdx.y == 0) mix_pass<DA, DC, kSum, kTerms, 0, kFine>(L);
+    else if (blockIdx.y == 1) mix_pass<DA, DC, kSum, kTerms, 1, kFine>(L);
+    else mix_pass<DA, DC, kSum, kTerms, 2, kFine>(L);
 }
 
 // The segments' sums to the states after them, in place: slot s <- λ^len_s (state before s) + slot s.
@@ -932,7 +957,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-template <int DA, int DC, int kTerms, int kPasses>
+template <int DA, int DC, int kTerms, int kPasses, bool kFine>
 cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
     constexpr int passes = kPasses;
     const MixArgs& p = pass[0];
@@ -965,27 +990,35 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
     const dim3 grid(unsigned(L.units), passes);
     constexpr int smem = Smem<DA, DC>::total;
     static_assert(smem <= 232448, "shared memory");
+    static_assert(Smem<DA, DC>::kM <= Smem<DA, DC>::kB, "the state's second term");
     static std::atomic<uint64_t> ready;   // a bit for each device whose kernels have their shared memory
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
-        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false, kTerms, kPasses>,
+        e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true, kTerms, kPasses>,
+            e = cudaFuncSetAttribute(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev <= 63) ready.fetch_or(uint64_t(1) << dev);
     }
     if (e == cudaSuccess && L.split) {
-        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses>, grid, kThreads, smem, st, false, L);
+        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, grid, kThreads, smem, st, false, L);
         if (e == cudaSuccess)
             e = launch(mix_scan_kernel,
                        dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024, passes), 256, 0, st,
                        true, L);
     }
     if (e == cudaSuccess)
-        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses>, grid, kThreads, smem, st, L.split != 0, L);
+        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>, grid, kThreads, smem, st, L.split != 0, L);
     return e;
+}
+
+template <int DA, int DC, int kPasses>
+cudaError_t choose(int how, const MixArgs* p, float* slots, cudaStream_t st) {
+    return how == 0   ? run<DA, DC, 3, kPasses, true>(p, slots, st)
+           : how == 1 ? run<DA, DC, 2, kPasses, false>(p, slots, st)
+                      : run<DA, DC, 3, kPasses, false>(p, slots, st);
 }
 
 }  // namespace
@@ -1011,19 +1044,14 @@ cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStr
     float* slots = static_cast<float*>(workspace);
     bool state = false;
     for (int i = 0; i < passes; ++i) state = state || p[i].m_out;
-    if (passes == 3 && p->da == p->dc) {
-        if (p->da == 128)
-            return state ? run<128, 128, 3, 3>(p, slots, st) : run<128, 128, 2, 3>(p, slots, st);
-        return state ? run<64, 64, 3, 3>(p, slots, st) : run<64, 64, 2, 3>(p, slots, st);
-    }
+    // 0: one chunk at most (whatever its terms: three), 1: two terms, 2: three
+    const int how = p->n_tokens <= kChunk ? 0 : state ? 2 : 1;
+    if (passes == 3 && p->da == p->dc)
+        return p->da == 128 ? choose<128, 128, 3>(how, p, slots, st) : choose<64, 64, 3>(how, p, slots, st);
     if (passes != 1) return cudaErrorInvalidValue;
-    const int kind = (p->da == 128 ? 2 : 0) + (p->dc == 128 ? 1 : 0);
-    switch (kind) {
-        case 3: return state ? run<128, 128, 3, 1>(p, slots, st) : run<128, 128, 2, 1>(p, slots, st);
-        case 2: return state ? run<128, 64, 3, 1>(p, slots, st) : run<128, 64, 2, 1>(p, slots, st);
-        case 1: return state ? run<64, 128, 3, 1>(p, slots, st) : run<64, 128, 2, 1>(p, slots, st);
-        default: return state ? run<64, 64, 3, 1>(p, slots, st) : run<64, 64, 2, 1>(p, slots, st);
-    }
+    if (p->da == 128)
+        return p->dc == 128 ? choose<128, 128, 1>(how, p, slots, st) : choose<128, 64, 1>(how, p, slots, st);
+    return p->dc == 128 ? choose<64, 128, 1>(how, p, slots, st) : choose<64, 64, 1>(how, p, slots, st);
 }
 
 int mixer_status(bool clear) {
