@@ -10,8 +10,7 @@
 //   2. run_sum_kernel     pieces of consecutive sorted positions × 512 channels: the rows of a run
 //                         (equal ids) are summed in registers in ascending t. A run inside the piece
 //                         goes to dE, one that crosses the piece's ends leaves a partial row.
-//   3. run_join_kernel    the piece a crossing run starts in adds up the run's partial rows, always in
-//                         the same order.
+//   3. run_join_kernel    the piece a crossing run starts in adds up the run's partial rows in order.
 // Tiles after the first add to dE, one after another.
 #include <math.h>
 
@@ -335,20 +334,17 @@ run_sum_kernel(const float* __restrict__ dR, const uint32_t* __restrict__ sid,
     }
 }
 
-// A block 128 channels; its 8 warps take the run's pieces in turn and are added up in order.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kSumThreads)
 run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int piece, float scale,
                 bool add, float* __restrict__ dE, const float* __restrict__ part) {
-    __shared__ float4 sums[kJoinThreads / 32][32];
     dep_wait();
     const int p = blockIdx.x, i0 = p * piece, i1 = i0 + piece;
     if (i1 >= n) return;
     const uint32_t id = sid[i1], before = sid[i1 - 1], head = sid[i0], prev = p > 0 ? sid[i0 - 1] : ~id;
     // the run that crosses this piece's end has to begin inside it
     if (id >= V || before != id || (head == id && prev == id)) return;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int c = (blockIdx.y * 32 + lane) * 4;
+    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+    if (c >= D) return;
     // the run's end by bisection: the first sorted index > i1 whose id differs
     int lo = i1 + 1, hi = n;
     while (lo < hi) {
@@ -356,32 +352,21 @@ run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int p
         if (sid[m] == id) lo = m + 1;
         else hi = m;
     }
-    const int pieces = (lo - 1) / piece - p + 1;   // with a share of the run, this one first
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < D) {
-#pragma unroll 4
-        for (int q = w; q < pieces; q += kJoinThreads / 32) {
-            const int64_t row = 2 * int64_t(p + q) + (q == 0 ? 1 : 0);
-            const float4 b = *reinterpret_cast<const float4*>(part + row * D + c);
-            acc.x += b.x, acc.y += b.y, acc.z += b.z, acc.w += b.w;
-        }
-    }
-    sums[w][lane] = acc;
-    __syncthreads();
-    if (w > 0 || c >= D) return;
-#pragma unroll
-    for (int k = 1; k < kJoinThreads / 32; ++k) {
-        const float4 b = sums[k][lane];
+    const int last = (lo - 1) / piece;   // the last piece with a share of the run
+    float4 acc = *reinterpret_cast<const float4*>(part + int64_t(2 * p + 1) * D + c);
+#pragma unroll 16
+    for (int q = p + 1; q <= last; ++q) {
+        const float4 b = *reinterpret_cast<const float4*>(part + int64_t(2 * q) * D + c);
         acc.x += b.x, acc.y += b.y, acc.z += b.z, acc.w += b.w;
     }
     flush(dE + int64_t(id) * D + c, acc, scale, add);
 }
 
-// Sorted positions a CTA of the sums takes: 32 for large tiles (few partial rows), fewer where the
+// Sorted positions a CTA of the sums takes: 64 for large tiles (few partial rows), fewer where the
 // pieces would not fill the SMs.
 int piece_of(int64_t n, int D) {
     const int64_t cols = (D + kSumThreads * 4 - 1) / (kSumThreads * 4);
-    int piece = 32;
+    int piece = 64;
     while (piece > 4 && (n + piece - 1) / piece * cols < int64_t(sm_count()) * 4) piece /= 2;
     return piece;
 }
@@ -461,8 +446,8 @@ cudaError_t launch_embed_backward(int64_t N, int64_t V, int D, int nb, int id_bi
         e = launch_after(nb == 1 ? run_sum_kernel<1> : run_sum_kernel<4>, grid, kSumThreads, 0, st,
                          rows, sid + t0, spos + t0, n, V, D, piece, scale, add, dE, part);
         if (e == cudaSuccess)
-            e = launch_after(run_join_kernel, dim3(grid.x, (D + 127) / 128), kJoinThreads, 0, st,
-                             sid + t0, n, V, D, piece, scale, add, dE, part);
+            e = launch_after(run_join_kernel, grid, kSumThreads, 0, st, sid + t0, n, V, D, piece,
+                             scale, add, dE, part);
     }
     return e;
 }

@@ -120,11 +120,8 @@ norm_kernel(int64_t N, int D, int G, float eps, const T* __restrict__ x,
     const int g = blockIdx.x % G;
     const int64_t first = blockIdx.x / G, step = gridDim.x / G;
     const int c0 = threadIdx.x * 8, c1 = c0 + blockDim.x * 8;
-    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;   // rows on their way: the same registers either way
-    Row<T> ahead[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-        if (first + k * step < N) ahead[k].load(x + ((first + k * step) * G + g) * int64_t(D), c0, c1, D);
+    Row<T> row;   // the next row, on its way (two of them ahead took 8% longer: fewer blocks an SM)
+    if (first < N) row.load(x + (first * G + g) * int64_t(D), c0, c1, D);
     Raw8<float> wr[2], br[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -140,11 +137,9 @@ norm_kernel(int64_t N, int D, int G, float eps, const T* __restrict__ x,
     int turn = 0;
     for (int64_t n = first; n < N; n += step) {
         float v[2][8];
-        ahead[0].v[0].get(v[0]);
-        ahead[0].v[1].get(v[1]);
-        if (kAhead == 2) ahead[0] = ahead[kAhead - 1];
-        if (n + kAhead * step < N)
-            ahead[kAhead - 1].load(x + ((n + kAhead * step) * G + g) * int64_t(D), c0, c1, D);
+        row.v[0].get(v[0]);
+        row.v[1].get(v[1]);
+        if (n + step < N) row.load(x + ((n + step) * G + g) * int64_t(D), c0, c1, D);
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[0][k] + v[1][k];
