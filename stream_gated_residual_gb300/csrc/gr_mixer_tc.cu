@@ -78,7 +78,7 @@ struct Aux {
         c_seen, c_clean[2], done;
     uint32_t tmem;
     int dead;
-    int seq, seg;
+    int seq, seg, index;
     alignas(16) float pw[kChunk + 4];   // λ^0 .. λ^128
     alignas(16) float rev[32];          // λ^31 .. λ^0
     // a block of 32 rows and columns on the diagonal: outer weight λ^|i−j| (rows 16 bytes off a multiple of
@@ -196,9 +196,12 @@ struct Segments {
     }
 };
 
-// The whole warp finds the sequence that holds segment `want`, 32 sequences at a time.
+// The whole warp finds the sequence that holds segment `want`, 32 sequences at a time; `index` is the
+// segment's place among all. kSum counts only the segments that have a successor: those whose sum is
+// needed.
+template <bool kSum>
 __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& sg, int want, int& seq,
-                                             int& seg) {
+                                             int& seg, int& index) {
     const int lane = threadIdx.x & 31;
     int before = 0;
     for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
@@ -207,7 +210,7 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
         if (b < p.n_seqs) {
             int64_t x, y;
             mix_span(p, b, x, y);
-            n = sg.count(x, y);
+            n = sg.count(x, y) - (kSum ? 1 : 0);
         }
         int inc = n;
 #pragma unroll
@@ -221,6 +224,7 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
             const int l = __ffs(hit) - 1;
             seq = b0 + l;
             seg = want - before - (__shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, n, l));
+            index = want + (kSum ? seq : 0);
             return true;
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
@@ -234,8 +238,8 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
 // own rounding is left: over few rows the others do not average out (one row's error was up to 2.6
 // times the output's; over a chunk's rows 1.41 ± 0.05 times), and such a call is bound by latency. The
 // second terms are P's in the columns of its own scores, and the state's in the second stage of b.
-// kSum: only the segment's own sum (no outputs), written to slot `unit`; else the pass, which reads
-// its first state from slot unit − H (the segment before) or from m_in.
+// kSum: only the segment's own sum (no outputs), written to its slot; else the pass, which reads its first
+// state from the slot of the segment before, or from m_in.
 struct Launch {
     CUtensorMap rows[4];             // the distinct row arguments
     MixArgs pass[kMostPasses];
@@ -244,7 +248,6 @@ struct Launch {
     float* slots;                    // [pass][segment][head] states
     float* firsts;                   // a copy of m_in, see mix_scan_kernel; else null
     int64_t units;                   // slots of a pass
-    int split;
 };
 
 template <int DA, int DC, bool kSum, int kTerms, int kPass, bool kFine>
@@ -254,21 +257,21 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
     const Segments sg = L.sg;
     float* const slots = L.slots + int64_t(kPass) * L.units * (DA * DC);
     const float* const firsts = p.m_in && p.m_in == p.m_out ? L.firsts : nullptr;
-    const bool split = L.split != 0;
     using S = Smem<DA, DC>;
     extern __shared__ __align__(1024) char raw[];
     char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);   // the swizzle's atoms
     Aux& x = *reinterpret_cast<Aux*>(sm + S::aux);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = blockIdx.x, h = unit % p.n_heads;
+    const int h = blockIdx.x % p.n_heads;
     const float g = p.log_decay[h], intra = p.weight * p.outer;
 
     if (warp == 0) {
-        int seq = 0, seg = 0;
-        const bool found = find_segment(p, sg, unit / p.n_heads, seq, seg);
+        int seq = 0, seg = 0, index = 0;
+        const bool found = find_segment<kSum>(p, sg, blockIdx.x / p.n_heads, seq, seg, index);
         if (lane == 0) {
             x.seq = found ? seq : -1;
             x.seg = seg;
+            x.index = index;
             x.dead = 0;
             x.bad[0] = x.bad[1] = x.bad[2] = x.bad[3] = 0;
             mbar_init(&x.a_full, 1), mbar_init(&x.a_empty, 1);
@@ -294,11 +297,8 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
     const int64_t all = (end - begin + kChunk - 1) / kChunk;   // the sequence's chunks
     const int64_t n0 = int64_t(seg) * sg.per_seg;              // the segment's first, in time
     const bool last_seg = n0 + sg.per_seg >= all;
-    if (seq < 0 || (kSum && last_seg)) {
-        // nothing to do here (the grid is an upper bound); the pass must not complete before the scan
-        if (!kSum && split && warp == 0) dep_wait();
-        return;
-    }
+    if (seq < 0) return;   // the grid is an upper bound
+    float* const slot = slots + (int64_t(x.index) * p.n_heads + h) * (DA * DC);   // of this segment
     const int chunks = int(min(int64_t(sg.per_seg), all - n0));
     const bool rev = p.reverse;
     // the chunk at step n of this segment: its first row, its rows, and whether the state enters
@@ -700,14 +700,10 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
 #pragma unroll
         for (int e = 0; e < DC; ++e) M[e] = 0.0f;
         const int64_t one = int64_t(DA) * DC;
-        // the states come from the scan (units that need none wait for it at their end: this launch must
-        // not complete before it)
-        const bool early = !kSum && split && (from_slot || (firsts && !last_seg));
-        if (early) dep_wait();
         if (has_in && owns) {
             const bool copied = firsts && !last_seg;
             if (from_slot || copied) {
-                const float* from = from_slot ? slots + int64_t(unit - p.n_heads) * one
+                const float* from = from_slot ? slot - p.n_heads * one
                                               : firsts + (int64_t(seq) * p.n_heads + h) * one;
                 const float4* s = reinterpret_cast<const float4*>(from + int64_t(d) * DC);
 #pragma unroll
@@ -779,7 +775,7 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
         }
         if (n == chunks && owns) {
             if (kSum) {
-                float* s = slots + int64_t(unit) * one + int64_t(d) * DC;
+                float* s = slot + int64_t(d) * DC;
 #pragma unroll
                 for (int e = 0; e < DC; e += 8) {
                     uint32_t u[8];
@@ -803,7 +799,6 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
             }
         }
     }
-    if (!kSum && split && warp == 3) dep_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -826,34 +821,52 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
 // m_out is m_in itself, takes a copy of m_in for the first segments of sequences of several: their
 // last segment may be done before the first one starts.
 __global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ Launch L) {
-    // the pass may start on SMs that are free: all CTAs of the sums are running by now
-    dep_launch_dependents();
-    dep_wait();
     const MixArgs& p = L.pass[blockIdx.z];
     const Segments sg = L.sg;
     float* const firsts = p.m_in && p.m_in == p.m_out ? L.firsts : nullptr;
-    const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
+    const int want = blockIdx.x / p.n_heads, h = blockIdx.x - want * p.n_heads;
     const int one = p.da * p.dc;
     float* const slots = L.slots + int64_t(blockIdx.z) * L.units * one;
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    // the want-th of the sequences that are cut, and the segments before its own
+    __shared__ int found[2];
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int seq = -1, before = 0, cut = 0;
+        for (int b0 = 0; b0 < p.n_seqs && seq < 0; b0 += 32) {
+            int n = 0;
+            if (b0 + lane < p.n_seqs) {
+                int64_t x, y;
+                mix_span(p, b0 + lane, x, y);
+                n = sg.count(x, y);
+            }
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const unsigned cuts = __ballot_sync(0xffffffffu, n > 1);
+            const int mine = cut + __popc(cuts & ((1u << lane) - 1u));
+            const unsigned hit = __ballot_sync(0xffffffffu, n > 1 && mine == want);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                seq = b0 + l;
+                before += __shfl_sync(0xffffffffu, inc - n, l);
+            } else {
+                before += __shfl_sync(0xffffffffu, inc, 31);
+                cut += __popc(cuts);
+            }
+        }
+        if (lane == 0) found[0] = seq, found[1] = before;
+    }
+    __syncthreads();
+    const int b = found[0], first = found[1];
+    if (b < 0 || at >= one) return;   // the grid is an upper bound
+    dep_wait();
     int64_t begin, end;
     mix_span(p, b, begin, end);
     const int n = sg.count(begin, end);
-    if (n < 2 || at >= one) return;
-    __shared__ int first;
-    // the segments of the sequences before this one
-    if (threadIdx.x < 32) {
-        int sum = 0;
-        for (int k = threadIdx.x; k < b; k += 32) {
-            int64_t x, y;
-            mix_span(p, k, x, y);
-            sum += sg.count(x, y);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (threadIdx.x == 0) first = sum;
-    }
-    __syncthreads();
     const float g = p.log_decay[h];
     float m[4] = {};
     if (p.m_in) {
@@ -896,15 +909,15 @@ __global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ L
 // launches. The host knows the sequences' number and sum, not their lengths:
 //   - too few of them to fill the SMs (rows < 152): taken as equally long, cut so that the estimated time
 //     is least (32768 tokens, 32 heads of 128: 256 chunks uncut 969 us, in 4 segments 423, in 9 389);
-//   - enough of them: only a sequence longer than an SM's even share of all chunks is cut, which
+//   - enough of them: only a sequence longer than twice an SM's even share of all chunks is cut, which
 //     bounds what a single long one can cost (equal ones are never cut).
-int plan_segments(int64_t N, int n_seqs, int64_t heads) {
+int plan_evenly(int64_t N, int n_seqs, int64_t heads) {
     const int64_t rows = n_seqs * heads;
     const int64_t mean = (N + n_seqs - 1) / n_seqs;
     const int64_t chunks = (mean + kChunk - 1) / kChunk;
     if (rows >= kSms) {
         const int64_t total = (N / kChunk + n_seqs) * heads;
-        const int64_t share = (total + kSms - 1) / kSms;
+        const int64_t share = 2 * ((total + kSms - 1) / kSms);
         return int(share < 1 << 20 ? share : 1 << 20);
     }
     if (chunks <= 1) return 1;
@@ -922,6 +935,13 @@ int plan_segments(int64_t N, int n_seqs, int64_t heads) {
         if (t < least) least = t, best = per;
     }
     return int(best < 1 << 20 ? best : 1 << 20);
+}
+
+int plan_segments(int64_t N, int n_seqs, int64_t heads) {
+    const int per = plan_evenly(N, n_seqs, heads);
+    // several sequences, but none can be twice as long: not cut, which saves the two launches that
+    // would look for one that is (13 us of 140 for the gradient of 2 · 4096 tokens, 16 heads of 128)
+    return n_seqs > 1 && N <= 2 * int64_t(per) * kChunk ? int(N / kChunk + 1) : per;
 }
 
 // An upper bound of the segments of all sequences, times the heads.
@@ -984,9 +1004,9 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
     L.sg.per_seg = plan_segments(p.n_tokens, p.n_seqs, int64_t(p.n_heads) * passes);
     L.units = most_units(p.n_tokens, p.n_seqs, p.n_heads, L.sg.per_seg);
     // no sequence is longer than all tokens
-    L.split = p.n_tokens > int64_t(L.sg.per_seg) * kChunk;
+    const bool split = p.n_tokens > int64_t(L.sg.per_seg) * kChunk;
     L.slots = slots;
-    L.firsts = L.split ? slots + passes * L.units * int64_t(DA * DC) : nullptr;
+    L.firsts = split ? slots + passes * L.units * int64_t(DA * DC) : nullptr;
     const dim3 grid(unsigned(L.units), passes);
     constexpr int smem = Smem<DA, DC>::total;
     static_assert(smem <= 232448, "shared memory");
@@ -1002,15 +1022,20 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev <= 63) ready.fetch_or(uint64_t(1) << dev);
     }
-    if (e == cudaSuccess && L.split) {
-        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, grid, kThreads, smem, st, false, L);
+    if (e == cudaSuccess && split) {
+        // a segment with a successor is a whole one
+        const dim3 sums(unsigned(p.n_tokens / (int64_t(L.sg.per_seg) * kChunk)) * p.n_heads, passes);
+        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, sums, kThreads, smem, st, false, L);
         if (e == cudaSuccess)
             e = launch(mix_scan_kernel,
-                       dim3(unsigned(p.n_seqs) * p.n_heads, (DA * DC + 1023) / 1024, passes), 256, 0, st,
-                       true, L);
+                       dim3(sums.x < unsigned(p.n_seqs) * p.n_heads ? sums.x : p.n_seqs * p.n_heads,
+                            (DA * DC + 1023) / 1024, passes),
+                       256, 0, st, true, L);
     }
+    // (launched after the scan in the plain order: as its programmatic dependent a gradient of 96 uncut
+    // rows took 176 us against 142)
     if (e == cudaSuccess)
-        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>, grid, kThreads, smem, st, L.split != 0, L);
+        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>, grid, kThreads, smem, st, false, L);
     return e;
 }
 
