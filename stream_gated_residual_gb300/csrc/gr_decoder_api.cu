@@ -104,15 +104,20 @@ bool tc_shape(const gr_mixer* m) {
            (m->d_value == 64 || m->d_value == 128);
 }
 
-// Workspace of a prompt, or of its gradient: all three passes at once where they have the same shape
-// (d_key == d_value), else one after another.
+// Workspace of a prompt, or of its gradient: on the tensor cores all three passes at once where they
+// have the same shape (d_key == d_value), else one after another. Both forms' needs are covered: a row's
+// strides may be beyond what the tensor cores' copies take.
 size_t mixer_workspace(const gr_mixer* m, bool gradient) {
-    if (!tc_shape(m)) return 0;
-    auto of = [&](int passes) {
-        return mix_tc_workspace(m->n_tokens, m->n_seqs, m->n_heads, m->d_key, m->d_value, passes);
-    };
-    const size_t one = of(1), three = gradient && m->d_key == m->d_value ? of(3) : 0;
-    return one > three ? one : three;
+    const int64_t N = m->n_tokens;
+    const int B = m->n_seqs, H = m->n_heads, dk = m->d_key, dv = m->d_value;
+    size_t need = mix_simt_workspace(N, B, H, dk, dv);
+    auto cover = [&](size_t n) { need = need > n ? need : n; };
+    if (gradient) cover(mix_simt_workspace(N, B, H, dv, dk));
+    if (tc_shape(m)) {
+        cover(mix_tc_workspace(N, B, H, dk, dv, 1));
+        if (gradient && dk == dv) cover(mix_tc_workspace(N, B, H, dk, dv, 3));
+    }
+    return need;
 }
 
 // Passes over the same rows: three in one launch on the tensor cores, else one after another.
@@ -122,7 +127,7 @@ int run_mix(const MixArgs* p, int passes, void* ws, cudaStream_t st) {
     if (tc && passes == 3) return as_status(launch_mix_tc(p, passes, ws, st));
     for (int i = 0; i < passes; ++i) {
         const cudaError_t e =
-            mix_tc_supported(p[i]) ? launch_mix_tc(p + i, 1, ws, st) : launch_mix_simt(p[i], st);
+            mix_tc_supported(p[i]) ? launch_mix_tc(p + i, 1, ws, st) : launch_mix_simt(p[i], ws, st);
         if (e != cudaSuccess) return GR_E_CUDA;
     }
     return GR_OK;

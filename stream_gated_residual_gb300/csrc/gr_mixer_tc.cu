@@ -41,7 +41,6 @@ constexpr int kChunk = 128;
 constexpr int kBox = kChunk * 128;        // 128 rows of 64 bf16 channels
 constexpr int kThreads = 640;
 constexpr int kSub = 16;                  // tokens of one step of the state's MMA
-constexpr int kSms = 152;                 // segments are planned for this many CTAs
 
 // Tensor-memory columns: scores (then P in place), Σ P c, Mᵀ a, the state's update.
 constexpr uint32_t kColS = 0, kColO = 128, kColE = 256, kColU = 384;
@@ -185,61 +184,6 @@ __device__ __forceinline__ void split_terms(uint32_t u, uint64_t w2, uint32_t& t
     }
 }
 
-// Where a CTA works: segment `seg` (in the order of time it is processed) of sequence `seq`. Every
-// sequence has at least one segment, so that an empty one passes its state on.
-struct Segments {
-    int per_seg;   // chunks of a segment
-    __device__ __forceinline__ int count(int64_t begin, int64_t end) const {
-        const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
-        const int64_t n = (chunks + per_seg - 1) / per_seg;
-        return n > 0 ? int(n) : 1;
-    }
-};
-
-// The whole warp finds the sequence that holds segment `want`, 32 sequences at a time; `index` is the
-// segment's place among all. kSum counts only the segments that have a successor: those whose sum is
-// needed.
-template <bool kSum>
-__device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& sg, int want, int& seq,
-                                             int& seg, int& index) {
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        int n = 0;
-        if (b < p.n_seqs) {
-            int64_t x, y;
-            mix_span(p, b, x, y);
-            n = sg.count(x, y) - (kSum ? 1 : 0);
-        }
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        const bool mine = n > 0 && want >= before + inc - n && want < before + inc;
-        const unsigned hit = __ballot_sync(0xffffffffu, mine);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            seq = b0 + l;
-            seg = want - before - (__shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, n, l));
-            index = want + (kSum ? seq : 0);
-            return true;
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    return false;
-}
-
-// kTerms: bf16 terms of the decayed values. Three where the state is a result; where only outputs read
-// it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
-// kFine: for calls of one chunk, P and the state's copy as two bf16 terms each, so that only the output's
-// own rounding is left: over few rows the others do not average out (one row's error was up to 2.6
-// times the output's; over a chunk's rows 1.41 ± 0.05 times), and such a call is bound by latency. The
-// second terms are P's in the columns of its own scores, and the state's in the second stage of b.
-// kSum: only the segment's own sum (no outputs), written to its slot; else the pass, which reads its first
-// state from the slot of the segment before, or from m_in.
 struct Launch {
     CUtensorMap rows[4];             // the distinct row arguments
     MixArgs pass[kMostPasses];
@@ -816,139 +760,6 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     else mix_pass<DA, DC, kSum, kTerms, 2, kFine>(L);
 }
 
-// The segments' sums to the states after them, in place: slot s <- λ^len_s (state before s) + slot s.
-// One thread four elements of a (sequence, head); the last segment's slot is not used. `firsts`, when
-// m_out is m_in itself, takes a copy of m_in for the first segments of sequences of several: their
-// last segment may be done before the first one starts.
-__global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ Launch L) {
-    const MixArgs& p = L.pass[blockIdx.z];
-    const Segments sg = L.sg;
-    float* const firsts = p.m_in && p.m_in == p.m_out ? L.firsts : nullptr;
-    const int want = blockIdx.x / p.n_heads, h = blockIdx.x - want * p.n_heads;
-    const int one = p.da * p.dc;
-    float* const slots = L.slots + int64_t(blockIdx.z) * L.units * one;
-    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
-    // the want-th of the sequences that are cut, and the segments before its own
-    __shared__ int found[2];
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int seq = -1, before = 0, cut = 0;
-        for (int b0 = 0; b0 < p.n_seqs && seq < 0; b0 += 32) {
-            int n = 0;
-            if (b0 + lane < p.n_seqs) {
-                int64_t x, y;
-                mix_span(p, b0 + lane, x, y);
-                n = sg.count(x, y);
-            }
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            const unsigned cuts = __ballot_sync(0xffffffffu, n > 1);
-            const int mine = cut + __popc(cuts & ((1u << lane) - 1u));
-            const unsigned hit = __ballot_sync(0xffffffffu, n > 1 && mine == want);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                seq = b0 + l;
-                before += __shfl_sync(0xffffffffu, inc - n, l);
-            } else {
-                before += __shfl_sync(0xffffffffu, inc, 31);
-                cut += __popc(cuts);
-            }
-        }
-        if (lane == 0) found[0] = seq, found[1] = before;
-    }
-    __syncthreads();
-    const int b = found[0], first = found[1];
-    if (b < 0 || at >= one) return;   // the grid is an upper bound
-    dep_wait();
-    int64_t begin, end;
-    mix_span(p, b, begin, end);
-    const int n = sg.count(begin, end);
-    const float g = p.log_decay[h];
-    float m[4] = {};
-    if (p.m_in) {
-        const float* s = p.m_in + (int64_t(b) * p.n_heads + h) * one;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = (at + k) / p.dc, j = (at + k) - i * p.dc;
-            m[k] = s[int64_t(i) * p.mr + int64_t(j) * p.mc];
-        }
-    }
-    if (firsts)
-        *reinterpret_cast<float4*>(firsts + (int64_t(b) * p.n_heads + h) * one + at) =
-            make_float4(m[0], m[1], m[2], m[3]);
-    const int64_t full = int64_t(sg.per_seg) * kChunk;
-    // backwards the first segment holds the sequence's partial chunk, and its state enters undecayed
-    const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
-    const int64_t len0 = p.reverse ? full - (chunks * kChunk - (end - begin)) - 1 : full;
-    const float l0 = decay_pow(g, len0), lf = decay_pow(g, full);
-    const int64_t step = int64_t(p.n_heads) * one;
-    float* s = slots + (int64_t(first) * p.n_heads + h) * one + at;
-    constexpr int kU = 4;
-    for (int i = 0; i < n - 1; i += kU) {
-        float4 v[kU];
-#pragma unroll
-        for (int k = 0; k < kU; ++k)
-            if (i + k < n - 1) v[k] = __ldcg(reinterpret_cast<const float4*>(s + (i + k) * step));
-#pragma unroll
-        for (int k = 0; k < kU; ++k)
-            if (i + k < n - 1) {
-                const float w = i + k == 0 ? l0 : lf;
-                m[0] = fmaf(w, m[0], v[k].x), m[1] = fmaf(w, m[1], v[k].y);
-                m[2] = fmaf(w, m[2], v[k].z), m[3] = fmaf(w, m[3], v[k].w);
-                *reinterpret_cast<float4*>(s + (i + k) * step) = make_float4(m[0], m[1], m[2], m[3]);
-            }
-    }
-}
-
-// Chunks a segment. A unit (a segment of a head) takes its chunks one after another, one unit an SM at a
-// time; cutting a sequence costs a second pass over b and c of all but its last segment, and two
-// launches. The host knows the sequences' number and sum, not their lengths:
-//   - too few of them to fill the SMs (rows < 152): taken as equally long, cut so that the estimated time
-//     is least (32768 tokens, 32 heads of 128: 256 chunks uncut 969 us, in 4 segments 423, in 9 389);
-//   - enough of them: only a sequence longer than twice an SM's even share of all chunks is cut, which
-//     bounds what a single long one can cost (equal ones are never cut).
-int plan_evenly(int64_t N, int n_seqs, int64_t heads) {
-    const int64_t rows = n_seqs * heads;
-    const int64_t mean = (N + n_seqs - 1) / n_seqs;
-    const int64_t chunks = (mean + kChunk - 1) / kChunk;
-    if (rows >= kSms) {
-        const int64_t total = (N / kChunk + n_seqs) * heads;
-        const int64_t share = 2 * ((total + kSms - 1) / kSms);
-        return int(share < 1 << 20 ? share : 1 << 20);
-    }
-    if (chunks <= 1) return 1;
-    int64_t most = (6 * kSms + rows - 1) / rows;
-    most = most < chunks ? most : chunks;
-    int64_t best = chunks;
-    double least = 1e300;
-    for (int64_t n = 1; n <= most; ++n) {
-        const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
-        const int64_t waves = (rows * segs + kSms - 1) / kSms;
-        const int64_t waves1 = (rows * (segs - 1) + kSms - 1) / kSms;
-        // in units of a chunk's time (about 4 us): 2 a unit to start and drain; sums 0.6 of a chunk
-        double t = waves * (per + 2.0);
-        if (segs > 1) t += waves1 * (0.6 * per + 1.5) + 2.0;
-        if (t < least) least = t, best = per;
-    }
-    return int(best < 1 << 20 ? best : 1 << 20);
-}
-
-int plan_segments(int64_t N, int n_seqs, int64_t heads) {
-    const int per = plan_evenly(N, n_seqs, heads);
-    // several sequences, but none can be twice as long: not cut, which saves the two launches that
-    // would look for one that is (13 us of 140 for the gradient of 2 · 4096 tokens, 16 heads of 128)
-    return n_seqs > 1 && N <= 2 * int64_t(per) * kChunk ? int(N / kChunk + 1) : per;
-}
-
-// An upper bound of the segments of all sequences, times the heads.
-int64_t most_units(int64_t N, int n_seqs, int H, int per_seg) {
-    return (N / (int64_t(per_seg) * kChunk) + n_seqs) * H;
-}
-
 bool map_rows(CUtensorMap* m, const MixRows& r, int64_t N, int H, int d) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
@@ -1001,10 +812,9 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
         L.c[i] = map_of(pass[i].c, DC);
         if (L.a[i] < 0 || L.b[i] < 0 || L.c[i] < 0) return cudaErrorInvalidValue;
     }
-    L.sg.per_seg = plan_segments(p.n_tokens, p.n_seqs, int64_t(p.n_heads) * passes);
-    L.units = most_units(p.n_tokens, p.n_seqs, p.n_heads, L.sg.per_seg);
-    // no sequence is longer than all tokens
-    const bool split = p.n_tokens > int64_t(L.sg.per_seg) * kChunk;
+    L.sg = mix_plan(p.n_tokens, p.n_seqs, int64_t(p.n_heads) * passes, kChunk);
+    L.units = mix_units(p.n_tokens, p.n_seqs, p.n_heads, L.sg);
+    const bool split = mix_cuts(p.n_tokens, L.sg);
     L.slots = slots;
     L.firsts = split ? slots + passes * L.units * int64_t(DA * DC) : nullptr;
     const dim3 grid(unsigned(L.units), passes);
@@ -1023,14 +833,10 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
         if (e == cudaSuccess && dev <= 63) ready.fetch_or(uint64_t(1) << dev);
     }
     if (e == cudaSuccess && split) {
-        // a segment with a successor is a whole one
-        const dim3 sums(unsigned(p.n_tokens / (int64_t(L.sg.per_seg) * kChunk)) * p.n_heads, passes);
+        const dim3 sums(mix_sums(p.n_tokens, p.n_heads, L.sg), passes);
         e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, sums, kThreads, smem, st, false, L);
         if (e == cudaSuccess)
-            e = launch(mix_scan_kernel,
-                       dim3(sums.x < unsigned(p.n_seqs) * p.n_heads ? sums.x : p.n_seqs * p.n_heads,
-                            (DA * DC + 1023) / 1024, passes),
-                       256, 0, st, true, L);
+            e = launch_mix_scan(L.pass, passes, L.sg, slots, L.firsts, L.units, st);
     }
     // (launched after the scan in the plain order: as its programmatic dependent a gradient of 96 uncut
     // rows took 176 us against 142)
@@ -1054,15 +860,15 @@ bool mix_tc_supported(const MixArgs& p) {
         if (r->ts > most || r->hs > most) return false;
     return p.dtype == GR_BF16 && (p.da == 64 || p.da == 128) && (p.dc == 64 || p.dc == 128) &&
            p.n_tokens > 0 && p.n_seqs > 0 &&
-           most_units(p.n_tokens, p.n_seqs, p.n_heads, 1) <= 0x7fffffff;
+           mix_units(p.n_tokens, p.n_seqs, p.n_heads, {1, kChunk}) <= 0x7fffffff;
 }
 
 // The slots of all passes and, for one of them, a copy of its first states.
 size_t mix_tc_workspace(int64_t N, int n_seqs, int H, int da, int dc, int passes) {
     if (N == 0 || n_seqs == 0) return 0;
-    const int per = plan_segments(N, n_seqs, int64_t(H) * passes);
-    if (N <= int64_t(per) * kChunk) return 0;
-    return align256(size_t(passes * most_units(N, n_seqs, H, per) + int64_t(n_seqs) * H) * da * dc * 4);
+    const Segments sg = mix_plan(N, n_seqs, int64_t(H) * passes, kChunk);
+    if (!mix_cuts(N, sg)) return 0;
+    return align256(size_t(passes * mix_units(N, n_seqs, H, sg) + int64_t(n_seqs) * H) * da * dc * 4);
 }
 
 cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStream_t st) {
