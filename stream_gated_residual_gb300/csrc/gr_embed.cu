@@ -10,7 +10,8 @@
 //   2. run_sum_kernel     pieces of consecutive sorted positions × 512 channels: the rows of a run
 //                         (equal ids) are summed in registers in ascending t. A run inside the piece
 //                         goes to dE, one that crosses the piece's ends leaves a partial row.
-//   3. run_join_kernel    the piece a crossing run starts in adds up the run's partial rows in order.
+//   3. run_join_kernel    the piece a crossing run starts in adds up the run's partial rows, always in
+//                         the same order.
 // Tiles after the first add to dE, one after another.
 #include <math.h>
 
@@ -121,120 +122,122 @@ void embed_types(int64_t N, int64_t V, int D, int nb, int table_dtype, int state
 // ---- the gradient's sort ------------------------------------------------------------------------
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortItems = 16;                          // a thread's items
+constexpr int kSortItems = 16;                          // a thread's items at most
 constexpr int kSortTile = kSortThreads * kSortItems;    // 16384: tokens of one tile
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kDigits = 256;
-// positions + keys, the warps' digit counts, the scan's warp sums
-constexpr size_t kSortSmem = size_t(kSortTile) * 6 + size_t(kDigits) * kSortWarps * 2 + 128;
+constexpr int kSortBits = 5;
+constexpr int kDigits = 1 << kSortBits;
+// Items lie in shared memory with a gap after every 16, so that threads reading 16 in a row meet no
+// bank twice.
+__device__ __forceinline__ int at(int i) { return i + (i >> 4); }
+constexpr int kSortSlots = kSortTile + kSortTile / 16;
+// keys, positions, the threads' digit counts, the scan's warp sums
+constexpr size_t kSortSmem =
+    size_t(kSortSlots) * 6 + size_t(kDigits) * kSortThreads * 2 + 32 * sizeof(uint32_t);
 
-// Stable radix sort of a tile's (id, position), 8 bits a pass, least significant first. Warp w
-// owns the items [w·32·items, (w+1)·32·items) in rounds of 32, so a digit's items keep their order:
-// rank = the warp's count of the digit so far + the equal lanes below (match), and the base comes
-// from a scan of the counts in (digit, warp) order. Ids outside [0, V) take the key V.
+// Stable radix sort of a tile's (id, position), 5 bits a pass, least significant first. A thread holds
+// consecutive items and counts its own digits one after another, so an item's rank among its thread's
+// equal digits comes with the count, and a scan of the counts in (digit, thread) order gives the
+// places: warp d scans digit d's counts. Few items take few of the threads, 4 to 8 each. (Ranks from warp-wide matches of 8-bit digits took 56 us for 16384 uniform ids of 15 bits: a
+// match costs a step for every distinct digit in the warp.) Ids outside [0, V) take the key V.
 template <typename TI>
 __device__ void sort_tile(const TI* __restrict__ ids, int64_t V, int n, int passes,
                           uint32_t* __restrict__ out_id, uint32_t* __restrict__ out_pos, char* smem) {
     uint32_t* skey = reinterpret_cast<uint32_t*>(smem);
-    uint16_t* spos = reinterpret_cast<uint16_t*>(smem + size_t(kSortTile) * 4);
-    uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + size_t(kSortTile) * 6);  // [digit][warp]
-    uint32_t* wsum = reinterpret_cast<uint32_t*>(smem + size_t(kSortTile) * 6 +
-                                                 size_t(kDigits) * kSortWarps * 2);
+    uint16_t* spos = reinterpret_cast<uint16_t*>(smem + size_t(kSortSlots) * 4);
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + size_t(kSortSlots) * 6);   // [digit][thread]
+    uint32_t* wsum = reinterpret_cast<uint32_t*>(cnt + size_t(kDigits) * kSortThreads);
+    static_assert(kDigits == kSortThreads / 32, "a warp a digit");
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    // items a warp holds: as few rounds as cover n (the ranges stay contiguous)
-    const int rounds = (n + kSortThreads - 1) / kSortThreads;
-    uint32_t key[kSortItems];
-    uint16_t pos[kSortItems];
-    uint16_t rank[kSortItems];
-#pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-        const int i = (w * rounds + j) * 32 + lane;
-        key[j] = 0xffffffffu;      // past the tile: sorts behind every key and is not written
-        pos[j] = uint16_t(i);
-        if (j < rounds && i < n) {
+    int holders = 32;                                   // threads that hold items
+    while (holders < kSortThreads && holders * 8 < n) holders *= 2;
+    const int per = (n + holders - 1) / holders;        // items of each
+    const bool holds = tid < holders;
+    for (int i = tid; i < per * holders; i += kSortThreads) {
+        uint32_t key = 0xffffffffu;   // past the tile: sorts behind every key and is not written
+        if (i < n) {
             const int64_t id = int64_t(ids[i]);
-            key[j] = uint32_t(id >= 0 && id < V ? id : V);
+            key = uint32_t(id >= 0 && id < V ? id : V);
         }
+        skey[at(i)] = key;
+        spos[at(i)] = uint16_t(i);
     }
+    const int quads = holders / 8;                      // 16-byte groups of a digit's counts
+    uint4* const counts = reinterpret_cast<uint4*>(cnt);
     for (int p = 0; p < passes; ++p) {
-        for (int i = tid; i < kDigits * kSortWarps / 2; i += kSortThreads)
-            reinterpret_cast<uint32_t*>(cnt)[i] = 0;
+        for (int i = tid; i < kDigits * quads; i += kSortThreads) counts[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
+        uint32_t key[kSortItems];
+        uint32_t pos[kSortItems / 2], rank[kSortItems / 4];   // two and four to a register
+        if (holds) {
 #pragma unroll
-        for (int j = 0; j < kSortItems; ++j) {
-            if (j < rounds) {
-                const uint32_t d = (key[j] >> (8 * p)) & 255u;
-                const uint32_t same = __match_any_sync(0xffffffffu, d);
-                const uint32_t below = __popc(same & ((1u << lane) - 1u));
-                uint16_t* c = cnt + d * kSortWarps + w;
-                const uint32_t base = *c;
-                rank[j] = uint16_t(base + below);
-                __syncwarp();
-                if (below == 0) *c = uint16_t(base + __popc(same));
-                __syncwarp();
+            for (int j = 0; j < kSortItems; ++j) {
+                if (j % 2 == 0) pos[j / 2] = 0;
+                if (j % 4 == 0) rank[j / 4] = 0;
+                if (j < per) {
+                    const int i = at(tid * per + j);
+                    key[j] = skey[i];
+                    pos[j / 2] |= uint32_t(spos[i]) << (16 * (j & 1));
+                    uint16_t* c = cnt + ((key[j] >> (kSortBits * p)) & (kDigits - 1)) * holders + tid;
+                    const uint32_t r = *c;
+                    *c = uint16_t(r + 1);
+                    rank[j / 4] |= r << (8 * (j & 3));
+                }
             }
         }
         __syncthreads();
-        // exclusive scan of the 8192 counts in (digit, warp) order, 8 a thread
-        uint4* mine = reinterpret_cast<uint4*>(cnt) + tid;
-        const uint4 u = *mine;
-        const uint32_t pk[4] = {u.x, u.y, u.z, u.w};
-        uint32_t v[8], sum = 0;
+        // exclusive scan within digit w, then of the digits' sums
+        uint32_t sum = 0;
+        for (int i0 = 0; i0 < quads; i0 += 32) {
+            const int i = w * quads + i0 + lane;
+            const uint4 u = i0 + lane < quads ? counts[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t pk[4] = {u.x, u.y, u.z, u.w};
+            uint32_t t = u.x + u.y + u.z + u.w;   // halves of at most 16 · 4 each: no carry
+            t = (t & 0xffffu) + (t >> 16);
+            uint32_t inc = t;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[k] = sum;
-            sum += (pk[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-        }
-        uint32_t inc = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            uint32_t base = sum + inc - t, q[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t next = base + (pk[k] & 0xffffu);
+                q[k] = (base & 0xffffu) | (next << 16);
+                base = next + (pk[k] >> 16);
+            }
+            if (i0 + lane < quads) counts[i] = make_uint4(q[0], q[1], q[2], q[3]);
+            sum += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 31) wsum[w] = inc;
+        if (lane == 0) wsum[w] = sum;
         __syncthreads();
         if (w == 0) {
-            uint32_t x = wsum[lane];
+            const uint32_t t = wsum[lane];
+            uint32_t x = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            wsum[lane] = x;
+            wsum[lane] = x - t;
         }
         __syncthreads();
-        const uint32_t base = (w ? wsum[w - 1] : 0) + inc - sum;
-        uint32_t q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            q[k] = ((base + v[2 * k]) & 0xffffu) | ((base + v[2 * k + 1]) << 16);
-        *mine = make_uint4(q[0], q[1], q[2], q[3]);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kSortItems; ++j) {
-            if (j < rounds) {
-                const uint32_t d = (key[j] >> (8 * p)) & 255u;
-                const uint32_t to = uint32_t(cnt[d * kSortWarps + w]) + rank[j];
-                skey[to] = key[j];
-                spos[to] = pos[j];
-            }
-        }
-        __syncthreads();
-        if (p + 1 < passes) {
+        if (holds) {
 #pragma unroll
             for (int j = 0; j < kSortItems; ++j) {
-                if (j < rounds) {
-                    const int i = (w * rounds + j) * 32 + lane;
-                    key[j] = skey[i];
-                    pos[j] = spos[i];
+                if (j < per) {
+                    const uint32_t d = (key[j] >> (kSortBits * p)) & (kDigits - 1);
+                    const int to = at(int(wsum[d] + cnt[d * holders + tid] + ((rank[j / 4] >> (8 * (j & 3))) & 255u)));
+                    skey[to] = key[j];
+                    spos[to] = uint16_t(pos[j / 2] >> (16 * (j & 1)));
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
     for (int i = tid; i < n; i += kSortThreads) {
-        out_id[i] = skey[i];
-        out_pos[i] = spos[i];
+        out_id[i] = skey[at(i)];
+        out_pos[i] = spos[at(i)];
     }
 }
 
@@ -334,17 +337,20 @@ run_sum_kernel(const float* __restrict__ dR, const uint32_t* __restrict__ sid,
     }
 }
 
-__global__ void __launch_bounds__(kSumThreads)
+// Four groups of threads take a run's pieces in turn and are added up in order.
+constexpr int kJoinGroups = 4;
+__global__ void __launch_bounds__(kSumThreads * kJoinGroups)
 run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int piece, float scale,
                 bool add, float* __restrict__ dE, const float* __restrict__ part) {
+    __shared__ float4 sums[kJoinGroups][kSumThreads];
     dep_wait();
     const int p = blockIdx.x, i0 = p * piece, i1 = i0 + piece;
     if (i1 >= n) return;
     const uint32_t id = sid[i1], before = sid[i1 - 1], head = sid[i0], prev = p > 0 ? sid[i0 - 1] : ~id;
     // the run that crosses this piece's end has to begin inside it
     if (id >= V || before != id || (head == id && prev == id)) return;
-    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
-    if (c >= D) return;
+    const int t = threadIdx.x % kSumThreads, group = threadIdx.x / kSumThreads;
+    const int c = (blockIdx.y * kSumThreads + t) * 4;
     // the run's end by bisection: the first sorted index > i1 whose id differs
     int lo = i1 + 1, hi = n;
     while (lo < hi) {
@@ -352,11 +358,22 @@ run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int p
         if (sid[m] == id) lo = m + 1;
         else hi = m;
     }
-    const int last = (lo - 1) / piece;   // the last piece with a share of the run
-    float4 acc = *reinterpret_cast<const float4*>(part + int64_t(2 * p + 1) * D + c);
-#pragma unroll 16
-    for (int q = p + 1; q <= last; ++q) {
-        const float4 b = *reinterpret_cast<const float4*>(part + int64_t(2 * q) * D + c);
+    const int pieces = (lo - 1) / piece - p + 1;   // with a share of the run, this one first
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < D) {
+#pragma unroll 8
+        for (int q = group; q < pieces; q += kJoinGroups) {
+            const int64_t row = 2 * int64_t(p + q) + (q == 0 ? 1 : 0);
+            const float4 b = *reinterpret_cast<const float4*>(part + row * D + c);
+            acc.x += b.x, acc.y += b.y, acc.z += b.z, acc.w += b.w;
+        }
+    }
+    sums[group][t] = acc;
+    __syncthreads();
+    if (group > 0 || c >= D) return;
+#pragma unroll
+    for (int k = 1; k < kJoinGroups; ++k) {
+        const float4 b = sums[k][t];
         acc.x += b.x, acc.y += b.y, acc.z += b.z, acc.w += b.w;
     }
     flush(dE + int64_t(id) * D + c, acc, scale, add);
@@ -390,8 +407,8 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
 template <typename TI>
 cudaError_t sort_fill(int64_t N, int64_t V, const void* ids, uint32_t* sid, uint32_t* spos,
                       float* fill, int64_t fill_n, cudaStream_t st) {
-    int passes = 1;
-    while (passes < 4 && (uint64_t(V) >> (8 * passes)) != 0) ++passes;
+    int passes = 1;   // the keys are 0 .. V
+    while ((uint64_t(V) >> (kSortBits * passes)) != 0) ++passes;
     const int tiles = int((N + kSortTile - 1) / kSortTile);
     const int64_t n4 = fill_n / 4;
     int64_t fillers = fill ? (n4 + kSortThreads * 4 - 1) / (kSortThreads * 4) : 0;
@@ -446,7 +463,7 @@ cudaError_t launch_embed_backward(int64_t N, int64_t V, int D, int nb, int id_bi
         e = launch_after(nb == 1 ? run_sum_kernel<1> : run_sum_kernel<4>, grid, kSumThreads, 0, st,
                          rows, sid + t0, spos + t0, n, V, D, piece, scale, add, dE, part);
         if (e == cudaSuccess)
-            e = launch_after(run_join_kernel, grid, kSumThreads, 0, st, sid + t0, n, V, D, piece,
+            e = launch_after(run_join_kernel, grid, kSumThreads * kJoinGroups, 0, st, sid + t0, n, V, D, piece,
                              scale, add, dE, part);
     }
     return e;
