@@ -450,7 +450,8 @@ int gr_linear_attention_workspace_size(const gr_mixer* m, int gradient, size_t* 
 /* Prompts: q, k [.., d_key], v, o [.., d_value]; state_in [n_seqs][n_heads][d_key][d_value] fp32 is S
  * before each sequence's first token (NULL: zero), state_out, if not NULL, S after its last (the
  * same buffer is allowed). On "mixer_tc" the scores and the state are rounded to bf16 where they
- * enter a product; the state itself is held and updated in fp32 (from bf16 triples of the decayed
+ * enter a product (in calls of at most 128 tokens to two bf16 terms, which leaves the output's own
+ * rounding); the state itself is held and updated in fp32 (from bf16 triples of the decayed
  * values, so its error is fp32's). A value that is not finite makes the outputs from its token on
  * not finite, and no earlier ones. */
 int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, const gr_rows* v,

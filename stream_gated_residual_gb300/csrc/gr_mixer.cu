@@ -273,10 +273,12 @@ __global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ S
     float* const slots = L.slots + int64_t(blockIdx.z) * L.units * one;
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     // the want-th of the sequences that are cut, and the segments before its own
-    __shared__ int found[2];
+    __shared__ int found;
+    __shared__ int64_t segments_before;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int seq = -1, before = 0, cut = 0;
+        int seq = -1, cut = 0;
+        int64_t before = 0;
         for (int b0 = 0; b0 < p.n_seqs && seq < 0; b0 += 32) {
             int n = 0;
             if (b0 + lane < p.n_seqs) {
@@ -302,15 +304,18 @@ __global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ S
                 cut += __popc(cuts);
             }
         }
-        if (lane == 0) found[0] = seq, found[1] = before;
+        if (lane == 0) found = seq, segments_before = before;
     }
     __syncthreads();
-    const int b = found[0], first = found[1];
+    const int b = found;
+    const int64_t first = segments_before;
     if (b < 0 || at >= one) return;   // the grid is an upper bound
     dep_wait();
     int64_t begin, end;
     mix_span(p, b, begin, end);
     const int n = sg.count(begin, end);
+    // starts that do not ascend may name more segments than the workspace has slots
+    if ((first + n) * p.n_heads > L.units) return;
     const float g = p.log_decay[h];
     float m[4] = {};
     if (p.m_in) {
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(256) mix_scan_kernel(const __grid_constant__ S
     const int64_t len0 = p.reverse ? full - (chunks * sg.chunk - (end - begin)) - 1 : full;
     const float l0 = decay_pow(g, len0), lf = decay_pow(g, full);
     const int64_t step = int64_t(p.n_heads) * one;
-    float* s = slots + (int64_t(first) * p.n_heads + h) * one + at;
+    float* s = slots + (first * p.n_heads + h) * one + at;
     constexpr int kU = 4;
     for (int i = 0; i < n - 1; i += kU) {
         float4 v[kU];

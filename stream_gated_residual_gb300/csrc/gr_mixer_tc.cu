@@ -4,26 +4,35 @@
 // gradients is one pass of it.
 //
 // A chunk's rows i = 0..127 (λ the head's decay, M the state before the chunk):
-//     P_ij  = outer weight λ^{i−j} (a_i·b_j) for j <= i                 MMA 1, then WG A (mask, decay, bf16)
-//     out_i = Σ_j P_ij c_j + outer λ^{i+1} (Mᵀ a_i)              MMA 4 and MMA 2, then WG A
-//     M'    = λ^len M + Σ_j b_j (weight λ^{len−1−j} c_j)ᵀ           MMA 3 (WG V0, V1 scale c), then WG M
-// (backwards in time the exponents run the other way.)
+//     P_ij  = outer weight λ^{i−j} (a_i·b_j) for j <= i           MMA 1, then WG A (mask, decay, bf16)
+//     out_i = Σ_j P_ij c_j + outer λ^{i+1} (Mᵀ a_i)               MMA 4 and MMA 2, then WG A
+//     M'    = λ^len M + Σ_j b_j (weight λ^{len−1−j} c_j)ᵀ         WG V0, V1 scale c, MMA 3, then WG M
+// (backwards in time the exponents run the other way.) No exponent is negative, so no decay overflows.
 //
 // The state M stays in registers, in fp32, for all chunks of a segment. Its update is a product of
 // bf16 operands, so the decayed values are split into three bf16 terms (24 bits together): the
-// state's error is that of fp32. P and the copy of M that the outputs read are rounded to bf16
-// once, 2^-9 of relative error each in the mean, as the output's own rounding.
+// state's error is that of fp32 (two terms leave 2.2e-6 of it). P and the copy of M that the outputs read
+// are rounded to bf16 once, each in its own share of the output: with the output's own rounding 1.41 times
+// that one's error alone.
 //
-// One CTA an SM (its shared memory and all 512 columns of tensor memory); bytes bound it: a chunk
-// moves 128 KB at head size 128 and takes 21 Mflop on the tensor cores, a quarter of the time its
-// bytes take. Prompts with too few heads and sequences to fill the SMs are cut into segments: a first
-// launch forms each segment's own sum, a scan turns the sums into the states the segments start
-// from, and the pass runs on all segments at once.
+// One CTA an SM (its shared memory and all 512 columns of tensor memory). At head size 128 a chunk moves
+// 128 KB, 2.9 us at an SM's share of the measured copy bandwidth, and takes 3072 cycles (1.6 us) of the
+// tensor cores; it is done every 3.9 us (8192 tokens of 152 heads: 249 us, 5.1 TB/s; head size 64: 182 us).
+// What bounds it are the 13 thousand warp instructions between the MMAs, at 6.6 cycles an instruction and
+// 41% of the issue slots, most of them the split of the decayed values. Each step has a warpgroup of its
+// own and works ahead of the next. Measured and not kept: outputs staged in c's tile and stored by
+// TMA (277 us: the tile's next load waits for them), the roles on seven warpgroups with M in tensor memory
+// (277 us), on three (377 us); M added up by the MMAs in tensor memory would round with every one.
+//
+// Prompts with too few heads and sequences to fill the SMs are cut into segments: a first launch
+// forms each segment's own sum, a scan turns the sums into the states the segments start from, and the pass
+// runs on all segments at once (32768 tokens of 32 heads: 144 + 8 + 241 us; uncut 945 us).
 //
 // Warps: 0 TMA producer, 1 issuer of the scores' and outputs' MMAs (owns the tensor memory), 2 issuer
 // of the state's MMAs, 4-7 WG A (scores and outputs), 8-15 WG V0 and V1 (decayed values, in turn),
-// 16-19 WG M (the state). The state's chain and the outputs' meet only where MMA 2 reads M. Every mbarrier wait is bounded; when one runs out the
-// status bit is set, all roles leave their loops, and copies and MMAs in flight are waited for.
+// 16-19 WG M (the state). The state's chain and the outputs' meet only where MMA 2 reads M. Every
+// mbarrier wait is bounded; when one runs out the status bit is set, all roles leave their loops, and
+// copies and MMAs in flight are waited for.
 #include <math.h>
 #include <string.h>
 
@@ -42,7 +51,7 @@ constexpr int kBox = kChunk * 128;        // 128 rows of 64 bf16 channels
 constexpr int kThreads = 640;
 constexpr int kSub = 16;                  // tokens of one step of the state's MMA
 
-// Tensor-memory columns: scores (then P in place), Σ P c, Mᵀ a, the state's update.
+// Tensor-memory columns: scores (then P in their place), Σ P c, Mᵀ a, the state's update.
 constexpr uint32_t kColS = 0, kColO = 128, kColE = 256, kColU = 384;
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzled layout: 64 elements
