@@ -110,7 +110,7 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
 // time; cutting a sequence costs a second pass over b and c of all but its last segment, and two
 // launches. The host knows the sequences' number and sum, not their lengths:
 //   - too few of them to fill the SMs (rows < 152): taken as equally long, cut so that the estimated time
-//     is least (32768 tokens, 32 heads of 128: 256 chunks uncut 969 us, in 4 segments 423, in 9 389);
+//     is least (32768 tokens, 32 heads of 128: 256 chunks uncut 945 us, in 4 segments 403, in 9 388);
 //   - enough of them: only a sequence longer than twice an SM's even share of all chunks is cut, which
 //     bounds what a single long one can cost (equal ones are never cut).
 inline int64_t mix_plan_evenly(int64_t N, int n_seqs, int64_t heads, int chunk) {
