@@ -285,6 +285,9 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
     const uint32_t tm = __shfl_sync(0xffffffffu, x.tmem, 0);
     const bool from_slot = seg > 0;
     const bool has_in = !kSum && (from_slot || p.m_in != nullptr);
+    // b's stage at step n and its parity: kFine's second stage holds the state's second term
+    auto b_at = [](int n) { return kFine ? 0 : n & 1; };
+    auto b_par = [](int n) { return uint32_t(kFine ? n : n >> 1) & 1u; };
     // whether the state after step n is still read (by the next chunk, or as a result)
     const bool wants_last = kSum || (last_seg && p.m_out != nullptr);
 
@@ -295,8 +298,8 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
             for (int n = 1; n < chunks; ++n) {
                 const int st = n & 1;
                 const uint32_t use2 = uint32_t(n >> 1) & 1u;
-                if (n >= 2 && !wait(&x.b_empty[st], use2 ^ 1u, &x.dead)) break;
-                load(&tmB, DA / 64, S::b + st * S::kB, &x.b_full[st], n);
+                if (n >= (kFine ? 1 : 2) && !wait(&x.b_empty[b_at(n)], b_par(n) ^ 1u, &x.dead)) break;
+                load(&tmB, DA / 64, S::b + b_at(n) * S::kB, &x.b_full[b_at(n)], n);
                 if (n >= 2 && !wait(&x.c_empty[st], use2 ^ 1u, &x.dead)) break;
                 load(&tmC, DC / 64, S::c + st * S::kC, &x.c_full[st], n);
                 if (kSum) continue;
@@ -322,8 +325,8 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
             for (int n = 0; !kSum && n < chunks; ++n) {
                 const int st = n & 1;
                 const uint32_t par2 = uint32_t(n >> 1) & 1u, par = uint32_t(n) & 1u;
-                const uint32_t b0 = base + S::b + st * S::kB, c0 = base + S::c + st * S::kC;
-                if (!wait_warp(&x.b_full[st], par2, &x.dead)) break;
+                const uint32_t b0 = base + S::b + b_at(n) * S::kB, c0 = base + S::c + st * S::kC;
+                if (!wait_warp(&x.b_full[b_at(n)], b_par(n), &x.dead)) break;
                 if (!wait_warp(&x.a_full, par, &x.dead)) break;
                 // the scores take the place of the last chunk's P
                 if (n > 0 && !wait_warp(&x.o_full, par ^ 1u, &x.dead)) break;
@@ -335,7 +338,7 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                         tc_mma(tm + kColS, sdesc_sw128(a0 + off), sdesc_sw128(b0 + off), iS, k > 0);
                     }
                     tc_commit(&x.s_full);
-                    tc_commit(&x.b_empty[st]);
+                    tc_commit(&x.b_empty[b_at(n)]);
                 }
                 if (n > 0 || has_in) {
                     if (!wait_warp(&x.m_ready, e_n & 1u, &x.dead)) break;
@@ -389,8 +392,8 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
             uint32_t v_use = 0;    // rounds of the two buffers so far
             for (int n = 0; n < chunks; ++n) {
                 const int st = n & 1;
-                const uint32_t b0 = base + S::b + st * S::kB;
-                if (!wait_warp(&x.b_full[st], uint32_t(n >> 1) & 1u, &x.dead)) break;
+                const uint32_t b0 = base + S::b + b_at(n) * S::kB;
+                if (!wait_warp(&x.b_full[b_at(n)], b_par(n), &x.dead)) break;
                 if (n + 1 < chunks || wants_last) {
                     if (n > 0 && !wait_warp(&x.u_free, uint32_t(n - 1) & 1u, &x.dead)) break;
                     bool ok = true;
@@ -414,7 +417,7 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
                     if (leader) tc_commit(&x.u_full);
                 }
                 if (leader) {
-                    tc_commit(&x.b_empty[st]);
+                    tc_commit(&x.b_empty[b_at(n)]);
                     if (kSum) tc_commit(&x.c_empty[st]);
                 }
             }
@@ -568,9 +571,9 @@ __device__ __forceinline__ void mix_pass(const Launch& L) {
             const int len = len_of(row_of(n));
             const bool need_u = n + 1 < chunks || wants_last;
             char* ct = sm + S::c + st * S::kC;
-            char* bt = sm + S::b + st * S::kB;
+            char* bt = sm + S::b + b_at(n) * S::kB;
             if (!wait_warp(&x.c_full[st], par2, &x.dead)) break;
-            if (len < kChunk && !wait_warp(&x.b_full[st], par2, &x.dead)) break;
+            if (len < kChunk && !wait_warp(&x.b_full[b_at(n)], b_par(n), &x.dead)) break;
             bool ok = true;
             uint64_t seen = 0;
 #pragma unroll 1
@@ -884,8 +887,13 @@ cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStr
     float* slots = static_cast<float*>(workspace);
     bool state = false;
     for (int i = 0; i < passes; ++i) state = state || p[i].m_out;
-    // 0: one chunk at most (whatever its terms: three), 1: two terms, 2: three
-    const int how = p->n_tokens <= kChunk ? 0 : state ? 2 : 1;
+    // Fine up to a chunk of tokens or the rows of 16 chunks: such calls wait more than they compute (the
+    // gradient of 512 tokens of 4 heads of 128 takes 23 us instead of 21, the prompt 25 instead of 24),
+    // larger ones do not (8192 tokens of 152 heads: 315 us instead of 248), and there the roundings
+    // average out over the rows.
+    const bool fine = p->n_tokens <= kChunk || p->n_tokens * p->n_heads <= 16 * kChunk;
+    // 0: fine (whatever its terms: three), 1: two terms, 2: three
+    const int how = fine ? 0 : state ? 2 : 1;
     if (passes == 3 && p->da == p->dc)
         return p->da == 128 ? choose<128, 128, 3>(how, p, slots, st) : choose<64, 64, 3>(how, p, slots, st);
     if (passes != 1) return cudaErrorInvalidValue;

@@ -341,6 +341,50 @@ def test_linear_attention_nothing_leaks(dk, dv, dtype, value):
     assert torch.equal(z[:at[3]], o[:at[3]]) and (z[at[3]:] == 7).all() and torch.equal(zl, last[:3])
 
 
+@pytest.mark.parametrize("lengths,H,dk,dv", [([129], 1, 128, 128), ([200, 1, 55], 1, 64, 64), ([300], 4, 64, 128),
+                                             ([511, 257], 2, 128, 64), ([2048], 1, 128, 128)])
+def test_linear_attention_few_rows_are_rounded_once(lengths, H, dk, dv):
+    """Calls of few rows have the error of the output's rounding, forwards and in every gradient: the
+    scores' and the state's two terms leave at most 2^-17 of them, less than 1/100 of that rounding."""
+    q, k, v, decay, starts, at, state, g = mixer_inputs(lengths, H, dk, dv, BF)
+    do, dstate = randn(g, *v.shape, dtype=BF), randn(g, *state.shape)
+    o, _ = gr.linear_attention(q, k, v, decay, 0.3, seq_starts=starts, state=state)
+    o64, _ = ref.recurrence(q, k, v, decay, 0.3, at, state)
+    got = gr.linear_attention_backward(do, q, k, v, decay, 0.3, seq_starts=starts, state=state, dstate=dstate)
+    want = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, state, dstate)
+    for a, b in ((o, o64), *zip(got[:3], want)):
+        assert rel(a, b) <= 1.05 * rel(b.to(BF), b)
+
+
+@pytest.mark.parametrize("lengths,H,dk,dv", [([127, 0, 129, 1], 9, 128, 128), ([300], 7, 64, 128), ([5, 257, 128], 6, 128, 64),
+                                             ([700], 3, 64, 64)])
+def test_linear_attention_more_rows(lengths, H, dk, dv):
+    """Sizes above those that are rounded once: forwards, gradients, and what is not finite stays where it is."""
+    q, k, v, decay, starts, at, state, g = mixer_inputs(lengths, H, dk, dv, BF, layout="plain")
+    do, dstate = randn(g, *v.shape, dtype=BF), randn(g, *state.shape)
+    o, last = gr.linear_attention(q, k, v, decay, 0.3, seq_starts=starts, state=state)
+    o64, l64 = ref.recurrence(q, k, v, decay, 0.3, at, state)
+    om, lm = ref.recurrence(q, k, v, decay, 0.3, at, state, magnitudes=True)
+    terms = dk + 64 + 4 * (max(lengths) // 32 + 1)
+    within(o, o64, mixer_bounds(o64, om, terms, BF), "o")
+    within(last, l64, (terms + 64) * U32 * lm, "state")
+    got = gr.linear_attention_backward(do, q, k, v, decay, 0.3, seq_starts=starts, state=state, dstate=dstate)
+    want = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, state, dstate)
+    for a, b in zip(got[:3], want):
+        assert rel(a, b) <= 5e-3
+    assert rel(got[3], want[3]) <= 2e-6
+    bad = 1 + lengths[0] // 2
+    for value in (float("nan"), float("inf")):
+        for name in ("q", "k", "v"):
+            args = {"q": q.clone(), "k": k.clone(), "v": v.clone()}
+            args[name][bad, 1, 5] = value
+            z, zl = gr.linear_attention(args["q"], args["k"], args["v"], decay, 0.3, seq_starts=starts, state=state)
+            hit = torch.zeros(len(o), H, dtype=torch.bool, device="cuda")
+            hit[bad:(bad + 1 if name == "q" else at[1]), 1] = True
+            assert torch.equal(z[~hit], o[~hit]), name
+            assert not torch.isfinite(z[bad, 1]).all(), name
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32)])
 def test_linear_attention_split_prompt_and_steps(dtype, d):
     """A prompt in two parts through the state, and its last tokens one by one, give the whole one's."""
