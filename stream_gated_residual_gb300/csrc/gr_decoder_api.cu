@@ -401,9 +401,11 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
     }
     for (const Rows& r : in)
         if (meet(so, r.span()) || meet(ws, r.span())) return GR_E_ALIAS;
-    for (const Span& f : flat)
-        if (meet(ws, f) || (f.p != dstate_in && meet(so, f)) || (f.p == state_in && meet(so, f)))
-            return GR_E_ALIAS;
+    for (const Span& f : flat) {
+        // dstate_in may be dstate_out itself (and that none of the others)
+        const bool onto = &f == &flat[3] && dstate_out == dstate_in;
+        if (meet(ws, f) || (!onto && meet(so, f))) return GR_E_ALIAS;
+    }
     if (meet(so, ws)) return GR_E_ALIAS;
     if ((st = usable_device())) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

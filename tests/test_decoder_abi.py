@@ -235,3 +235,21 @@ def test_binding_refuses_on_the_host():
                  lambda: gr.linear_attention(t[:, None], t[:, None], t[:, None], t[0])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_state_gradient_over_the_other_inputs(lib):
+    """dstate_in may be dstate_out and nothing else, not at the same address either."""
+    m = mixer()
+    need = ctypes.c_size_t(0)
+    assert lib.gr_linear_attention_workspace_size(byref(m), 1, byref(need)) == 0
+    r = [rows(i) for i in range(7)]
+
+    def call(dsi, si=P(9), dso=P(10)):
+        return lib.gr_linear_attention_backward(byref(m), *map(byref, r[:4]), P(7), P(8), si, dso, *map(byref, r[4:]),
+                                                dsi, P(12), need.value, NULL)
+
+    assert call(P(10)) == call(P(11)) == E("GR_E_DEVICE")
+    for k in (7, 8, 9):                     # log_decay, seq_starts, state_in
+        assert call(P(k)) == E("GR_E_ALIAS")
+    assert call(P(7, -16)) == call(P(8, -16)) == call(P(10, 16)) == E("GR_E_ALIAS")
+    assert call(P(9), si=P(9), dso=P(9)) == E("GR_E_ALIAS")
