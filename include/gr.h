@@ -434,7 +434,10 @@ typedef struct gr_mixer {
 /* Rows [n_tokens][n_heads][d] at any strides (in elements): views of one projection's output, or
  * head-major tensors. The channels are contiguous; data and both strides are multiples of 16
  * bytes, each stride at least d (of a dimension longer than one). An output's rows must not
- * overlap, but may lie between an input's or another output's rows of the same token stride. */
+ * overlap each other, an input's or another output's. They may lie between those of a fused
+ * buffer in any order of its axes, [N][3][H][d], [N][H][3][d], [H][N][3][d] or [H][3][N][d]: a token's
+ * heads between tokens of the same stride (a head's tokens between heads), or single rows
+ * between rows of the same two strides. Other interleavings are refused (GR_E_ALIAS). */
 typedef struct gr_rows {
     void* data;
     int64_t token_stride, head_stride;

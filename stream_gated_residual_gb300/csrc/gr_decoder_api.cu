@@ -76,21 +76,33 @@ struct Rows {
         if (output && !token_major() && h > 1 && hs < (n - 1) * ts + d) return GR_E_SHAPE;
         return GR_OK;
     }
-    // Whether two rows arguments touch a common byte; interleaved views of one buffer with the same
-    // token stride do not.
+    // Whether two rows arguments may touch a common byte. Views of one fused buffer do not: their
+    // tokens' rows lie between each other's (the same token stride), their heads' (the same head
+    // stride), or, at the same two strides, the heads of every token or the tokens of every head.
     bool meets(const Rows& o) const {
         if (!meet(span(), o.span())) return false;
-        const int64_t ts = r->token_stride * int64_t(w);
-        if (n > 1 && w == o.w && r->token_stride == o.r->token_stride && token_major() &&
-            o.token_major()) {
-            const int64_t gap = int64_t(reinterpret_cast<uintptr_t>(o.r->data)) -
-                                int64_t(reinterpret_cast<uintptr_t>(r->data));
-            const int64_t at = ((gap % ts) + ts) % ts;
-            const int64_t mine = ((h - 1) * r->head_stride + d) * int64_t(w);
-            const int64_t its = ((o.h - 1) * o.r->head_stride + o.d) * int64_t(w);
-            return !(at >= mine && at + its <= ts);
-        }
-        return true;
+        if (w != o.w) return true;
+        const int64_t gap = (int64_t(reinterpret_cast<uintptr_t>(o.r->data)) -
+                             int64_t(reinterpret_cast<uintptr_t>(r->data))) / int64_t(w);
+        const int64_t ts = r->token_stride, hs = r->head_stride;
+        const bool same_t = n > 1 && ts == o.r->token_stride, same_h = h > 1 && hs == o.r->head_stride;
+        auto mod = [](int64_t x, int64_t y) { return ((x % y) + y) % y; };
+        // blocks of `mine` and `its` elements that repeat with one period, beside each other in it
+        auto beside = [&](int64_t g, int64_t period, int64_t mine, int64_t its) {
+            const int64_t at = mod(g, period);
+            return at >= mine && at + its <= period;
+        };
+        if (same_t && beside(gap, ts, (h - 1) * hs + d, (o.h - 1) * o.r->head_stride + o.d)) return false;
+        if (same_h && beside(gap, hs, (n - 1) * ts + d, (o.n - 1) * o.r->token_stride + o.d)) return false;
+        // `count` rows at the inner stride within each outer period, the later block not past its end
+        auto between = [&](int64_t outer, int64_t inner, int64_t count) {
+            const int64_t mine = (count - 1) * inner + d, its = (count - 1) * inner + o.d;
+            if (mine > outer || its > outer) return false;
+            const int64_t after = mod(gap, outer), ahead = mod(-gap, outer);
+            return (after + its <= outer && beside(after, inner, d, o.d)) ||
+                   (ahead + mine <= outer && beside(ahead, inner, o.d, d));
+        };
+        return !(same_t && same_h && (between(ts, hs, h) || between(hs, ts, n)));
     }
     MixRows mix() const {
         // strides of a dimension of one are never used to step, but reach the tensor maps

@@ -253,3 +253,61 @@ def test_state_gradient_over_the_other_inputs(lib):
         assert call(P(k)) == E("GR_E_ALIAS")
     assert call(P(7, -16)) == call(P(8, -16)) == call(P(10, 16)) == E("GR_E_ALIAS")
     assert call(P(9), si=P(9), dso=P(9)) == E("GR_E_ALIAS")
+
+
+def test_rows_between_other_rows(lib):
+    """Outputs between the heads (or tokens) of one fused buffer are taken, in every order of its axes."""
+    m = mixer()                              # 20 tokens, 3 heads of 64, bf16
+    N, H, d = 20, 3, 64
+    need = ctypes.c_size_t(0)
+    assert lib.gr_linear_attention_workspace_size(byref(m), 1, byref(need)) == 0
+
+    def prompt(q, k, v, o):
+        return lib.gr_linear_attention(byref(m), *map(byref, (q, k, v)), P(4), P(5), NULL, byref(o), NULL, P(8), 1 << 33,
+                                       NULL)
+
+    def grads(dq, dk, dv):
+        return lib.gr_linear_attention_backward(byref(m), *(byref(rows(i)) for i in range(4)), P(4), P(5), NULL, NULL,
+                                                *map(byref, (dq, dk, dv)), NULL, P(8), need.value, NULL)
+
+    for ts, hs, step in ((H * 4 * d, 4 * d, d),                # [N][H][4][d]
+                         (H * 4 * d + 64, 4 * d, d),           # the same in a longer row
+                         (4 * H * d, d, H * d),                # [N][4][H][d]
+                         (4 * d, N * 4 * d, d),                # [H][N][4][d]
+                         (d, 4 * N * d, N * d)):               # [H][4][N][d]
+        at = [gr.RowsStruct(20 * BIG + 2 * i * step, ts, hs) for i in range(4)]
+        for order in ((0, 1, 2, 3), (1, 2, 3, 0), (3, 2, 1, 0)):
+            assert prompt(*(at[i] for i in order)) == E("GR_E_DEVICE"), (ts, hs, order)
+            assert grads(*(at[i] for i in order[:3])) == E("GR_E_DEVICE"), (ts, hs, order)
+        for i in range(3):
+            assert prompt(*at[:3], at[i]) == E("GR_E_ALIAS")
+            off = gr.RowsStruct(20 * BIG + 2 * i * step + 16, ts, hs)
+            assert prompt(*at[:3], off) == E("GR_E_ALIAS"), (ts, hs, i)
+
+
+def test_rows_that_share_a_byte_are_refused(lib):
+    """Small layouts at random against every byte of theirs: what overlaps is never taken."""
+    import random
+    rng = random.Random(1)
+    taken = 0
+    for _ in range(4000):
+        n, h, d = rng.randint(1, 4), rng.randint(1, 4), 8
+        m = mixer(n=n, b=1, h=h, dk=d, dv=d)
+        same = rng.random() < 0.7
+        strides = [(8 * rng.randint(1, 12), 8 * rng.randint(1, 12)) for _ in range(2)]
+        if same:
+            strides[1] = strides[0]
+        gap = 16 * rng.randint(-40, 40)
+        q = gr.RowsStruct(BIG, *strides[0])
+        o = gr.RowsStruct(BIG + gap, *strides[1])
+        got = lib.gr_linear_attention(byref(m), byref(q), byref(rows(2)), byref(rows(3)), P(4), NULL, NULL, byref(o), NULL,
+                                      P(8), 1 << 33, NULL)
+        cells = [{base // 16 + (i * ts + j * hs) // 8 for i in range(n) for j in range(h)}
+                 for base, (ts, hs) in ((0, strides[0]), (gap, strides[1]))]
+        if got == E("GR_E_DEVICE"):
+            taken += 1
+            assert not cells[0] & cells[1], (n, h, strides, gap)
+            assert len(cells[1]) == n * h      # and its own rows do not overlap
+        else:
+            assert got in (E("GR_E_ALIAS"), E("GR_E_SHAPE"))
+    assert taken > 400

@@ -520,3 +520,26 @@ def test_operators_in_a_graph():
         torch.cuda.synchronize()
         for a, c in zip(outs, step()):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype,H,d", [(BF, 3, 64), (BF, 2, 128), (F32, 3, 24)])
+def test_linear_attention_outputs_between_heads(dtype, H, d):
+    """o between q, k and v of every head in one buffer [N, H, 4, d], and the gradients in one [N, H, 3, d]: the
+    same bits as in buffers of their own, and nothing else is written."""
+    q, k, v, decay, starts, at, _, g = mixer_inputs([100, 29, 140], H, d, d, dtype, layout="plain")
+    N = len(q)
+    do = randn(g, N, H, d, dtype=dtype)
+    want, last = gr.linear_attention(q, k, v, decay, seq_starts=starts)
+    grads = gr.linear_attention_backward(do, q, k, v, decay, seq_starts=starts)
+    buf = torch.stack([q, k, v, torch.zeros_like(q)], 2)
+    parts = buf.unbind(2)
+    o, end = gr.linear_attention(*parts[:3], decay, seq_starts=starts, o=parts[3])
+    assert torch.equal(o, want) and torch.equal(end, last)
+    for a, b in zip(parts, (q, k, v)):
+        assert torch.equal(a, b)
+    out = torch.zeros(N, H, 3, d, dtype=dtype, device="cuda")
+    got = gr.linear_attention_backward(do, *parts[:3], decay, seq_starts=starts, out=out.unbind(2))
+    for a, b in zip(got[:3], grads[:3]):
+        assert torch.equal(a, b)
+    with pytest.raises(gr.GRError):
+        gr.linear_attention(*parts[:3], decay, seq_starts=starts, o=parts[1])
