@@ -173,6 +173,16 @@ def _dev(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _new(stream, shape, dtype: torch.dtype, device) -> torch.Tensor:
+    """An output (or a workspace) made here, from the memory of torch's current stream: `stream`,
+    where given, is recorded on it, so that the allocator hands the memory out again only after
+    the work queued there."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def make_shape(n_tokens: int, d_model: int, rank: int, dtype: torch.dtype,
                eps: float = 1e-6) -> Shape:
     if dtype not in _SHAPE_DTYPES:
@@ -625,9 +635,7 @@ def _ws(need: int, workspace: torch.Tensor | None, like: torch.Tensor, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need == 0:
         return None, 0, None
-    buf = torch.empty(need, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        buf.record_stream(stream)
+    buf = _new(stream, need, torch.uint8, like.device)
     return buf.data_ptr(), need, buf
 
 
@@ -668,7 +676,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: 
     (V, D), N = table.shape, ids.numel()
     shape = (N, D) if branches == 1 else (N, branches, D)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=table.device)
+        out = _new(stream, shape, dtype, table.device)
     else:
         _dev(out, "out")
         if out.shape != shape or out.dtype != dtype:
@@ -692,7 +700,7 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
         raise ValueError("accumulate needs the dtable to add to")
     N, D = dR.shape[0], dR.shape[-1]
     if dtable is None:
-        dtable = torch.empty((n_vocab, D), dtype=torch.float32, device=dR.device)
+        dtable = _new(stream, (n_vocab, D), torch.float32, dR.device)
     else:
         _f32(dtable, "dtable", (n_vocab, D))
     e = _embed_desc(N, n_vocab, D, 1 if nd == 2 else dR.shape[1], GR_F32, GR_F32, bits, scale)
@@ -720,15 +728,14 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     n = _norm_rows(x, weight, eps)
     _f32(bias, "bias", x.shape[1:])
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(stream, x.shape, x.dtype, x.device)
     else:
         _dev(y, "y")
         if y.shape != x.shape or y.dtype != x.dtype:
             raise ValueError("y must match x")
     mean = rstd = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x.device) for _ in range(2))
     _call("gr_layer_norm", n, x.data_ptr(), weight.data_ptr(), _opt(bias), y.data_ptr(), _opt(mean),
           _opt(rstd), _raw_stream(stream, x))
     return (y, mean, rstd) if stats else y
@@ -746,11 +753,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     _f32(mean, "mean", shape[:-1])
     _f32(rstd, "rstd", shape[:-1])
     if dx is None:
-        dx = torch.empty_like(dy)
+        dx = _new(stream, shape, torch.float32, x.device)
     else:
         _f32(dx, "dx", shape)
-    dweight = torch.empty_like(weight)
-    dbias = torch.empty_like(weight) if bias else None
+    dweight = _new(stream, shape[1:], torch.float32, x.device)
+    dbias = _new(stream, shape[1:], torch.float32, x.device) if bias else None
     wp, wn, _keep = _ws(_need("gr_layer_norm_backward_workspace_size", n), workspace, x, stream)
     _call("gr_layer_norm_backward", n, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
           mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _opt(dbias), wp, wn,
@@ -814,9 +821,9 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     N, H, dk, dv, m, rows = _mixer(q, k, v, log_decay, scale, B)
     _f32(state, "state", (B, H, dk, dv))
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        o = _new(stream, (N, H, dv), q.dtype, q.device)
     if state_out is None:
-        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        state_out = _new(stream, (B, H, dk, dv), torch.float32, q.device)
     else:
         _f32(state_out, "state_out", (B, H, dk, dv))
     orow = _rows(o, "o", N, H, dv, q.dtype)
@@ -844,7 +851,7 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     elif state.shape[0] < N:
         raise ValueError("state must hold a slot for every request")
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        o = _new(stream, (N, H, dv), q.dtype, q.device)
     _call("gr_linear_attention_step", m, *rows, log_decay.data_ptr(), state.data_ptr(),
           state.shape[0], _opt(slots), _rows(o, "o", N, H, dv, q.dtype), _raw_stream(stream, q))
     return o
@@ -865,12 +872,12 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     _f32(dstate, "dstate", (B, H, dk, dv))
     dorow = _rows(do, "do", N, H, dv, q.dtype)
     if out is None:
-        out = [torch.empty((N, H, d), dtype=q.dtype, device=q.device) for d in (dk, dk, dv)]
+        out = [_new(stream, (N, H, d), q.dtype, q.device) for d in (dk, dk, dv)]
     outs = [_rows(t, n, N, H, d, q.dtype)
             for t, n, d in zip(out, ("dq", "dk", "dv"), (dk, dk, dv))]
     dstate_in = None
     if state is not None or dstate is not None:
-        dstate_in = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        dstate_in = _new(stream, (B, H, dk, dv), torch.float32, q.device)
     wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 1), workspace, q, stream)
     _call("gr_linear_attention_backward", m, dorow, *rows, log_decay.data_ptr(), _opt(seq_starts),
           _opt(state), _opt(dstate), *outs, _opt(dstate_in), wp, wn, _raw_stream(stream, q))

@@ -543,3 +543,22 @@ def test_linear_attention_outputs_between_heads(dtype, H, d):
         assert torch.equal(a, b)
     with pytest.raises(gr.GRError):
         gr.linear_attention(*parts[:3], decay, seq_starts=starts, o=parts[1])
+
+
+def test_outputs_dropped_early_on_another_stream():
+    """An output that the caller drops while its stream still runs is not handed out again before that."""
+    g = gen(3)
+    x, w = randn(g, 20000, 4, 1024), torch.ones(4, 1024, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gr.layer_norm(x, w)                                   # (the library and its kernel are loaded)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                    # about 0.1 s: what follows on `side` is still to come
+    y = gr.layer_norm(x, w, stream=side)
+    at = y.data_ptr()
+    del y
+    other = torch.zeros_like(x)
+    assert not side.query() and other.data_ptr() != at
+    side.synchronize()
+    assert (other == 0).all()
