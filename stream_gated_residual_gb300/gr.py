@@ -228,7 +228,7 @@ def pack_params(gamma: torch.Tensor, w_down: torch.Tensor, w_up: torch.Tensor,
                          "W_w [4,4D]")
     shape = make_shape(0, D, r, dtype, eps)
     nbytes = packed_size(D, r, dtype)
-    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=gamma.device)
+    buf = _new(stream, nbytes + 256, torch.uint8, gamma.device)
     off = (-buf.data_ptr()) % 256
     view = buf[off:off + nbytes]
     st = ParamsStruct()
@@ -258,7 +258,7 @@ def step_workspace_size(n_tokens: int, d_model: int, rank: int, dtype: torch.dty
     return need.value
 
 
-def _step_ws(shape: Shape, device, workspace):
+def _step_ws(shape: Shape, device, workspace, stream):
     """(pointer, bytes) of the step's workspace: the caller's, else a fresh 256-byte aligned
     buffer when the shape needs one."""
     need = ctypes.c_size_t(0)
@@ -269,7 +269,7 @@ def _step_ws(shape: Shape, device, workspace):
         return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
     if need.value == 0:
         return ctypes.c_void_p(None), 0, None
-    buf = torch.empty(need.value + 256, dtype=torch.uint8, device=device)
+    buf = _new(stream, need.value + 256, torch.uint8, device)
     view = buf[(-buf.data_ptr()) % 256:][:need.value]
     return _ptr(view), need.value, buf
 
@@ -280,15 +280,13 @@ def read(R: torch.Tensor, params: Params, x: torch.Tensor | None = None,
     needs a device workspace: the caller's (256-byte aligned), else one allocated here."""
     shape = _state_shape(R, params, params.eps)
     N, _, D = R.shape
-    x = torch.empty((N, D), dtype=R.dtype, device=R.device) if x is None else x
-    s = torch.empty((N, 4), dtype=torch.float32, device=R.device) if s is None else s
+    x = _new(stream, (N, D), R.dtype, R.device) if x is None else x
+    s = _new(stream, (N, 4), torch.float32, R.device) if s is None else s
     _dev(x, "x")
     _dev(s, "s")
-    wp, wn, keep = _step_ws(shape, R.device, workspace)
+    wp, wn, _keep = _step_ws(shape, R.device, workspace, stream)
     _check(load().gr_read_ws(ctypes.byref(shape), _ptr(R), params.ref(), _ptr(x), _ptr(s), wp,
                              wn, _stream(stream)), "gr_read")
-    if keep is not None and stream is not None:
-        keep.record_stream(stream)   # the allocator may hand it out again only after `stream`
     return x, s
 
 
@@ -309,17 +307,15 @@ def write_then_read(R: torch.Tensor, y: torch.Tensor, s_prev: torch.Tensor, para
     (x, s_next) = read(R, params). Workspace as for read()."""
     shape = _state_shape(R, params, params.eps)
     N, _, D = R.shape
-    x = torch.empty((N, D), dtype=R.dtype, device=R.device) if x is None else x
-    s_next = torch.empty((N, 4), dtype=torch.float32, device=R.device) if s_next is None \
+    x = _new(stream, (N, D), R.dtype, R.device) if x is None else x
+    s_next = _new(stream, (N, 4), torch.float32, R.device) if s_next is None \
         else s_next
     for t, n in ((y, "y"), (s_prev, "s_prev"), (x, "x"), (s_next, "s_next")):
         _dev(t, n)
-    wp, wn, keep = _step_ws(shape, R.device, workspace)
+    wp, wn, _keep = _step_ws(shape, R.device, workspace, stream)
     _check(load().gr_write_then_read_ws(ctypes.byref(shape), _ptr(R), _ptr(y), _ptr(s_prev),
                                         params.ref(), _ptr(x), _ptr(s_next), wp, wn,
                                         _stream(stream)), "gr_write_then_read")
-    if keep is not None and stream is not None:
-        keep.record_stream(stream)
     return x, s_next
 
 
@@ -328,7 +324,7 @@ def read_fixed_gates(R: torch.Tensor, gamma: torch.Tensor, G: torch.Tensor, eps:
     """gr_read_fixed_gates: x = (1/4) sum_i G_i * RMSNorm(R_i; gamma_i)."""
     shape = _state_shape(R, 1, eps)
     N, _, D = R.shape
-    x = torch.empty((N, D), dtype=R.dtype, device=R.device) if x is None else x
+    x = _new(stream, (N, D), R.dtype, R.device) if x is None else x
     for t, n in ((gamma, "gamma"), (G, "G"), (x, "x")):
         _dev(t, n)
     _check(load().gr_read_fixed_gates(ctypes.byref(shape), _ptr(R), _ptr(gamma), _ptr(G),
@@ -423,12 +419,12 @@ def read_backward(R: torch.Tensor, gamma: torch.Tensor, w_down: torch.Tensor, w_
     _check(load().gr_read_backward_workspace_size(ctypes.byref(shape), ctypes.byref(need)),
            "gr_read_backward_workspace_size")
     if workspace is None:
-        buf = torch.empty(need.value + 256, dtype=torch.uint8, device=R.device)
+        buf = _new(stream, need.value + 256, torch.uint8, R.device)
         workspace = buf[(-buf.data_ptr()) % 256:][:need.value]
     dev = R.device
-    dR = torch.empty((N, 4, D), dtype=torch.float32, device=dev)
-    g = {"gamma": torch.empty_like(gamma), "w_down": torch.empty_like(w_down),
-         "w_up": torch.empty_like(w_up), "w_write": torch.empty_like(w_write)}
+    dR = _new(stream, (N, 4, D), torch.float32, dev)
+    g = {k: _new(stream, t.shape, torch.float32, dev)
+         for k, t in (("gamma", gamma), ("w_down", w_down), ("w_up", w_up), ("w_write", w_write))}
     _check(load().gr_read_backward(
         ctypes.byref(shape), _ptr(R), _ptr(gamma), _ptr(w_down), _ptr(w_up), _ptr(w_write),
         _ptr(dx), _ptr(ds), _ptr(dR), _ptr(g["gamma"]), _ptr(g["w_down"]), _ptr(g["w_up"]),
@@ -443,9 +439,9 @@ def write_backward(dR_next: torch.Tensor, y: torch.Tensor, s: torch.Tensor, stre
         _dev(t, n)
     N, _, D = dR_next.shape
     shape = make_shape(N, D, 1, y.dtype)
-    dR = torch.empty_like(dR_next)
-    dy = torch.empty((N, D), dtype=torch.float32, device=dR_next.device)
-    ds = torch.empty((N, 4), dtype=torch.float32, device=dR_next.device)
+    dR = _new(stream, dR_next.shape, dR_next.dtype, dR_next.device)
+    dy = _new(stream, (N, D), torch.float32, dR_next.device)
+    ds = _new(stream, (N, 4), torch.float32, dR_next.device)
     _check(load().gr_write_backward(ctypes.byref(shape), _ptr(dR_next), _ptr(y), _ptr(s),
                                     _ptr(dR), _ptr(dy), _ptr(ds), _stream(stream)),
            "gr_write_backward")
@@ -482,13 +478,13 @@ def decompose(R: torch.Tensor, gamma: torch.Tensor, w_down: torch.Tensor, w_up: 
         if R0.dtype != R.dtype or R0.shape != R.shape:
             raise ValueError("R0 must match R")
     dev = R.device
-    out = {"norm": torch.empty((N, U), dtype=torch.float32, device=dev)}
+    out = {"norm": _new(stream, (N, U), torch.float32, dev)}
     if branch_norm:
-        out["branch_norm"] = torch.empty((N, U, 4), dtype=torch.float32, device=dev)
+        out["branch_norm"] = _new(stream, (N, U, 4), torch.float32, dev)
     if pi:
-        out["pi"] = torch.empty((N, U), dtype=torch.float32, device=dev)
+        out["pi"] = _new(stream, (N, U), torch.float32, dev)
     if R0 is not None:
-        out["a0_norm"] = torch.empty((N,), dtype=torch.float32, device=dev)
+        out["a0_norm"] = _new(stream, (N,), torch.float32, dev)
 
     def p(k):
         t = out.get(k)
@@ -523,8 +519,8 @@ def fp8_encode(R: torch.Tensor, codes: torch.Tensor | None = None,
     if R.dtype not in _DTYPES or R.dim() != 3 or R.shape[1] != 4:
         raise ValueError("R must be a float32 or bfloat16 tensor of shape [N, 4, D]")
     N, _, D = R.shape
-    codes = torch.empty((N, 4, D), dtype=torch.uint8, device=R.device) if codes is None else codes
-    scales = torch.empty((N, 4, D // 32), dtype=torch.uint8, device=R.device) if scales is None \
+    codes = _new(stream, (N, 4, D), torch.uint8, R.device) if codes is None else codes
+    scales = _new(stream, (N, 4, D // 32), torch.uint8, R.device) if scales is None \
         else scales
     _fp8_state(codes, scales)
     shape = make_shape(N, D, 1, FP8)
@@ -539,7 +535,7 @@ def fp8_decode(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     N, D = _fp8_state(codes, scales)
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
-    out = torch.empty((N, 4, D), dtype=dtype, device=codes.device) if out is None else out
+    out = _new(stream, (N, 4, D), dtype, codes.device) if out is None else out
     _dev(out, "out")
     shape = make_shape(N, D, 1, FP8)
     _check(load().gr_fp8_decode(ctypes.byref(shape), _ptr(codes), _ptr(scales), _ptr(out),
@@ -552,8 +548,8 @@ def read_fp8(codes: torch.Tensor, scales: torch.Tensor, params: Params,
     """gr_read_fp8: FP8 state -> (x [N,D] bf16, s [N,4] fp32)."""
     N, D = _fp8_state(codes, scales)
     shape = make_shape(N, D, params.rank, FP8, params.eps)
-    x = torch.empty((N, D), dtype=torch.bfloat16, device=codes.device) if x is None else x
-    s = torch.empty((N, 4), dtype=torch.float32, device=codes.device) if s is None else s
+    x = _new(stream, (N, D), torch.bfloat16, codes.device) if x is None else x
+    s = _new(stream, (N, 4), torch.float32, codes.device) if s is None else s
     _dev(x, "x")
     _dev(s, "s")
     _check(load().gr_read_fp8(ctypes.byref(shape), _ptr(codes), _ptr(scales), params.ref(),
@@ -580,8 +576,8 @@ def write_then_read_fp8(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tens
     `params` -> (x [N,D] bf16, s_next [N,4] fp32)."""
     N, D = _fp8_state(codes, scales)
     shape = make_shape(N, D, params.rank, FP8, params.eps)
-    x = torch.empty((N, D), dtype=torch.bfloat16, device=codes.device) if x is None else x
-    s_next = torch.empty((N, 4), dtype=torch.float32, device=codes.device) if s_next is None \
+    x = _new(stream, (N, D), torch.bfloat16, codes.device) if x is None else x
+    s_next = _new(stream, (N, 4), torch.float32, codes.device) if s_next is None \
         else s_next
     for t, n in ((y, "y"), (s_prev, "s_prev"), (x, "x"), (s_next, "s_next")):
         _dev(t, n)

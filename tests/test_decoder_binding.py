@@ -69,3 +69,59 @@ def test_outputs_are_recorded_on_the_stream_that_writes_them(calls, i):
     name, call = operators(stream)[i]
     made = [t.data_ptr() for t in call()]
     assert {p for p, s in calls.recorded if s is stream} >= set(made), name
+
+
+class Launches:
+    """The library with its launching entries answering 0."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name) if name.endswith("_size") else lambda *args: 0
+
+
+@pytest.mark.parametrize("name", ["pack_params", "read", "read large rank", "write_then_read", "read_fixed_gates",
+                                  "read_backward", "write_backward", "decompose", "fp8_encode", "fp8_decode", "read_fp8",
+                                  "write_then_read_fp8"])
+def test_residual_outputs_are_recorded_on_the_stream(calls, monkeypatch, name):
+    """The same for the reads and writes, and for the workspaces that a call makes and drops itself."""
+    lib = Launches(gr.load())
+    monkeypatch.setattr(gr, "load", lambda: lib)
+    stream, made, empty = Stream(), [], torch.empty
+    N, D, r = 3, 64, 4
+    F, B = torch.float32, torch.bfloat16
+    rank = 320 if name == "read large rank" else r
+    if rank > r:
+        N, D = 5, 2560
+    R, y, s = torch.zeros(N, 4, D, dtype=B), torch.zeros(N, D, dtype=B), torch.zeros(N, 4)
+    weights = torch.ones(4, D), torch.zeros(r, 4 * D), torch.zeros(4 * D, r), torch.zeros(4, 4 * D)
+    fp8 = torch.zeros(N, 4, D, dtype=torch.uint8), torch.zeros(N, 4, D // 32, dtype=torch.uint8)
+    params = gr.Params(torch.zeros(1), gr.ParamsStruct(None, D, 4, rank, gr.GR_BF16, gr.GR_PARAMS_TAG), B, 1e-6)
+
+    def counted(*args, **kw):
+        made.append(empty(*args, **kw))
+        return made[-1]
+
+    def counted_like(t, **kw):
+        return counted(t.shape, dtype=t.dtype, device=t.device)
+
+    run = {
+        "pack_params": lambda: gr.pack_params(*weights, B, stream=stream),
+        "read": lambda: gr.read(R, params, stream=stream),
+        "read large rank": lambda: gr.read(R, params, stream=stream),
+        "write_then_read": lambda: gr.write_then_read(R, y, s, params, stream=stream),
+        "read_fixed_gates": lambda: gr.read_fixed_gates(R, weights[0], R, stream=stream),
+        "read_backward": lambda: gr.read_backward(R, *weights, torch.zeros(N, D), s, stream=stream),
+        "write_backward": lambda: gr.write_backward(R.float(), y, s, stream=stream),
+        "decompose": lambda: gr.decompose(R, *weights, y[None], s[None], R, stream=stream),
+        "fp8_encode": lambda: gr.fp8_encode(R, stream=stream),
+        "fp8_decode": lambda: gr.fp8_decode(*fp8, stream=stream),
+        "read_fp8": lambda: gr.read_fp8(*fp8, params, stream=stream),
+        "write_then_read_fp8": lambda: gr.write_then_read_fp8(*fp8, y, s, params, stream=stream),
+    }[name]
+    monkeypatch.setattr(torch, "empty", counted)
+    monkeypatch.setattr(torch, "empty_like", counted_like)
+    run()
+    got = {p for p, on in calls.recorded if on is stream}
+    assert made and all(t.data_ptr() in got for t in made)
