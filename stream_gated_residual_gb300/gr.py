@@ -602,11 +602,23 @@ _norm_desc = functools.lru_cache(1024)(_NORM.pack)
 _mixer_desc = functools.lru_cache(1024)(_MIXER.pack)
 
 
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    """cudaStream_t of `stream`, or of torch's current stream on t's device."""
+_current_device = torch._C._cuda_getDevice
+
+
+def _raw_stream(stream, t: torch.Tensor, *others: torch.Tensor | None) -> int:
+    """cudaStream_t of `stream`, or of torch's current stream. The library launches on the current
+    device, so all tensors of the call have to be there."""
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is "
+                         f"{_current_device()}")
+    for o in others:
+        if o is not None and o.get_device() != device:
+            raise ValueError(f"all tensors of a call must be on one device, got devices {device} "
+                             f"and {o.get_device()}")
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _call(name: str, *args) -> None:
@@ -678,7 +690,8 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: 
         if out.shape != shape or out.dtype != dtype:
             raise ValueError(f"out must be {dtype} of shape {list(shape)}")
     e = _embed_desc(N, V, D, branches, _DTYPES[table.dtype], _DTYPES[dtype], bits, scale)
-    _call("gr_embed", e, table.data_ptr(), ids.data_ptr(), out.data_ptr(), _raw_stream(stream, table))
+    _call("gr_embed", e, table.data_ptr(), ids.data_ptr(), out.data_ptr(),
+          _raw_stream(stream, table, ids, out))
     return out
 
 
@@ -702,7 +715,7 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
     e = _embed_desc(N, n_vocab, D, 1 if nd == 2 else dR.shape[1], GR_F32, GR_F32, bits, scale)
     wp, wn, _keep = _ws(_need("gr_embed_backward_workspace_size", e), workspace, dR, stream)
     _call("gr_embed_backward", e, dR.data_ptr(), ids.data_ptr(), dtable.data_ptr(),
-          1 if accumulate else 0, wp, wn, _raw_stream(stream, dR))
+          1 if accumulate else 0, wp, wn, _raw_stream(stream, dR, ids, dtable, workspace))
     return dtable
 
 
@@ -733,7 +746,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     if stats:
         mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x.device) for _ in range(2))
     _call("gr_layer_norm", n, x.data_ptr(), weight.data_ptr(), _opt(bias), y.data_ptr(), _opt(mean),
-          _opt(rstd), _raw_stream(stream, x))
+          _opt(rstd), _raw_stream(stream, x, weight, bias, y))
     return (y, mean, rstd) if stats else y
 
 
@@ -757,7 +770,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     wp, wn, _keep = _ws(_need("gr_layer_norm_backward_workspace_size", n), workspace, x, stream)
     _call("gr_layer_norm_backward", n, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
           mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _opt(dbias), wp, wn,
-          _raw_stream(stream, x))
+          _raw_stream(stream, x, dy, weight, mean, rstd, dx, workspace))
     return dx, dweight, dbias
 
 
@@ -825,7 +838,8 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     orow = _rows(o, "o", N, H, dv, q.dtype)
     wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 0), workspace, q, stream)
     _call("gr_linear_attention", m, *rows, log_decay.data_ptr(), _opt(seq_starts), _opt(state), orow,
-          state_out.data_ptr(), wp, wn, _raw_stream(stream, q))
+          state_out.data_ptr(), wp, wn,
+          _raw_stream(stream, q, k, v, log_decay, seq_starts, state, o, state_out, workspace))
     return o, state_out
 
 
@@ -849,7 +863,8 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if o is None:
         o = _new(stream, (N, H, dv), q.dtype, q.device)
     _call("gr_linear_attention_step", m, *rows, log_decay.data_ptr(), state.data_ptr(),
-          state.shape[0], _opt(slots), _rows(o, "o", N, H, dv, q.dtype), _raw_stream(stream, q))
+          state.shape[0], _opt(slots), _rows(o, "o", N, H, dv, q.dtype),
+          _raw_stream(stream, q, k, v, log_decay, state, slots, o))
     return o
 
 
@@ -876,5 +891,6 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
         dstate_in = _new(stream, (B, H, dk, dv), torch.float32, q.device)
     wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 1), workspace, q, stream)
     _call("gr_linear_attention_backward", m, dorow, *rows, log_decay.data_ptr(), _opt(seq_starts),
-          _opt(state), _opt(dstate), *outs, _opt(dstate_in), wp, wn, _raw_stream(stream, q))
+          _opt(state), _opt(dstate), *outs, _opt(dstate_in), wp, wn,
+          _raw_stream(stream, q, do, k, v, log_decay, seq_starts, state, dstate, *out, workspace))
     return (*out, dstate_in)

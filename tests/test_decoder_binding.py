@@ -35,6 +35,7 @@ def calls(monkeypatch):
         seen.append((name, args))
 
     monkeypatch.setattr(gr, "_call", call)
+    monkeypatch.setattr(gr, "_current_device", lambda: -1)   # where CPU tensors are
     monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.recorded.append((t.data_ptr(), s)),
                         raising=False)
@@ -125,3 +126,33 @@ def test_residual_outputs_are_recorded_on_the_stream(calls, monkeypatch, name):
     run()
     got = {p for p, on in calls.recorded if on is stream}
     assert made and all(t.data_ptr() in got for t in made)
+
+
+@pytest.mark.parametrize("i", range(7))
+def test_tensors_of_another_device_are_refused(calls, monkeypatch, i):
+    """Every launch goes to the current device: a tensor of another one is a ValueError, whichever argument it is."""
+    monkeypatch.setattr(gr, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1, raising=False)
+    name, call = operators(Stream())[i]
+    made, new = [], gr._new
+    monkeypatch.setattr(gr, "_new", lambda *a: made.append(new(*a)) or made[-1])
+    call()
+    assert len(calls) == 1
+    pointers = [struct.unpack("=Q", a[:8])[0] if isinstance(a, bytes) and len(a) == 24 else a
+                for a in calls[0][1][1:]]
+    arguments = {p for p in pointers if isinstance(p, int) and p > 1 << 20 and p != STREAM}
+    arguments -= {t.data_ptr() for t in made}           # which are made on the first tensor's device
+    asked = []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: asked.append(t.data_ptr()) or 1, raising=False)
+    call()
+    assert len(asked) >= len(arguments), name           # every tensor whose address goes to the library was asked
+    for at in range(len(asked)):
+        count = iter(range(1000))
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0 if next(count) == at else 1, raising=False)
+        before = len(calls)
+        with pytest.raises(ValueError, match="device"):
+            call()
+        assert len(calls) == before
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0, raising=False)
+    with pytest.raises(ValueError, match="device"):     # all on one device, another one than the current
+        call()
