@@ -590,8 +590,9 @@ def write_then_read_fp8(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tens
 # ---- the parts of a decoder around the Gated Residual: embedding, layer norm, linear attention ----
 #
 # These calls are also made for a few tokens at a time, where the binding itself is what a call costs.
-# Descriptors are packed bytes, kept by their values; workspace sizes are kept by the descriptor (both are
-# pure functions of the arguments), and pointers go as plain integers.
+# Descriptors are packed bytes, kept by their values (numbers of Python: a tensor would be kept by its
+# identity); workspace sizes are kept by the descriptor (both are pure functions of the arguments), and
+# pointers go as plain integers.
 
 _EMBED = struct.Struct("=qqiiiiif")    # gr_embedding
 _NORM = struct.Struct("=qiiif")        # gr_norm
@@ -689,7 +690,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, branches: 
         _dev(out, "out")
         if out.shape != shape or out.dtype != dtype:
             raise ValueError(f"out must be {dtype} of shape {list(shape)}")
-    e = _embed_desc(N, V, D, branches, _DTYPES[table.dtype], _DTYPES[dtype], bits, scale)
+    e = _embed_desc(N, V, D, int(branches), _DTYPES[table.dtype], _DTYPES[dtype], bits, float(scale))
     _call("gr_embed", e, table.data_ptr(), ids.data_ptr(), out.data_ptr(),
           _raw_stream(stream, table, ids, out))
     return out
@@ -712,7 +713,8 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
         dtable = _new(stream, (n_vocab, D), torch.float32, dR.device)
     else:
         _f32(dtable, "dtable", (n_vocab, D))
-    e = _embed_desc(N, n_vocab, D, 1 if nd == 2 else dR.shape[1], GR_F32, GR_F32, bits, scale)
+    e = _embed_desc(N, int(n_vocab), D, 1 if nd == 2 else dR.shape[1], GR_F32, GR_F32, bits,
+                    float(scale))
     wp, wn, _keep = _ws(_need("gr_embed_backward_workspace_size", e), workspace, dR, stream)
     _call("gr_embed_backward", e, dR.data_ptr(), ids.data_ptr(), dtable.data_ptr(),
           1 if accumulate else 0, wp, wn, _raw_stream(stream, dR, ids, dtable, workspace))
@@ -726,7 +728,8 @@ def _norm_rows(x: torch.Tensor, weight: torch.Tensor, eps: float) -> bytes:
         raise ValueError("x must be a float32 or bfloat16 tensor [N, D] or [N, 4, D]")
     shape = x.shape
     _f32(weight, "weight", shape[1:])
-    return _norm_desc(shape[0], shape[-1], 1 if len(shape) == 2 else shape[1], _DTYPES[x.dtype], eps)
+    return _norm_desc(shape[0], shape[-1], 1 if len(shape) == 2 else shape[1], _DTYPES[x.dtype],
+                      float(eps))
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -798,7 +801,8 @@ def _mixer(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.T
     rows = (_rows(q, "q", N, H, dk, dtype), _rows(k, "k", N, H, dk, dtype),
             _rows(v, "v", N, H, dv, dtype))
     _f32(log_decay, "log_decay", (H,))
-    m = _mixer_desc(N, n_seqs, H, dk, dv, _DTYPES[dtype], dk ** -0.5 if scale is None else scale)
+    m = _mixer_desc(N, n_seqs, H, dk, dv, _DTYPES[dtype],
+                    dk ** -0.5 if scale is None else float(scale))
     return N, H, dk, dv, m, rows
 
 
@@ -813,7 +817,8 @@ def _seqs(seq_starts: torch.Tensor | None) -> int:
 
 def mixer_path(n_tokens: int, n_heads: int, d_key: int, d_value: int, dtype: torch.dtype) -> str:
     """Which kernels a linear-attention prompt of this shape runs: "mixer_tc" or "mixer_simt"."""
-    m = _mixer_desc(n_tokens, 1, n_heads, d_key, d_value, _DTYPES.get(dtype, -1), 1.0)
+    m = _mixer_desc(int(n_tokens), 1, int(n_heads), int(d_key), int(d_value), _DTYPES.get(dtype, -1),
+                    1.0)
     return load().gr_mixer_path(m).decode()
 
 

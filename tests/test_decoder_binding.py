@@ -156,3 +156,21 @@ def test_tensors_of_another_device_are_refused(calls, monkeypatch, i):
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0, raising=False)
     with pytest.raises(ValueError, match="device"):     # all on one device, another one than the current
         call()
+
+
+def test_descriptors_hold_values_not_tensors(calls):
+    """A scale or eps given as a tensor counts at its value of the call, also when it changed since the last one."""
+    D, N, H, d = 16, 4, 1, 64
+    ids, w, x = torch.zeros(N, dtype=torch.int64), torch.ones(4, D), torch.zeros(N, 4, D)
+    q, decay, state = torch.zeros(N, H, d), torch.zeros(H), torch.zeros(N, H, d, d)
+    s, at = torch.tensor(0.5), torch.zeros(5, D)
+    forms = [lambda: gr.embed(at, ids, s, stream=Stream()), lambda: gr.embed_backward(x, ids, 5, s, stream=Stream()),
+             lambda: gr.layer_norm(x, w, None, s, stream=Stream()),
+             lambda: gr.linear_attention(q, q, q, decay, s, stream=Stream()),
+             lambda: gr.linear_attention_step(q, q, q, decay, state, s, stream=Stream()),
+             lambda: gr.linear_attention_backward(q, q, q, q, decay, s, stream=Stream())]
+    for form in forms:
+        for value in (0.5, 0.25):
+            s.fill_(value)
+            form()
+            assert struct.unpack("=f", calls[-1][1][0][-4:])[0] == value, calls[-1][0]
