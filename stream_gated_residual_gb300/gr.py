@@ -878,10 +878,12 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
                               seq_starts: torch.Tensor | None = None,
                               state: torch.Tensor | None = None,
                               dstate: torch.Tensor | None = None, out=None,
-                              workspace: torch.Tensor | None = None, stream=None):
+                              workspace: torch.Tensor | None = None, stream=None,
+                              dstate_in: torch.Tensor | None = None):
     """gr_linear_attention_backward: (dq, dk, dv, dstate_in) from do [N, H, dv] and, optionally, the
     gradient dstate [B, H, dk, dv] of state_out. dq, dk, dv come in q's dtype (out: a triple to write,
-    strided views allowed); dstate_in is None unless dstate or state is given."""
+    strided views allowed); dstate_in, the gradient of state, is made where dstate or state is given, or
+    written to the tensor given for it, which may be dstate."""
     B = _seqs(seq_starts)
     N, H, dk, dv, m, rows = _mixer(q, k, v, log_decay, scale, B)
     _f32(state, "state", (B, H, dk, dv))
@@ -891,11 +893,13 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
         out = [_new(stream, (N, H, d), q.dtype, q.device) for d in (dk, dk, dv)]
     outs = [_rows(t, n, N, H, d, q.dtype)
             for t, n, d in zip(out, ("dq", "dk", "dv"), (dk, dk, dv))]
-    dstate_in = None
-    if state is not None or dstate is not None:
+    if dstate_in is not None:
+        _f32(dstate_in, "dstate_in", (B, H, dk, dv))
+    elif state is not None or dstate is not None:
         dstate_in = _new(stream, (B, H, dk, dv), torch.float32, q.device)
     wp, wn, _keep = _ws(_need("gr_linear_attention_workspace_size", m, 1), workspace, q, stream)
     _call("gr_linear_attention_backward", m, dorow, *rows, log_decay.data_ptr(), _opt(seq_starts),
           _opt(state), _opt(dstate), *outs, _opt(dstate_in), wp, wn,
-          _raw_stream(stream, q, do, k, v, log_decay, seq_starts, state, dstate, *out, workspace))
+          _raw_stream(stream, q, do, k, v, log_decay, seq_starts, state, dstate, *out, dstate_in,
+                      workspace))
     return (*out, dstate_in)

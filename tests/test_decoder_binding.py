@@ -174,3 +174,17 @@ def test_descriptors_hold_values_not_tensors(calls):
             s.fill_(value)
             form()
             assert struct.unpack("=f", calls[-1][1][0][-4:])[0] == value, calls[-1][0]
+
+
+def test_state_gradient_in_place(calls):
+    """dstate_in is the caller's where it is given, dstate itself among them."""
+    q, decay, ds = torch.zeros(3, 1, 64), torch.zeros(1), torch.zeros(1, 1, 64, 64)
+    got = gr.linear_attention_backward(q, q, q, q, decay, dstate=ds, dstate_in=ds, stream=Stream())
+    args = calls[-1][1]
+    assert got[3] is ds and args[8] == ds.data_ptr() == args[12]
+    alone = torch.zeros_like(ds)                        # also with neither state nor dstate
+    got = gr.linear_attention_backward(q, q, q, q, decay, dstate_in=alone, stream=Stream())
+    assert got[3] is alone and calls[-1][1][8] is None and calls[-1][1][12] == alone.data_ptr()
+    for bad in (torch.zeros(1, 1, 64, 32), ds.to(torch.bfloat16), ds.transpose(2, 3)):
+        with pytest.raises(ValueError, match="dstate_in"):
+            gr.linear_attention_backward(q, q, q, q, decay, dstate_in=bad)

@@ -562,3 +562,26 @@ def test_outputs_dropped_early_on_another_stream():
     assert not side.query() and other.data_ptr() != at
     side.synchronize()
     assert (other == 0).all()
+
+
+@pytest.mark.parametrize("lengths", [[5, 0, 130, 1], [1500, 1, 0, 2100, 130]])
+@pytest.mark.parametrize("dk,dv,dtype", [(128, 128, BF), (64, 64, BF), (64, 128, BF), (64, 64, F32), (200, 72, F32)])
+def test_linear_attention_state_gradient_in_place(lengths, dk, dv, dtype):
+    """dstate_in in dstate's own buffer: the gradients of the definition. (dv then runs after dk by itself,
+    cut by a plan of its own.)"""
+    q, k, v, decay, starts, at, state, g = mixer_inputs(lengths, 2, dk, dv, dtype)
+    decay = torch.tensor([-2e-3, -0.3], device="cuda")
+    do, dstate = randn(g, *v.shape, dtype=dtype), randn(g, *state.shape)
+    onto = dstate.clone()
+    got = gr.linear_attention_backward(do, q, k, v, decay, 0.3, seq_starts=starts, state=state, dstate=onto,
+                                       dstate_in=onto)
+    assert got[3] is onto
+    want = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, state, dstate)
+    for a, b in zip(got[:3], want):
+        assert rel(a, b) <= (5e-3 if dtype == BF else 1e-5)
+    assert rel(onto, want[3]) <= 2e-6
+    mags = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, state, dstate, magnitudes=True)
+    terms = max(dk, dv) + 64 + 4 * (max(lengths) // 32 + 1)
+    for a, b, m in zip(got[:3], want, mags):
+        within(a, b, mixer_bounds(b, m, terms, dtype), "gradient")
+    within(onto, want[3], (terms + 64) * U32 * mags[3], "dstate_in")
