@@ -380,12 +380,17 @@ run_join_kernel(const uint32_t* __restrict__ sid, int n, int64_t V, int D, int p
 }
 
 // Sorted positions a CTA of the sums takes: 64 for large tiles (few partial rows), fewer where the
-// pieces would not fill the SMs.
+// pieces would not fill the SMs (a constant, so that the workspace can be sized without a device).
 int piece_of(int64_t n, int D) {
+    constexpr int64_t kSms = 152;
     const int64_t cols = (D + kSumThreads * 4 - 1) / (kSumThreads * 4);
     int piece = 64;
-    while (piece > 4 && (n + piece - 1) / piece * cols < int64_t(sm_count()) * 4) piece /= 2;
+    while (piece > 4 && (n + piece - 1) / piece * cols < kSms * 4) piece /= 2;
     return piece;
+}
+int64_t pieces_of(int64_t n, int D) {
+    const int piece = piece_of(n, D);
+    return (n + piece - 1) / piece;
 }
 
 template <typename... KArgs, typename... Args>
@@ -436,11 +441,12 @@ cudaError_t launch_embed(int64_t N, int64_t V, int D, int nb, int table_dtype, i
     return cudaGetLastError();
 }
 
-// The sorted ids and positions [N] each, then two partial rows [D] a piece of the largest tile.
+// The sorted ids and positions [N] each, then two partial rows [D] a piece, for the whole tiles or the
+// last one (a smaller tile may have more pieces), whichever have more.
 size_t embed_backward_workspace(int64_t N, int D) {
-    const int64_t tile = N < kSortTile ? N : kSortTile;
-    // piece_of() gives at least 4 positions a piece
-    const int64_t pieces = (tile + 3) / 4;
+    const int64_t whole = N < kSortTile ? 0 : pieces_of(kSortTile, D);
+    const int64_t last = pieces_of(N % kSortTile, D);
+    const int64_t pieces = whole > last ? whole : last;
     return 2 * align256(size_t(N) * 4) + align256(size_t(2 * pieces) * D * 4);
 }
 
@@ -457,7 +463,7 @@ cudaError_t launch_embed_backward(int64_t N, int64_t V, int D, int nb, int id_bi
     for (int64_t t0 = 0; e == cudaSuccess && t0 < N; t0 += kSortTile) {
         const int n = int(N - t0 < kSortTile ? N - t0 : kSortTile);
         const int piece = piece_of(n, D);
-        const dim3 grid((n + piece - 1) / piece, (D + kSumThreads * 4 - 1) / (kSumThreads * 4));
+        const dim3 grid(pieces_of(n, D), (D + kSumThreads * 4 - 1) / (kSumThreads * 4));
         const float* rows = dR + t0 * nb * int64_t(D);
         const bool add = accumulate || t0 > 0;
         e = launch_after(nb == 1 ? run_sum_kernel<1> : run_sum_kernel<4>, grid, kSumThreads, 0, st,

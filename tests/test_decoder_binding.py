@@ -188,3 +188,19 @@ def test_state_gradient_in_place(calls):
     for bad in (torch.zeros(1, 1, 64, 32), ds.to(torch.bfloat16), ds.transpose(2, 3)):
         with pytest.raises(ValueError, match="dstate_in"):
             gr.linear_attention_backward(q, q, q, q, decay, dstate_in=bad)
+
+
+def test_embedding_workspace_is_what_the_plan_uses():
+    """Two partial rows a piece of the largest tile: pieces of 64 sorted positions once they fill the SMs (four
+    of a piece's columns an SM), 4 at least; twice that and the sort's 8 bytes a token cover any plan."""
+    gbuild.build()
+    for D in (8, 512, 520, 1024, 2560, 4096, 12288):
+        cols = -(-D // 512)
+        for N in (1, 3, 4, 777, 1024, 4096, 10000, 16383, 16384, 16385, 100000, 1 << 24):
+            tile = min(N, 16384)
+            fill = 2 * (4 * 152) // cols + 1            # pieces that a halved piece can still reach
+            pieces = min(-(-tile // 4), max(-(-tile // 64), fill))
+            e = gr._embed_desc(N, 1000, D, 4, gr.GR_F32, gr.GR_F32, 64, 1.0)
+            need = gr._need("gr_embed_backward_workspace_size", e)
+            assert need <= 8 * N + 2 * 2 * pieces * D * 4 + 1024, (N, D)
+            assert need >= 8 * N + 2 * -(-tile // 64) * D * 4

@@ -585,3 +585,20 @@ def test_linear_attention_state_gradient_in_place(lengths, dk, dv, dtype):
     for a, b, m in zip(got[:3], want, mags):
         within(a, b, mixer_bounds(b, m, terms, dtype), "gradient")
     within(onto, want[3], (terms + 64) * U32 * mags[3], "dstate_in")
+
+
+@pytest.mark.parametrize("N,V,D,nb", [(1, 3, 8, 1), (777, 50, 1000, 1), (2048, 9, 64, 4), (16384, 300, 520, 1),
+                                      (16384 + 600, 400, 520, 1), (2 * 16384 + 6000, 100, 16, 4)])
+def test_embed_backward_stays_in_its_workspace(N, V, D, nb):
+    """A workspace of the size asked for, between guards: the same gradient, the guards untouched."""
+    g = gen(N)
+    ids = torch.randint(-1, V + 1, (N,), generator=g, device="cuda")
+    dR = randn(g, N, D) if nb == 1 else randn(g, N, nb, D)
+    e = gr._embed_desc(N, V, D, nb, gr.GR_F32, gr.GR_F32, 64, 0.5)
+    need = gr._need("gr_embed_backward_workspace_size", e)
+    assert need % 256 == 0
+    buf = torch.full((need + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    got = gr.embed_backward(dR, ids, V, 0.5, workspace=buf[4096:4096 + need])
+    assert (buf[:4096] == 0x5a).all() and (buf[4096 + need:] == 0x5a).all()
+    g64, m64, rows = ref.embed_grad(dR, ids, V, 0.5)
+    within(got, g64, (rows * nb + 8) * U32 * m64, "gradient")
