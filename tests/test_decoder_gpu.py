@@ -602,3 +602,168 @@ def test_embed_backward_stays_in_its_workspace(N, V, D, nb):
     assert (buf[:4096] == 0x5a).all() and (buf[4096 + need:] == 0x5a).all()
     g64, m64, rows = ref.embed_grad(dR, ids, V, 0.5)
     within(got, g64, (rows * nb + 8) * U32 * m64, "gradient")
+
+
+# Prompts and gradients on the tensor cores come in variants: `fine` up to 128 tokens or 2048 rows (tokens ·
+# heads), and above that with or without a state as a result. The tests below say which one they mean.
+
+def above_few_rows(lengths, H):
+    N = sum(lengths)
+    assert N > 128 and N * H > 2048, "the sizes of the variant that rounds scores and states once"
+
+
+def cut(N, B, H, dk, dv, dtype, gradient):
+    """Whether a call of these sizes can be cut into segments: only then it needs a workspace."""
+    m = gr._mixer_desc(N, B, H, dk, dv, gr._DTYPES[dtype], 1.0)
+    return gr._need("gr_linear_attention_workspace_size", m, int(gradient)) > 0
+
+
+NO_STATE = [([127, 0, 129, 1], 9, 128, 128), ([300], 7, 64, 128), ([5, 257, 128], 6, 128, 64), ([700], 3, 64, 64),
+            ([1500, 1, 0, 2100, 130], 2, 128, 128), ([1500, 1, 0, 2100, 130], 2, 64, 64), ([2900, 300], 1, 64, 128),
+            ([3000], 2, 128, 64)]
+
+
+@pytest.mark.parametrize("lengths,H,dk,dv", NO_STATE)
+def test_linear_attention_no_state_is_a_result(lengths, H, dk, dv):
+    """Training's ordinary call: no state in or out. The decayed values are then two bf16 terms (2^-17 of them is
+    cut off, less than 1/100 of the roundings that mixer_bounds() counts)."""
+    above_few_rows(lengths, H)
+    assert max(lengths) < 1000 or cut(sum(lengths), len(lengths), H, dk, dv, BF, True)
+    q, k, v, _, starts, at, _, g = mixer_inputs(lengths, H, dk, dv, BF)
+    decay = -torch.exp2(-torch.linspace(2.0, 9.0, H, device="cuda"))
+    do = randn(g, *v.shape, dtype=BF)
+    terms = max(dk, dv) + 64 + 4 * (max(lengths) // 32 + 1)
+    got = gr.linear_attention_backward(do, q, k, v, decay, 0.3, seq_starts=starts)
+    assert got[3] is None
+    want = ref.recurrence_grad(do, q, k, v, decay, 0.3, at)
+    mags = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, magnitudes=True)
+    for name, a, b, m in zip(("dq", "dk", "dv"), got, want, mags):
+        within(a, b, mixer_bounds(b, m, terms, BF) + 2 ** -16 * m, name)
+        assert rel(a, b) <= 5e-3, name
+    # a prompt whose last states nobody asks for (the C entry's state_out NULL)
+    N = len(q)
+    o = torch.empty(N, H, dv, dtype=BF, device="cuda")
+    m = gr._mixer_desc(N, len(lengths), H, dk, dv, gr.GR_BF16, 0.3)
+    wp, wn, _keep = gr._ws(gr._need("gr_linear_attention_workspace_size", m, 0), None, q, None)
+    gr._call("gr_linear_attention", m, gr._rows(q, "q", N, H, dk, BF), gr._rows(k, "k", N, H, dk, BF),
+             gr._rows(v, "v", N, H, dv, BF), decay.data_ptr(), starts.data_ptr(), None, gr._rows(o, "o", N, H, dv, BF),
+             None, wp, wn, gr._raw_stream(None, q))
+    o64, _ = ref.recurrence(q, k, v, decay, 0.3, at)
+    om, _ = ref.recurrence(q, k, v, decay, 0.3, at, magnitudes=True)
+    within(o, o64, mixer_bounds(o64, om, terms, BF) + 2 ** -16 * om, "o")
+    assert rel(o, o64) <= 5e-3
+
+
+@pytest.mark.parametrize("with_state", [True, False])
+@pytest.mark.parametrize("dk,dv,dtype", [(128, 128, BF), (64, 64, BF), (64, 128, BF), (64, 64, F32)])
+def test_linear_attention_decays_of_many_rows(dk, dv, dtype, with_state):
+    """No decay, decays that underflow within a few tokens, and none of the past at all, forwards and backwards, in
+    more rows than are rounded once and in prompts that are cut."""
+    lengths, H = [190, 1300, 130], 5
+    above_few_rows(lengths, H)
+    assert cut(sum(lengths), 3, H, dk, dv, dtype, False)
+    q, k, v, _, starts, at, state, g = mixer_inputs(lengths, H, dk, dv, dtype)
+    decay = torch.tensor([0.0, -float("inf"), -100.0, -20.0, -3e-3], device="cuda")
+    do, dstate = randn(g, *v.shape, dtype=dtype), randn(g, *state.shape)
+    if not with_state:
+        state = dstate = None
+    terms = max(dk, dv) + 64 + 4 * (max(lengths) // 32 + 1)
+    o, last = gr.linear_attention(q, k, v, decay, 0.1, seq_starts=starts, state=state)
+    o64, l64 = ref.recurrence(q, k, v, decay, 0.1, at, state)
+    om, lm = ref.recurrence(q, k, v, decay, 0.1, at, state, magnitudes=True)
+    within(o, o64, mixer_bounds(o64, om, terms, dtype) + 1e-30, "o")
+    within(last, l64, (terms + 64) * U32 * lm + 1e-30, "state")
+    got = gr.linear_attention_backward(do, q, k, v, decay, 0.1, seq_starts=starts, state=state, dstate=dstate)
+    want = ref.recurrence_grad(do, q, k, v, decay, 0.1, at, state, dstate)
+    mags = ref.recurrence_grad(do, q, k, v, decay, 0.1, at, state, dstate, magnitudes=True)
+    for name, a, b, m in zip(("dq", "dk", "dv"), got, want, mags):
+        within(a, b, mixer_bounds(b, m, terms, dtype) + (2 ** -16 * m if dtype == BF else 0) + 1e-30, name)
+    if with_state:
+        within(got[3], want[3], (terms + 64) * U32 * mags[3] + 1e-30, "dstate_in")
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, BF), (128, 64, BF), (32, 40, F32)])
+def test_linear_attention_many_sequences(dk, dv, dtype):
+    """More sequences than a warp has lanes, more (sequence, head) rows than SMs, and long ones behind the 32nd and the
+    64th that are cut all the same."""
+    g = gen(17)
+    lengths = torch.randint(0, 25, (70,), generator=g, device="cuda").tolist()
+    lengths[3], lengths[40], lengths[66] = 0, 5000, 3500
+    H, N, tol = 4, sum(lengths), 5e-3 if dtype == BF else 1e-5
+    assert len(lengths) * H >= 152
+    assert cut(N, 70, H, dk, dv, dtype, False) and cut(N, 70, H, dk, dv, dtype, True)
+    q, k, v, _, starts, at, state, g = mixer_inputs(lengths, H, dk, dv, dtype)
+    decay = torch.tensor([-1e-3, -0.05, 0.0, -4e-4], device="cuda")
+    do, dstate = randn(g, *v.shape, dtype=dtype), randn(g, *state.shape)
+    terms = max(dk, dv) + 64 + 4 * (max(lengths) // 32 + 1)
+    for st, ds in ((state, dstate), (None, None)):
+        o, last = gr.linear_attention(q, k, v, decay, 0.3, seq_starts=starts, state=st)
+        o64, l64 = ref.recurrence(q, k, v, decay, 0.3, at, st)
+        om, lm = ref.recurrence(q, k, v, decay, 0.3, at, st, magnitudes=True)
+        within(o, o64, mixer_bounds(o64, om, terms, dtype), "o")
+        within(last, l64, (terms + 64) * U32 * lm, "state")
+        got = gr.linear_attention_backward(do, q, k, v, decay, 0.3, seq_starts=starts, state=st, dstate=ds)
+        want = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, st, ds)
+        mags = ref.recurrence_grad(do, q, k, v, decay, 0.3, at, st, ds, magnitudes=True)
+        assert rel(o, o64) <= tol
+        for name, a, b, m in zip(("dq", "dk", "dv"), got, want, mags):
+            within(a, b, mixer_bounds(b, m, terms, dtype) + (2 ** -16 * m if dtype == BF else 0), name)
+            assert rel(a, b) <= tol, name
+        if ds is not None:
+            within(got[3], want[3], (terms + 64) * U32 * mags[3], "dstate_in")
+
+
+@pytest.mark.parametrize("lengths,H,with_state", [([70, 150, 9, 40], 2, True), ([70, 300, 9, 140], 6, True),
+                                                  ([70, 300, 9, 140], 6, False), ([70, 2000, 9, 140], 2, True),
+                                                  ([70, 2000, 9, 140], 2, False)])
+@pytest.mark.parametrize("dk,dv,dtype", [(128, 128, BF), (64, 64, BF), (64, 128, BF), (64, 64, F32)])
+def test_linear_attention_gradient_nothing_leaks(lengths, H, with_state, dk, dv, dtype):
+    """What is not finite reaches only the gradients that it is a part of: through the past of dq, the future of dk and
+    dv, never another sequence or head. In the middle of a sequence (of several chunks and segments), and in the rows
+    right behind and before another one's end."""
+    if H == 6:
+        above_few_rows(lengths, H)
+    if lengths[1] == 2000:
+        assert cut(sum(lengths), 4, H, dk, dv, dtype, True)
+    q, k, v, _, starts, at, state, g = mixer_inputs(lengths, H, dk, dv, dtype, layout="plain")
+    decay = -torch.exp2(-torch.linspace(3.0, 12.0, H, device="cuda"))
+    do, dstate = randn(g, *v.shape, dtype=dtype), randn(g, *state.shape)
+    if not with_state:
+        state = dstate = None
+    clean = {"do": do, "q": q, "k": k, "v": v}
+
+    def grads(a, **kw):
+        return gr.linear_attention_backward(a["do"], a["q"], a["k"], a["v"], decay, 0.3, **kw)
+
+    want = grads(clean, seq_starts=starts, state=state, dstate=dstate)
+    for value in (float("nan"), float("inf")):
+        for seq, t in ((1, at[1] + lengths[1] // 2), (1, at[1]), (1, at[2] - 1), (3, at[3] + 1)):
+            past, future = (at[seq], t + 1), (t, at[seq + 1])      # rows whose future, past holds t
+            own = (t, t + 1)
+            hits = {"do": (own, past, past), "q": (None, past, past), "k": (future, None, own), "v": (future, own, None)}
+            for name, hit in hits.items():
+                args = dict(clean)
+                args[name] = clean[name].clone()
+                args[name][t, 1, 5] = value
+                got = grads(args, seq_starts=starts, state=state, dstate=dstate)
+                for what, a, b, rows in zip(("dq", "dk", "dv"), got, want, hit):
+                    touched = torch.zeros(len(q), H, dtype=torch.bool, device="cuda")
+                    if rows is not None:
+                        touched[rows[0]:rows[1], 1] = True
+                    assert torch.equal(a[~touched], b[~touched]), (name, what, t)
+                    if rows is not None:
+                        assert not torch.isfinite(a[t, 1]).all(), (name, what, t)
+                if with_state:
+                    keep = torch.ones(len(lengths), H, dtype=torch.bool, device="cuda")
+                    keep[seq, 1] = name in ("k", "v")
+                    assert torch.equal(got[3][keep], want[3][keep]), (name, t)
+    # rows that no sequence holds are not read into one and not written
+    args = {name: t.clone() for name, t in clean.items()}
+    for t in args.values():
+        t[at[3]:] = float("nan")
+    out = [torch.full_like(t, 7.0) for t in want[:3]]
+    part = None if state is None else state[:3].contiguous()
+    dpart = None if dstate is None else dstate[:3].contiguous()
+    grads(args, seq_starts=starts[:4].contiguous(), state=part, dstate=dpart, out=out)
+    for a in out:
+        assert (a[at[3]:] == 7).all() and torch.isfinite(a[:at[3]]).all()
