@@ -786,17 +786,12 @@ bool map_rows(CUtensorMap* m, const MixRows& r, int64_t N, int H, int d) {
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                   bool after, Args... args) {
+                   Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = after ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
@@ -846,14 +841,14 @@ cudaError_t run(const MixArgs* pass, float* slots, cudaStream_t st) {
     }
     if (e == cudaSuccess && split) {
         const dim3 sums(mix_sums(p.n_tokens, p.n_heads, L.sg), passes);
-        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, sums, kThreads, smem, st, false, L);
+        e = launch(mix_tc_kernel<DA, DC, true, kTerms, kPasses, false>, sums, kThreads, smem, st, L);
         if (e == cudaSuccess)
             e = launch_mix_scan(L.pass, passes, L.sg, slots, L.firsts, L.units, st);
     }
     // (launched after the scan in the plain order: as its programmatic dependent a gradient of 96 uncut
     // rows took 176 us against 142)
     if (e == cudaSuccess)
-        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>, grid, kThreads, smem, st, false, L);
+        e = launch(mix_tc_kernel<DA, DC, false, kTerms, kPasses, kFine>, grid, kThreads, smem, st, L);
     return e;
 }
 
