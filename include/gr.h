@@ -381,7 +381,8 @@ int gr_embed(const gr_embedding* e, const void* table, const void* ids, void* R,
  * and partial rows. */
 int gr_embed_backward_workspace_size(const gr_embedding* e, size_t* bytes);
 
-/* dtable[v][:] = scale · Σ_{t: ids[t] = v} Σ_i dR[t][i][:], fp32, summed in the order of t. With
+/* dtable[v][:] = scale · Σ_{t: ids[t] = v} Σ_i dR[t][i][:], fp32, summed in a fixed order: in
+ * pieces of at most 64 terms, each in the order of t, then over the pieces. With
  * accumulate == 0 all V rows are overwritten (rows no id names are zero, also when N == 0); else
  * the sums are added to dtable. Ids outside [0, V) are left out. dR [N][n_branch][D] fp32.
  * `workspace` 256-byte aligned, clear of the other buffers. */
@@ -452,11 +453,14 @@ int gr_linear_attention_workspace_size(const gr_mixer* m, int gradient, size_t* 
 
 /* Prompts: q, k [.., d_key], v, o [.., d_value]; state_in [n_seqs][n_heads][d_key][d_value] fp32 is S
  * before each sequence's first token (NULL: zero), state_out, if not NULL, S after its last (the
- * same buffer is allowed). On "mixer_tc" the scores and the state are rounded to bf16 where they
- * enter a product (in calls of at most 128 tokens to two bf16 terms, which leaves the output's own
- * rounding); the state itself is held and updated in fp32 (from bf16 triples of the decayed
- * values, so its error is fp32's). A value that is not finite makes the outputs from its token on
- * not finite, and no earlier ones. */
+ * same buffer is allowed). On "mixer_tc" the scores and the state are rounded to bf16 once where
+ * they enter a product: with the output's own rounding, 1.4 times that one's error. Calls of at
+ * most 128 tokens, or 2048 rows (n_tokens · n_heads), are cheap enough to take them as two bf16
+ * terms, which leaves the output's rounding alone; so a sequence's bits and error depend on the rows
+ * of the whole call. The state itself is held and updated in fp32, from the decayed values as three
+ * bf16 terms, exactly, so its error is fp32's; larger calls take two (2^-17 of each value) where
+ * only outputs read it, no state_out and, in the gradient, no dstate_in comes from it.
+ * A value that is not finite makes the outputs from its token on not finite, and no earlier ones. */
 int gr_linear_attention(const gr_mixer* m, const gr_rows* q, const gr_rows* k, const gr_rows* v,
                         const float* log_decay, const int32_t* seq_starts, const float* state_in,
                         const gr_rows* o, float* state_out, void* workspace, size_t workspace_bytes,

@@ -98,15 +98,6 @@ __device__ __forceinline__ bool find_segment(const MixArgs& p, const Segments& s
     return false;
 }
 
-// kTerms: bf16 terms of the decayed values. Three where the state is a result; where only outputs read
-// it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
-// kFine: P and the state's copy as two bf16 terms each, so that only the output's own rounding is left.
-// Over few rows the roundings of P do not average out: a row's error was up to 2.6 times the output's own,
-// a head's over 160 tokens 1.41 ± 0.04 times (up to 1.51), over 2048 tokens 1.41 ± 0.01. So calls of few
-// rows are fine (see launch_mix_tc): 1.00 times. P's second term lies in the columns of its own scores,
-// the state's in the second stage of b, which leaves b with one.
-// kSum: only the segment's own sum (no outputs), written to its slot; else the pass, which reads its first
-// state from the slot of the segment before, or from m_in.
 // Chunks a segment. A unit (a segment of a head) takes its chunks one after another, one unit an SM at a
 // time; cutting a sequence costs a second pass over b and c of all but its last segment, and two
 // launches. The host knows the sequences' number and sum, not their lengths:

@@ -203,6 +203,15 @@ struct Launch {
     int64_t units;                   // slots of a pass
 };
 
+// kSum: only the segment's own sum (no outputs), written to its slot; else the pass, which reads its first
+// state from the slot of the segment before, or from m_in.
+// kTerms: bf16 terms of the decayed values. Three where the state is a result; where only outputs read
+// it, through a rounding to bf16, two (relative error 2^-17) leave that rounding as it is.
+// kFine: P and the state's copy as two bf16 terms each, so that only the output's own rounding is left:
+// 1.00 times its error. Rounded once, the norm of the error is 1.41 times that (± 0.04 over 160 rows of a
+// head, ± 0.01 over 2048), a single row's up to 2.6 times, however many rows the call has. P's second
+// term lies in the columns of its own scores, the state's in the second stage of b, which leaves b with one:
+// launch_mix_tc says which calls can afford that.
 template <int DA, int DC, bool kSum, int kTerms, int kPass, bool kFine>
 __device__ __forceinline__ void mix_pass(const Launch& L) {
     const MixArgs& p = L.pass[kPass];
@@ -882,10 +891,10 @@ cudaError_t launch_mix_tc(const MixArgs* p, int passes, void* workspace, cudaStr
     float* slots = static_cast<float*>(workspace);
     bool state = false;
     for (int i = 0; i < passes; ++i) state = state || p[i].m_out;
-    // Fine up to a chunk of tokens or the rows of 16 chunks: such calls wait more than they compute (the
-    // gradient of 512 tokens of 4 heads of 128 takes 23 us instead of 21, the prompt 25 instead of 24),
-    // larger ones do not (8192 tokens of 152 heads: 315 us instead of 248), and there the roundings
-    // average out over the rows.
+    // Fine where it costs little, up to a chunk of tokens or the rows of 16 chunks: such calls wait more
+    // than they compute (the gradient of 512 tokens of 4 heads of 128 takes 23 us instead of 21, the prompt
+    // 25 instead of 24). Larger ones do not (8192 tokens of 152 heads: 315 us instead of 248). The rule
+    // looks at the call, so the same sequence may be fine alone and not among others.
     const bool fine = p->n_tokens <= kChunk || p->n_tokens * p->n_heads <= 16 * kChunk;
     // 0: fine (whatever its terms: three), 1: two terms, 2: three
     const int how = fine ? 0 : state ? 2 : 1;

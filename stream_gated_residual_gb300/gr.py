@@ -606,17 +606,23 @@ _mixer_desc = functools.lru_cache(1024)(_MIXER.pack)
 _current_device = torch._C._cuda_getDevice
 
 
+@functools.cache
+def _several_devices() -> bool:
+    return torch.cuda.device_count() > 1
+
+
 def _raw_stream(stream, t: torch.Tensor, *others: torch.Tensor | None) -> int:
     """cudaStream_t of `stream`, or of torch's current stream. The library launches on the current
-    device, so all tensors of the call have to be there."""
+    device, so all tensors of the call have to be there (asked where the process sees several)."""
     device = t.get_device()
-    if device != _current_device():
-        raise ValueError(f"the tensors are on device {device}, the current device is "
-                         f"{_current_device()}")
-    for o in others:
-        if o is not None and o.get_device() != device:
-            raise ValueError(f"all tensors of a call must be on one device, got devices {device} "
-                             f"and {o.get_device()}")
+    if _several_devices():
+        if device != _current_device():
+            raise ValueError(f"the tensors are on device {device}, the current device is "
+                             f"{_current_device()}")
+        for o in others:
+            if o is not None and o.get_device() != device:
+                raise ValueError("all tensors of a call must be on one device, got devices "
+                                 f"{device} and {o.get_device()}")
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)
@@ -700,7 +706,7 @@ def embed_backward(dR: torch.Tensor, ids: torch.Tensor, n_vocab: int, scale: flo
                    dtable: torch.Tensor | None = None, accumulate: bool = False,
                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gr_embed_backward: the table's gradient [n_vocab, D] fp32 from dR [N, 4, D] or [N, D] fp32;
-    rows of equal ids are summed in token order. accumulate=True adds to the given dtable."""
+    rows of equal ids are summed in a fixed order. accumulate=True adds to the given dtable."""
     _f32(dR, "dR")
     bits = _ids(ids)
     nd = dR.dim()
@@ -747,7 +753,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
             raise ValueError("y must match x")
     mean = rstd = None
     if stats:
-        mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x.device) for _ in range(2))
+        mean = _new(stream, x.shape[:-1], torch.float32, x.device)
+        rstd = _new(stream, x.shape[:-1], torch.float32, x.device)
     _call("gr_layer_norm", n, x.data_ptr(), weight.data_ptr(), _opt(bias), y.data_ptr(), _opt(mean),
           _opt(rstd), _raw_stream(stream, x, weight, bias, y))
     return (y, mean, rstd) if stats else y

@@ -35,6 +35,7 @@ def calls(monkeypatch):
         seen.append((name, args))
 
     monkeypatch.setattr(gr, "_call", call)
+    monkeypatch.setattr(gr, "_several_devices", lambda: True)
     monkeypatch.setattr(gr, "_current_device", lambda: -1)   # where CPU tensors are
     monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.recorded.append((t.data_ptr(), s)),
