@@ -485,6 +485,82 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
                                  const gr_rows* dv, float* dstate_in, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ---- the gated feed-forward sublayer --------------------------------------------------------------
+ * The sublayer F that the second GR module of a layer wraps ("【论文解读】 Qwen3.8 Flash Next", §二.4: one
+ * module around the token mixer, one around the MLP). Per token, with f the activation:
+ *     gate = W_g x,  up = W_u x,     h = f(gate) ⊙ up,     y = W_o h
+ * in bf16 or fp32, with its gradient, and on FP8 weights. Conventions as above; sums and activations are
+ * fp32, two runs on the same inputs give the same bits. */
+typedef struct gr_feed {
+    int64_t n_tokens;    /* N: 0 .. 2^31 − 1                                             */
+    int32_t d_model;     /* D: a multiple of 8 (FP8: 16) in [8, GR_MAX_D]                */
+    int32_t d_ff;        /* F: a multiple of 8 (FP8: 16) in [8, GR_MAX_FF]               */
+    int32_t dtype;       /* GR_F32 or GR_BF16: of every tensor of the call; GR_FP8 only
+                            for gr_feed_forward_fp8, whose x and y are bf16              */
+    int32_t activation;  /* GR_SILU or GR_GELU                                           */
+} gr_feed;
+#define GR_MAX_FF 131072
+enum {
+    GR_SILU = 0,  /* g σ(g)                                   */
+    GR_GELU = 1   /* g Φ(g), Φ the normal distribution (erf)  */
+};
+
+/* Bytes of device workspace that gr_feed_forward (or gr_feed_forward_fp8, by the dtype) or, gradient != 0,
+ * gr_feed_forward_backward needs (host only). */
+int gr_feed_workspace_size(const gr_feed* f, int gradient, size_t* bytes);
+
+/* x, y [N][D]; w_in [2][F][D]: W_g, then W_u; w_out [D][F]: W_o. pre [N][2][F], unless NULL, receives gate and
+ * up, rounded to the call's dtype: what the gradient needs. h is rounded to the dtype once, formed from the
+ * unrounded gate and up. `workspace` 256-byte aligned; outputs and workspace clear of every other buffer. */
+int gr_feed_forward(const gr_feed* f, const void* x, const void* w_in, const void* w_out, void* y, void* pre,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient, given dy [N][D] and pre as the forward pass left it: dx [N][D], dw_in [2][F][D] and dw_out
+ * [D][F], in the call's dtype (overwritten; the weights' are zeros when N == 0). With dh = W_oᵀ dy:
+ *     dgate = dh ⊙ up ⊙ f'(gate),  dup = dh ⊙ f(gate),   dx = W_gᵀ dgate + W_uᵀ dup,
+ *     dW_g = dgateᵀ x,  dW_u = dupᵀ x,  dW_o = dyᵀ h.
+ * dh stays fp32; dgate, dup and h are rounded to the dtype once, where they enter a product. */
+int gr_feed_forward_backward(const gr_feed* f, const void* dy, const void* x, const void* w_in,
+                             const void* w_out, const void* pre, void* dx, void* dw_in, void* dw_out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- FP8 blocks and their product ------------------------------------------------------------------
+ * A matrix [rows][cols] in FP8 blocks is codes [rows][cols] (uint8, OCP e4m3) and biased exponents, one for each
+ * block of 128 columns of block_rows rows: scales [ceil(rows / block_rows)][ceil(cols / 128)] (uint8). An
+ * element is decode(code) · 2^(scale − 127); exponents and codes follow the FP8 branch state's rules above. A
+ * block that holds a value that is not finite gets the scale 255 and codes 0x7F: NaN throughout. Activations
+ * have blocks of one row, weights of 128 (the last ones of either direction may be part-full). */
+typedef struct gr_blocks {
+    int64_t n_rows;      /* of a matrix, >= 0                                            */
+    int64_t n_cols;      /* a multiple of 16, 16 .. GR_MAX_FF                            */
+    int32_t n_matrix;    /* matrices [n_rows][n_cols] one after another, each with blocks
+                            of its own; >= 1                                             */
+    int32_t block_rows;  /* 1 or 128                                                     */
+    int32_t dtype;       /* of the matrices: GR_F32 or GR_BF16                           */
+} gr_blocks;
+
+/* m [n_matrix][n_rows][n_cols] into codes and scales. scales need no alignment. */
+int gr_fp8_encode_blocks(const gr_blocks* b, const void* m, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* out [N][O] bf16 = A Bᵀ, A [N][K] in blocks of one row, B [O][K] in blocks of 128: products and sums of the
+ * stored values in fp32, rounded once. n_tokens N 0 .. 2^31 − 1, K a multiple of 16 in [16, GR_MAX_FF], O a multiple
+ * of 8 in [8, 2 GR_MAX_FF]. Codes and out 16-byte aligned, scales anywhere. */
+typedef struct gr_product {
+    int64_t n_tokens;    /* N */
+    int32_t d_in;        /* K */
+    int32_t d_out;       /* O */
+} gr_product;
+int gr_fp8_matmul_workspace_size(const gr_product* p, size_t* bytes);
+int gr_fp8_matmul(const gr_product* p, const uint8_t* a, const uint8_t* a_scales, const uint8_t* b,
+                  const uint8_t* b_scales, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The feed-forward sublayer on FP8 weights (serving; f->dtype GR_FP8): x [N][D] and y bf16, w_in two matrices
+ * [F][D] (n_matrix 2) and w_out [D][F] in blocks of 128 rows. x and the fp32 h are encoded in blocks of one
+ * row on the way into their products. */
+int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, const uint8_t* w_in_scales,
+                        const uint8_t* w_out, const uint8_t* w_out_scales, void* y, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

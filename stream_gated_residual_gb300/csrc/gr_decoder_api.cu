@@ -2,26 +2,12 @@
 // and their gradients): host-side validation, dispatch, status codes. Contracts in include/gr.h.
 #include <math.h>
 
+#include "gr_check.h"
 #include "gr_internal.h"
 #include "gr_mixer.h"
 
 namespace gr {
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-size_t width(int dtype) { return dtype == GR_BF16 ? 2 : 4; }
-bool real_dtype(int dtype) { return dtype == GR_F32 || dtype == GR_BF16; }
-int as_status(cudaError_t e) { return e == cudaSuccess ? GR_OK : GR_E_CUDA; }
-
-// A buffer of a call: where it starts and how many bytes the call may touch.
-struct Span {
-    const void* p;
-    size_t n;
-};
-bool meet(const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
-}
 
 int check_embedding(const gr_embedding* e) {
     if (!e) return GR_E_NULL;

@@ -1,0 +1,57 @@
+// Internal declarations of the gated feed-forward sublayer and of the products on FP8 blocks.
+#pragma once
+
+#include <stdint.h>
+
+#include "gr_internal.h"
+
+namespace gr {
+
+constexpr int kBlock = 128;   // channels of an FP8 block
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A matrix in FP8 blocks: e4m3 codes [rows][k] and biased exponents [rows / block_rows][k / 128].
+struct Fp8Matrix {
+    const uint8_t* codes;
+    const uint8_t* scales;
+};
+
+// FP8 blocks of `n_matrix` matrices [rows][cols] (gr_blocks.cu).
+cudaError_t launch_encode_blocks(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, int dtype,
+                                 const void* m, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+
+// Products on CUDA cores (gr_feed_simt.cu). dtype: GR_F32, GR_BF16.
+// h = act(x Wgᵀ) ⊙ (x Wuᵀ), pre [N][2][F] unless null.
+cudaError_t simt_gated(int64_t N, int D, int F, int dtype, int act, const void* x, const void* w_in, void* h,
+                       void* pre, cudaStream_t st);
+// dh = dy W_out, then dpre [N][2][F] and h from it and pre.
+cudaError_t simt_gated_grad(int64_t N, int D, int F, int dtype, int act, const void* dy, const void* w_out,
+                            const void* pre, void* dpre, void* h, cudaStream_t st);
+// out [M][N] = A Bᵀ over K. a_k, b_k: whether A is [M][K] (else [K][M]) and B [N][K] (else [K][N]).
+cudaError_t simt_product(int64_t M, int64_t N, int64_t K, int dtype, const void* a, bool a_k, const void* b,
+                         bool b_k, void* out, cudaStream_t st);
+// The same on FP8 blocks: out [N][O] bf16; and h fp32 of the gated pair.
+cudaError_t simt_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, Fp8Matrix b, void* out,
+                             cudaStream_t st);
+cudaError_t simt_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, Fp8Matrix w_in, float* h,
+                           cudaStream_t st);
+
+#ifdef __CUDACC__
+// The activations and their slopes in fp32 with the accurate expf and erff.
+template <int ACT> __device__ __forceinline__ float activate(float g) {
+    if constexpr (ACT == GR_SILU) return g / (1.0f + expf(-g));
+    else return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+}
+template <int ACT> __device__ __forceinline__ float activate_slope(float g) {
+    if constexpr (ACT == GR_SILU) {
+        const float s = 1.0f / (1.0f + expf(-g));
+        return s * (1.0f + g * (1.0f - s));
+    } else {
+        return 0.5f * (1.0f + erff(g * 0.70710678118654752f)) +
+               g * expf(-0.5f * g * g) * 0.39894228040143268f;
+    }
+}
+#endif
+
+}  // namespace gr

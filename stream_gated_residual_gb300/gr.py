@@ -63,6 +63,20 @@ class MixerStruct(ctypes.Structure):
                 ("d_value", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class FeedStruct(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class BlocksStruct(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("n_cols", ctypes.c_int64), ("n_matrix", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class ProductStruct(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32)]
+
+
 class RowsStruct(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
@@ -131,6 +145,13 @@ def load() -> ctypes.CDLL:
                                      ctypes.c_int),
         "gr_linear_attention_backward": ([M, RW, RW, RW, RW, V, V, V, V, RW, RW, RW, V, V,
                                           ctypes.c_size_t, V], ctypes.c_int),
+        "gr_feed_workspace_size": ([V, ctypes.c_int, sz], ctypes.c_int),
+        "gr_feed_forward": ([V] * 7 + [ctypes.c_size_t, V], ctypes.c_int),
+        "gr_feed_forward_backward": ([V] * 10 + [ctypes.c_size_t, V], ctypes.c_int),
+        "gr_feed_forward_fp8": ([V] * 8 + [ctypes.c_size_t, V], ctypes.c_int),
+        "gr_fp8_encode_blocks": ([V] * 5, ctypes.c_int),
+        "gr_fp8_matmul_workspace_size": ([V, sz], ctypes.c_int),
+        "gr_fp8_matmul": ([V] * 7 + [ctypes.c_size_t, V], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -598,9 +619,15 @@ _EMBED = struct.Struct("=qqiiiiif")    # gr_embedding
 _NORM = struct.Struct("=qiiif")        # gr_norm
 _MIXER = struct.Struct("=qiiiiif")     # gr_mixer
 _ROWS = struct.Struct("=Qqq")          # gr_rows
+_FEED = struct.Struct("=qiiii")        # gr_feed
+_BLOCKS = struct.Struct("=qqiiixxxx")  # gr_blocks
+_PRODUCT = struct.Struct("=qii")       # gr_product
 _embed_desc = functools.lru_cache(1024)(_EMBED.pack)
 _norm_desc = functools.lru_cache(1024)(_NORM.pack)
 _mixer_desc = functools.lru_cache(1024)(_MIXER.pack)
+_feed_desc = functools.lru_cache(1024)(_FEED.pack)
+_blocks_desc = functools.lru_cache(1024)(_BLOCKS.pack)
+_product_desc = functools.lru_cache(1024)(_PRODUCT.pack)
 
 
 _current_device = torch._C._cuda_getDevice
@@ -910,3 +937,147 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
           _raw_stream(stream, q, do, k, v, log_decay, seq_starts, state, dstate, *out, dstate_in,
                       workspace))
     return (*out, dstate_in)
+
+
+# ---- the gated feed-forward sublayer, and FP8 blocks ----------------------------------------------
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
+BLOCK = 128    # channels of an FP8 block
+
+
+def _like(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> None:
+    if not t.is_cuda or not t.is_contiguous():
+        _dev(t, name)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
+
+
+def _out(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, like: torch.Tensor,
+         stream) -> torch.Tensor:
+    if t is None:
+        return _new(stream, shape, dtype, like.device)
+    _like(t, name, shape, dtype)
+    return t
+
+
+def _feed(x: torch.Tensor, F: int, dtype: int, activation: str) -> bytes:
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    return _feed_desc(x.shape[0], x.shape[1], F, dtype, _ACTIVATIONS[activation])
+
+
+def _feed_args(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activation: str):
+    """(N, D, F, descriptor) of a call on bf16 or fp32 tensors."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be a float32 or bfloat16 tensor [N, D]")
+    if w_in.dim() != 3 or w_in.shape[0] != 2:
+        raise ValueError("w_in must be [2, F, D]: the gate's weights, then the up projection's")
+    (N, D), F = x.shape, w_in.shape[1]
+    _like(x, "x", (N, D), x.dtype)
+    _like(w_in, "w_in", (2, F, D), x.dtype)
+    _like(w_out, "w_out", (D, F), x.dtype)
+    return N, D, F, _feed(x, F, _DTYPES[x.dtype], activation)
+
+
+def feed_forward(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activation: str = "silu",
+                 keep: bool = False, y: torch.Tensor | None = None, pre: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """gr_feed_forward: y = (f(x W_gᵀ) * (x W_uᵀ)) W_oᵀ of x [N, D], w_in [2, F, D] (W_g, W_u) and w_out
+    [D, F], all bf16 or all fp32; f is "silu" or "gelu" (erf). Returns y [N, D]; with keep=True (or a pre to
+    write) (y, pre), pre [N, 2, F] the gate and up values that the gradient needs."""
+    N, D, F, f = _feed_args(x, w_in, w_out, activation)
+    y = _out(y, "y", (N, D), x.dtype, x, stream)
+    if keep or pre is not None:
+        pre = _out(pre, "pre", (N, 2, F), x.dtype, x, stream)
+    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 0), workspace, x, stream)
+    _call("gr_feed_forward", f, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), y.data_ptr(), _opt(pre), wp,
+          wn, _raw_stream(stream, x, w_in, w_out, y, pre, workspace))
+    return y if pre is None else (y, pre)
+
+
+def feed_forward_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
+                          pre: torch.Tensor, activation: str = "silu", dx: torch.Tensor | None = None,
+                          dw_in: torch.Tensor | None = None, dw_out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """gr_feed_forward_backward: (dx, dw_in, dw_out) in x's dtype from dy [N, D] and the pre that
+    feed_forward(keep=True) returned."""
+    N, D, F, f = _feed_args(x, w_in, w_out, activation)
+    _like(dy, "dy", (N, D), x.dtype)
+    _like(pre, "pre", (N, 2, F), x.dtype)
+    dx = _out(dx, "dx", (N, D), x.dtype, x, stream)
+    dw_in = _out(dw_in, "dw_in", (2, F, D), x.dtype, x, stream)
+    dw_out = _out(dw_out, "dw_out", (D, F), x.dtype, x, stream)
+    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 1), workspace, x, stream)
+    _call("gr_feed_forward_backward", f, dy.data_ptr(), x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(),
+          pre.data_ptr(), dx.data_ptr(), dw_in.data_ptr(), dw_out.data_ptr(), wp, wn,
+          _raw_stream(stream, x, dy, w_in, w_out, pre, dx, dw_in, dw_out, workspace))
+    return dx, dw_in, dw_out
+
+
+def _up(n: int, step: int) -> int:
+    return -(-n // step)
+
+
+def fp8_encode_blocks(m: torch.Tensor, block_rows: int = 1, codes: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None, stream=None):
+    """gr_fp8_encode_blocks: m [R, K] or [M, R, K] (bf16 or fp32) -> (codes, like m, scales
+    [.., ceil(R / block_rows), ceil(K / 128)]), both uint8: e4m3 codes with a power-of-two scale for each 128
+    channels of a row (block_rows=1, activations) or of 128 rows (block_rows=128, weights)."""
+    if m.dim() not in (2, 3) or m.dtype not in _DTYPES:
+        raise ValueError("m must be a float32 or bfloat16 tensor [R, K] or [M, R, K]")
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
+    _dev(m, "m")
+    shape = m.shape
+    codes = _out(codes, "codes", shape, torch.uint8, m, stream)
+    scales = _out(scales, "scales", (*shape[:-2], _up(shape[-2], block_rows), _up(shape[-1], BLOCK)),
+                  torch.uint8, m, stream)
+    b = _blocks_desc(shape[-2], shape[-1], 1 if m.dim() == 2 else shape[0], int(block_rows), _DTYPES[m.dtype])
+    _call("gr_fp8_encode_blocks", b, m.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          _raw_stream(stream, m, codes, scales))
+    return codes, scales
+
+
+def _fp8_pair(pair, name: str, lead: tuple, block_rows: int):
+    """(codes, scales, rows, channels) of a matrix in blocks, with `lead` dimensions before its own two."""
+    codes, scales = pair
+    if codes.dim() != len(lead) + 2 or codes.shape[:len(lead)] != lead:
+        raise ValueError(f"the codes of {name} must be [{', '.join([*map(str, lead), 'rows', 'channels'])}]")
+    R, K = codes.shape[-2:]
+    _like(codes, f"the codes of {name}", (*lead, R, K), torch.uint8)
+    _like(scales, f"the scales of {name}", (*lead, _up(R, block_rows), _up(K, BLOCK)), torch.uint8)
+    return codes, scales, R, K
+
+
+def fp8_matmul(a, b, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """gr_fp8_matmul: out [N, O] bf16 = A Bᵀ of a = (codes [N, K], scales [N, K/128]) in blocks of one row and
+    b = (codes [O, K], scales [O/128, K/128]) in blocks of 128 rows, as fp8_encode_blocks gives them."""
+    ac, asc, N, K = _fp8_pair(a, "a", (), 1)
+    bc, bsc, O, Kb = _fp8_pair(b, "b", (), BLOCK)
+    if K != Kb:
+        raise ValueError(f"a has {K} channels, b {Kb}")
+    out = _out(out, "out", (N, O), torch.bfloat16, ac, stream)
+    p = _product_desc(N, K, O)
+    wp, wn, _keep = _ws(_need("gr_fp8_matmul_workspace_size", p), workspace, ac, stream)
+    _call("gr_fp8_matmul", p, ac.data_ptr(), asc.data_ptr(), bc.data_ptr(), bsc.data_ptr(), out.data_ptr(),
+          wp, wn, _raw_stream(stream, ac, asc, bc, bsc, out, workspace))
+    return out
+
+
+def feed_forward_fp8(x: torch.Tensor, w_in, w_out, activation: str = "silu", y: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gr_feed_forward_fp8: feed_forward of x [N, D] bf16 on FP8 weights, w_in the (codes, scales) of
+    [2, F, D] and w_out those of [D, F] from fp8_encode_blocks(.., 128); x and the hidden values are encoded in
+    blocks of one row on the way. Returns y [N, D] bf16."""
+    ic, isc, F, D = _fp8_pair(w_in, "w_in", (2,), BLOCK)
+    oc, osc, Do, Fo = _fp8_pair(w_out, "w_out", (), BLOCK)
+    if x.dim() != 2 or (Do, Fo) != (D, F):
+        raise ValueError(f"x must be [N, {D}] and w_out [{D}, {F}]")
+    _like(x, "x", (x.shape[0], D), torch.bfloat16)
+    y = _out(y, "y", x.shape, torch.bfloat16, x, stream)
+    f = _feed(x, F, GR_FP8, activation)
+    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 0), workspace, x, stream)
+    _call("gr_feed_forward_fp8", f, x.data_ptr(), ic.data_ptr(), isc.data_ptr(), oc.data_ptr(), osc.data_ptr(),
+          y.data_ptr(), wp, wn, _raw_stream(stream, x, ic, isc, oc, osc, y, workspace))
+    return y
