@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "gr_internal.h"
+#include "gr_feed.h"
 #include "gr_mixer.h"
 
 namespace gr {
@@ -639,9 +640,9 @@ int gr_device_status(int clear) {
     if (st) return st;
     if (cudaDeviceSynchronize() != cudaSuccess) return GR_E_CUDA;
     const int v = fused_status(clear != 0), w = tiled_status(clear != 0);
-    const int m = mixer_status(clear != 0);
-    if (v < 0 || w < 0 || m < 0) return GR_E_CUDA;
-    return (v | w | m) ? GR_E_TIMEOUT : GR_OK;
+    const int m = mixer_status(clear != 0), f = feed_status(clear != 0);
+    if (v < 0 || w < 0 || m < 0 || f < 0) return GR_E_CUDA;
+    return (v | w | m | f) ? GR_E_TIMEOUT : GR_OK;
 }
 
 int gr_selftest_bounded_wait(int64_t limit_cycles, void* stream) {

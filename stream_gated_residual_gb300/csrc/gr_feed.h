@@ -37,6 +37,19 @@ cudaError_t simt_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, Fp8Ma
 cudaError_t simt_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, Fp8Matrix w_in, float* h,
                            cudaStream_t st);
 
+// Products on the tcgen05 tensor cores, bf16 (gr_feed_tc.cu); `ws` as tc_feed_workspace says. `tokens`: of a
+// product whose other dimensions are the weights' (few of them go in parts over k), else INT64_MAX. Each
+// tc_product is a programmatic dependent of the launch before it on `st`, which must be this file's.
+cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void* w_in, void* h, void* pre,
+                     float* ws, cudaStream_t st);
+cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, const void* w_out, const void* pre,
+                          void* dpre, void* h, float* ws, cudaStream_t st);
+cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const void* a, bool a_k, const void* b,
+                       bool b_k, void* out, float* ws, cudaStream_t st);
+size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient);
+// Status bits of the bounded waits of gr_feed_tc.cu (0 = none; -1 = could not be read).
+int feed_status(bool clear);
+
 #ifdef __CUDACC__
 // The activations and their slopes in fp32 with the accurate expf and erff.
 template <int ACT> __device__ __forceinline__ float activate(float g) {

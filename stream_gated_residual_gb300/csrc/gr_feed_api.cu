@@ -80,6 +80,7 @@ struct Parts {
 
 struct FeedParts {
     void *h = nullptr, *dpre = nullptr;              // gr_feed_forward and its gradient
+    float* parts = nullptr;                          // bf16: sums over ranges of k
     uint8_t *xc = nullptr, *xs = nullptr;            // FP8: x in blocks
     uint8_t *hc = nullptr, *hs = nullptr;            // and h
     size_t bytes = 0;
@@ -95,6 +96,8 @@ struct FeedParts {
         } else {
             h = w.take(N * F * width(f->dtype));
             if (gradient) dpre = w.take(2 * N * F * width(f->dtype));
+            if (f->dtype == GR_BF16 && N > 0)
+                parts = w.take<float>(tc_feed_workspace(f->n_tokens, f->d_model, f->d_ff, gradient));
         }
         bytes = w.used;
     }
@@ -130,6 +133,11 @@ int gr_feed_forward(const gr_feed* f, const void* x, const void* w_in, const voi
         return st;
     if ((st = usable_device())) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (f->dtype == GR_BF16) {
+        cudaError_t e = tc_gated(N, D, F, f->activation, x, w_in, p.h, pre, p.parts, s);
+        if (e == cudaSuccess) e = tc_product(N, D, F, N, p.h, true, w_out, true, y, p.parts, s);
+        return as_status(e);
+    }
     cudaError_t e = simt_gated(N, D, F, f->dtype, f->activation, x, w_in, p.h, pre, s);
     if (e == cudaSuccess) e = simt_product(N, D, F, f->dtype, p.h, true, w_out, true, y, s);
     return as_status(e);
@@ -152,6 +160,14 @@ int gr_feed_forward_backward(const gr_feed* f, const void* dy, const void* x, co
     if (N == 0) {
         cudaError_t e = cudaMemsetAsync(dw_in, 0, 2 * fd, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(dw_out, 0, fd, s);
+        return as_status(e);
+    }
+    if (f->dtype == GR_BF16) {
+        cudaError_t e = tc_gated_grad(N, D, F, f->activation, dy, w_out, pre, p.dpre, p.h, p.parts, s);
+        if (e == cudaSuccess) e = tc_product(N, D, 2 * F, N, p.dpre, true, w_in, false, dx, p.parts, s);
+        if (e == cudaSuccess)
+            e = tc_product(2 * F, D, N, INT64_MAX, p.dpre, false, x, false, dw_in, p.parts, s);
+        if (e == cudaSuccess) e = tc_product(D, F, N, INT64_MAX, dy, false, p.h, false, dw_out, p.parts, s);
         return as_status(e);
     }
     cudaError_t e = simt_gated_grad(N, D, F, f->dtype, f->activation, dy, w_out, pre, p.dpre, p.h, s);

@@ -42,7 +42,7 @@ def weights(D, F, dtype, seed=0):
 SIZES = [(1, 8, 8), (1, 256, 1024), (2, 2560, 1288), (5, 72, 4104), (16, 64, 128), (17, 136, 520), (33, 1000, 2728),
          (64, 512, 256), (127, 128, 640), (128, 264, 264), (129, 256, 2048), (200, 1032, 136), (256, 4096, 256),
          (257, 256, 512), (300, 2560, 1288), (511, 136, 3336), (700, 384, 1024), (1025, 512, 1160), (2305, 520, 776),
-         (4099, 264, 1032)]
+         (4099, 264, 1032), (3400, 1160, 1160), (301, 1800, 2056)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -267,11 +267,15 @@ def test_nothing_is_written_behind_the_outputs(N):
 
     made = [framed(N, D), framed(N, 2, F), framed(N, D), framed(2, F, D), framed(D, F)]
     y, p, dx, dwi, dwo = (t for _, t in made)
-    need = gr._need("gr_feed_workspace_size", gr._feed(x, F, gr.GR_BF16, "silu"), 1)
-    ws = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
-    gr.feed_forward(x, w_in, w_out, y=y, pre=p, workspace=ws[:need])
-    gr.feed_forward_backward(dy, x, w_in, w_out, pre, dx=dx, dw_in=dwi, dw_out=dwo, workspace=ws[:need])
-    assert (ws[need:] == 77).all()
+    feed = gr._feed(x, F, gr.GR_BF16, "silu")
+    for gradient in (0, 1):
+        need = gr._need("gr_feed_workspace_size", feed, gradient)
+        ws = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+        if gradient:
+            gr.feed_forward_backward(dy, x, w_in, w_out, pre, dx=dx, dw_in=dwi, dw_out=dwo, workspace=ws[:need])
+        else:
+            gr.feed_forward(x, w_in, w_out, y=y, pre=p, workspace=ws[:need])
+        assert (ws[need:] == 77).all()
     for buf, t in made:
         assert (buf[:pad] == 5).all() and (buf[pad + t.numel():] == 5).all()
 
