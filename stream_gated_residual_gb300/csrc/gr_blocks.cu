@@ -4,28 +4,11 @@
 // stay in registers between their maximum and their codes.
 #include "gr_feed.h"
 #include "gr_ptx.cuh"
+#include "gr_blocks.cuh"
 
 namespace gr {
 namespace {
 
-// Magnitudes compare as their bits do; infinity and NaN lie above every finite one.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// The biased exponent of a block from its largest magnitude's bits, and the factor 2^-e (0: not finite).
-__device__ __forceinline__ uint8_t block_scale(uint32_t top, float& inv) {
-    if (top >= 0x7f800000u) {
-        inv = 0.0f;
-        return 255;
-    }
-    const int e = fp8_block_exp(__uint_as_float(top));
-    inv = pow2f(-e);
-    return uint8_t(e + 127);
-}
-__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-    if (inv == 0.0f) return 0x7f7f7f7fu;
-    return uint32_t(f2_to_e4m3x2(v[0] * inv, v[1] * inv)) |
-           (uint32_t(f2_to_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
-}
 __device__ __forceinline__ void load16(const float* p, float (&v)[4]) {
     const float4 f = __ldg(reinterpret_cast<const float4*>(p));
     v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -40,10 +23,10 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[8]) {
     }
 }
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[4], float inv) {
-    *reinterpret_cast<uint32_t*>(p) = codes4(v, inv);
+    *reinterpret_cast<uint32_t*>(p) = block_codes4(v, inv);
 }
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], float inv) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+    *reinterpret_cast<uint2*>(p) = make_uint2(block_codes4(v, inv), block_codes4(v + 4, inv));
 }
 
 constexpr int kThreads = 256;
@@ -52,7 +35,8 @@ constexpr int kThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 encode_rows_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                   int64_t blocks, int64_t cols, int nb) {
+                   int64_t blocks, int64_t cols, int nb, int pitch) {
+    dep_launch_dependents();
     constexpr int kV = 16 / sizeof(T), kLanes = kBlock / kV;
     const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
@@ -62,13 +46,13 @@ encode_rows_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_t
     if (in) load16(m + row * cols + c, v);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) top = max(top, mag(v[i]));
+    for (int i = 0; i < kV; ++i) top = max(top, block_mag(v[i]));
 #pragma unroll
     for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
     float inv;
     const uint8_t s = block_scale(top, inv);
     if (in) store_codes(codes + row * cols + c, v, inv);
-    if (lane == 0 && at < blocks) scales[at] = s;
+    if (lane == 0 && at < blocks) scales[row * pitch + (at - row * nb)] = s;
 }
 
 // Blocks of 128 rows: a CTA each, 64 values a thread.
@@ -91,7 +75,7 @@ encode_tiles_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_
 #pragma unroll
     for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int j = 0; j < kV; ++j) top = max(top, mag(v[i][j]));
+        for (int j = 0; j < kV; ++j) top = max(top, block_mag(v[i][j]));
     top = __reduce_max_sync(~0u, top);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
     __syncthreads();
@@ -108,14 +92,14 @@ encode_tiles_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_
 
 template <typename T>
 cudaError_t encode(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, const T* m, uint8_t* codes,
-                   uint8_t* scales, cudaStream_t st) {
+                   uint8_t* scales, int pitch, cudaStream_t st) {
     const int64_t nb = ceil_div(cols, kBlock);
     int64_t grid;
     if (block_rows == 1) {
         const int64_t blocks = n_matrix * rows * nb;
         grid = ceil_div(blocks, kThreads / (kBlock / (16 / sizeof(T))));
         if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        encode_rows_kernel<<<unsigned(grid), kThreads, 0, st>>>(m, codes, scales, blocks, cols, int(nb));
+        encode_rows_kernel<<<unsigned(grid), kThreads, 0, st>>>(m, codes, scales, blocks, cols, int(nb), pitch);
     } else {
         const int64_t tiles_r = ceil_div(rows, kBlock);
         grid = n_matrix * tiles_r * nb;
@@ -128,10 +112,11 @@ cudaError_t encode(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows,
 }  // namespace
 
 cudaError_t launch_encode_blocks(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, int dtype,
-                                 const void* m, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-    return dtype == GR_F32 ? encode(n_matrix, rows, cols, block_rows, static_cast<const float*>(m), codes, scales, st)
+                                 const void* m, uint8_t* codes, uint8_t* scales, int pitch, cudaStream_t st) {
+    return dtype == GR_F32 ? encode(n_matrix, rows, cols, block_rows, static_cast<const float*>(m), codes, scales,
+                                    pitch, st)
                            : encode(n_matrix, rows, cols, block_rows, static_cast<const __nv_bfloat16*>(m), codes,
-                                    scales, st);
+                                    scales, pitch, st);
 }
 
 }  // namespace gr

@@ -17,9 +17,10 @@ struct Fp8Matrix {
     const uint8_t* scales;
 };
 
-// FP8 blocks of `n_matrix` matrices [rows][cols] (gr_blocks.cu).
+// FP8 blocks of `n_matrix` matrices [rows][cols] (gr_blocks.cu). pitch: bytes from one row's scales to the next's
+// (blocks of one row).
 cudaError_t launch_encode_blocks(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, int dtype,
-                                 const void* m, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+                                 const void* m, uint8_t* codes, uint8_t* scales, int pitch, cudaStream_t st);
 
 // Products on CUDA cores (gr_feed_simt.cu). dtype: GR_F32, GR_BF16.
 // h = act(x Wgᵀ) ⊙ (x Wuᵀ), pre [N][2][F] unless null.
@@ -31,12 +32,6 @@ cudaError_t simt_gated_grad(int64_t N, int D, int F, int dtype, int act, const v
 // out [M][N] = A Bᵀ over K. a_k, b_k: whether A is [M][K] (else [K][M]) and B [N][K] (else [K][N]).
 cudaError_t simt_product(int64_t M, int64_t N, int64_t K, int dtype, const void* a, bool a_k, const void* b,
                          bool b_k, void* out, cudaStream_t st);
-// The same on FP8 blocks: out [N][O] bf16; and h fp32 of the gated pair.
-cudaError_t simt_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, Fp8Matrix b, void* out,
-                             cudaStream_t st);
-cudaError_t simt_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, Fp8Matrix w_in, float* h,
-                           cudaStream_t st);
-
 // Products on the tcgen05 tensor cores, bf16 (gr_feed_tc.cu); `ws` as tc_feed_workspace says. `tokens`: of a
 // product whose other dimensions are the weights' (few of them go in parts over k), else INT64_MAX. Each
 // tc_product is a programmatic dependent of the launch before it on `st`, which must be this file's.
@@ -46,6 +41,13 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
                           void* dpre, void* h, float* ws, cudaStream_t st);
 cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const void* a, bool a_k, const void* b,
                        bool b_k, void* out, float* ws, cudaStream_t st);
+// On FP8 blocks: h in blocks of one row; out bf16. The pitches are those of scales of blocks of one row.
+cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, int x_pitch, Fp8Matrix w_in, uint8_t* h,
+                         uint8_t* hs, int hs_pitch, float* ws, cudaStream_t st, bool programmatic);
+cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, int a_pitch, Fp8Matrix b, void* out,
+                           float* ws, cudaStream_t st, bool programmatic);
+size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K);
+size_t tc_feed_fp8_workspace(int64_t N, int D, int F);
 size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient);
 // Status bits of the bounded waits of gr_feed_tc.cu (0 = none; -1 = could not be read).
 int feed_status(bool clear);

@@ -80,19 +80,22 @@ struct Parts {
 
 struct FeedParts {
     void *h = nullptr, *dpre = nullptr;              // gr_feed_forward and its gradient
-    float* parts = nullptr;                          // bf16: sums over ranges of k
+    float* parts = nullptr;                          // tensor cores: sums over ranges of k
     uint8_t *xc = nullptr, *xs = nullptr;            // FP8: x in blocks
     uint8_t *hc = nullptr, *hs = nullptr;            // and h
+    int xp = 0, hp = 0;                              // bytes of a row's scales
     size_t bytes = 0;
     FeedParts(const gr_feed* f, bool gradient, void* base) {
         Parts w{static_cast<char*>(base)};
         const size_t N = size_t(f->n_tokens), D = size_t(f->d_model), F = size_t(f->d_ff);
         if (f->dtype == GR_FP8) {
+            // rows of scales in whole words, as the products read them fastest
+            xp = int(ceil_div(ceil_div(D, kBlock), 4) * 4), hp = int(ceil_div(ceil_div(F, kBlock), 4) * 4);
             xc = w.take<uint8_t>(N * D);
-            xs = w.take<uint8_t>(N * ceil_div(D, kBlock));
+            xs = w.take<uint8_t>(N * xp);
             hc = w.take<uint8_t>(N * F);
-            hs = w.take<uint8_t>(N * ceil_div(F, kBlock));
-            h = w.take(N * F * 4);
+            hs = w.take<uint8_t>(N * hp);
+            if (N > 0) parts = w.take<float>(tc_feed_fp8_workspace(f->n_tokens, f->d_model, f->d_ff));
         } else {
             h = w.take(N * F * width(f->dtype));
             if (gradient) dpre = w.take(2 * N * F * width(f->dtype));
@@ -189,14 +192,15 @@ int gr_fp8_encode_blocks(const gr_blocks* b, const void* m, uint8_t* codes, uint
     if (meet(in, c) || meet(in, s) || meet(c, s)) return GR_E_ALIAS;
     if ((st = usable_device())) return st;
     return as_status(launch_encode_blocks(b->n_matrix, b->n_rows, b->n_cols, b->block_rows, b->dtype, m, codes,
-                                          scales, static_cast<cudaStream_t>(stream)));
+                                          scales, int(ceil_div(b->n_cols, kBlock)),
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 int gr_fp8_matmul_workspace_size(const gr_product* p, size_t* bytes) {
     const int st = check_product(p);
     if (st) return st;
     if (!bytes) return GR_E_NULL;
-    *bytes = 0;
+    *bytes = p->n_tokens == 0 ? 0 : tc_product_fp8_workspace(p->n_tokens, p->d_out, p->d_in);
     return GR_OK;
 }
 
@@ -207,11 +211,11 @@ int gr_fp8_matmul(const gr_product* p, const uint8_t* a, const uint8_t* a_scales
     if (p->n_tokens == 0) return GR_OK;
     const size_t N = size_t(p->n_tokens), K = size_t(p->d_in), O = size_t(p->d_out), nb = ceil_div(K, kBlock);
     if ((st = check_buffers({{a, N * K}, {b, O * K}}, {{a_scales, N * nb}, {b_scales, ceil_div(O, kBlock) * nb}},
-                            {{out, N * O * 2}}, {workspace, 0}, workspace_bytes)))
+                            {{out, N * O * 2}}, {workspace, tc_product_fp8_workspace(N, O, K)}, workspace_bytes)))
         return st;
     if ((st = usable_device())) return st;
-    return as_status(simt_product_fp8(N, O, K, {a, a_scales}, {b, b_scales}, out,
-                                      static_cast<cudaStream_t>(stream)));
+    return as_status(tc_product_fp8(N, O, K, {a, a_scales}, int(nb), {b, b_scales}, out,
+                                    static_cast<float*>(workspace), static_cast<cudaStream_t>(stream), false));
 }
 
 int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, const uint8_t* w_in_scales,
@@ -230,12 +234,12 @@ int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, co
         return st;
     if ((st = usable_device())) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_encode_blocks(1, N, D, 1, GR_BF16, x, p.xc, p.xs, s);
+    cudaError_t e = launch_encode_blocks(1, N, D, 1, GR_BF16, x, p.xc, p.xs, p.xp, s);
     if (e == cudaSuccess)
-        e = simt_gated_fp8(N, D, F, f->activation, {p.xc, p.xs}, {w_in, w_in_scales},
-                           static_cast<float*>(p.h), s);
-    if (e == cudaSuccess) e = launch_encode_blocks(1, N, F, 1, GR_F32, p.h, p.hc, p.hs, s);
-    if (e == cudaSuccess) e = simt_product_fp8(N, D, F, {p.hc, p.hs}, {w_out, w_out_scales}, y, s);
+        e = tc_gated_fp8(N, D, F, f->activation, {p.xc, p.xs}, p.xp, {w_in, w_in_scales}, p.hc, p.hs, p.hp, p.parts,
+                         s, true);
+    if (e == cudaSuccess)
+        e = tc_product_fp8(N, D, F, {p.hc, p.hs}, p.hp, {w_out, w_out_scales}, y, p.parts, s, true);
     return as_status(e);
 }
 

@@ -62,34 +62,6 @@ template <typename T> struct RowMajor {
         if (row < rows && at < k) load4(p + at * rows + row, v);
     }
 };
-__device__ __forceinline__ void decode4(const uint8_t* codes, uint8_t scale, float (&v)[4]) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(codes);
-    const float e = exp2f(float(scale) - 127.0f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(u >> (16 * i))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[2 * i] = f.x * e, v[2 * i + 1] = f.y * e;
-    }
-}
-template <int BR, bool PAIR> struct Fp8Rows {
-    static constexpr bool kContiguousK = true;
-    Fp8Matrix m;
-    int64_t rows, k;   // of one matrix
-    __device__ int64_t row(int64_t t0, int r) const {
-        if (!PAIR) return t0 + r < rows ? t0 + r : -1;
-        const int64_t c = (t0 >> 1) + (r & 63);
-        return c < rows ? c + (r >> 6) * rows : -1;
-    }
-    __device__ void get(int64_t row, int64_t at, float (&v)[4]) const {
-        if (row < 0 || at >= k) return;
-        const int64_t nb = (rows + BR - 1) / BR, which = row / rows;
-        const int64_t s = which * nb + (row - which * rows) / BR;
-        decode4(m.codes + row * k + at, m.scales[s * ((k + 127) / 128) + at / 128], v);
-    }
-};
-
 // What becomes of a thread's sums of row m, columns n..n+3 and n+64.. of the tile at n0.
 template <typename T> struct Store {
     T* out;
@@ -260,21 +232,6 @@ cudaError_t simt_product(int64_t M, int64_t N, int64_t K, int dtype, const void*
                          bool b_k, void* out, cudaStream_t st) {
     return dtype == GR_F32 ? product<float>(M, N, K, a, a_k, b, b_k, out, st)
                            : product<__nv_bfloat16>(M, N, K, a, a_k, b, b_k, out, st);
-}
-
-cudaError_t simt_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, Fp8Matrix b, void* out,
-                             cudaStream_t st) {
-    return run(Fp8Rows<1, false>{a, N, K}, Fp8Rows<kBlock, false>{b, O, K},
-               Store<__nv_bfloat16>{static_cast<__nv_bfloat16*>(out), O}, N, O, K, st);
-}
-
-cudaError_t simt_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, Fp8Matrix w_in, float* h,
-                           cudaStream_t st) {
-    const Fp8Rows<1, false> a{x, N, D};
-    const Fp8Rows<kBlock, true> b{w_in, F, D};
-    const int64_t n = ceil_div(F, 64) * 128;
-    return act == GR_SILU ? run(a, b, Gated<float, float, GR_SILU>{h, nullptr, F}, N, n, D, st)
-                          : run(a, b, Gated<float, float, GR_GELU>{h, nullptr, F}, N, n, D, st);
 }
 
 }  // namespace gr

@@ -12,6 +12,7 @@
 
 #include "gr_feed.h"
 #include "gr_ptx.cuh"
+#include "gr_blocks.cuh"
 #include "gr_tc.cuh"
 
 namespace gr {
@@ -75,6 +76,30 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block) {
     return d;
 }
 
+// ---- FP8 blocks: kind::mxf8f6f4 with a power-of-two scale for each row and 32 k ------------------
+// The scales lie in tensor memory: row r of 128 in column r / 32, lane r % 32 (of every quadrant), a byte for each
+// of four steps of k. Both operands e4m3; the descriptor names the byte.
+__device__ __forceinline__ uint32_t idesc_fp8(int N, int step) {
+    return (uint32_t(step) << 4) | (uint32_t(N >> 3) << 17) | (1u << 23) | (16u << 24) | (uint32_t(step) << 29);
+}
+__device__ __forceinline__ void tc_mma2_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::
+            "r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+// 512 bytes (the scales of 128 rows) of shared memory into four columns of every quadrant, in both CTAs.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFFu);
+    d |= uint64_t((128u >> 4) & 0x3FFFu) << 32;   // 8 rows of 16 bytes
+    d |= uint64_t(1u) << 46;
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
 // ---- what a launch computes ---------------------------------------------------------------------
 enum Mode {
     kStore,    // C as bf16
@@ -83,24 +108,42 @@ enum Mode {
     kPart,     // C's sums over a range of k, fp32, to the workspace
 };
 
+// Where the scale bytes of an operand's rows lie: `per` rows a matrix, `block` rows a scale row.
+struct Scales {
+    const uint8_t* p;
+    int64_t rows, per;
+    int block, pitch;
+    __device__ const uint8_t* at(int64_t row) const {
+        if (block == 1) return p + row * pitch;
+        const uint32_t r = uint32_t(row), m = uint32_t(per), which = r / m;
+        return p + int64_t(which * ((m + kBlock - 1) / kBlock) + (r - which * m) / kBlock) * pitch;
+    }
+};
+
 struct Args {
-    int nk;                 // blocks of 64 k
+    int nk;                 // blocks of 64 k (FP8: 128), 128 bytes of a row
     int tiles_m, tiles_n;   // of 256 x bn
     int bn;                 // columns of a tile: kPart 16 .. 256, else 256 (kGated: 128 channels)
     int group;              // row tiles that are taken together
     int stages;
     int act;
     int keep;               // kGated: write pre
-    int64_t total;          // kPart: tiles · nk, divided evenly among the pairs
+    int steps;              // kPart: nk in steps of one block (FP8: four, what a word of scales covers)
+    int64_t total;          // kPart: tiles · steps, divided evenly among the pairs
     int slots;              // kPart: partial tiles a pair may write
     float* part;
     int64_t rows, cols;     // of C (kGated: channels of h): boxes that start behind them are not stored
+    Scales sa, sb;          // FP8
+    uint8_t* hs;            // FP8 kGated: h's scales
+    int hs_pitch;
 };
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 320;      // FP8: a warp more
+constexpr uint32_t kColScales = 256;   // FP8: the scales' columns, behind the accumulators'
+constexpr int kScaleSlot = 512 + 1024; // of a step of four blocks: 128 rows of A, 256 of B
 constexpr int kTileM = 256, kRowsA = 128, kBoxA = kRowsA * 128;
 constexpr int kMaxStages = 12;
-constexpr int kAuxBytes = 512;
+constexpr int kAuxBytes = 512, kAuxFp8 = 512 + 2048 + 2 * kScaleSlot;
 constexpr int kSmemMax = 232448;
 
 // Staging for the outputs of a warp: kStore and kGated one box of 32 rows x 64 columns, twice; kGrad three boxes
@@ -112,15 +155,17 @@ __host__ __device__ constexpr int stage_out(int mode) {
 struct Aux {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2], done, loaded[8];
+    uint64_t scales_full[2], scales_empty[2], top_full[4];
     uint32_t tmem;
 };
 static_assert(sizeof(Aux) <= kAuxBytes, "aux");
+// FP8, behind it: the rows' largest magnitudes in the two halves of a block [2][2][128], then two slots of scales.
 
 // A pair's pieces of work, in the order all its roles go through them.
 struct Unit {
     int m, n, k0, k1;
 };
-template <int MODE> struct Units {
+template <int MODE, int STEP> struct Units {
     const Args& a;
     int pair, pairs;
     int64_t at, end;
@@ -132,11 +177,10 @@ template <int MODE> struct Units {
     __device__ bool next(Unit& u) {
         if (at >= end) return false;
         if constexpr (MODE == kPart) {
-            const int64_t t = at / a.nk;
-            u.k0 = int(at - t * a.nk);
-            u.k1 = int(min(int64_t(a.nk), u.k0 + end - at));
+            const int64_t t = at / a.steps, s0 = at - t * a.steps, s1 = min(int64_t(a.steps), s0 + end - at);
+            u.k0 = int(s0) * STEP, u.k1 = min(int(s1) * STEP, a.nk);
             u.m = int(t % a.tiles_m), u.n = int(t / a.tiles_m);
-            at += u.k1 - u.k0;
+            at += s1 - s0;
         } else {
             // groups of row tiles, so that the tiles in flight share rows of both operands in the L2
             const int64_t per = int64_t(a.group) * a.tiles_n, g = at / per, r = at - g * per;
@@ -179,8 +223,9 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
 // channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGated; kGrad: read); tmC2: dpre.
-template <int MODE, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
+template <int MODE, bool FP8, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
             const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ Args args) {
@@ -189,6 +234,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = kBoxA + box_b, stages = args.stages;
     uint8_t* out = sm + stages * stage;
     Aux& x = *reinterpret_cast<Aux*>(out + 8 * stage_out(MODE));
+    uint32_t* const tops = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&x) + kAuxBytes);
+    uint8_t* const sf = reinterpret_cast<uint8_t*>(tops + 512);
+    constexpr int kK = FP8 ? 128 : 64;
+    // The scales take columns behind 256: one accumulator of up to 256 columns, or two of 128.
+    const int accs = FP8 && args.bn > 128 ? 1 : 2, acc_cols = FP8 ? 128 : 256;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool first = rank == 0;
@@ -197,6 +247,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int s = 0; s < stages; ++s) mbar_init(&x.full[s], 1), mbar_init(&x.empty[s], 1);
         for (int b = 0; b < 2; ++b) mbar_init(&x.acc_full[b], 1), mbar_init(&x.acc_empty[b], 16);
         for (int w = 0; w < 8; ++w) mbar_init(&x.loaded[w], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&x.scales_full[i], 2), mbar_init(&x.scales_empty[i], 1);
+        for (int q = 0; q < 4; ++q) mbar_init(&x.top_full[q], 2);
         mbar_init(&x.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -210,7 +262,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     fence_async_global();
     dep_launch_dependents();
 
-    Units<MODE> units(args, int(cluster_id_x()), int(ncluster_x()));
+    Units<MODE, FP8 ? 4 : 1> units(args, int(cluster_id_x()), int(ncluster_x()));
     Unit u;
     if (warp == 0) {
         if (lane == 0) {
@@ -231,18 +283,18 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
                     uint8_t *pa = sm + s * stage, *pb = pa + kBoxA;
                     if constexpr (A_MN) {
-                        tma_pair_2d(pa, &tmA, m0, kb * 64, bar);
-                        tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * 64, bar);
+                        tma_pair_2d(pa, &tmA, m0, kb * kK, bar);
+                        tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar);
                     } else {
-                        tma_pair_2d(pa, &tmA, kb * 64, m0, bar);
+                        tma_pair_2d(pa, &tmA, kb * kK, m0, bar);
                     }
                     if constexpr (MODE == kGated) {
-                        tma_pair_3d(pb, &tmB, kb * 64, n0, int(rank), bar);
+                        tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar);
                     } else if constexpr (B_MN) {
                         for (int i = 0; i < rows_b; i += 64)
-                            tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * 64, bar);
+                            tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar);
                     } else {
-                        tma_pair_2d(pb, &tmB, kb * 64, n0, bar);
+                        tma_pair_2d(pb, &tmB, kb * kK, n0, bar);
                     }
                 }
             }
@@ -254,15 +306,26 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     } else if (warp == 1) {
         if (first && lane == 0) {
             const uint32_t idesc = idesc_bf16_f32(256, args.bn) | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0);
-            uint32_t g = 0;
+            uint32_t g = 0, q = 0;
             bool ok = true;
             for (int j = 0; ok && units.next(u); ++j) {
-                const int b = j & 1;
-                if (j >= 2 && !mbar_wait(&x.acc_empty[b], ((j >> 1) - 1) & 1)) break;
+                const int b = j % accs;
+                if (j >= accs && !mbar_wait(&x.acc_empty[b], (j / accs - 1) & 1)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + b * 256;
+                const uint32_t d = tmem + b * acc_cols;
                 for (int kb = u.k0; kb < u.k1; ++kb, ++g) {
-                    const uint32_t s = g % stages;
+                    const uint32_t s = g % stages, step = uint32_t(kb - u.k0) & 3;
+                    if (FP8 && step == 0) {
+                        // the scales of this and the next three blocks; the copies run in order with the MMAs
+                        if (!mbar_wait(&x.scales_full[q & 1], (q >> 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t at = smem_u32(sf) + (q & 1) * kScaleSlot, to = tmem + kColScales + (q & 1) * 16;
+                        for (int i = 0; i < 1 + (args.bn + 127) / 128; ++i) tc_copy_scales(to + i * 4, at + i * 512);
+                        ++q;
+                    }
                     if (!mbar_wait(&x.full[s], (g / stages) & 1)) {
                         ok = false;
                         break;
@@ -270,16 +333,93 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc_fence_after();
                     const uint32_t pa = smem_u32(sm + s * stage), pb = pa + kBoxA;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma2(d, A_MN ? sdesc_mn(pa + k * 2048, 8192) : sdesc_sw128(pa + k * 32),
-                                B_MN ? sdesc_mn(pb + k * 2048, 8192) : sdesc_sw128(pb + k * 32), idesc,
-                                kb > u.k0 || k > 0);
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (FP8) {
+                            const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
+                            tc_mma2_fp8(d, sdesc_sw128(pa + k * 32), sdesc_sw128(pb + k * 32),
+                                        idesc_fp8(args.bn, int(step)), sfa, sfa + 4, kb > u.k0 || k > 0);
+                        } else {
+                            tc_mma2(d, A_MN ? sdesc_mn(pa + k * 2048, 8192) : sdesc_sw128(pa + k * 32),
+                                    B_MN ? sdesc_mn(pb + k * 2048, 8192) : sdesc_sw128(pb + k * 32), idesc,
+                                    kb > u.k0 || k > 0);
+                        }
+                    }
                     tc_commit2(&x.empty[s]);
+                    if (FP8 && (step == 3 || kb + 1 == u.k1)) tc_commit2(&x.scales_empty[(q - 1) & 1]);
                 }
                 if (ok) tc_commit2(&x.acc_full[b]);
             }
             tc_commit2(&x.done);
             mbar_wait(&x.done, 0);
+        }
+    } else if (FP8 && warp == 10) {
+        // Scales: four bytes (blocks) of 128 rows of A and bn of B into shared memory, where row r's word lies at
+        // 16 (r % 32) + 4 (r / 32) of its 128 rows. The next step's are on their way while a slot is waited for.
+        struct Words {
+            uint32_t a[4], b[8];
+        };
+        const Scales &sa = args.sa, &sb = args.sb;
+        const bool whole_a = ((reinterpret_cast<uintptr_t>(sa.p) | sa.pitch) & 3) == 0;
+        const bool whole_b = ((reinterpret_cast<uintptr_t>(sb.p) | sb.pitch) & 3) == 0;
+        // a lane's rows of a tile: where their scales begin, null behind the last row
+        const uint8_t *pa[4], *pb[8];
+        auto find = [&](const Unit& t) {
+            const int64_t m0 = int64_t(t.m) * kTileM + rank * kRowsA;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = m0 + i * 32 + lane;
+                pa[i] = row < sa.rows ? sa.at(row) : nullptr;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 32 + lane;
+                int64_t row = int64_t(t.n) * args.bn + r;
+                if (MODE == kGated) {
+                    const int64_t ch = int64_t(t.n) * 128 + (r & 127);
+                    row = ch < sb.per ? ch + (r >> 7) * sb.per : sb.rows;
+                }
+                pb[i] = r < args.bn && row < sb.rows ? sb.at(row) : nullptr;
+            }
+        };
+        auto word = [&](const uint8_t* p, bool whole, int kb) -> uint32_t {
+            if (!p) return 0x7f7f7f7fu;
+            p += kb;
+            if (whole) return *reinterpret_cast<const uint32_t*>(p);   // within the padded row
+            uint32_t v = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (kb + i < args.nk) v |= uint32_t(p[i]) << (8 * i);
+            return v;
+        };
+        auto fetch = [&](int kb, Words& v) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.a[i] = word(pa[i], whole_a, kb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.b[i] = word(pb[i], whole_b, kb);
+        };
+        Words v;
+        uint32_t q = 0;
+        bool more = units.next(u);
+        int kb = u.k0;
+        if (more) find(u), fetch(kb, v);
+        while (more) {
+            const Words now = v;
+            kb += 4;
+            if (kb >= u.k1) {
+                more = units.next(u);
+                kb = u.k0;
+                if (more) find(u);
+            }
+            if (more) fetch(kb, v);
+            if (q >= 2 && !mbar_wait(&x.scales_empty[q & 1], ((q >> 1) - 1) & 1)) break;
+            const uint32_t at = smem_u32(sf) + (q & 1) * kScaleSlot + lane * 16;
+            st_shared16(at, make_uint4(now.a[0], now.a[1], now.a[2], now.a[3]));
+            st_shared16(at + 512, make_uint4(now.b[0], now.b[1], now.b[2], now.b[3]));
+            st_shared16(at + 1024, make_uint4(now.b[4], now.b[5], now.b[6], now.b[7]));
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) arrive_remote(map_rank(smem_u32(&x.scales_full[q & 1]), 0));
+            ++q;
         }
     } else {
         const int w = warp - 2, half = w >> 2, quad = warp & 3;
@@ -301,11 +441,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (MODE == kGrad && more)
             load_pre(u.m * kTileM + int(rank) * kRowsA + quad * 32, u.n * 256 + half * 128);
         for (int j = 0; more; ++j) {
-            const int b = j & 1;
+            const int b = j % accs;
             const Unit now = u;
-            if (!mbar_wait(&x.acc_full[b], (j >> 1) & 1)) break;
+            if (!mbar_wait(&x.acc_full[b], (j / accs) & 1)) break;
             tc_fence_after();
-            const uint32_t acc = tmem + b * 256 + lanes;
+            const uint32_t acc = tmem + b * acc_cols + lanes;
             const int row = now.m * kTileM + int(rank) * kRowsA + quad * 32;   // the warp's first
             auto drained = [&]() {
                 tc_fence_before();
@@ -369,7 +509,36 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                     for (int i = 0; i < 64; ++i) ga[i] = activate<GR_GELU>(ga[i]) * up[i];
                 }
-                if (in) put_box(ga, [&] { tma_store_2d(&tmC0, minep, col, row); });
+                if constexpr (FP8) {
+                    // the block's largest magnitude: this half's and the other's, from the warp that has the same rows
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) top = max(top, block_mag(ga[i]));
+                    uint32_t* t = tops + (j & 1) * 256 + quad * 32 + lane;
+                    t[half * 128] = top;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x.top_full[quad]);
+                    if (!mbar_wait(&x.top_full[quad], j & 1)) break;
+                    top = max(top, *const_cast<volatile uint32_t*>(t + (half ^ 1) * 128));
+                    float inv;
+                    const uint8_t e = block_scale(top, inv);
+                    if (half == 0 && row + lane < args.rows)
+                        args.hs[int64_t(row + lane) * args.hs_pitch + now.n] = e;
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        st_shared16(mine + swz64(lane, c),
+                                    make_uint4(block_codes4(ga + 16 * c, inv), block_codes4(ga + 16 * c + 4, inv),
+                                               block_codes4(ga + 16 * c + 8, inv),
+                                               block_codes4(ga + 16 * c + 12, inv)));
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && in && row < args.rows) {
+                        tma_store_2d(&tmC0, minep, col, row);
+                        bulk_commit();
+                    }
+                } else if (in) put_box(ga, [&] { tma_store_2d(&tmC0, minep, col, row); });
             } else if constexpr (MODE == kGrad) {
                 const int col = now.n * 256 + half * 128;
                 more = units.next(u);
@@ -462,26 +631,28 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // ---- the sums of the pairs' parts ---------------------------------------------------------------
 // C's tile t of kPart is spread over the pairs whose ranges of k meet it, in order; a pair's slots hold its tiles
 // [column][256 rows]. Four rows of a column a thread, rows contiguous in the output.
-enum Join { kJoinStore, kJoinGated, kJoinGrad };
+enum Join { kJoinStore, kJoinGated, kJoinGrad, kJoinGatedFp8 };
 
 struct JoinArgs {
     const float* part;
     int64_t total, rows, cols;   // of the output (kJoinGated: channels)
-    int nk, tiles_m, bn, slots, pairs, act;
+    int steps, tiles_m, bn, slots, pairs, act;
     __nv_bfloat16 *out, *pre_out;
     const __nv_bfloat16* pre;
     __nv_bfloat16* dpre;
+    uint8_t *codes, *scales;     // kJoinGatedFp8: h
+    int pitch;
 };
 
 __device__ __forceinline__ float4 joined(const JoinArgs& a, int64_t row, int64_t col) {
-    const int64_t tn = col / a.bn, t = tn * a.tiles_m + row / kTileM, k0 = t * a.nk;
+    const int64_t tn = col / a.bn, t = tn * a.tiles_m + row / kTileM, k0 = t * a.steps;
     const int64_t at = (col - tn * a.bn) * kTileM + row % kTileM, tile = int64_t(kTileM) * a.bn;
     int64_t c = ((k0 + 1) * a.pairs - 1) / a.total;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (; c < a.pairs; ++c) {
         const int64_t begin = a.total * c / a.pairs;
-        if (begin >= k0 + a.nk) break;
-        const int64_t slot = c * a.slots + (t - begin / a.nk);
+        if (begin >= k0 + a.steps) break;
+        const int64_t slot = c * a.slots + (t - begin / a.steps);
         const float4 v = __ldcs(reinterpret_cast<const float4*>(a.part + slot * tile + at));
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
@@ -535,6 +706,30 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     }
 }
 
+// h in blocks of 128 channels of a column, a warp each.
+__global__ void __launch_bounds__(256) join_fp8_kernel(const __grid_constant__ JoinArgs a) {
+    dep_wait();
+    dep_launch_dependents();
+    const int nb = int((a.rows + kBlock - 1) / kBlock);
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 32;
+    if (i >= a.cols * nb) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t col = i / nb, row = (i - col * nb) * kBlock + lane * 4;
+    float h[4] = {};
+    if (row < a.rows) {
+        const float4 s = joined(a, row, col), p = joined(a, a.rows + row, col);
+        const float g[4] = {s.x, s.y, s.z, s.w}, up[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = act_of(a.act, g[k]) * up[k];
+    }
+    uint32_t top = max(max(block_mag(h[0]), block_mag(h[1])), max(block_mag(h[2]), block_mag(h[3])));
+    top = __reduce_max_sync(~0u, top);
+    float inv;
+    const uint8_t e = block_scale(top, inv);
+    if (row < a.rows) *reinterpret_cast<uint32_t*>(a.codes + col * a.rows + row) = block_codes4(h, inv);
+    if (lane == 0) a.scales[col * a.pitch + (i - col * nb)] = e;
+}
+
 // ---- host ---------------------------------------------------------------------------------------
 bool map_box(CUtensorMap* m, CUtensorMapDataType type, const void* p, int nd, const cuuint64_t* dims,
              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
@@ -559,6 +754,20 @@ bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t co
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_b), cuuint32_t(box_a)};
     return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, strides, box,
                    box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Codes [rows][cols] in boxes of 128 (64: h's) columns.
+bool map_codes(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows, int box_cols) {
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(cols)};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    return map_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 2, dims, strides, box,
+                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool map_codes_pair(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), 2};
+    const cuuint64_t strides[2] = {cuuint64_t(cols), cuuint64_t(cols * rows)};
+    const cuuint32_t box[3] = {128, 128, 1};
+    return map_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <typename... KArgs, typename... Args>
@@ -589,34 +798,41 @@ struct Operand {
     int64_t rows;
 };
 
-template <int MODE>
+template <int MODE, bool FP8>
 int stages_for(int bn) {
     const int stage = kBoxA + bn / 2 * 128;
-    const int room = (kSmemMax - 1024 - kAuxBytes - 8 * stage_out(MODE)) / stage;
+    const int room = (kSmemMax - 1024 - (FP8 ? kAuxFp8 : kAuxBytes) - 8 * stage_out(MODE)) / stage;
     return room > kMaxStages ? kMaxStages : room;
 }
 
-template <int MODE, bool A_MN, bool B_MN>
+template <int MODE, bool FP8, bool A_MN, bool B_MN>
 cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, Args args, int pairs, const CUtensorMap& c0,
                          const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic) {
     CUtensorMap ma, mb;
     const int rows_b = args.bn / 2;
-    bool ok = A_MN ? map_bf16(&ma, a.p, K, a.rows, 64, 64) : map_bf16(&ma, a.p, a.rows, K, kRowsA, 64);
-    if (MODE == kGated)
-        ok = ok && map_bf16_3d(&mb, b.p, 2, b.rows, K, 1, 128, 64);
-    else
-        ok = ok && (B_MN ? map_bf16(&mb, b.p, K, b.rows, 64, 64) : map_bf16(&mb, b.p, b.rows, K, rows_b, 64));
+    bool ok;
+    if constexpr (FP8) {
+        ok = map_codes(&ma, a.p, a.rows, K, kRowsA, 128) &&
+             (MODE == kGated ? map_codes_pair(&mb, b.p, b.rows, K) : map_codes(&mb, b.p, b.rows, K, rows_b, 128));
+    } else {
+        ok = A_MN ? map_bf16(&ma, a.p, K, a.rows, 64, 64) : map_bf16(&ma, a.p, a.rows, K, kRowsA, 64);
+        if (MODE == kGated)
+            ok = ok && map_bf16_3d(&mb, b.p, 2, b.rows, K, 1, 128, 64);
+        else
+            ok = ok && (B_MN ? map_bf16(&mb, b.p, K, b.rows, 64, 64) : map_bf16(&mb, b.p, b.rows, K, rows_b, 64));
+    }
     if (!ok) return cudaErrorInvalidValue;
-    args.stages = stages_for<MODE>(args.bn);
-    const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE) + kAuxBytes;
-    return launch(pair_kernel<MODE, A_MN, B_MN>, unsigned(2 * pairs), kThreads, smem, st, programmatic, ma, mb, c0,
-                  c1, c2, args);
+    args.stages = stages_for<MODE, FP8>(args.bn);
+    const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE) +
+                        (FP8 ? kAuxFp8 : kAuxBytes);
+    return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
+                  programmatic, ma, mb, c0, c1, c2, args);
 }
 
 // ---- whole tiles ----
-Args whole(int64_t rows, int64_t cols, int64_t K, int per_tile) {
+Args whole(int64_t rows, int64_t cols, int64_t K, int per_tile, int kk = 64) {
     Args a{};
-    a.nk = int(ceil_div(K, 64));
+    a.nk = int(ceil_div(K, kk));
     a.tiles_m = int(ceil_div(rows, kTileM));
     a.tiles_n = int(ceil_div(cols, per_tile));
     a.bn = 256;
@@ -634,30 +850,35 @@ struct Parts {
     int pairs = 0;
     size_t bytes = 0;
 };
-// C [rows][cols] over K in parts: the tiles' columns as even as the steps of 16 (128) allow, k divided among the
-// pairs in ranges of at least four blocks.
-Parts parts_of(int64_t rows, int64_t cols, int64_t K, int step) {
+// C [rows][cols] over K in parts: the tiles' columns as even as the steps of 16 (FP8: 32; 128) allow, k divided among
+// the pairs in ranges of at least four blocks.
+Parts parts_of(int64_t rows, int64_t cols, int64_t K, int step, bool fp8 = false) {
     Parts p;
-    p.a.nk = int(ceil_div(K, 64));
+    p.a.nk = int(ceil_div(K, fp8 ? 128 : 64));
+    p.a.steps = fp8 ? int(ceil_div(p.a.nk, 4)) : p.a.nk;
     p.a.tiles_m = int(ceil_div(rows, kTileM));
     p.a.tiles_n = int(ceil_div(cols, 256));
     p.a.bn = int(ceil_div(ceil_div(cols, p.a.tiles_n), step) * step);
     p.a.tiles_n = int(ceil_div(cols, p.a.bn));
-    p.a.total = int64_t(p.a.tiles_m) * p.a.tiles_n * p.a.nk;
-    const int64_t most = ceil_div(p.a.total, 4);
+    p.a.total = int64_t(p.a.tiles_m) * p.a.tiles_n * p.a.steps;
+    const int64_t most = fp8 ? p.a.total : ceil_div(p.a.total, 4);
     p.pairs = int(most < pairs_of() ? most : pairs_of());
-    p.a.slots = int(ceil_div(ceil_div(p.a.total, p.pairs), p.a.nk)) + 1;
+    p.a.slots = int(ceil_div(ceil_div(p.a.total, p.pairs), p.a.steps)) + 1;
     p.bytes = size_t(p.pairs) * p.a.slots * kTileM * p.a.bn * 4;
     return p;
 }
 
-template <int JOIN>
-cudaError_t join(const Parts& p, float* ws, int64_t rows, int64_t cols, int act, void* out, const void* pre,
-                 void* pre_out, void* dpre, cudaStream_t st) {
+JoinArgs join_args(const Parts& p, float* ws, int64_t rows, int64_t cols, int act) {
     JoinArgs j{};
     j.part = ws;
     j.total = p.a.total, j.rows = rows, j.cols = cols;
-    j.nk = p.a.nk, j.tiles_m = p.a.tiles_m, j.bn = p.a.bn, j.slots = p.a.slots, j.pairs = p.pairs, j.act = act;
+    j.steps = p.a.steps, j.tiles_m = p.a.tiles_m, j.bn = p.a.bn, j.slots = p.a.slots, j.pairs = p.pairs, j.act = act;
+    return j;
+}
+template <int JOIN>
+cudaError_t join(const Parts& p, float* ws, int64_t rows, int64_t cols, int act, void* out, const void* pre,
+                 void* pre_out, void* dpre, cudaStream_t st) {
+    JoinArgs j = join_args(p, ws, rows, cols, act);
     j.out = static_cast<__nv_bfloat16*>(out);
     j.pre_out = static_cast<__nv_bfloat16*>(pre_out);
     j.pre = static_cast<const __nv_bfloat16*>(pre);
@@ -682,12 +903,12 @@ cudaError_t product(const void* a, const void* b, void* out, int64_t M, int64_t 
         CUtensorMap c;
         if (!map_bf16(&c, out, M, N, 32, 64)) return cudaErrorInvalidValue;
         w.rows = M, w.cols = N;
-        return launch_pairs<kStore, !A_K, !B_K>({a, M}, {b, N}, K, w, pairs_for(w), c, kNone, kNone, st,
+        return launch_pairs<kStore, false, !A_K, !B_K>({a, M}, {b, N}, K, w, pairs_for(w), c, kNone, kNone, st,
                                                 programmatic);
     }
     Parts p = parts_of(N, M, K, A_K ? 16 : 128);
     p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, !B_K, !A_K>({b, N}, {a, M}, K, p.a, p.pairs, kNone, kNone, kNone, st,
+    const cudaError_t e = launch_pairs<kPart, false, !B_K, !A_K>({b, N}, {a, M}, K, p.a, p.pairs, kNone, kNone, kNone, st,
                                                           programmatic);
     return e != cudaSuccess ? e : join<kJoinStore>(p, ws, N, M, 0, out, nullptr, nullptr, nullptr, st);
 }
@@ -705,11 +926,11 @@ cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void
         if (!map_bf16(&c, h, N, F, 32, 64) || (pre && !map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 64)))
             return cudaErrorInvalidValue;
         w.rows = N, w.cols = F, w.act = act, w.keep = pre != nullptr;
-        return launch_pairs<kGated, false, false>({x, N}, {w_in, F}, D, w, pairs_for(w), c, cp, kNone, st, false);
+        return launch_pairs<kGated, false, false, false>({x, N}, {w_in, F}, D, w, pairs_for(w), c, cp, kNone, st, false);
     }
     Parts p = parts_of(2 * int64_t(F), N, D, 16);
     p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, false, false>({w_in, 2 * int64_t(F)}, {x, N}, D, p.a, p.pairs, kNone,
+    const cudaError_t e = launch_pairs<kPart, false, false, false>({w_in, 2 * int64_t(F)}, {x, N}, D, p.a, p.pairs, kNone,
                                                             kNone, kNone, st, false);
     return e != cudaSuccess ? e : join<kJoinGated>(p, ws, F, N, act, h, nullptr, pre, nullptr, st);
 }
@@ -723,11 +944,11 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
             !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32))
             return cudaErrorInvalidValue;
         w.rows = N, w.cols = F, w.act = act;
-        return launch_pairs<kGrad, false, true>({dy, N}, {w_out, F}, D, w, pairs_for(w), c, cp, cd, st, false);
+        return launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, w, pairs_for(w), c, cp, cd, st, false);
     }
     Parts p = parts_of(F, N, D, 16);
     p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, true, false>({w_out, F}, {dy, N}, D, p.a, p.pairs, kNone, kNone,
+    const cudaError_t e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p.a, p.pairs, kNone, kNone,
                                                            kNone, st, false);
     return e != cudaSuccess ? e : join<kJoinGrad>(p, ws, F, N, act, h, pre, nullptr, dpre, st);
 }
@@ -738,6 +959,57 @@ cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const vo
         return b_k ? product<true, true>(a, b, out, M, N, K, tokens, ws, st, true)
                    : product<true, false>(a, b, out, M, N, K, tokens, ws, st, true);
     return b_k ? cudaErrorInvalidValue : product<false, false>(a, b, out, M, N, K, tokens, ws, st, true);
+}
+
+// ---- FP8 ----
+cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, int x_pitch, Fp8Matrix w_in, uint8_t* h,
+                         uint8_t* hs, int hs_pitch, float* ws, cudaStream_t st, bool programmatic) {
+    const int db = int(ceil_div(D, kBlock));
+    const Scales sx{x.scales, N, N, 1, x_pitch}, sw{w_in.scales, 2 * int64_t(F), F, kBlock, db};
+    Args w = whole(N, F, D, 128, 128);
+    if (!in_parts(N, w)) {
+        CUtensorMap c;
+        if (!map_codes(&c, h, N, F, 32, 64)) return cudaErrorInvalidValue;
+        w.rows = N, w.cols = F, w.act = act, w.sa = sx, w.sb = sw, w.hs = hs, w.hs_pitch = hs_pitch;
+        return launch_pairs<kGated, true, false, false>({x.codes, N}, {w_in.codes, F}, D, w, pairs_for(w), c, kNone,
+                                                        kNone, st, programmatic);
+    }
+    Parts p = parts_of(2 * int64_t(F), N, D, 32, true);
+    p.a.part = ws, p.a.sa = sw, p.a.sb = sx;
+    cudaError_t e = launch_pairs<kPart, true, false, false>({w_in.codes, 2 * int64_t(F)}, {x.codes, N}, D, p.a,
+                                                            p.pairs, kNone, kNone, kNone, st, programmatic);
+    if (e != cudaSuccess) return e;
+    JoinArgs j = join_args(p, ws, F, N, act);
+    j.codes = h, j.scales = hs, j.pitch = hs_pitch;
+    return launch(join_fp8_kernel, unsigned(ceil_div(N * ceil_div(F, kBlock), 8)), 256, 0, st, true, j);
+}
+
+cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, int a_pitch, Fp8Matrix b, void* out,
+                           float* ws, cudaStream_t st, bool programmatic) {
+    const int kb = int(ceil_div(K, kBlock));
+    const Scales sa{a.scales, N, N, 1, a_pitch}, sb{b.scales, O, O, kBlock, kb};
+    Args w = whole(N, O, K, 256, 128);
+    if (!in_parts(N, w)) {
+        CUtensorMap c;
+        if (!map_bf16(&c, out, N, O, 32, 64)) return cudaErrorInvalidValue;
+        w.rows = N, w.cols = O, w.sa = sa, w.sb = sb;
+        return launch_pairs<kStore, true, false, false>({a.codes, N}, {b.codes, O}, K, w, pairs_for(w), c, kNone,
+                                                        kNone, st, programmatic);
+    }
+    Parts p = parts_of(O, N, K, 32, true);
+    p.a.part = ws, p.a.sa = sb, p.a.sb = sa;
+    const cudaError_t e = launch_pairs<kPart, true, false, false>({b.codes, O}, {a.codes, N}, K, p.a, p.pairs, kNone,
+                                                                  kNone, kNone, st, programmatic);
+    return e != cudaSuccess ? e : join<kJoinStore>(p, ws, O, N, 0, out, nullptr, nullptr, nullptr, st);
+}
+
+size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K) {
+    return in_parts(N, whole(N, O, K, 256, 128)) ? parts_of(O, N, K, 32, true).bytes : 0;
+}
+size_t tc_feed_fp8_workspace(int64_t N, int D, int F) {
+    const size_t down = tc_product_fp8_workspace(N, D, F);
+    const size_t in = in_parts(N, whole(N, F, D, 128, 128)) ? parts_of(2 * int64_t(F), N, D, 32, true).bytes : 0;
+    return in > down ? in : down;
 }
 
 size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient) {

@@ -174,7 +174,7 @@ def test_encode_of_what_is_not_finite(value, rows, dtype):
 @pytest.mark.parametrize("N,K,O", [(1, 16, 8), (1, 4096, 512), (3, 144, 136), (16, 128, 128), (17, 1040, 264),
                                    (64, 512, 1024), (100, 272, 2056), (128, 4096, 256), (129, 528, 520), (255, 2560, 128),
                                    (256, 640, 1032), (257, 1168, 384), (600, 512, 2560), (1111, 1040, 1288),
-                                   (3000, 656, 776)])
+                                   (3000, 656, 776), (3400, 400, 1160), (3400, 1040, 1096)])
 def test_fp8_matmul(N, K, O):
     a = gr.fp8_encode_blocks(randn(N, N, K) * torch.exp2(3 * randn(K, N, 1)))
     b = gr.fp8_encode_blocks(randn(O, O, K) * torch.exp2(2 * randn(1, -(-O // 128), 1)).repeat_interleave(128, 0)[:O],
@@ -199,7 +199,7 @@ def test_fp8_matmul_of_nan_blocks():
 
 @pytest.mark.parametrize("i,size", list(enumerate([
     (1, 16, 16), (1, 256, 1024), (3, 2560, 1296), (16, 64, 128), (33, 144, 400), (64, 1024, 512), (127, 272, 640),
-    (128, 512, 272), (200, 1040, 2064), (257, 256, 512), (500, 528, 784), (1030, 384, 1168), (2300, 272, 656)])))
+    (128, 512, 272), (200, 1040, 2064), (257, 256, 512), (500, 528, 784), (1030, 384, 1168), (2300, 272, 656), (4400, 1168, 1040)])))
 def test_feed_forward_fp8(i, size):
     N, D, F = size
     name = ("silu", "gelu")[i % 2]
