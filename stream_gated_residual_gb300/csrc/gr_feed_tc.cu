@@ -128,14 +128,30 @@ struct Args {
     int stages;
     int act;
     int keep;               // kGated: write pre
-    int steps;              // kPart: nk in steps of one block (FP8: four, what a word of scales covers)
-    int64_t total;          // kPart: tiles · steps, divided evenly among the pairs
-    int slots;              // kPart: partial tiles a pair may write
+    int early;              // A is not the launch before's: its first stages are read ahead of it
+    // Tiles 0 .. whole - 1 are done by a pair each; the others' steps of k, one after another, in even ranges
+    uint32_t whole;
+    uint32_t steps;         // of a tile: nk in steps of one block (FP8: four, what a word of scales covers)
+    uint32_t range, longer; // steps of a range; the first `longer` have one more
+    int slots;              // partial tiles a pair may write
     float* part;
     int64_t rows, cols;     // of C (kGated: channels of h): boxes that start behind them are not stored
     Scales sa, sb;          // FP8
     uint8_t* hs;            // FP8 kGated: h's scales
     int hs_pitch;
+    const __nv_bfloat16* pre;   // kGrad
+    __host__ __device__ uint32_t begin(uint32_t pair) const { return pair * range + (pair < longer ? pair : longer); }
+    // The pair whose range holds a step.
+    __device__ uint32_t owner(uint32_t step) const {
+        const uint32_t split = longer * (range + 1);
+        return step < split ? step / (range + 1) : longer + (step - split) / range;
+    }
+    // Tile t's place: groups of row tiles, so that the tiles in flight share rows of both operands in the L2.
+    __device__ void place(uint32_t t, int& m, int& n) const {
+        const uint32_t per = uint32_t(group) * uint32_t(tiles_n), g = t / per, r = t - g * per;
+        const uint32_t rows = min(uint32_t(group), uint32_t(tiles_m) - g * group);
+        n = int(r / rows), m = int(g * group + r % rows);
+    }
 };
 
 constexpr int kThreads = 320;      // FP8: a warp more
@@ -143,7 +159,8 @@ constexpr uint32_t kColScales = 256;   // FP8: the scales' columns, behind the a
 constexpr int kScaleSlot = 512 + 1024; // of a step of four blocks: 128 rows of A, 256 of B
 constexpr int kTileM = 256, kRowsA = 128, kBoxA = kRowsA * 128;
 constexpr int kMaxStages = 12;
-constexpr int kAuxBytes = 512, kAuxFp8 = 512 + 2048 + 2 * kScaleSlot;
+constexpr int kScaleSlots = 4;
+constexpr int kAuxBytes = 512, kAuxFp8 = 512 + 2048 + kScaleSlots * kScaleSlot;
 constexpr int kSmemMax = 232448;
 
 // Staging for the outputs of a warp: kStore and kGated one box of 32 rows x 64 columns, twice; kGrad three boxes
@@ -154,42 +171,37 @@ __host__ __device__ constexpr int stage_out(int mode) {
 
 struct Aux {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2], done, loaded[8];
-    uint64_t scales_full[2], scales_empty[2], top_full[4];
+    uint64_t acc_full[2], acc_empty[2], done;
+    uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots], top_full[4];
     uint32_t tmem;
 };
 static_assert(sizeof(Aux) <= kAuxBytes, "aux");
-// FP8, behind it: the rows' largest magnitudes in the two halves of a block [2][2][128], then two slots of scales.
+// FP8, behind it: the rows' largest magnitudes in the two halves of a block [2][2][128], then the slots of scales.
 
 // A pair's pieces of work, in the order all its roles go through them.
 struct Unit {
     int m, n, k0, k1;
+    int slot;   // of the pair's partial tiles; -1: a whole tile
 };
-template <int MODE, int STEP> struct Units {
+template <int STEP> struct Units {
     const Args& a;
-    int pair, pairs;
-    int64_t at, end;
-    int j = 0;
-    __device__ Units(const Args& a, int pair, int pairs) : a(a), pair(pair), pairs(pairs) {
-        at = MODE == kPart ? a.total * pair / pairs : pair;
-        end = MODE == kPart ? a.total * (pair + 1) / pairs : int64_t(a.tiles_m) * a.tiles_n;
-    }
+    uint32_t tile, pairs, at, end;
+    int slot = 0;
+    __device__ Units(const Args& a, uint32_t pair, uint32_t pairs)
+        : a(a), tile(pair), pairs(pairs), at(a.begin(pair)), end(a.begin(pair + 1)) {}
     __device__ bool next(Unit& u) {
-        if (at >= end) return false;
-        if constexpr (MODE == kPart) {
-            const int64_t t = at / a.steps, s0 = at - t * a.steps, s1 = min(int64_t(a.steps), s0 + end - at);
-            u.k0 = int(s0) * STEP, u.k1 = min(int(s1) * STEP, a.nk);
-            u.m = int(t % a.tiles_m), u.n = int(t / a.tiles_m);
-            at += s1 - s0;
-        } else {
-            // groups of row tiles, so that the tiles in flight share rows of both operands in the L2
-            const int64_t per = int64_t(a.group) * a.tiles_n, g = at / per, r = at - g * per;
-            const int rows = min(a.group, a.tiles_m - int(g) * a.group);
-            u.m = int(g) * a.group + int(r % rows), u.n = int(r / rows);
-            u.k0 = 0, u.k1 = a.nk;
-            at += pairs;
+        if (tile < a.whole) {
+            a.place(tile, u.m, u.n);
+            u.k0 = 0, u.k1 = a.nk, u.slot = -1;
+            tile += pairs;
+            return true;
         }
-        ++j;
+        if (at >= end) return false;
+        const uint32_t t = at / a.steps, s0 = at - t * a.steps, s1 = min(a.steps, s0 + end - at);
+        a.place(a.whole + t, u.m, u.n);
+        u.k0 = int(s0) * STEP, u.k1 = min(int(s1) * STEP, a.nk);
+        u.slot = slot++;
+        at += s1 - s0;
         return true;
     }
 };
@@ -197,20 +209,27 @@ template <int MODE, int STEP> struct Units {
 __device__ __forceinline__ void pack8(uint4& v, const float (&f)[8]) {
     v = make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
 }
+// σ(g) of a value whose product is rounded to bf16 or coarser: exp by the hardware's 2^x, off by (2 + |g|) units, and a
+// division that gives 0 where 1 + exp(-g) is above 2^126.
+__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// f(g) and f'(g)
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& slope) {
+    if (act == GR_SILU) {
+        const float s = fast_sigmoid(g);
+        a = g * s;
+        slope = fmaf(a, 1.0f - s, s);
+    } else {
+        const float below = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        a = g * below;
+        slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), below);
+    }
+}
 __device__ __forceinline__ float act_of(int act, float g) {
-    return act == GR_SILU ? activate<GR_SILU>(g) : activate<GR_GELU>(g);
+    return act == GR_SILU ? g * fast_sigmoid(g) : activate<GR_GELU>(g);
 }
 __device__ __forceinline__ void st_shared16(uint32_t at, const uint4& v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
 }
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -222,7 +241,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 }
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
-// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGated; kGrad: read); tmC2: dpre.
+// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGated); tmC2: dpre.
 // FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
@@ -246,8 +265,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&x.full[s], 1), mbar_init(&x.empty[s], 1);
         for (int b = 0; b < 2; ++b) mbar_init(&x.acc_full[b], 1), mbar_init(&x.acc_empty[b], 16);
-        for (int w = 0; w < 8; ++w) mbar_init(&x.loaded[w], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&x.scales_full[i], 2), mbar_init(&x.scales_empty[i], 1);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&x.scales_full[i], 2), mbar_init(&x.scales_empty[i], 1);
         for (int q = 0; q < 4; ++q) mbar_init(&x.top_full[q], 2);
         mbar_init(&x.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -257,19 +275,50 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = x.tmem;
-    // what the launches before this one wrote is read from here on
-    dep_wait();
-    fence_async_global();
+    // The next launch may start as soon as there is room: it waits for this one's end in its turn. What the launch
+    // before wrote (or still reads) is touched after dep_wait only.
     dep_launch_dependents();
+    if (warp != 0) dep_wait();
 
-    Units<MODE, FP8 ? 4 : 1> units(args, int(cluster_id_x()), int(ncluster_x()));
+    Units<FP8 ? 4 : 1> units(args, cluster_id_x(), ncluster_x());
     Unit u;
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t bytes = 2u * uint32_t(stage);
             uint32_t g = 0;
             bool ok = true;
-            while (ok && units.next(u)) {
+            auto load_a = [&](uint32_t s, int m0, int kb) {
+                // the first CTA's barrier counts both CTAs' bytes
+                if (first) mbar_expect_tx(&x.full[s], bytes);
+                const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
+                uint8_t* pa = sm + s * stage;
+                if constexpr (A_MN) {
+                    tma_pair_2d(pa, &tmA, m0, kb * kK, bar);
+                    tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar);
+                } else {
+                    tma_pair_2d(pa, &tmA, kb * kK, m0, bar);
+                }
+            };
+            auto load_b = [&](uint32_t s, int n0, int kb) {
+                const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
+                uint8_t* pb = sm + s * stage + kBoxA;
+                if constexpr (MODE == kGated) {
+                    tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar);
+                } else if constexpr (B_MN) {
+                    for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar);
+                } else {
+                    tma_pair_2d(pb, &tmB, kb * kK, n0, bar);
+                }
+            };
+            int ahead = 0;   // blocks of the first unit whose A is on its way already
+            bool more = units.next(u);
+            if (args.early && more) {
+                for (; ahead < stages && u.k0 + ahead < u.k1; ++ahead)
+                    load_a(ahead, u.m * kTileM + int(rank) * kRowsA, u.k0 + ahead);
+            }
+            dep_wait();
+            fence_async_global();
+            for (; ok && more; more = units.next(u)) {
                 const int m0 = u.m * kTileM + int(rank) * kRowsA;
                 const int n0 = u.n * (MODE == kGated ? 128 : args.bn) + (MODE == kGated ? 0 : int(rank) * rows_b);
                 for (int kb = u.k0; kb < u.k1; ++kb, ++g) {
@@ -278,24 +327,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         ok = false;
                         break;
                     }
-                    // the first CTA's barrier counts both CTAs' bytes
-                    if (first) mbar_expect_tx(&x.full[s], bytes);
-                    const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
-                    uint8_t *pa = sm + s * stage, *pb = pa + kBoxA;
-                    if constexpr (A_MN) {
-                        tma_pair_2d(pa, &tmA, m0, kb * kK, bar);
-                        tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar);
-                    } else {
-                        tma_pair_2d(pa, &tmA, kb * kK, m0, bar);
-                    }
-                    if constexpr (MODE == kGated) {
-                        tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar);
-                    } else if constexpr (B_MN) {
-                        for (int i = 0; i < rows_b; i += 64)
-                            tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar);
-                    } else {
-                        tma_pair_2d(pb, &tmB, kb * kK, n0, bar);
-                    }
+                    if (g >= uint32_t(ahead)) load_a(s, m0, kb);
+                    load_b(s, n0, kb);
                 }
             }
             // no copy is under way when the CTAs leave: the first CTA sees both CTAs' arrive
@@ -317,12 +350,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     const uint32_t s = g % stages, step = uint32_t(kb - u.k0) & 3;
                     if (FP8 && step == 0) {
                         // the scales of this and the next three blocks; the copies run in order with the MMAs
-                        if (!mbar_wait(&x.scales_full[q & 1], (q >> 1) & 1)) {
+                        if (!mbar_wait(&x.scales_full[q % kScaleSlots], (q / kScaleSlots) & 1)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t at = smem_u32(sf) + (q & 1) * kScaleSlot, to = tmem + kColScales + (q & 1) * 16;
+                        const uint32_t at = smem_u32(sf) + (q % kScaleSlots) * kScaleSlot,
+                                       to = tmem + kColScales + (q & 1) * 16;
                         for (int i = 0; i < 1 + (args.bn + 127) / 128; ++i) tc_copy_scales(to + i * 4, at + i * 512);
                         ++q;
                     }
@@ -345,7 +379,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
                     tc_commit2(&x.empty[s]);
-                    if (FP8 && (step == 3 || kb + 1 == u.k1)) tc_commit2(&x.scales_empty[(q - 1) & 1]);
+                    if (FP8 && (step == 3 || kb + 1 == u.k1)) tc_commit2(&x.scales_empty[(q - 1) % kScaleSlots]);
                 }
                 if (ok) tc_commit2(&x.acc_full[b]);
             }
@@ -354,10 +388,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     } else if (FP8 && warp == 10) {
         // Scales: four bytes (blocks) of 128 rows of A and bn of B into shared memory, where row r's word lies at
-        // 16 (r % 32) + 4 (r / 32) of its 128 rows. The next step's are on their way while a slot is waited for.
-        struct Words {
-            uint32_t a[4], b[8];
-        };
+        // 16 (r % 32) + 4 (r / 32) of its 128 rows; the copies of three steps are under way at once. Words are
+        // copied where a row's scales are whole words, else they are put together from bytes.
         const Scales &sa = args.sa, &sb = args.sb;
         const bool whole_a = ((reinterpret_cast<uintptr_t>(sa.p) | sa.pitch) & 3) == 0;
         const bool whole_b = ((reinterpret_cast<uintptr_t>(sb.p) | sb.pitch) & 3) == 0;
@@ -381,72 +413,79 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 pb[i] = r < args.bn && row < sb.rows ? sb.at(row) : nullptr;
             }
         };
-        auto word = [&](const uint8_t* p, bool whole, int kb) -> uint32_t {
-            if (!p) return 0x7f7f7f7fu;
-            p += kb;
-            if (whole) return *reinterpret_cast<const uint32_t*>(p);   // within the padded row
-            uint32_t v = 0;
+        auto word = [&](uint32_t to, const uint8_t* p, bool whole, int kb) {
+            if (p && whole) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p + kb) : "memory");
+                return;
+            }
+            uint32_t v = p ? 0 : 0x7f7f7f7fu;   // rows behind the last are zero under any finite scale
+            if (p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (kb + i < args.nk) v |= uint32_t(p[i]) << (8 * i);
-            return v;
+                for (int i = 0; i < 4; ++i)
+                    if (kb + i < args.nk) v |= uint32_t(p[kb + i]) << (8 * i);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
         };
-        auto fetch = [&](int kb, Words& v) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v.a[i] = word(pa[i], whole_a, kb);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v.b[i] = word(pb[i], whole_b, kb);
-        };
-        Words v;
-        uint32_t q = 0;
-        bool more = units.next(u);
+        uint32_t issued = 0;
+        bool more = units.next(u), ok = true;
         int kb = u.k0;
-        if (more) find(u), fetch(kb, v);
-        while (more) {
-            const Words now = v;
+        if (more) find(u);
+        auto issue = [&]() {
+            const uint32_t slot = issued % kScaleSlots, at = smem_u32(sf) + slot * kScaleSlot + lane * 16;
+            if (issued >= kScaleSlots) ok = mbar_wait(&x.scales_empty[slot], ((issued / kScaleSlots) - 1) & 1);
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) word(at + i * 4, pa[i], whole_a, kb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i * 32 < args.bn) word(at + 512 + (i >> 2) * 512 + (i & 3) * 4, pb[i], whole_b, kb);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
             kb += 4;
             if (kb >= u.k1) {
                 more = units.next(u);
                 kb = u.k0;
                 if (more) find(u);
             }
-            if (more) fetch(kb, v);
-            if (q >= 2 && !mbar_wait(&x.scales_empty[q & 1], ((q >> 1) - 1) & 1)) break;
-            const uint32_t at = smem_u32(sf) + (q & 1) * kScaleSlot + lane * 16;
-            st_shared16(at, make_uint4(now.a[0], now.a[1], now.a[2], now.a[3]));
-            st_shared16(at + 512, make_uint4(now.b[0], now.b[1], now.b[2], now.b[3]));
-            st_shared16(at + 1024, make_uint4(now.b[4], now.b[5], now.b[6], now.b[7]));
+        };
+        for (uint32_t q = 0; ok; ++q) {
+            while (ok && more && issued < q + kScaleSlots - 1) issue();
+            if (!ok || q >= issued) break;
+            const uint32_t later = issued - q - 1;
+            if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 2;" ::: "memory");
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) arrive_remote(map_rank(smem_u32(&x.scales_full[q & 1]), 0));
-            ++q;
+            if (lane == 0) arrive_remote(map_rank(smem_u32(&x.scales_full[q % kScaleSlots]), 0));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         const int w = warp - 2, half = w >> 2, quad = warp & 3;
         const uint32_t mine = smem_u32(out) + w * stage_out(MODE);
         uint8_t* const minep = out + w * stage_out(MODE);
         const uint32_t lanes = uint32_t(quad) << 21;   // lane field of a tensor-memory address: quad * 32 << 16
-        // kGrad: pre's boxes of the next 32 channels, read ahead
-        uint32_t loads = 0, waits = 0;
-        auto load_pre = [&](int row, int ch) {
-            ++loads;
-            if (lane == 0) {
-                bulk_wait_read<0>();
-                mbar_expect_tx(&x.loaded[w], 4096);
-                tma_load_3d(minep, &tmC1, ch, 0, row, &x.loaded[w]);
-                tma_load_3d(minep + 2048, &tmC1, ch, 1, row, &x.loaded[w]);
+        // kGrad: gate and up of the next 32 channels of the thread's row, read ahead
+        uint4 next[8];
+        auto load_pre = [&](int64_t row, int ch) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                next[i] = make_uint4(0, 0, 0, 0);
+                const int c = ch + (i & 3) * 8;
+                if (row < args.rows && c < args.cols)
+                    next[i] = __ldcs(reinterpret_cast<const uint4*>(args.pre + (2 * row + (i >> 2)) * args.cols + c));
             }
         };
+        auto row_of = [&](const Unit& t) { return t.m * kTileM + int(rank) * kRowsA + quad * 32; };
         bool more = units.next(u);
-        if (MODE == kGrad && more)
-            load_pre(u.m * kTileM + int(rank) * kRowsA + quad * 32, u.n * 256 + half * 128);
+        if (MODE == kGrad && more) load_pre(int64_t(row_of(u)) + lane, u.n * 256 + half * 128);
         for (int j = 0; more; ++j) {
             const int b = j % accs;
             const Unit now = u;
             if (!mbar_wait(&x.acc_full[b], (j / accs) & 1)) break;
             tc_fence_after();
             const uint32_t acc = tmem + b * acc_cols + lanes;
-            const int row = now.m * kTileM + int(rank) * kRowsA + quad * 32;   // the warp's first
+            const int row = row_of(now);   // the warp's first
             auto drained = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -480,7 +519,25 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int k = 0; k < 16; ++k) v[i * 16 + k] = __uint_as_float(r[i][k]);
                 }
             };
-            if constexpr (MODE == kStore) {
+            // a partial tile's sums: [256 / 8 columns][256 rows][8]
+            auto put_part = [&](uint32_t col, const float (&v)[64]) {
+                float4* p = reinterpret_cast<float4*>(args.part) +
+                            (int64_t(cluster_id_x()) * args.slots + now.slot) * (kTileM * 64) +
+                            (int64_t(col >> 3) * kTileM + int(rank) * kRowsA + quad * 32 + lane) * 2;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    p[(i >> 1) * (kTileM * 2) + (i & 1)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            };
+            if (MODE != kPart && now.slot >= 0) {
+                float v[64];
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t col = half * 128 + i * 64;
+                    get64(col, v);
+                    if (i == 1) drained();
+                    put_part(col, v);
+                }
+            } else if constexpr (MODE == kStore) {
                 const int col = now.n * 256 + half * 128;
                 float v[64];
 #pragma unroll 1
@@ -504,7 +561,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
                 if (args.act == GR_SILU) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) ga[i] = activate<GR_SILU>(ga[i]) * up[i];
+                    for (int i = 0; i < 64; ++i) ga[i] = ga[i] * fast_sigmoid(ga[i]) * up[i];
                 } else {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) ga[i] = activate<GR_GELU>(ga[i]) * up[i];
@@ -541,8 +598,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 } else if (in) put_box(ga, [&] { tma_store_2d(&tmC0, minep, col, row); });
             } else if constexpr (MODE == kGrad) {
                 const int col = now.n * 256 + half * 128;
-                more = units.next(u);
-                bool ok = true;
+                // the tile after this one, whose first values are read behind this one's last
+                Units<1> peek = units;
+                Unit after;
+                const bool follows = peek.next(after) && after.slot < 0;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     float dh[32];
@@ -558,24 +617,26 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
                     if (i == 3) drained();
-                    ok = ok && mbar_wait(&x.loaded[w], waits++ & 1);
+                    uint4 pre[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) pre[k] = next[k];
+                    if (i < 3)
+                        load_pre(int64_t(row) + lane, col + (i + 1) * 32);
+                    else if (follows)
+                        load_pre(int64_t(row_of(after)) + lane, after.n * 256 + half * 128);
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float g[8], p[8], a[8], s[8];
-                        unpack8(ld_shared16(mine + swz64(lane, c)), g);
-                        unpack8(ld_shared16(mine + 2048 + swz64(lane, c)), p);
+                        unpack8(pre[c], g);
+                        unpack8(pre[4 + c], p);
                         if (args.act == GR_SILU) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                a[k] = activate<GR_SILU>(g[k]);
-                                s[k] = activate_slope<GR_SILU>(g[k]);
-                            }
+                            for (int k = 0; k < 8; ++k) act_both(GR_SILU, g[k], a[k], s[k]);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                a[k] = activate<GR_GELU>(g[k]);
-                                s[k] = activate_slope<GR_GELU>(g[k]);
-                            }
+                            for (int k = 0; k < 8; ++k) act_both(GR_GELU, g[k], a[k], s[k]);
                         }
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -593,20 +654,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0 && ok && row < args.rows && col + i * 32 < args.cols) {
+                    if (lane == 0 && row < args.rows && col + i * 32 < args.cols) {
                         tma_store_3d(&tmC2, minep, col + i * 32, 0, row);
                         tma_store_3d(&tmC2, minep + 2048, col + i * 32, 1, row);
                         tma_store_2d(&tmC0, minep + 4096, col + i * 32, row);
                         bulk_commit();
                     }
-                    if (ok && i < 3)
-                        load_pre(row, col + (i + 1) * 32);
-                    else if (ok && more)
-                        load_pre(u.m * kTileM + int(rank) * kRowsA + quad * 32, u.n * 256 + half * 128);
                 }
-                if (!ok) break;
             } else {
-                float* p = args.part + (int64_t(cluster_id_x()) * args.slots + j) * (int64_t(kTileM) * args.bn) +
+                float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
                            int(rank) * kRowsA + quad * 32 + lane;
                 for (int c = half * 16; c < args.bn; c += 32) {
                     float v[16];
@@ -616,9 +672,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
                 drained();
             }
-            if (MODE != kGrad) more = units.next(u);
+            more = units.next(u);
         }
-        if (MODE == kGrad && waits < loads) mbar_wait(&x.loaded[w], waits & 1);
         if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
@@ -629,105 +684,151 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }
 
 // ---- the sums of the pairs' parts ---------------------------------------------------------------
-// C's tile t of kPart is spread over the pairs whose ranges of k meet it, in order; a pair's slots hold its tiles
-// [column][256 rows]. Four rows of a column a thread, rows contiguous in the output.
-enum Join { kJoinStore, kJoinGated, kJoinGrad, kJoinGatedFp8 };
-
+// A tile that is not whole is spread over the pairs whose ranges of k meet it, in order: the first of them may have
+// begun with earlier tiles, for the others it is their first partial tile.
 struct JoinArgs {
-    const float* part;
-    int64_t total, rows, cols;   // of the output (kJoinGated: channels)
-    int steps, tiles_m, bn, slots, pairs, act;
+    Args a;                      // of the products
+    int64_t rows, cols;          // of the output (h's channels)
     __nv_bfloat16 *out, *pre_out;
     const __nv_bfloat16* pre;
     __nv_bfloat16* dpre;
-    uint8_t *codes, *scales;     // kJoinGatedFp8: h
+    uint8_t *codes, *scales;     // h in FP8 blocks
     int pitch;
 };
 
-__device__ __forceinline__ float4 joined(const JoinArgs& a, int64_t row, int64_t col) {
-    const int64_t tn = col / a.bn, t = tn * a.tiles_m + row / kTileM, k0 = t * a.steps;
-    const int64_t at = (col - tn * a.bn) * kTileM + row % kTileM, tile = int64_t(kTileM) * a.bn;
-    int64_t c = ((k0 + 1) * a.pairs - 1) / a.total;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (; c < a.pairs; ++c) {
-        const int64_t begin = a.total * c / a.pairs;
-        if (begin >= k0 + a.steps) break;
-        const int64_t slot = c * a.slots + (t - begin / a.steps);
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(a.part + slot * tile + at));
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    return s;
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(a, b), pack_bf2(c, d));
-}
-__device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&v)[4]) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-
-template <int JOIN>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
-    dep_wait();
-    dep_launch_dependents();
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (i >= a.rows * a.cols) return;
-    const int64_t col = i / a.rows, row = i - col * a.rows;
-    const float4 s = joined(a, row, col);
-    if constexpr (JOIN == kJoinStore) {
-        put4(a.out + i, s.x, s.y, s.z, s.w);
-    } else if constexpr (JOIN == kJoinGated) {
-        const float4 p = joined(a, a.rows + row, col);
-        const float g[4] = {s.x, s.y, s.z, s.w}, up[4] = {p.x, p.y, p.z, p.w};
-        float h[4];
+// The sums at `at` (in fours) of the partial tiles of tile t (counted from the first that is not whole).
+template <int FOURS>
+__device__ __forceinline__ void joined(const Args& a, uint32_t t, int64_t at, float (&v)[4 * FOURS]) {
+    const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
+    const int64_t tile = int64_t(kTileM) * a.bn / 4;
+    const float4* p = reinterpret_cast<const float4*>(a.part) + at;
+    const float4* q = p + (int64_t(first) * a.slots + (t - a.begin(first) / a.steps)) * tile;
+    float4 s[FOURS];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = act_of(a.act, g[k]) * up[k];
-        put4(a.out + i, h[0], h[1], h[2], h[3]);
-        if (a.pre_out) {
-            put4(a.pre_out + 2 * col * a.rows + row, g[0], g[1], g[2], g[3]);
-            put4(a.pre_out + (2 * col + 1) * a.rows + row, up[0], up[1], up[2], up[3]);
+    for (int i = 0; i < FOURS; ++i) s[i] = __ldcs(q + i);
+#pragma unroll 4
+    for (uint32_t c = first + 1; c <= last; ++c) {
+#pragma unroll
+        for (int i = 0; i < FOURS; ++i) {
+            const float4 w = __ldcs(p + int64_t(c) * a.slots * tile + i);
+            s[i].x += w.x, s[i].y += w.y, s[i].z += w.z, s[i].w += w.w;
         }
-    } else {
-        const float dh[4] = {s.x, s.y, s.z, s.w};
-        float g[4], p[4], f[4], d[4];
-        get4(a.pre + 2 * col * a.rows + row, g);
-        get4(a.pre + (2 * col + 1) * a.rows + row, p);
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f[k] = act_of(a.act, g[k]);
-            d[k] = dh[k] * p[k] * (a.act == GR_SILU ? activate_slope<GR_SILU>(g[k]) : activate_slope<GR_GELU>(g[k]));
-            p[k] *= f[k];
-            f[k] *= dh[k];
-        }
-        put4(a.dpre + 2 * col * a.rows + row, d[0], d[1], d[2], d[3]);
-        put4(a.dpre + (2 * col + 1) * a.rows + row, f[0], f[1], f[2], f[3]);
-        put4(a.out + i, p[0], p[1], p[2], p[3]);
+    for (int i = 0; i < FOURS; ++i) v[4 * i] = s[i].x, v[4 * i + 1] = s[i].y, v[4 * i + 2] = s[i].z, v[4 * i + 3] = s[i].w;
+}
+template <int N> __device__ __forceinline__ void put_bf16(__nv_bfloat16* p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf2(v[i], v[i + 1]), pack_bf2(v[i + 2], v[i + 3]));
+}
+template <int N> __device__ __forceinline__ void get_bf16(const __nv_bfloat16* p, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p + i);
+        v[i] = __uint_as_float(u.x << 16), v[i + 1] = __uint_as_float(u.x & 0xffff0000u);
+        v[i + 2] = __uint_as_float(u.y << 16), v[i + 3] = __uint_as_float(u.y & 0xffff0000u);
     }
 }
-
-// h in blocks of 128 channels of a column, a warp each.
-__global__ void __launch_bounds__(256) join_fp8_kernel(const __grid_constant__ JoinArgs a) {
-    dep_wait();
-    dep_launch_dependents();
-    const int nb = int((a.rows + kBlock - 1) / kBlock);
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 32;
-    if (i >= a.cols * nb) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t col = i / nb, row = (i - col * nb) * kBlock + lane * 4;
-    float h[4] = {};
-    if (row < a.rows) {
-        const float4 s = joined(a, row, col), p = joined(a, a.rows + row, col);
-        const float g[4] = {s.x, s.y, s.z, s.w}, up[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = act_of(a.act, g[k]) * up[k];
+// What the epilogues do with whole tiles, on N neighbouring channels of a token.
+template <int N>
+__device__ __forceinline__ void finish_gated(const JoinArgs& j, int64_t token, int64_t ch, float (&g)[N], float (&up)[N]) {
+    if (j.pre_out) {
+        put_bf16(j.pre_out + 2 * token * j.rows + ch, g);
+        put_bf16(j.pre_out + (2 * token + 1) * j.rows + ch, up);
     }
-    uint32_t top = max(max(block_mag(h[0]), block_mag(h[1])), max(block_mag(h[2]), block_mag(h[3])));
-    top = __reduce_max_sync(~0u, top);
+#pragma unroll
+    for (int k = 0; k < N; ++k) g[k] = act_of(j.a.act, g[k]) * up[k];
+}
+template <int N>
+__device__ __forceinline__ void finish_grad(const JoinArgs& j, int64_t token, int64_t ch, float (&dh)[N]) {
+    float g[N], p[N], s[N];
+    get_bf16(j.pre + 2 * token * j.rows + ch, g);
+    get_bf16(j.pre + (2 * token + 1) * j.rows + ch, p);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float a, slope;
+        act_both(j.a.act, g[k], a, slope);
+        s[k] = slope * (dh[k] * p[k]);
+        p[k] *= a;
+        dh[k] *= a;
+    }
+    put_bf16(j.dpre + 2 * token * j.rows + ch, s);
+    put_bf16(j.dpre + (2 * token + 1) * j.rows + ch, dh);
+    put_bf16(j.out + token * j.rows + ch, p);
+}
+// N channels of each of LANES neighbouring lanes, a block of 128, as codes.
+template <int N, int LANES>
+__device__ __forceinline__ void finish_fp8(const JoinArgs& j, int64_t token, int64_t ch, const float (&h)[N], bool in) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) top = max(top, block_mag(h[k]));
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
     float inv;
     const uint8_t e = block_scale(top, inv);
-    if (row < a.rows) *reinterpret_cast<uint32_t*>(a.codes + col * a.rows + row) = block_codes4(h, inv);
-    if (lane == 0) a.scales[col * a.pitch + (i - col * nb)] = e;
+    if (!in) return;
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+        *reinterpret_cast<uint32_t*>(j.codes + token * j.rows + ch + k) = block_codes4(h + k, inv);
+    if ((ch & (kBlock - 1)) == 0) j.scales[token * j.pitch + ch / kBlock] = e;
+}
+
+// After kPart: C's rows are the output's channels, contiguous, its columns the tokens. A thread has four rows of a
+// column; in FP8 a warp has a block.
+enum Join { kJoinStore, kJoinGated, kJoinGrad, kJoinGatedFp8 };
+constexpr int kJoinThreads = 128;
+
+template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_columns_kernel(const __grid_constant__ JoinArgs j) {
+    dep_launch_dependents();
+    dep_wait();
+    const Args& a = j.a;
+    const uint32_t rows = uint32_t(j.rows), lines = JOIN == kJoinGatedFp8 ? (rows + kBlock - 1) / kBlock * kBlock : rows;
+    const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x, col = i / (lines / 4), row = (i - col * (lines / 4)) * 4;
+    const bool in = col < uint32_t(j.cols) && row < rows;
+    if (JOIN != kJoinGatedFp8 && !in) return;
+    const uint32_t tn = col / uint32_t(a.bn);
+    auto sum = [&](uint32_t r, float (&v)[4]) {
+        joined<1>(a, tn * a.tiles_m + r / kTileM, (int64_t(col - tn * a.bn) * kTileM + r % kTileM) / 4, v);
+    };
+    float v[4] = {}, up[4];
+    if (in) sum(row, v);
+    if constexpr (JOIN == kJoinGated || JOIN == kJoinGatedFp8) {
+        if (in) {
+            sum(rows + row, up);
+            finish_gated(j, col, row, v, up);
+        }
+    }
+    if constexpr (JOIN == kJoinGatedFp8) finish_fp8<4, 32>(j, col, row, v, in);
+    else if constexpr (JOIN == kJoinGrad) finish_grad(j, col, row, v);
+    else put_bf16(j.out + int64_t(col) * rows + row, v);
+}
+
+// After the other modes: the tiles behind the whole ones, C as the output. A thread has eight columns of a row.
+template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const __grid_constant__ JoinArgs j) {
+    dep_launch_dependents();
+    dep_wait();
+    constexpr bool kPair = JOIN == kJoinGated || JOIN == kJoinGatedFp8;
+    constexpr uint32_t kCols = kPair ? 128 : 256, kPer = kCols / 8, kBlocks = kTileM * kPer / kJoinThreads;
+    const Args& a = j.a;
+    const uint32_t t = blockIdx.x / kBlocks, i = (blockIdx.x - t * kBlocks) * kJoinThreads + threadIdx.x;
+    const uint32_t r = i / kPer, c = i % kPer * 8;
+    int m, n;
+    a.place(a.whole + t, m, n);
+    const int64_t row = int64_t(m) * kTileM + r, col = int64_t(n) * kCols + c;
+    const bool in = row < a.rows && col < a.cols;
+    if (JOIN != kJoinGatedFp8 && !in) return;
+    float v[8] = {}, up[8];
+    if (in) joined<2>(a, t, (int64_t(c >> 3) * kTileM + r) * 2, v);
+    if constexpr (kPair) {
+        if (in) {
+            joined<2>(a, t, (int64_t((c + 128) >> 3) * kTileM + r) * 2, up);
+            finish_gated(j, row, col, v, up);
+        }
+    }
+    if constexpr (JOIN == kJoinGatedFp8) finish_fp8<8, 16>(j, row, col, v, in);
+    else if constexpr (JOIN == kJoinGrad) finish_grad(j, row, col, v);
+    else put_bf16(j.out + row * a.cols + col, v);
 }
 
 // ---- host ---------------------------------------------------------------------------------------
@@ -792,6 +893,9 @@ cudaError_t launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t sm
 
 int pairs_of() { return sm_count() / 2; }
 
+constexpr int kFewTokens = 512;    // up to which the tokens are C's columns
+constexpr int kDivideBlocks = 48;  // blocks of k a pair has to save by dividing the last tiles
+
 // An operand's memory and its rows along M or N.
 struct Operand {
     const void* p;
@@ -805,10 +909,20 @@ int stages_for(int bn) {
     return room > kMaxStages ? kMaxStages : room;
 }
 
+// How a product is divided: the tiles, the pairs, the partial tiles.
+struct Plan {
+    Args a{};
+    bool columns = false;   // kPart
+    int pairs = 0;
+    uint32_t rest = 0;      // tiles in parts
+    size_t bytes = 0;       // of the parts
+};
+
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
-cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, Args args, int pairs, const CUtensorMap& c0,
+cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Plan& p, const CUtensorMap& c0,
                          const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic) {
     CUtensorMap ma, mb;
+    Args args = p.a;
     const int rows_b = args.bn / 2;
     bool ok;
     if constexpr (FP8) {
@@ -825,206 +939,220 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, Args arg
     args.stages = stages_for<MODE, FP8>(args.bn);
     const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
-    return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
+    return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
                   programmatic, ma, mb, c0, c1, c2, args);
 }
 
-// ---- whole tiles ----
-Args whole(int64_t rows, int64_t cols, int64_t K, int per_tile, int kk = 64) {
-    Args a{};
-    a.nk = int(ceil_div(K, kk));
-    a.tiles_m = int(ceil_div(rows, kTileM));
-    a.tiles_n = int(ceil_div(cols, per_tile));
-    a.bn = 256;
-    a.group = 8;
-    return a;
-}
-int pairs_for(const Args& a) {
-    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
-    return int(tiles < pairs_of() ? tiles : pairs_of());
+// ---- plans ----
+// The tiles behind `whole` in ranges of at least `least` steps.
+void spread(Plan& p, int64_t tiles, int64_t whole, int least) {
+    p.a.whole = uint32_t(whole);
+    p.rest = uint32_t(tiles - whole);
+    p.pairs = pairs_of();
+    const int64_t total = int64_t(p.rest) * p.a.steps;
+    if (whole == 0) {
+        const int64_t most = ceil_div(total, least);
+        p.pairs = int(most < p.pairs ? most : p.pairs);
+    }
+    p.a.range = uint32_t(total / p.pairs), p.a.longer = uint32_t(total % p.pairs);
+    p.a.slots = int(ceil_div(ceil_div(total, p.pairs), p.a.steps)) + 1;
+    p.bytes = p.rest ? size_t(p.pairs) * p.a.slots * kTileM * p.a.bn * 4 : 0;
 }
 
-// ---- parts ----
-struct Parts {
-    Args a{};
-    int pairs = 0;
-    size_t bytes = 0;
-};
-// C [rows][cols] over K in parts: the tiles' columns as even as the steps of 16 (FP8: 32; 128) allow, k divided among
-// the pairs in ranges of at least four blocks.
-Parts parts_of(int64_t rows, int64_t cols, int64_t K, int step, bool fp8 = false) {
-    Parts p;
+// Whole tiles of 256 x 256 (kGated: 128 channels), a pair each, as long as there are as many as pairs. The last
+// ones, fewer than that, are divided along k among all the pairs where that saves more than the parts cost.
+Plan plan_tiles(int64_t rows, int64_t cols, int64_t K, int per_tile, bool fp8) {
+    Plan p;
     p.a.nk = int(ceil_div(K, fp8 ? 128 : 64));
-    p.a.steps = fp8 ? int(ceil_div(p.a.nk, 4)) : p.a.nk;
+    p.a.steps = fp8 ? uint32_t(ceil_div(p.a.nk, 4)) : uint32_t(p.a.nk);
     p.a.tiles_m = int(ceil_div(rows, kTileM));
-    p.a.tiles_n = int(ceil_div(cols, 256));
-    p.a.bn = int(ceil_div(ceil_div(cols, p.a.tiles_n), step) * step);
-    p.a.tiles_n = int(ceil_div(cols, p.a.bn));
-    p.a.total = int64_t(p.a.tiles_m) * p.a.tiles_n * p.a.steps;
-    const int64_t most = fp8 ? p.a.total : ceil_div(p.a.total, 4);
-    p.pairs = int(most < pairs_of() ? most : pairs_of());
-    p.a.slots = int(ceil_div(ceil_div(p.a.total, p.pairs), p.a.steps)) + 1;
-    p.bytes = size_t(p.pairs) * p.a.slots * kTileM * p.a.bn * 4;
+    p.a.tiles_n = int(ceil_div(cols, per_tile));
+    p.a.bn = 256;
+    p.a.group = 8;
+    p.a.rows = rows, p.a.cols = cols;
+    const int64_t tiles = int64_t(p.a.tiles_m) * p.a.tiles_n, pairs = pairs_of(), rest = tiles % pairs;
+    const bool divide = rest && (pairs - rest) * p.a.nk > kDivideBlocks * pairs && rest * p.a.nk >= 2 * pairs;
+    spread(p, tiles, divide ? tiles - rest : tiles, fp8 ? 1 : 4);
+    if (tiles < p.pairs && !divide) p.pairs = int(tiles);
     return p;
 }
 
-JoinArgs join_args(const Parts& p, float* ws, int64_t rows, int64_t cols, int act) {
-    JoinArgs j{};
-    j.part = ws;
-    j.total = p.a.total, j.rows = rows, j.cols = cols;
-    j.steps = p.a.steps, j.tiles_m = p.a.tiles_m, j.bn = p.a.bn, j.slots = p.a.slots, j.pairs = p.pairs, j.act = act;
-    return j;
-}
-template <int JOIN>
-cudaError_t join(const Parts& p, float* ws, int64_t rows, int64_t cols, int act, void* out, const void* pre,
-                 void* pre_out, void* dpre, cudaStream_t st) {
-    JoinArgs j = join_args(p, ws, rows, cols, act);
-    j.out = static_cast<__nv_bfloat16*>(out);
-    j.pre_out = static_cast<__nv_bfloat16*>(pre_out);
-    j.pre = static_cast<const __nv_bfloat16*>(pre);
-    j.dpre = static_cast<__nv_bfloat16*>(dpre);
-    return launch(join_kernel<JOIN>, unsigned(ceil_div(rows * cols / 4, 256)), 256, 0, st, true, j);
-}
-
-// Whether a product goes in parts. Its tokens are the columns of the parts' form.
-bool in_parts(int64_t tokens, const Args& direct) {
-    const int64_t tiles = int64_t(direct.tiles_m) * direct.tiles_n, slots = ceil_div(tiles, pairs_of()) * pairs_of();
-    return tokens <= 256 || tiles * 10 < slots * 7;
+// Few tokens: C's rows are the weights' and its columns the tokens, in tiles of as few columns as the steps of 16 (FP8:
+// 32; 128 where the tokens' operand is not K-major) allow; all of them in parts.
+Plan plan_columns(int64_t rows, int64_t tokens, int64_t K, int step, bool fp8) {
+    Plan p;
+    p.columns = true;
+    p.a.nk = int(ceil_div(K, fp8 ? 128 : 64));
+    p.a.steps = fp8 ? uint32_t(ceil_div(p.a.nk, 4)) : uint32_t(p.a.nk);
+    p.a.tiles_m = int(ceil_div(rows, kTileM));
+    p.a.tiles_n = int(ceil_div(tokens, 256));
+    p.a.bn = int(ceil_div(ceil_div(tokens, p.a.tiles_n), step) * step);
+    p.a.tiles_n = int(ceil_div(tokens, p.a.bn));
+    p.a.group = p.a.tiles_m;   // tile t: row tile t % tiles_m
+    p.a.early = 1;
+    spread(p, int64_t(p.a.tiles_m) * p.a.tiles_n, 0, fp8 ? 1 : 4);
+    return p;
 }
 
 const CUtensorMap kNone = {};
 
-// C [M][N] = A Bᵀ as whole tiles, or in parts as Cᵀ with the rows along N.
+template <int JOIN> cudaError_t join(const Plan& p, JoinArgs j, cudaStream_t st) {
+    j.a = p.a;
+    if (p.columns) {
+        const int64_t lines = JOIN == kJoinGatedFp8 ? ceil_div(j.rows, kBlock) * kBlock : j.rows;
+        return launch(join_columns_kernel<JOIN>, unsigned(ceil_div(lines / 4 * j.cols, kJoinThreads)), kJoinThreads, 0,
+                      st, true, j);
+    }
+    const int blocks = kTileM * (JOIN == kJoinGated || JOIN == kJoinGatedFp8 ? 16 : 32) / kJoinThreads;
+    return p.rest ? launch(join_tiles_kernel<JOIN>, p.rest * blocks, kJoinThreads, 0, st, true, j) : cudaSuccess;
+}
+
+bool few(int64_t tokens) { return tokens <= kFewTokens; }
+
+// C [M][N] = A Bᵀ.
+Plan plan_product(int64_t M, int64_t N, int64_t K, int64_t tokens, bool fp8) {
+    return few(tokens) ? plan_columns(N, M, K, fp8 ? 32 : 16, fp8) : plan_tiles(M, N, K, 256, fp8);
+}
 template <bool A_K, bool B_K>
 cudaError_t product(const void* a, const void* b, void* out, int64_t M, int64_t N, int64_t K, int64_t tokens,
-                    float* ws, cudaStream_t st, bool programmatic) {
-    Args w = whole(M, N, K, 256);
-    if (!in_parts(tokens, w)) {
+                    float* ws, cudaStream_t st) {
+    Plan p = plan_product(M, N, K, tokens, false);
+    p.a.part = ws;
+    JoinArgs j{};
+    j.out = static_cast<__nv_bfloat16*>(out);
+    j.rows = N, j.cols = M;
+    cudaError_t e;
+    if (p.columns) {
+        if constexpr (A_K)
+            e = launch_pairs<kPart, false, !B_K, false>({b, N}, {a, M}, K, p, kNone, kNone, kNone, st, true);
+        else
+            e = cudaErrorInvalidValue;
+    } else {
         CUtensorMap c;
         if (!map_bf16(&c, out, M, N, 32, 64)) return cudaErrorInvalidValue;
-        w.rows = M, w.cols = N;
-        return launch_pairs<kStore, false, !A_K, !B_K>({a, M}, {b, N}, K, w, pairs_for(w), c, kNone, kNone, st,
-                                                programmatic);
+        e = launch_pairs<kStore, false, !A_K, !B_K>({a, M}, {b, N}, K, p, c, kNone, kNone, st, true);
     }
-    Parts p = parts_of(N, M, K, A_K ? 16 : 128);
-    p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, false, !B_K, !A_K>({b, N}, {a, M}, K, p.a, p.pairs, kNone, kNone, kNone, st,
-                                                          programmatic);
-    return e != cudaSuccess ? e : join<kJoinStore>(p, ws, N, M, 0, out, nullptr, nullptr, nullptr, st);
+    return e != cudaSuccess ? e : join<kJoinStore>(p, j, st);
 }
-size_t product_bytes(int64_t M, int64_t N, int64_t K, int64_t tokens, bool a_k) {
-    return in_parts(tokens, whole(M, N, K, 256)) ? parts_of(N, M, K, a_k ? 16 : 128).bytes : 0;
+
+Plan plan_gated(int64_t N, int64_t D, int64_t F, bool fp8) {
+    return few(N) ? plan_columns(2 * F, N, D, fp8 ? 32 : 16, fp8) : plan_tiles(N, F, D, 128, fp8);
+}
+Plan plan_grad(int64_t N, int64_t D, int64_t F) {
+    return few(N) ? plan_columns(F, N, D, 16, false) : plan_tiles(N, F, D, 256, false);
 }
 
 }  // namespace
 
 cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void* w_in, void* h, void* pre,
                      float* ws, cudaStream_t st) {
-    Args w = whole(N, F, D, 128);
-    if (!in_parts(N, w)) {
+    Plan p = plan_gated(N, D, F, false);
+    p.a.part = ws, p.a.act = act, p.a.keep = pre != nullptr;
+    JoinArgs j{};
+    j.out = static_cast<__nv_bfloat16*>(h), j.pre_out = static_cast<__nv_bfloat16*>(pre);
+    j.rows = F, j.cols = N;
+    cudaError_t e;
+    if (p.columns) {
+        e = launch_pairs<kPart, false, false, false>({w_in, 2 * int64_t(F)}, {x, N}, D, p, kNone, kNone, kNone, st, false);
+    } else {
         CUtensorMap c, cp = kNone;
         if (!map_bf16(&c, h, N, F, 32, 64) || (pre && !map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 64)))
             return cudaErrorInvalidValue;
-        w.rows = N, w.cols = F, w.act = act, w.keep = pre != nullptr;
-        return launch_pairs<kGated, false, false, false>({x, N}, {w_in, F}, D, w, pairs_for(w), c, cp, kNone, st, false);
+        e = launch_pairs<kGated, false, false, false>({x, N}, {w_in, F}, D, p, c, cp, kNone, st, false);
     }
-    Parts p = parts_of(2 * int64_t(F), N, D, 16);
-    p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, false, false, false>({w_in, 2 * int64_t(F)}, {x, N}, D, p.a, p.pairs, kNone,
-                                                            kNone, kNone, st, false);
-    return e != cudaSuccess ? e : join<kJoinGated>(p, ws, F, N, act, h, nullptr, pre, nullptr, st);
+    return e != cudaSuccess ? e : join<kJoinGated>(p, j, st);
 }
 
 cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, const void* w_out, const void* pre,
                           void* dpre, void* h, float* ws, cudaStream_t st) {
-    Args w = whole(N, F, D, 256);
-    if (!in_parts(N, w)) {
-        CUtensorMap c, cp, cd;
-        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 32) ||
-            !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32))
-            return cudaErrorInvalidValue;
-        w.rows = N, w.cols = F, w.act = act;
-        return launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, w, pairs_for(w), c, cp, cd, st, false);
+    Plan p = plan_grad(N, D, F);
+    p.a.part = ws, p.a.act = act, p.a.pre = static_cast<const __nv_bfloat16*>(pre);
+    JoinArgs j{};
+    j.out = static_cast<__nv_bfloat16*>(h), j.dpre = static_cast<__nv_bfloat16*>(dpre), j.pre = p.a.pre;
+    j.rows = F, j.cols = N;
+    cudaError_t e;
+    if (p.columns) {
+        e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p, kNone, kNone, kNone, st, false);
+    } else {
+        CUtensorMap c, cd;
+        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32)) return cudaErrorInvalidValue;
+        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, kNone, cd, st, false);
     }
-    Parts p = parts_of(F, N, D, 16);
-    p.a.part = ws;
-    const cudaError_t e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p.a, p.pairs, kNone, kNone,
-                                                           kNone, st, false);
-    return e != cudaSuccess ? e : join<kJoinGrad>(p, ws, F, N, act, h, pre, nullptr, dpre, st);
+    return e != cudaSuccess ? e : join<kJoinGrad>(p, j, st);
 }
 
 cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const void* a, bool a_k, const void* b,
                        bool b_k, void* out, float* ws, cudaStream_t st) {
     if (a_k)
-        return b_k ? product<true, true>(a, b, out, M, N, K, tokens, ws, st, true)
-                   : product<true, false>(a, b, out, M, N, K, tokens, ws, st, true);
-    return b_k ? cudaErrorInvalidValue : product<false, false>(a, b, out, M, N, K, tokens, ws, st, true);
+        return b_k ? product<true, true>(a, b, out, M, N, K, tokens, ws, st)
+                   : product<true, false>(a, b, out, M, N, K, tokens, ws, st);
+    return b_k ? cudaErrorInvalidValue : product<false, false>(a, b, out, M, N, K, tokens, ws, st);
+}
+
+size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient) {
+    size_t need = 0;
+    auto cover = [&](const Plan& p) { need = p.bytes > need ? p.bytes : need; };
+    if (gradient) {
+        cover(plan_grad(N, D, F));
+        cover(plan_product(N, D, 2 * int64_t(F), N, false));
+        cover(plan_product(2 * int64_t(F), D, N, INT64_MAX, false));
+        cover(plan_product(D, F, N, INT64_MAX, false));
+    } else {
+        cover(plan_gated(N, D, F, false));
+        cover(plan_product(N, D, F, N, false));
+    }
+    return need;
 }
 
 // ---- FP8 ----
 cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, int x_pitch, Fp8Matrix w_in, uint8_t* h,
                          uint8_t* hs, int hs_pitch, float* ws, cudaStream_t st, bool programmatic) {
-    const int db = int(ceil_div(D, kBlock));
-    const Scales sx{x.scales, N, N, 1, x_pitch}, sw{w_in.scales, 2 * int64_t(F), F, kBlock, db};
-    Args w = whole(N, F, D, 128, 128);
-    if (!in_parts(N, w)) {
+    const Scales sx{x.scales, N, N, 1, x_pitch}, sw{w_in.scales, 2 * int64_t(F), F, kBlock, int(ceil_div(D, kBlock))};
+    Plan p = plan_gated(N, D, F, true);
+    p.a.part = ws, p.a.act = act;
+    JoinArgs j{};
+    j.codes = h, j.scales = hs, j.pitch = hs_pitch;
+    j.rows = F, j.cols = N;
+    cudaError_t e;
+    if (p.columns) {
+        p.a.sa = sw, p.a.sb = sx;
+        e = launch_pairs<kPart, true, false, false>({w_in.codes, 2 * int64_t(F)}, {x.codes, N}, D, p, kNone, kNone, kNone,
+                                                    st, programmatic);
+    } else {
         CUtensorMap c;
         if (!map_codes(&c, h, N, F, 32, 64)) return cudaErrorInvalidValue;
-        w.rows = N, w.cols = F, w.act = act, w.sa = sx, w.sb = sw, w.hs = hs, w.hs_pitch = hs_pitch;
-        return launch_pairs<kGated, true, false, false>({x.codes, N}, {w_in.codes, F}, D, w, pairs_for(w), c, kNone,
-                                                        kNone, st, programmatic);
+        p.a.sa = sx, p.a.sb = sw, p.a.hs = hs, p.a.hs_pitch = hs_pitch;
+        e = launch_pairs<kGated, true, false, false>({x.codes, N}, {w_in.codes, F}, D, p, c, kNone, kNone, st,
+                                                     programmatic);
     }
-    Parts p = parts_of(2 * int64_t(F), N, D, 32, true);
-    p.a.part = ws, p.a.sa = sw, p.a.sb = sx;
-    cudaError_t e = launch_pairs<kPart, true, false, false>({w_in.codes, 2 * int64_t(F)}, {x.codes, N}, D, p.a,
-                                                            p.pairs, kNone, kNone, kNone, st, programmatic);
-    if (e != cudaSuccess) return e;
-    JoinArgs j = join_args(p, ws, F, N, act);
-    j.codes = h, j.scales = hs, j.pitch = hs_pitch;
-    return launch(join_fp8_kernel, unsigned(ceil_div(N * ceil_div(F, kBlock), 8)), 256, 0, st, true, j);
+    return e != cudaSuccess ? e : join<kJoinGatedFp8>(p, j, st);
 }
 
 cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, int a_pitch, Fp8Matrix b, void* out,
                            float* ws, cudaStream_t st, bool programmatic) {
-    const int kb = int(ceil_div(K, kBlock));
-    const Scales sa{a.scales, N, N, 1, a_pitch}, sb{b.scales, O, O, kBlock, kb};
-    Args w = whole(N, O, K, 256, 128);
-    if (!in_parts(N, w)) {
+    const Scales sa{a.scales, N, N, 1, a_pitch}, sb{b.scales, O, O, kBlock, int(ceil_div(K, kBlock))};
+    Plan p = plan_product(N, O, K, N, true);
+    p.a.part = ws;
+    JoinArgs j{};
+    j.out = static_cast<__nv_bfloat16*>(out);
+    j.rows = O, j.cols = N;
+    cudaError_t e;
+    if (p.columns) {
+        p.a.sa = sb, p.a.sb = sa;
+        e = launch_pairs<kPart, true, false, false>({b.codes, O}, {a.codes, N}, K, p, kNone, kNone, kNone, st, programmatic);
+    } else {
         CUtensorMap c;
         if (!map_bf16(&c, out, N, O, 32, 64)) return cudaErrorInvalidValue;
-        w.rows = N, w.cols = O, w.sa = sa, w.sb = sb;
-        return launch_pairs<kStore, true, false, false>({a.codes, N}, {b.codes, O}, K, w, pairs_for(w), c, kNone,
-                                                        kNone, st, programmatic);
+        p.a.sa = sa, p.a.sb = sb;
+        e = launch_pairs<kStore, true, false, false>({a.codes, N}, {b.codes, O}, K, p, c, kNone, kNone, st, programmatic);
     }
-    Parts p = parts_of(O, N, K, 32, true);
-    p.a.part = ws, p.a.sa = sb, p.a.sb = sa;
-    const cudaError_t e = launch_pairs<kPart, true, false, false>({b.codes, O}, {a.codes, N}, K, p.a, p.pairs, kNone,
-                                                                  kNone, kNone, st, programmatic);
-    return e != cudaSuccess ? e : join<kJoinStore>(p, ws, O, N, 0, out, nullptr, nullptr, nullptr, st);
+    return e != cudaSuccess ? e : join<kJoinStore>(p, j, st);
 }
 
-size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K) {
-    return in_parts(N, whole(N, O, K, 256, 128)) ? parts_of(O, N, K, 32, true).bytes : 0;
-}
+size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K) { return plan_product(N, O, K, N, true).bytes; }
 size_t tc_feed_fp8_workspace(int64_t N, int D, int F) {
-    const size_t down = tc_product_fp8_workspace(N, D, F);
-    const size_t in = in_parts(N, whole(N, F, D, 128, 128)) ? parts_of(2 * int64_t(F), N, D, 32, true).bytes : 0;
+    const size_t in = plan_gated(N, D, F, true).bytes, down = plan_product(N, D, F, N, true).bytes;
     return in > down ? in : down;
-}
-
-size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient) {
-    size_t need = 0;
-    auto cover = [&](size_t n) { need = n > need ? n : need; };
-    if (gradient) {
-        if (in_parts(N, whole(N, F, D, 256))) cover(parts_of(F, N, D, 16).bytes);
-        cover(product_bytes(N, D, 2 * int64_t(F), N, true));
-        cover(product_bytes(2 * int64_t(F), D, N, INT64_MAX, false));
-        cover(product_bytes(D, F, N, INT64_MAX, false));
-    } else {
-        if (in_parts(N, whole(N, F, D, 128))) cover(parts_of(2 * int64_t(F), N, D, 16).bytes);
-        cover(product_bytes(N, D, F, N, true));
-    }
-    return need;
 }
 
 int feed_status(bool clear) {
