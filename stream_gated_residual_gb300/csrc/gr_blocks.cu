@@ -31,28 +31,74 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], flo
 
 constexpr int kThreads = 256;
 
-// Blocks of one row: 16 bytes a lane, so 16 lanes (bf16) or 32 (fp32) hold a block.
+// Blocks of one row: 16 bytes a lane, so 16 lanes (bf16) or 32 (fp32) hold a block; kPer blocks of each group of
+// lanes are read before the first is encoded. TOKENS: scales as a product takes them.
+constexpr int kPer = 4;
+template <typename T, bool TOKENS>
+__device__ __forceinline__ void encode_rows(const T* __restrict__ m, uint8_t* __restrict__ codes,
+                                            uint8_t* __restrict__ scales, int64_t blocks, int64_t cols, uint32_t nb,
+                                            int64_t cta) {
+    constexpr int kV = 16 / sizeof(T), kLanes = kBlock / kV, kGroups = kThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const int64_t first = cta * (kGroups * kPer) + threadIdx.x / kLanes;
+    float v[kPer][kV];
+    int64_t row[kPer];
+    uint32_t blk[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t at = first + i * kGroups;
+        row[i] = at < (int64_t(1) << 32) ? uint32_t(at) / nb : at / nb;
+        blk[i] = uint32_t(at - row[i] * nb);
+        const int64_t c = int64_t(blk[i]) * kBlock + lane * kV;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[i][k] = 0.0f;
+        if (at < blocks && c < cols) load16(m + row[i] * cols + c, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t at = first + i * kGroups, c = int64_t(blk[i]) * kBlock + lane * kV;
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) top = max(top, block_mag(v[i][k]));
+#pragma unroll
+        for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+        float inv;
+        const uint8_t s = block_scale(top, inv);
+        if (at < blocks && c < cols) store_codes(codes + row[i] * cols + c, v[i], inv);
+        if (lane == 0 && at < blocks) scales[TOKENS ? scale_at(row[i], blk[i], int(nb + 3) / 4) : at] = s;
+    }
+}
+template <typename T>
+constexpr int kRowsPerCta = kThreads / (kBlock / (16 / int(sizeof(T)))) * kPer;   // blocks
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 encode_rows_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                   int64_t blocks, int64_t cols, int nb, int pitch) {
+                   int64_t blocks, int64_t cols, uint32_t nb) {
+    encode_rows<T, false>(m, codes, scales, blocks, cols, nb, blockIdx.x);
+}
+
+// The operands of products on FP8 blocks: CTAs for the scales' words first, then for x's blocks.
+__device__ __forceinline__ void lay_out(const ScaleRows& s, int64_t i) {
+    const int steps = (s.blocks + 3) / 4;
+    const int64_t row = i / steps;
+    if (row >= s.rows) return;
+    const int st = int(i - row * steps);
+    uint32_t v = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (st * 4 + k < s.blocks) v |= uint32_t(s.from[row * s.blocks + st * 4 + k]) << (8 * k);
+    *reinterpret_cast<uint32_t*>(s.to + (s.tokens ? scale_at(row, st * 4, steps) : i * 4)) = v;
+}
+__global__ void __launch_bounds__(kThreads)
+fp8_operands_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                    int64_t blocks, int64_t cols, uint32_t nb, const ScaleRows a, const ScaleRows b, int64_t ctas_a,
+                    int64_t ctas_b) {
     dep_launch_dependents();
-    constexpr int kV = 16 / sizeof(T), kLanes = kBlock / kV;
-    const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t row = at / nb, c = (at - row * nb) * kBlock + lane * kV;
-    const bool in = at < blocks && c < cols;
-    float v[kV] = {};
-    if (in) load16(m + row * cols + c, v);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) top = max(top, block_mag(v[i]));
-#pragma unroll
-    for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-    float inv;
-    const uint8_t s = block_scale(top, inv);
-    if (in) store_codes(codes + row * cols + c, v, inv);
-    if (lane == 0 && at < blocks) scales[row * pitch + (at - row * nb)] = s;
+    const int64_t c = blockIdx.x;
+    if (c < ctas_a) lay_out(a, c * kThreads + threadIdx.x);
+    else if (c < ctas_a + ctas_b) lay_out(b, (c - ctas_a) * kThreads + threadIdx.x);
+    else encode_rows<__nv_bfloat16, true>(x, codes, scales, blocks, cols, nb, c - ctas_a - ctas_b);
 }
 
 // Blocks of 128 rows: a CTA each, 64 values a thread.
@@ -92,17 +138,14 @@ encode_tiles_kernel(const T* __restrict__ m, uint8_t* __restrict__ codes, uint8_
 
 template <typename T>
 cudaError_t encode(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, const T* m, uint8_t* codes,
-                   uint8_t* scales, int pitch, cudaStream_t st) {
+                   uint8_t* scales, cudaStream_t st) {
     const int64_t nb = ceil_div(cols, kBlock);
-    int64_t grid;
     if (block_rows == 1) {
-        const int64_t blocks = n_matrix * rows * nb;
-        grid = ceil_div(blocks, kThreads / (kBlock / (16 / sizeof(T))));
+        const int64_t blocks = n_matrix * rows * nb, grid = ceil_div(blocks, kRowsPerCta<T>);
         if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-        encode_rows_kernel<<<unsigned(grid), kThreads, 0, st>>>(m, codes, scales, blocks, cols, int(nb), pitch);
+        encode_rows_kernel<<<unsigned(grid), kThreads, 0, st>>>(m, codes, scales, blocks, cols, uint32_t(nb));
     } else {
-        const int64_t tiles_r = ceil_div(rows, kBlock);
-        grid = n_matrix * tiles_r * nb;
+        const int64_t tiles_r = ceil_div(rows, kBlock), grid = n_matrix * tiles_r * nb;
         if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
         encode_tiles_kernel<<<unsigned(grid), kThreads, 0, st>>>(m, codes, scales, rows, cols, nb, tiles_r);
     }
@@ -112,11 +155,21 @@ cudaError_t encode(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows,
 }  // namespace
 
 cudaError_t launch_encode_blocks(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, int dtype,
-                                 const void* m, uint8_t* codes, uint8_t* scales, int pitch, cudaStream_t st) {
-    return dtype == GR_F32 ? encode(n_matrix, rows, cols, block_rows, static_cast<const float*>(m), codes, scales,
-                                    pitch, st)
+                                 const void* m, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+    return dtype == GR_F32 ? encode(n_matrix, rows, cols, block_rows, static_cast<const float*>(m), codes, scales, st)
                            : encode(n_matrix, rows, cols, block_rows, static_cast<const __nv_bfloat16*>(m), codes,
-                                    scales, pitch, st);
+                                    scales, st);
+}
+
+cudaError_t launch_fp8_operands(const void* x, int64_t n, int64_t cols, uint8_t* codes, uint8_t* token_scales,
+                                const ScaleRows& a, const ScaleRows& b, cudaStream_t st) {
+    auto ctas = [](const ScaleRows& s) { return ceil_div(s.rows * ((s.blocks + 3) / 4), kThreads); };
+    const int64_t nb = ceil_div(cols, kBlock), blocks = x ? n * nb : 0;
+    const int64_t grid = ctas(a) + ctas(b) + ceil_div(blocks, kRowsPerCta<__nv_bfloat16>);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    fp8_operands_kernel<<<unsigned(grid), kThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), codes, token_scales,
+                                                             blocks, cols, uint32_t(nb), a, b, ctas(a), ctas(b));
+    return cudaGetLastError();
 }
 
 }  // namespace gr

@@ -11,16 +11,29 @@ constexpr int kBlock = 128;   // channels of an FP8 block
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A matrix in FP8 blocks: e4m3 codes [rows][k] and biased exponents [rows / block_rows][k / 128].
-struct Fp8Matrix {
-    const uint8_t* codes;
-    const uint8_t* scales;
-};
-
-// FP8 blocks of `n_matrix` matrices [rows][cols] (gr_blocks.cu). pitch: bytes from one row's scales to the next's
-// (blocks of one row).
+// FP8 blocks of `n_matrix` matrices [rows][cols] (gr_blocks.cu).
 cudaError_t launch_encode_blocks(int64_t n_matrix, int64_t rows, int64_t cols, int block_rows, int dtype,
-                                 const void* m, uint8_t* codes, uint8_t* scales, int pitch, cudaStream_t st);
+                                 const void* m, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+
+// Scales as the products on tensor cores take them: the tokens' in words of four blocks, 512 bytes for 128 rows with
+// row r's word at 16 (r % 32) + 4 (r / 32), [ceil(rows / 128)][scale_steps(k)][512]; the weights' in rows of whole words.
+inline int scale_steps(int64_t k) { return int(ceil_div(ceil_div(k, kBlock), 4)); }
+inline int scale_pitch(int64_t k) { return 4 * scale_steps(k); }
+inline size_t token_scale_bytes(int64_t rows, int64_t k) { return size_t(ceil_div(rows, kBlock)) * scale_steps(k) * 512; }
+struct Fp8Product {
+    const uint8_t *tokens, *token_scales, *weights, *weight_scales;
+};
+// Rows of scales [rows][blocks] to be laid out: as tokens, or with the weights' pitch.
+struct ScaleRows {
+    const uint8_t* from;
+    uint8_t* to;
+    int64_t rows;
+    int blocks;
+    bool tokens;
+};
+// Lays out up to two sets of scales and, where x is not null, encodes the bf16 rows x [n][cols] in blocks of one row.
+cudaError_t launch_fp8_operands(const void* x, int64_t n, int64_t cols, uint8_t* codes, uint8_t* token_scales,
+                                const ScaleRows& a, const ScaleRows& b, cudaStream_t st);
 
 // Products on CUDA cores (gr_feed_simt.cu). dtype: GR_F32, GR_BF16.
 // h = act(x Wgᵀ) ⊙ (x Wuᵀ), pre [N][2][F] unless null.
@@ -41,11 +54,12 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
                           void* dpre, void* h, float* ws, cudaStream_t st);
 cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const void* a, bool a_k, const void* b,
                        bool b_k, void* out, float* ws, cudaStream_t st);
-// On FP8 blocks: h in blocks of one row; out bf16. The pitches are those of scales of blocks of one row.
-cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, int x_pitch, Fp8Matrix w_in, uint8_t* h,
-                         uint8_t* hs, int hs_pitch, float* ws, cudaStream_t st, bool programmatic);
-cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, int a_pitch, Fp8Matrix b, void* out,
-                           float* ws, cudaStream_t st, bool programmatic);
+// On FP8 blocks, programmatic dependents of the launch that laid out their scales; h in blocks of one row, its
+// scales laid out as the tokens of the next product; out bf16.
+cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, const Fp8Product& in, uint8_t* h, uint8_t* hs, float* ws,
+                         cudaStream_t st);
+cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, const Fp8Product& in, void* out, float* ws,
+                           cudaStream_t st);
 size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K);
 size_t tc_feed_fp8_workspace(int64_t N, int D, int F);
 size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient);
@@ -53,6 +67,10 @@ size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient);
 int feed_status(bool clear);
 
 #ifdef __CUDACC__
+// The byte of a token's block among scales of `steps` steps.
+__device__ __forceinline__ int64_t scale_at(int64_t row, uint32_t block, int steps) {
+    return ((row >> 7) * steps + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (block & 3);
+}
 // The activations and their slopes in fp32 with the accurate expf and erff.
 template <int ACT> __device__ __forceinline__ float activate(float g) {
     if constexpr (ACT == GR_SILU) return g / (1.0f + expf(-g));

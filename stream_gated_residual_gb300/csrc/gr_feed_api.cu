@@ -83,18 +83,18 @@ struct FeedParts {
     float* parts = nullptr;                          // tensor cores: sums over ranges of k
     uint8_t *xc = nullptr, *xs = nullptr;            // FP8: x in blocks
     uint8_t *hc = nullptr, *hs = nullptr;            // and h
-    int xp = 0, hp = 0;                              // bytes of a row's scales
+    uint8_t *w_in = nullptr, *w_out = nullptr;       // and the weights' scales
     size_t bytes = 0;
     FeedParts(const gr_feed* f, bool gradient, void* base) {
         Parts w{static_cast<char*>(base)};
         const size_t N = size_t(f->n_tokens), D = size_t(f->d_model), F = size_t(f->d_ff);
         if (f->dtype == GR_FP8) {
-            // rows of scales in whole words, as the products read them fastest
-            xp = int(ceil_div(ceil_div(D, kBlock), 4) * 4), hp = int(ceil_div(ceil_div(F, kBlock), 4) * 4);
             xc = w.take<uint8_t>(N * D);
-            xs = w.take<uint8_t>(N * xp);
+            xs = w.take<uint8_t>(token_scale_bytes(N, D));
             hc = w.take<uint8_t>(N * F);
-            hs = w.take<uint8_t>(N * hp);
+            hs = w.take<uint8_t>(token_scale_bytes(N, F));
+            w_in = w.take<uint8_t>(2 * ceil_div(F, kBlock) * scale_pitch(D));
+            w_out = w.take<uint8_t>(ceil_div(D, kBlock) * scale_pitch(F));
             if (N > 0) parts = w.take<float>(tc_feed_fp8_workspace(f->n_tokens, f->d_model, f->d_ff));
         } else {
             h = w.take(N * F * width(f->dtype));
@@ -102,6 +102,20 @@ struct FeedParts {
             if (f->dtype == GR_BF16 && N > 0)
                 parts = w.take<float>(tc_feed_workspace(f->n_tokens, f->d_model, f->d_ff, gradient));
         }
+        bytes = w.used;
+    }
+};
+
+// gr_fp8_matmul: both operands' scales as the product takes them, and its parts.
+struct ProductParts {
+    uint8_t *a, *b;
+    float* parts;
+    size_t bytes;
+    ProductParts(const gr_product* p, void* base) {
+        Parts w{static_cast<char*>(base)};
+        a = w.take<uint8_t>(token_scale_bytes(p->n_tokens, p->d_in));
+        b = w.take<uint8_t>(ceil_div(p->d_out, kBlock) * scale_pitch(p->d_in));
+        parts = w.take<float>(tc_product_fp8_workspace(p->n_tokens, p->d_out, p->d_in));
         bytes = w.used;
     }
 };
@@ -192,15 +206,14 @@ int gr_fp8_encode_blocks(const gr_blocks* b, const void* m, uint8_t* codes, uint
     if (meet(in, c) || meet(in, s) || meet(c, s)) return GR_E_ALIAS;
     if ((st = usable_device())) return st;
     return as_status(launch_encode_blocks(b->n_matrix, b->n_rows, b->n_cols, b->block_rows, b->dtype, m, codes,
-                                          scales, int(ceil_div(b->n_cols, kBlock)),
-                                          static_cast<cudaStream_t>(stream)));
+                                          scales, static_cast<cudaStream_t>(stream)));
 }
 
 int gr_fp8_matmul_workspace_size(const gr_product* p, size_t* bytes) {
     const int st = check_product(p);
     if (st) return st;
     if (!bytes) return GR_E_NULL;
-    *bytes = p->n_tokens == 0 ? 0 : tc_product_fp8_workspace(p->n_tokens, p->d_out, p->d_in);
+    *bytes = p->n_tokens == 0 ? 0 : ProductParts(p, nullptr).bytes;
     return GR_OK;
 }
 
@@ -210,12 +223,16 @@ int gr_fp8_matmul(const gr_product* p, const uint8_t* a, const uint8_t* a_scales
     if (st) return st;
     if (p->n_tokens == 0) return GR_OK;
     const size_t N = size_t(p->n_tokens), K = size_t(p->d_in), O = size_t(p->d_out), nb = ceil_div(K, kBlock);
+    const ProductParts w(p, workspace);
     if ((st = check_buffers({{a, N * K}, {b, O * K}}, {{a_scales, N * nb}, {b_scales, ceil_div(O, kBlock) * nb}},
-                            {{out, N * O * 2}}, {workspace, tc_product_fp8_workspace(N, O, K)}, workspace_bytes)))
+                            {{out, N * O * 2}}, {workspace, w.bytes}, workspace_bytes)))
         return st;
     if ((st = usable_device())) return st;
-    return as_status(tc_product_fp8(N, O, K, {a, a_scales}, int(nb), {b, b_scales}, out,
-                                    static_cast<float*>(workspace), static_cast<cudaStream_t>(stream), false));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_fp8_operands(nullptr, 0, 0, nullptr, nullptr, {a_scales, w.a, int64_t(N), int(nb), true},
+                                        {b_scales, w.b, int64_t(ceil_div(O, kBlock)), int(nb), false}, s);
+    if (e == cudaSuccess) e = tc_product_fp8(N, O, K, {a, w.a, b, w.b}, out, w.parts, s);
+    return as_status(e);
 }
 
 int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, const uint8_t* w_in_scales,
@@ -234,12 +251,12 @@ int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, co
         return st;
     if ((st = usable_device())) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_encode_blocks(1, N, D, 1, GR_BF16, x, p.xc, p.xs, p.xp, s);
+    cudaError_t e = launch_fp8_operands(x, N, D, p.xc, p.xs,
+                                        {w_in_scales, p.w_in, int64_t(2 * fb), int(db), false},
+                                        {w_out_scales, p.w_out, int64_t(db), int(fb), false}, s);
     if (e == cudaSuccess)
-        e = tc_gated_fp8(N, D, F, f->activation, {p.xc, p.xs}, p.xp, {w_in, w_in_scales}, p.hc, p.hs, p.hp, p.parts,
-                         s, true);
-    if (e == cudaSuccess)
-        e = tc_product_fp8(N, D, F, {p.hc, p.hs}, p.hp, {w_out, w_out_scales}, y, p.parts, s, true);
+        e = tc_gated_fp8(N, D, F, f->activation, {p.xc, p.xs, w_in, p.w_in}, p.hc, p.hs, p.parts, s);
+    if (e == cudaSuccess) e = tc_product_fp8(N, D, F, {p.hc, p.hs, w_out, p.w_out}, y, p.parts, s);
     return as_status(e);
 }
 

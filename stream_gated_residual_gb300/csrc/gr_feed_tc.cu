@@ -61,6 +61,12 @@ __device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -78,7 +84,7 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block) {
 
 // ---- FP8 blocks: kind::mxf8f6f4 with a power-of-two scale for each row and 32 k ------------------
 // The scales lie in tensor memory: row r of 128 in column r / 32, lane r % 32 (of every quadrant), a byte for each
-// of four steps of k. Both operands e4m3; the descriptor names the byte.
+// of four blocks of k. Both operands e4m3; the descriptor names the byte.
 __device__ __forceinline__ uint32_t idesc_fp8(int N, int step) {
     return (uint32_t(step) << 4) | (uint32_t(N >> 3) << 17) | (1u << 23) | (16u << 24) | (uint32_t(step) << 29);
 }
@@ -108,15 +114,16 @@ enum Mode {
     kPart,     // C's sums over a range of k, fp32, to the workspace
 };
 
-// Where the scale bytes of an operand's rows lie: `per` rows a matrix, `block` rows a scale row.
+// The scales of a product's operands. The tokens' as the tensor cores take them: for each 128 rows and four blocks of
+// k 512 bytes, row r's word at 16 (r % 32) + 4 (r / 32). The weights' in rows of whole words, one for each `per` rows'
+// (a matrix') 128.
 struct Scales {
-    const uint8_t* p;
-    int64_t rows, per;
-    int block, pitch;
-    __device__ const uint8_t* at(int64_t row) const {
-        if (block == 1) return p + row * pitch;
-        const uint32_t r = uint32_t(row), m = uint32_t(per), which = r / m;
-        return p + int64_t(which * ((m + kBlock - 1) / kBlock) + (r - which * m) / kBlock) * pitch;
+    const uint8_t *tokens, *weights;
+    int64_t n_tokens, n_weights, per;
+    int pitch;
+    __device__ const uint8_t* weight_row(uint32_t row) const {
+        const uint32_t m = uint32_t(per), which = row / m;
+        return weights + int64_t(which * ((m + kBlock - 1) / kBlock) + (row - which * m) / kBlock) * pitch;
     }
 };
 
@@ -136,9 +143,9 @@ struct Args {
     int slots;              // partial tiles a pair may write
     float* part;
     int64_t rows, cols;     // of C (kGated: channels of h): boxes that start behind them are not stored
-    Scales sa, sb;          // FP8
-    uint8_t* hs;            // FP8 kGated: h's scales
-    int hs_pitch;
+    Scales scales;          // FP8
+    uint8_t* hs;            // FP8 kGated: h's scales, as a product's tokens
+    int hs_steps;
     const __nv_bfloat16* pre;   // kGrad
     __host__ __device__ uint32_t begin(uint32_t pair) const { return pair * range + (pair < longer ? pair : longer); }
     // The pair whose range holds a step.
@@ -159,14 +166,14 @@ constexpr uint32_t kColScales = 256;   // FP8: the scales' columns, behind the a
 constexpr int kScaleSlot = 512 + 1024; // of a step of four blocks: 128 rows of A, 256 of B
 constexpr int kTileM = 256, kRowsA = 128, kBoxA = kRowsA * 128;
 constexpr int kMaxStages = 12;
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 8;
 constexpr int kAuxBytes = 512, kAuxFp8 = 512 + 2048 + kScaleSlots * kScaleSlot;
 constexpr int kSmemMax = 232448;
 
-// Staging for the outputs of a warp: kStore and kGated one box of 32 rows x 64 columns, twice; kGrad three boxes
+// Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad three
 // of 32 rows x 32 columns.
-__host__ __device__ constexpr int stage_out(int mode) {
-    return mode == kPart ? 0 : mode == kGrad ? 3 * 2048 : 4096;
+__host__ __device__ constexpr int stage_out(int mode, bool fp8) {
+    return mode == kPart ? 0 : mode == kGrad ? 3 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
 }
 
 struct Aux {
@@ -241,7 +248,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 }
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
-// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGated); tmC2: dpre.
+// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGrad: to prefetch); tmC2: dpre.
 // FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
@@ -252,7 +259,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = kBoxA + box_b, stages = args.stages;
     uint8_t* out = sm + stages * stage;
-    Aux& x = *reinterpret_cast<Aux*>(out + 8 * stage_out(MODE));
+    Aux& x = *reinterpret_cast<Aux*>(out + 8 * stage_out(MODE, FP8));
     uint32_t* const tops = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&x) + kAuxBytes);
     uint8_t* const sf = reinterpret_cast<uint8_t*>(tops + 512);
     constexpr int kK = FP8 ? 128 : 64;
@@ -310,6 +317,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tma_pair_2d(pb, &tmB, kb * kK, n0, bar);
                 }
             };
+            // kGrad: the tile's gate and up values into the L2 while its sums are formed
+            auto prefetch_pre = [&](const Unit& t) {
+                if constexpr (MODE == kGrad) {
+                    const int m0 = t.m * kTileM + int(rank) * kRowsA;
+                    if (t.slot < 0 && m0 < args.rows) {
+                        tma_prefetch_3d(&tmC1, t.n * 256, 0, m0);
+                        tma_prefetch_3d(&tmC1, t.n * 256, 1, m0);
+                    }
+                }
+            };
             int ahead = 0;   // blocks of the first unit whose A is on its way already
             bool more = units.next(u);
             if (args.early && more) {
@@ -321,6 +338,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (; ok && more; more = units.next(u)) {
                 const int m0 = u.m * kTileM + int(rank) * kRowsA;
                 const int n0 = u.n * (MODE == kGated ? 128 : args.bn) + (MODE == kGated ? 0 : int(rank) * rows_b);
+                prefetch_pre(u);
                 for (int kb = u.k0; kb < u.k1; ++kb, ++g) {
                     const uint32_t s = g % stages;
                     if (g >= uint32_t(stages) && !mbar_wait(&x.empty[s], ((g / stages) - 1) & 1)) {
@@ -387,58 +405,58 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             mbar_wait(&x.done, 0);
         }
     } else if (FP8 && warp == 10) {
-        // Scales: four bytes (blocks) of 128 rows of A and bn of B into shared memory, where row r's word lies at
-        // 16 (r % 32) + 4 (r / 32) of its 128 rows; the copies of three steps are under way at once. Words are
-        // copied where a row's scales are whole words, else they are put together from bytes.
-        const Scales &sa = args.sa, &sb = args.sb;
-        const bool whole_a = ((reinterpret_cast<uintptr_t>(sa.p) | sa.pitch) & 3) == 0;
-        const bool whole_b = ((reinterpret_cast<uintptr_t>(sb.p) | sb.pitch) & 3) == 0;
-        // a lane's rows of a tile: where their scales begin, null behind the last row
-        const uint8_t *pa[4], *pb[8];
+        // Scales: a word (four blocks) for each of 128 rows of A and bn of B into shared memory, copies of several steps
+        // under way at once. Rows behind the last have any scales: their rows or columns of C may
+        // come out NaN, and are not stored.
+        constexpr bool kTokensB = MODE == kPart;   // else A's rows are the tokens
+        const Scales& sc = args.scales;
+        const uint32_t steps = args.steps;
+        const uint8_t* pw[8];   // the lane's rows of weights in the tile
+        int64_t t0 = 0;         // the tile's first token
         auto find = [&](const Unit& t) {
-            const int64_t m0 = int64_t(t.m) * kTileM + rank * kRowsA;
+            t0 = kTokensB ? int64_t(t.n) * args.bn : int64_t(t.m) * kTileM + rank * kRowsA;
+            const int64_t w0 = kTokensB ? int64_t(t.m) * kTileM + rank * kRowsA : int64_t(t.n) * args.bn;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = m0 + i * 32 + lane;
-                pa[i] = row < sa.rows ? sa.at(row) : nullptr;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < (kTokensB ? 4 : 8); ++i) {
                 const int r = i * 32 + lane;
-                int64_t row = int64_t(t.n) * args.bn + r;
+                int64_t row = w0 + r;
                 if (MODE == kGated) {
                     const int64_t ch = int64_t(t.n) * 128 + (r & 127);
-                    row = ch < sb.per ? ch + (r >> 7) * sb.per : sb.rows;
+                    row = ch < sc.per ? ch + (r >> 7) * sc.per : sc.n_weights;
                 }
-                pb[i] = r < args.bn && row < sb.rows ? sb.at(row) : nullptr;
+                pw[i] = row < sc.n_weights ? sc.weight_row(uint32_t(row)) : sc.weights;
             }
         };
-        auto word = [&](uint32_t to, const uint8_t* p, bool whole, int kb) {
-            if (p && whole) {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p + kb) : "memory");
-                return;
-            }
-            uint32_t v = p ? 0 : 0x7f7f7f7fu;   // rows behind the last are zero under any finite scale
-            if (p)
+        auto copy4 = [](uint32_t to, const uint8_t* p) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+        };
+        auto copy_step = [&](uint32_t at, int kb) {
+            const uint32_t st = uint32_t(kb) >> 2, w = kTokensB ? at : at + 512, to = kTokensB ? at + 512 : at;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (kb + i < args.nk) v |= uint32_t(p[kb + i]) << (8 * i);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+            for (int i = 0; i < (kTokensB ? 4 : 8); ++i) copy4(w + (i >> 2) * 512 + (i & 3) * 4, pw[i] + kb);
+            if constexpr (kTokensB) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t row = t0 + i * 32;   // 32 rows from a multiple of 32 on
+                    if (i * 32 < args.bn && row < sc.n_tokens)
+                        copy4(to + (i >> 2) * 512 + (i & 3) * 4,
+                              sc.tokens + ((row >> 7) * steps + st) * 512 + lane * 16 + ((row >> 5) & 3) * 4);
+                }
+            } else if (t0 < sc.n_tokens) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+                             "l"(sc.tokens + ((t0 >> 7) * steps + st) * 512 + lane * 16)
+                             : "memory");
+            }
         };
+        constexpr uint32_t kAhead = kScaleSlots - 2;
         uint32_t issued = 0;
         bool more = units.next(u), ok = true;
         int kb = u.k0;
         if (more) find(u);
         auto issue = [&]() {
-            const uint32_t slot = issued % kScaleSlots, at = smem_u32(sf) + slot * kScaleSlot + lane * 16;
+            const uint32_t slot = issued % kScaleSlots;
             if (issued >= kScaleSlots) ok = mbar_wait(&x.scales_empty[slot], ((issued / kScaleSlots) - 1) & 1);
-            if (ok) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) word(at + i * 4, pa[i], whole_a, kb);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i * 32 < args.bn) word(at + 512 + (i >> 2) * 512 + (i & 3) * 4, pb[i], whole_b, kb);
-            }
+            if (ok) copy_step(smem_u32(sf) + slot * kScaleSlot + lane * 16, kb);
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++issued;
             kb += 4;
@@ -449,12 +467,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         };
         for (uint32_t q = 0; ok; ++q) {
-            while (ok && more && issued < q + kScaleSlots - 1) issue();
+            while (ok && more && issued < q + kAhead) issue();
             if (!ok || q >= issued) break;
-            const uint32_t later = issued - q - 1;
-            if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-            else if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else asm volatile("cp.async.wait_group 2;" ::: "memory");
+            // the groups behind step q's may stay under way: kAhead - 1 of them, none once there are no more steps
+            if (issued == q + kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
             fence_async_shared();
             __syncwarp();
             if (lane == 0) arrive_remote(map_rank(smem_u32(&x.scales_full[q % kScaleSlots]), 0));
@@ -462,8 +479,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         const int w = warp - 2, half = w >> 2, quad = warp & 3;
-        const uint32_t mine = smem_u32(out) + w * stage_out(MODE);
-        uint8_t* const minep = out + w * stage_out(MODE);
+        const uint32_t mine = smem_u32(out) + w * stage_out(MODE, FP8);
+        uint8_t* const minep = out + w * stage_out(MODE, FP8);
         const uint32_t lanes = uint32_t(quad) << 21;   // lane field of a tensor-memory address: quad * 32 << 16
         // kGrad: gate and up of the next 32 channels of the thread's row, read ahead
         uint4 next[8];
@@ -567,6 +584,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int i = 0; i < 64; ++i) ga[i] = activate<GR_GELU>(ga[i]) * up[i];
                 }
                 if constexpr (FP8) {
+                    if (col + 64 > args.cols)   // channels behind the last are not the block's
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (col + i >= args.cols) ga[i] = 0.0f;
                     // the block's largest magnitude: this half's and the other's, from the warp that has the same rows
                     uint32_t top = 0;
 #pragma unroll
@@ -580,7 +601,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     float inv;
                     const uint8_t e = block_scale(top, inv);
                     if (half == 0 && row + lane < args.rows)
-                        args.hs[int64_t(row + lane) * args.hs_pitch + now.n] = e;
+                        args.hs[scale_at(row + lane, now.n, args.hs_steps)] = e;
                     if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
 #pragma unroll
@@ -693,7 +714,7 @@ struct JoinArgs {
     const __nv_bfloat16* pre;
     __nv_bfloat16* dpre;
     uint8_t *codes, *scales;     // h in FP8 blocks
-    int pitch;
+    int scale_steps;
 };
 
 // The sums at `at` (in fours) of the partial tiles of tile t (counted from the first that is not whole).
@@ -771,7 +792,7 @@ __device__ __forceinline__ void finish_fp8(const JoinArgs& j, int64_t token, int
 #pragma unroll
     for (int k = 0; k < N; k += 4)
         *reinterpret_cast<uint32_t*>(j.codes + token * j.rows + ch + k) = block_codes4(h + k, inv);
-    if ((ch & (kBlock - 1)) == 0) j.scales[token * j.pitch + ch / kBlock] = e;
+    if ((ch & (kBlock - 1)) == 0) j.scales[scale_at(token, uint32_t(ch / kBlock), j.scale_steps)] = e;
 }
 
 // After kPart: C's rows are the output's channels, contiguous, its columns the tokens. A thread has four rows of a
@@ -854,7 +875,9 @@ bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t co
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols * b) * 2};
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_b), cuuint32_t(box_a)};
     return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, strides, box,
-                   box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                   box_cols == 32   ? CU_TENSOR_MAP_SWIZZLE_64B
+                   : box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                    : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Codes [rows][cols] in boxes of 128 (64: h's) columns.
@@ -905,7 +928,7 @@ struct Operand {
 template <int MODE, bool FP8>
 int stages_for(int bn) {
     const int stage = kBoxA + bn / 2 * 128;
-    const int room = (kSmemMax - 1024 - (FP8 ? kAuxFp8 : kAuxBytes) - 8 * stage_out(MODE)) / stage;
+    const int room = (kSmemMax - 1024 - (FP8 ? kAuxFp8 : kAuxBytes) - 8 * stage_out(MODE, FP8)) / stage;
     return room > kMaxStages ? kMaxStages : room;
 }
 
@@ -937,7 +960,7 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
     }
     if (!ok) return cudaErrorInvalidValue;
     args.stages = stages_for<MODE, FP8>(args.bn);
-    const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE) +
+    const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
     return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
                   programmatic, ma, mb, c0, c1, c2, args);
@@ -1074,9 +1097,9 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
     if (p.columns) {
         e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p, kNone, kNone, kNone, st, false);
     } else {
-        CUtensorMap c, cd;
-        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32)) return cudaErrorInvalidValue;
-        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, kNone, cd, st, false);
+        CUtensorMap c, cp, cd;   // cp: only to prefetch whole tiles' rows
+        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cp, pre, N, 2, F, kRowsA, 1, 256) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32)) return cudaErrorInvalidValue;
+        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, cp, cd, st, false);
     }
     return e != cudaSuccess ? e : join<kJoinGrad>(p, j, st);
 }
@@ -1105,46 +1128,42 @@ size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient) {
 }
 
 // ---- FP8 ----
-cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, Fp8Matrix x, int x_pitch, Fp8Matrix w_in, uint8_t* h,
-                         uint8_t* hs, int hs_pitch, float* ws, cudaStream_t st, bool programmatic) {
-    const Scales sx{x.scales, N, N, 1, x_pitch}, sw{w_in.scales, 2 * int64_t(F), F, kBlock, int(ceil_div(D, kBlock))};
+cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, const Fp8Product& in, uint8_t* h, uint8_t* hs, float* ws,
+                         cudaStream_t st) {
     Plan p = plan_gated(N, D, F, true);
     p.a.part = ws, p.a.act = act;
+    p.a.scales = {in.token_scales, in.weight_scales, N, 2 * int64_t(F), F, scale_pitch(D)};
     JoinArgs j{};
-    j.codes = h, j.scales = hs, j.pitch = hs_pitch;
+    j.codes = h, j.scales = hs, j.scale_steps = scale_steps(F);
     j.rows = F, j.cols = N;
     cudaError_t e;
     if (p.columns) {
-        p.a.sa = sw, p.a.sb = sx;
-        e = launch_pairs<kPart, true, false, false>({w_in.codes, 2 * int64_t(F)}, {x.codes, N}, D, p, kNone, kNone, kNone,
-                                                    st, programmatic);
+        e = launch_pairs<kPart, true, false, false>({in.weights, 2 * int64_t(F)}, {in.tokens, N}, D, p, kNone, kNone, kNone,
+                                                    st, true);
     } else {
         CUtensorMap c;
         if (!map_codes(&c, h, N, F, 32, 64)) return cudaErrorInvalidValue;
-        p.a.sa = sx, p.a.sb = sw, p.a.hs = hs, p.a.hs_pitch = hs_pitch;
-        e = launch_pairs<kGated, true, false, false>({x.codes, N}, {w_in.codes, F}, D, p, c, kNone, kNone, st,
-                                                     programmatic);
+        p.a.hs = hs, p.a.hs_steps = scale_steps(F);
+        e = launch_pairs<kGated, true, false, false>({in.tokens, N}, {in.weights, F}, D, p, c, kNone, kNone, st, true);
     }
     return e != cudaSuccess ? e : join<kJoinGatedFp8>(p, j, st);
 }
 
-cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, Fp8Matrix a, int a_pitch, Fp8Matrix b, void* out,
-                           float* ws, cudaStream_t st, bool programmatic) {
-    const Scales sa{a.scales, N, N, 1, a_pitch}, sb{b.scales, O, O, kBlock, int(ceil_div(K, kBlock))};
+cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, const Fp8Product& in, void* out, float* ws,
+                           cudaStream_t st) {
     Plan p = plan_product(N, O, K, N, true);
     p.a.part = ws;
+    p.a.scales = {in.token_scales, in.weight_scales, N, O, O, scale_pitch(K)};
     JoinArgs j{};
     j.out = static_cast<__nv_bfloat16*>(out);
     j.rows = O, j.cols = N;
     cudaError_t e;
     if (p.columns) {
-        p.a.sa = sb, p.a.sb = sa;
-        e = launch_pairs<kPart, true, false, false>({b.codes, O}, {a.codes, N}, K, p, kNone, kNone, kNone, st, programmatic);
+        e = launch_pairs<kPart, true, false, false>({in.weights, O}, {in.tokens, N}, K, p, kNone, kNone, kNone, st, true);
     } else {
         CUtensorMap c;
         if (!map_bf16(&c, out, N, O, 32, 64)) return cudaErrorInvalidValue;
-        p.a.sa = sa, p.a.sb = sb;
-        e = launch_pairs<kStore, true, false, false>({a.codes, N}, {b.codes, O}, K, p, c, kNone, kNone, st, programmatic);
+        e = launch_pairs<kStore, true, false, false>({in.tokens, N}, {in.weights, O}, K, p, c, kNone, kNone, st, true);
     }
     return e != cudaSuccess ? e : join<kJoinStore>(p, j, st);
 }
