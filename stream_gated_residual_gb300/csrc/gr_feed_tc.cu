@@ -67,6 +67,37 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, 
                  "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
+// Bounded wait on a phase. Acquires at CTA scope: what is handed over here is TMA's, the tensor cores' or, scales, read
+// by them.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    long long t0 = 0;
+    for (int k = 0;; ++k) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (done) return true;
+        if (k == 0) t0 = clock64();
+        else if (clock64() - t0 > kWaitLimit) {
+            atomicOr(&g_wait_status, 1u);
+            return false;
+        }
+    }
+}
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait_on(bar, parity)); }
+// One lane of a warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -289,120 +320,127 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 
     Units<FP8 ? 4 : 1> units(args, cluster_id_x(), ncluster_x());
     Unit u;
+    // The producer's and the issuer's whole warps run their loops and one lane issues: descriptors and addresses stay in
+    // uniform registers (from a branch of one lane a stage took the issuer 1000 cycles, twice what its MMAs take).
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t bytes = 2u * uint32_t(stage);
-            uint32_t g = 0;
-            bool ok = true;
-            auto load_a = [&](uint32_t s, int m0, int kb) {
-                // the first CTA's barrier counts both CTAs' bytes
-                if (first) mbar_expect_tx(&x.full[s], bytes);
-                const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
-                uint8_t* pa = sm + s * stage;
-                if constexpr (A_MN) {
-                    tma_pair_2d(pa, &tmA, m0, kb * kK, bar);
-                    tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar);
-                } else {
-                    tma_pair_2d(pa, &tmA, kb * kK, m0, bar);
-                }
-            };
-            auto load_b = [&](uint32_t s, int n0, int kb) {
-                const uint32_t bar = map_rank(smem_u32(&x.full[s]), 0);
-                uint8_t* pb = sm + s * stage + kBoxA;
-                if constexpr (MODE == kGated) {
-                    tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar);
-                } else if constexpr (B_MN) {
-                    for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar);
-                } else {
-                    tma_pair_2d(pb, &tmB, kb * kK, n0, bar);
-                }
-            };
-            // kGrad: the tile's gate and up values into the L2 while its sums are formed
-            auto prefetch_pre = [&](const Unit& t) {
-                if constexpr (MODE == kGrad) {
-                    const int m0 = t.m * kTileM + int(rank) * kRowsA;
-                    if (t.slot < 0 && m0 < args.rows) {
-                        tma_prefetch_3d(&tmC1, t.n * 256, 0, m0);
-                        tma_prefetch_3d(&tmC1, t.n * 256, 1, m0);
-                    }
-                }
-            };
-            int ahead = 0;   // blocks of the first unit whose A is on its way already
-            bool more = units.next(u);
-            if (args.early && more) {
-                for (; ahead < stages && u.k0 + ahead < u.k1; ++ahead)
-                    load_a(ahead, u.m * kTileM + int(rank) * kRowsA, u.k0 + ahead);
+        const bool leader = elect_one();
+        const uint32_t bytes = 2u * uint32_t(stage);
+        const uint32_t bar0 = map_rank(smem_u32(&x.full[0]), 0);   // the first CTA's barriers count both CTAs' bytes
+        uint32_t g = 0, s = 0, lap = 0;                            // block, its stage, how often the ring went round
+        auto load_a = [&](uint32_t s, int m0, int kb) {
+            if (first) mbar_expect_tx(&x.full[s], bytes);
+            uint8_t* pa = sm + s * stage;
+            if constexpr (A_MN) {
+                tma_pair_2d(pa, &tmA, m0, kb * kK, bar0 + s * 8);
+                tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar0 + s * 8);
+            } else {
+                tma_pair_2d(pa, &tmA, kb * kK, m0, bar0 + s * 8);
             }
-            dep_wait();
-            fence_async_global();
-            for (; ok && more; more = units.next(u)) {
-                const int m0 = u.m * kTileM + int(rank) * kRowsA;
-                const int n0 = u.n * (MODE == kGated ? 128 : args.bn) + (MODE == kGated ? 0 : int(rank) * rows_b);
-                prefetch_pre(u);
-                for (int kb = u.k0; kb < u.k1; ++kb, ++g) {
-                    const uint32_t s = g % stages;
-                    if (g >= uint32_t(stages) && !mbar_wait(&x.empty[s], ((g / stages) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
+        };
+        auto load_b = [&](uint32_t s, int n0, int kb) {
+            uint8_t* pb = sm + s * stage + kBoxA;
+            if constexpr (MODE == kGated) {
+                tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar0 + s * 8);
+            } else if constexpr (B_MN) {
+                for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar0 + s * 8);
+            } else {
+                tma_pair_2d(pb, &tmB, kb * kK, n0, bar0 + s * 8);
+            }
+        };
+        bool more = units.next(u);
+        int ahead = 0;   // blocks of the first unit whose A is on its way already
+        if (args.early && more) {
+            const int m0 = uniform(u.m * kTileM + int(rank) * kRowsA), k0 = uniform(u.k0);
+            ahead = min(stages, uniform(u.k1) - k0);
+            if (leader)
+                for (int i = 0; i < ahead; ++i) load_a(i, m0, k0 + i);
+        }
+        dep_wait();
+        fence_async_global();
+        for (bool ok = true; ok && more; more = units.next(u)) {
+            const int m0 = uniform(u.m * kTileM + int(rank) * kRowsA);
+            const int n0 = uniform(u.n * (MODE == kGated ? 128 : args.bn) + (MODE == kGated ? 0 : int(rank) * rows_b));
+            const int k0 = uniform(u.k0), k1 = uniform(u.k1);
+            // the tile's gate and up values into the L2 while its sums are formed
+            if constexpr (MODE == kGrad) {
+                if (leader && u.slot < 0 && m0 < args.rows) {
+                    tma_prefetch_3d(&tmC1, n0 - int(rank) * rows_b, 0, m0);
+                    tma_prefetch_3d(&tmC1, n0 - int(rank) * rows_b, 1, m0);
+                }
+            }
+            for (int kb = k0; kb < k1; ++kb, ++g) {
+                if (lap > 0 && !wait_warp(&x.empty[s], (lap - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
                     if (g >= uint32_t(ahead)) load_a(s, m0, kb);
                     load_b(s, n0, kb);
                 }
+                if (++s == uint32_t(stages)) s = 0, ++lap;
             }
-            // no copy is under way when the CTAs leave: the first CTA sees both CTAs' arrive
-            if (first)
-                for (uint32_t i = g > uint32_t(stages) ? g - stages : 0; i < g; ++i)
-                    mbar_wait(&x.full[i % stages], (i / stages) & 1);
         }
+        // no copy is under way when the CTAs leave: the first CTA sees both CTAs' arrive
+        if (first)
+            for (uint32_t i = g > uint32_t(stages) ? g - stages : 0; i < g; ++i)
+                wait_warp(&x.full[i % stages], (i / stages) & 1);
     } else if (warp == 1) {
-        if (first && lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(256, args.bn) | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0);
-            uint32_t g = 0, q = 0;
+        if (first) {
+            const bool leader = elect_one();
+            const uint32_t idesc = FP8 ? idesc_fp8(args.bn, 0)
+                                       : idesc_bf16_f32(256, args.bn) | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0);
+            const uint32_t base = smem_u32(sm), sf0 = smem_u32(sf), copies = 1 + (args.bn + 127) / 128;
+            const uint64_t da0 = A_MN ? sdesc_mn(base, 8192) : sdesc_sw128(base);
+            const uint64_t db0 = B_MN ? sdesc_mn(base + kBoxA, 8192) : sdesc_sw128(base + kBoxA);
+            const uint32_t hop = uint32_t(stage) >> 4;   // from a stage to the next, in a descriptor
+            uint32_t s = 0, lap = 0, q = 0;              // stage, laps, steps of scales
             bool ok = true;
             for (int j = 0; ok && units.next(u); ++j) {
-                const int b = j % accs;
-                if (j >= accs && !mbar_wait(&x.acc_empty[b], (j / accs - 1) & 1)) break;
+                const int b = j % accs, blocks = uniform(u.k1 - u.k0);
+                if (j >= accs && !wait_warp(&x.acc_empty[b], (j / accs - 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + b * acc_cols;
-                for (int kb = u.k0; kb < u.k1; ++kb, ++g) {
-                    const uint32_t s = g % stages, step = uint32_t(kb - u.k0) & 3;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    const uint32_t step = uint32_t(kb) & 3;
                     if (FP8 && step == 0) {
                         // the scales of this and the next three blocks; the copies run in order with the MMAs
-                        if (!mbar_wait(&x.scales_full[q % kScaleSlots], (q / kScaleSlots) & 1)) {
+                        if (!wait_warp(&x.scales_full[q % kScaleSlots], (q / kScaleSlots) & 1)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t at = smem_u32(sf) + (q % kScaleSlots) * kScaleSlot,
-                                       to = tmem + kColScales + (q & 1) * 16;
-                        for (int i = 0; i < 1 + (args.bn + 127) / 128; ++i) tc_copy_scales(to + i * 4, at + i * 512);
+                        if (leader)
+                            for (uint32_t i = 0; i < copies; ++i)
+                                tc_copy_scales(tmem + kColScales + (q & 1) * 16 + i * 4,
+                                               sf0 + (q % kScaleSlots) * kScaleSlot + i * 512);
                         ++q;
                     }
-                    if (!mbar_wait(&x.full[s], (g / stages) & 1)) {
+                    if (!wait_warp(&x.full[s], lap & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t pa = smem_u32(sm + s * stage), pb = pa + kBoxA;
+                    if (leader) {
+                        const uint64_t da = da0 + s * hop, db = db0 + s * hop;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (FP8) {
-                            const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
-                            tc_mma2_fp8(d, sdesc_sw128(pa + k * 32), sdesc_sw128(pb + k * 32),
-                                        idesc_fp8(args.bn, int(step)), sfa, sfa + 4, kb > u.k0 || k > 0);
-                        } else {
-                            tc_mma2(d, A_MN ? sdesc_mn(pa + k * 2048, 8192) : sdesc_sw128(pa + k * 32),
-                                    B_MN ? sdesc_mn(pb + k * 2048, 8192) : sdesc_sw128(pb + k * 32), idesc,
-                                    kb > u.k0 || k > 0);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t a = da + k * (A_MN ? 128 : 2), bb = db + k * (B_MN ? 128 : 2);
+                            if constexpr (FP8) {
+                                const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
+                                tc_mma2_fp8(d, a, bb, idesc | (step << 4) | (step << 29), sfa, sfa + 4, kb > 0 || k > 0);
+                            } else {
+                                tc_mma2(d, a, bb, idesc, kb > 0 || k > 0);
+                            }
                         }
+                        tc_commit2(&x.empty[s]);
+                        if (FP8 && (step == 3 || kb + 1 == blocks)) tc_commit2(&x.scales_empty[(q - 1) % kScaleSlots]);
                     }
-                    tc_commit2(&x.empty[s]);
-                    if (FP8 && (step == 3 || kb + 1 == u.k1)) tc_commit2(&x.scales_empty[(q - 1) % kScaleSlots]);
+                    if (++s == uint32_t(stages)) s = 0, ++lap;
                 }
-                if (ok) tc_commit2(&x.acc_full[b]);
+                if (ok && leader) tc_commit2(&x.acc_full[b]);
             }
-            tc_commit2(&x.done);
-            mbar_wait(&x.done, 0);
+            if (leader) tc_commit2(&x.done);
+            wait_warp(&x.done, 0);
         }
     } else if (FP8 && warp == 10) {
         // Scales: a word (four blocks) for each of 128 rows of A and bn of B into shared memory, copies of several steps
@@ -455,7 +493,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (more) find(u);
         auto issue = [&]() {
             const uint32_t slot = issued % kScaleSlots;
-            if (issued >= kScaleSlots) ok = mbar_wait(&x.scales_empty[slot], ((issued / kScaleSlots) - 1) & 1);
+            if (issued >= kScaleSlots) ok = wait_on(&x.scales_empty[slot], ((issued / kScaleSlots) - 1) & 1);
             if (ok) copy_step(smem_u32(sf) + slot * kScaleSlot + lane * 16, kb);
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++issued;
@@ -499,7 +537,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int j = 0; more; ++j) {
             const int b = j % accs;
             const Unit now = u;
-            if (!mbar_wait(&x.acc_full[b], (j / accs) & 1)) break;
+            if (!wait_on(&x.acc_full[b], (j / accs) & 1)) break;
             tc_fence_after();
             const uint32_t acc = tmem + b * acc_cols + lanes;
             const int row = row_of(now);   // the warp's first
@@ -596,7 +634,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     t[half * 128] = top;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&x.top_full[quad]);
-                    if (!mbar_wait(&x.top_full[quad], j & 1)) break;
+                    if (!wait_on(&x.top_full[quad], j & 1)) break;
                     top = max(top, *const_cast<volatile uint32_t*>(t + (half ^ 1) * 128));
                     float inv;
                     const uint8_t e = block_scale(top, inv);
