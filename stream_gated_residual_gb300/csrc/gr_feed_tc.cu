@@ -177,7 +177,6 @@ struct Args {
     Scales scales;          // FP8
     uint8_t* hs;            // FP8 kGated: h's scales, as a product's tokens
     int hs_steps;
-    const __nv_bfloat16* pre;   // kGrad
     __host__ __device__ uint32_t begin(uint32_t pair) const { return pair * range + (pair < longer ? pair : longer); }
     // The pair whose range holds a step.
     __device__ uint32_t owner(uint32_t step) const {
@@ -198,18 +197,18 @@ constexpr int kScaleSlot = 512 + 1024; // of a step of four blocks: 128 rows of 
 constexpr int kTileM = 256, kRowsA = 128, kBoxA = kRowsA * 128;
 constexpr int kMaxStages = 12;
 constexpr int kScaleSlots = 8;
-constexpr int kAuxBytes = 512, kAuxFp8 = 512 + 2048 + kScaleSlots * kScaleSlot;
+constexpr int kAuxBytes = 640, kAuxFp8 = kAuxBytes + 2048 + kScaleSlots * kScaleSlot;
 constexpr int kSmemMax = 232448;
 
-// Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad three
-// of 32 rows x 32 columns.
+// Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad two
+// sets of three boxes of 32 rows x 32 columns.
 __host__ __device__ constexpr int stage_out(int mode, bool fp8) {
-    return mode == kPart ? 0 : mode == kGrad ? 3 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
+    return mode == kPart ? 0 : mode == kGrad ? 2 * 3 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
 }
 
 struct Aux {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2], done;
+    uint64_t acc_full[2], acc_empty[2], done, loaded[8][2];
     uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots], top_full[4];
     uint32_t tmem;
 };
@@ -269,6 +268,14 @@ __device__ __forceinline__ void st_shared16(uint32_t at, const uint4& v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -279,13 +286,14 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 }
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
-// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGrad: to prefetch); tmC2: dpre.
+// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGrad: to prefetch); tmC2: dpre; tmC3: pre.
 // FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-            const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ Args args) {
+            const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ CUtensorMap tmC3,
+            const __grid_constant__ Args args) {
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = kBoxA + box_b, stages = args.stages;
@@ -305,6 +313,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int b = 0; b < 2; ++b) mbar_init(&x.acc_full[b], 1), mbar_init(&x.acc_empty[b], 16);
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&x.scales_full[i], 2), mbar_init(&x.scales_empty[i], 1);
         for (int q = 0; q < 4; ++q) mbar_init(&x.top_full[q], 2);
+        for (int w = 0; w < 8; ++w) mbar_init(&x.loaded[w][0], 1), mbar_init(&x.loaded[w][1], 1);
         mbar_init(&x.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -520,20 +529,24 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         const uint32_t mine = smem_u32(out) + w * stage_out(MODE, FP8);
         uint8_t* const minep = out + w * stage_out(MODE, FP8);
         const uint32_t lanes = uint32_t(quad) << 21;   // lane field of a tensor-memory address: quad * 32 << 16
-        // kGrad: gate and up of the next 32 channels of the thread's row, read ahead
-        uint4 next[8];
-        auto load_pre = [&](int64_t row, int ch) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                next[i] = make_uint4(0, 0, 0, 0);
-                const int c = ch + (i & 3) * 8;
-                if (row < args.rows && c < args.cols)
-                    next[i] = __ldcs(reinterpret_cast<const uint4*>(args.pre + (2 * row + (i >> 2)) * args.cols + c));
-            }
-        };
         auto row_of = [&](const Unit& t) { return t.m * kTileM + int(rank) * kRowsA + quad * 32; };
+        // kGrad: gate and up of 32 channels of the warp's rows into one of two sets of boxes, which dgate, dup and h
+        // leave from. The set's last stores have read it by then.
+        uint32_t reads = 0, used = 0;
+        auto read_pre = [&](int row, int ch) {
+            uint8_t* to = minep + (reads & 1) * 6144;
+            if (lane == 0) {
+                mbar_expect_tx(&x.loaded[w][reads & 1], 4096);
+                tma_load_3d(to, &tmC3, ch, 0, row, &x.loaded[w][reads & 1]);
+                tma_load_3d(to + 2048, &tmC3, ch, 1, row, &x.loaded[w][reads & 1]);
+            }
+            ++reads;
+        };
         bool more = units.next(u);
-        if (MODE == kGrad && more) load_pre(int64_t(row_of(u)) + lane, u.n * 256 + half * 128);
+        if (MODE == kGrad && more && u.slot < 0) {
+            read_pre(row_of(u), u.n * 256 + half * 128);
+            read_pre(row_of(u), u.n * 256 + half * 128 + 32);
+        }
         for (int j = 0; more; ++j) {
             const int b = j % accs;
             const Unit now = u;
@@ -661,6 +674,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 Units<1> peek = units;
                 Unit after;
                 const bool follows = peek.next(after) && after.slot < 0;
+                bool ok = true;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     float dh[32];
@@ -676,20 +690,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
                     if (i == 3) drained();
-                    uint4 pre[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) pre[k] = next[k];
-                    if (i < 3)
-                        load_pre(int64_t(row) + lane, col + (i + 1) * 32);
-                    else if (follows)
-                        load_pre(int64_t(row_of(after)) + lane, after.n * 256 + half * 128);
-                    if (lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
+                    const uint32_t set = used & 1, box = mine + set * 6144;
+                    uint8_t* const boxp = minep + set * 6144;
+                    ok = ok && wait_on(&x.loaded[w][set], (used >> 1) & 1);
+                    ++used;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float g[8], p[8], a[8], s[8];
-                        unpack8(pre[c], g);
-                        unpack8(pre[4 + c], p);
+                        unpack8(ld_shared16(box + swz64(lane, c)), g);
+                        unpack8(ld_shared16(box + 2048 + swz64(lane, c)), p);
                         if (args.act == GR_SILU) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) act_both(GR_SILU, g[k], a[k], s[k]);
@@ -705,21 +714,28 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                         uint4 v;
                         pack8(v, s);
-                        st_shared16(mine + swz64(lane, c), v);
+                        st_shared16(box + swz64(lane, c), v);
                         pack8(v, a);
-                        st_shared16(mine + 2048 + swz64(lane, c), v);
+                        st_shared16(box + 2048 + swz64(lane, c), v);
                         pack8(v, p);
-                        st_shared16(mine + 4096 + swz64(lane, c), v);
+                        st_shared16(box + 4096 + swz64(lane, c), v);
                     }
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0 && row < args.rows && col + i * 32 < args.cols) {
-                        tma_store_3d(&tmC2, minep, col + i * 32, 0, row);
-                        tma_store_3d(&tmC2, minep + 2048, col + i * 32, 1, row);
-                        tma_store_2d(&tmC0, minep + 4096, col + i * 32, row);
+                    if (lane == 0 && ok && row < args.rows && col + i * 32 < args.cols) {
+                        tma_store_3d(&tmC2, boxp, col + i * 32, 0, row);
+                        tma_store_3d(&tmC2, boxp + 2048, col + i * 32, 1, row);
+                        tma_store_2d(&tmC0, boxp + 4096, col + i * 32, row);
                         bulk_commit();
                     }
+                    // two chunks on, in this tile or the next whole one
+                    if (i < 2 || follows) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        if (i < 2) read_pre(row, col + (i + 2) * 32);
+                        else read_pre(row_of(after), after.n * 256 + half * 128 + (i - 2) * 32);
+                    }
                 }
+                if (!ok) break;
             } else {
                 float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
                            int(rank) * kRowsA + quad * 32 + lane;
@@ -733,6 +749,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             more = units.next(u);
         }
+        for (; used < reads; ++used) wait_on(&x.loaded[w][used & 1], (used >> 1) & 1);   // after a wait that ran out
         if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
@@ -981,7 +998,8 @@ struct Plan {
 
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Plan& p, const CUtensorMap& c0,
-                         const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic) {
+                         const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic,
+                         const CUtensorMap& c3 = {}) {
     CUtensorMap ma, mb;
     Args args = p.a;
     const int rows_b = args.bn / 2;
@@ -1001,7 +1019,7 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
     const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
     return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
-                  programmatic, ma, mb, c0, c1, c2, args);
+                  programmatic, ma, mb, c0, c1, c2, c3, args);
 }
 
 // ---- plans ----
@@ -1127,17 +1145,19 @@ cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void
 cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, const void* w_out, const void* pre,
                           void* dpre, void* h, float* ws, cudaStream_t st) {
     Plan p = plan_grad(N, D, F);
-    p.a.part = ws, p.a.act = act, p.a.pre = static_cast<const __nv_bfloat16*>(pre);
+    p.a.part = ws, p.a.act = act;
     JoinArgs j{};
-    j.out = static_cast<__nv_bfloat16*>(h), j.dpre = static_cast<__nv_bfloat16*>(dpre), j.pre = p.a.pre;
+    j.out = static_cast<__nv_bfloat16*>(h), j.dpre = static_cast<__nv_bfloat16*>(dpre), j.pre = static_cast<const __nv_bfloat16*>(pre);
     j.rows = F, j.cols = N;
     cudaError_t e;
     if (p.columns) {
         e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p, kNone, kNone, kNone, st, false);
     } else {
-        CUtensorMap c, cp, cd;   // cp: only to prefetch whole tiles' rows
-        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cp, pre, N, 2, F, kRowsA, 1, 256) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32)) return cudaErrorInvalidValue;
-        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, cp, cd, st, false);
+        CUtensorMap c, cp, cd, cr;   // cp: only to prefetch whole tiles' rows
+        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cp, pre, N, 2, F, kRowsA, 1, 256) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32) ||
+            !map_bf16_3d(&cr, pre, N, 2, F, 32, 1, 32))
+            return cudaErrorInvalidValue;
+        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, cp, cd, st, false, cr);
     }
     return e != cudaSuccess ? e : join<kJoinGrad>(p, j, st);
 }
