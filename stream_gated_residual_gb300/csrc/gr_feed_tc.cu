@@ -61,12 +61,6 @@ __device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
 // Bounded wait on a phase. Acquires at CTA scope: what is handed over here is TMA's, the tensor cores' or, scales, read
 // by them.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
@@ -177,6 +171,7 @@ struct Args {
     Scales scales;          // FP8
     uint8_t* hs;            // FP8 kGated: h's scales, as a product's tokens
     int hs_steps;
+    __nv_bfloat16* h;       // kGrad
     __host__ __device__ uint32_t begin(uint32_t pair) const { return pair * range + (pair < longer ? pair : longer); }
     // The pair whose range holds a step.
     __device__ uint32_t owner(uint32_t step) const {
@@ -201,9 +196,9 @@ constexpr int kAuxBytes = 640, kAuxFp8 = kAuxBytes + 2048 + kScaleSlots * kScale
 constexpr int kSmemMax = 232448;
 
 // Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad two
-// sets of three boxes of 32 rows x 32 columns.
+// pairs of boxes of 32 rows x 32 columns.
 __host__ __device__ constexpr int stage_out(int mode, bool fp8) {
-    return mode == kPart ? 0 : mode == kGrad ? 2 * 3 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
+    return mode == kPart ? 0 : mode == kGrad ? 2 * 2 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
 }
 
 struct Aux {
@@ -286,14 +281,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 }
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
-// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre (kGrad: to prefetch); tmC2: dpre; tmC3: pre.
-// FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
+// channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre; tmC2: dpre.
+// FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes. kGrad: no tmC0.
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-            const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ CUtensorMap tmC3,
-            const __grid_constant__ Args args) {
+            const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ Args args) {
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = kBoxA + box_b, stages = args.stages;
@@ -370,13 +364,6 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const int m0 = uniform(u.m * kTileM + int(rank) * kRowsA);
             const int n0 = uniform(u.n * (MODE == kGated ? 128 : args.bn) + (MODE == kGated ? 0 : int(rank) * rows_b));
             const int k0 = uniform(u.k0), k1 = uniform(u.k1);
-            // the tile's gate and up values into the L2 while its sums are formed
-            if constexpr (MODE == kGrad) {
-                if (leader && u.slot < 0 && m0 < args.rows) {
-                    tma_prefetch_3d(&tmC1, n0 - int(rank) * rows_b, 0, m0);
-                    tma_prefetch_3d(&tmC1, n0 - int(rank) * rows_b, 1, m0);
-                }
-            }
             for (int kb = k0; kb < k1; ++kb, ++g) {
                 if (lap > 0 && !wait_warp(&x.empty[s], (lap - 1) & 1)) {
                     ok = false;
@@ -530,15 +517,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint8_t* const minep = out + w * stage_out(MODE, FP8);
         const uint32_t lanes = uint32_t(quad) << 21;   // lane field of a tensor-memory address: quad * 32 << 16
         auto row_of = [&](const Unit& t) { return t.m * kTileM + int(rank) * kRowsA + quad * 32; };
-        // kGrad: gate and up of 32 channels of the warp's rows into one of two sets of boxes, which dgate, dup and h
-        // leave from. The set's last stores have read it by then.
+        // kGrad: gate and up of 32 channels of the warp's rows into one of two sets of boxes, which dgate and dup leave
+        // from. The set's last stores have read it by then.
         uint32_t reads = 0, used = 0;
         auto read_pre = [&](int row, int ch) {
-            uint8_t* to = minep + (reads & 1) * 6144;
+            uint8_t* to = minep + (reads & 1) * 4096;
             if (lane == 0) {
                 mbar_expect_tx(&x.loaded[w][reads & 1], 4096);
-                tma_load_3d(to, &tmC3, ch, 0, row, &x.loaded[w][reads & 1]);
-                tma_load_3d(to + 2048, &tmC3, ch, 1, row, &x.loaded[w][reads & 1]);
+                tma_load_3d(to, &tmC1, ch, 0, row, &x.loaded[w][reads & 1]);
+                tma_load_3d(to + 2048, &tmC1, ch, 1, row, &x.loaded[w][reads & 1]);
             }
             ++reads;
         };
@@ -690,8 +677,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
                     if (i == 3) drained();
-                    const uint32_t set = used & 1, box = mine + set * 6144;
-                    uint8_t* const boxp = minep + set * 6144;
+                    const uint32_t set = used & 1, box = mine + set * 4096;
+                    uint8_t* const boxp = minep + set * 4096;
                     ok = ok && wait_on(&x.loaded[w][set], (used >> 1) & 1);
                     ++used;
 #pragma unroll
@@ -717,15 +704,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         st_shared16(box + swz64(lane, c), v);
                         pack8(v, a);
                         st_shared16(box + 2048 + swz64(lane, c), v);
+                        // h straight from the registers: a third box would cost the ring a stage
                         pack8(v, p);
-                        st_shared16(box + 4096 + swz64(lane, c), v);
+                        const int ch = col + i * 32 + c * 8;
+                        if (row + lane < args.rows && ch < args.cols)
+                            __stcs(reinterpret_cast<uint4*>(args.h + int64_t(row + lane) * args.cols + ch), v);
                     }
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0 && ok && row < args.rows && col + i * 32 < args.cols) {
                         tma_store_3d(&tmC2, boxp, col + i * 32, 0, row);
                         tma_store_3d(&tmC2, boxp + 2048, col + i * 32, 1, row);
-                        tma_store_2d(&tmC0, boxp + 4096, col + i * 32, row);
                         bulk_commit();
                     }
                     // two chunks on, in this tile or the next whole one
@@ -930,9 +919,7 @@ bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t co
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols * b) * 2};
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_b), cuuint32_t(box_a)};
     return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, strides, box,
-                   box_cols == 32   ? CU_TENSOR_MAP_SWIZZLE_64B
-                   : box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                    : CU_TENSOR_MAP_SWIZZLE_NONE);
+                   box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Codes [rows][cols] in boxes of 128 (64: h's) columns.
@@ -998,8 +985,7 @@ struct Plan {
 
 template <int MODE, bool FP8, bool A_MN, bool B_MN>
 cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Plan& p, const CUtensorMap& c0,
-                         const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic,
-                         const CUtensorMap& c3 = {}) {
+                         const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic) {
     CUtensorMap ma, mb;
     Args args = p.a;
     const int rows_b = args.bn / 2;
@@ -1019,7 +1005,7 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
     const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
     return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
-                  programmatic, ma, mb, c0, c1, c2, c3, args);
+                  programmatic, ma, mb, c0, c1, c2, args);
 }
 
 // ---- plans ----
@@ -1145,7 +1131,7 @@ cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void
 cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, const void* w_out, const void* pre,
                           void* dpre, void* h, float* ws, cudaStream_t st) {
     Plan p = plan_grad(N, D, F);
-    p.a.part = ws, p.a.act = act;
+    p.a.part = ws, p.a.act = act, p.a.h = static_cast<__nv_bfloat16*>(h);
     JoinArgs j{};
     j.out = static_cast<__nv_bfloat16*>(h), j.dpre = static_cast<__nv_bfloat16*>(dpre), j.pre = static_cast<const __nv_bfloat16*>(pre);
     j.rows = F, j.cols = N;
@@ -1153,11 +1139,10 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
     if (p.columns) {
         e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p, kNone, kNone, kNone, st, false);
     } else {
-        CUtensorMap c, cp, cd, cr;   // cp: only to prefetch whole tiles' rows
-        if (!map_bf16(&c, h, N, F, 32, 32) || !map_bf16_3d(&cp, pre, N, 2, F, kRowsA, 1, 256) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32) ||
-            !map_bf16_3d(&cr, pre, N, 2, F, 32, 1, 32))
+        CUtensorMap cp, cd;
+        if (!map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 32) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32))
             return cudaErrorInvalidValue;
-        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, cp, cd, st, false, cr);
+        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, kNone, cp, cd, st, false);
     }
     return e != cudaSuccess ? e : join<kJoinGrad>(p, j, st);
 }
