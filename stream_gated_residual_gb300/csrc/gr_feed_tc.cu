@@ -761,27 +761,39 @@ struct JoinArgs {
     int scale_steps;
 };
 
-// The sums at `at` (in fours) of the partial tiles of tile t (counted from the first that is not whole).
-template <int FOURS>
-__device__ __forceinline__ void joined(const Args& a, uint32_t t, int64_t at, float (&v)[4 * FOURS]) {
-    const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
-    const int64_t tile = int64_t(kTileM) * a.bn / 4;
-    const float4* p = reinterpret_cast<const float4*>(a.part) + at;
-    const float4* q = p + (int64_t(first) * a.slots + (t - a.begin(first) / a.steps)) * tile;
-    float4 s[FOURS];
-#pragma unroll
-    for (int i = 0; i < FOURS; ++i) s[i] = __ldcs(q + i);
-#pragma unroll 4
-    for (uint32_t c = first + 1; c <= last; ++c) {
-#pragma unroll
-        for (int i = 0; i < FOURS; ++i) {
-            const float4 w = __ldcs(p + int64_t(c) * a.slots * tile + i);
-            s[i].x += w.x, s[i].y += w.y, s[i].z += w.z, s[i].w += w.w;
-        }
+// Where the partial sums of one place of a tile lie (t counted from the first that is not whole, `at` in fours): found
+// before the products are waited for.
+struct Sums {
+    const float4 *from, *rest;
+    int64_t hop;
+    uint32_t more;
+    __device__ Sums(const Args& a, uint32_t t, int64_t at) {
+        const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
+        const int64_t tile = int64_t(kTileM) * a.bn / 4;
+        hop = a.slots * tile;
+        const float4* p = reinterpret_cast<const float4*>(a.part) + at;
+        from = p + first * hop + (t - a.begin(first) / a.steps) * tile;
+        rest = p + (first + 1) * hop;
+        more = last - first;
     }
+    template <int FOURS> __device__ __forceinline__ void add(float (&v)[4 * FOURS]) const {
+        float4 s[FOURS];
 #pragma unroll
-    for (int i = 0; i < FOURS; ++i) v[4 * i] = s[i].x, v[4 * i + 1] = s[i].y, v[4 * i + 2] = s[i].z, v[4 * i + 3] = s[i].w;
-}
+        for (int i = 0; i < FOURS; ++i) s[i] = __ldcg(from + i);
+        const float4* q = rest;
+#pragma unroll 4
+        for (uint32_t c = 0; c < more; ++c, q += hop) {
+#pragma unroll
+            for (int i = 0; i < FOURS; ++i) {
+                const float4 w = __ldcg(q + i);
+                s[i].x += w.x, s[i].y += w.y, s[i].z += w.z, s[i].w += w.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FOURS; ++i)
+            v[4 * i] = s[i].x, v[4 * i + 1] = s[i].y, v[4 * i + 2] = s[i].z, v[4 * i + 3] = s[i].w;
+    }
+};
 template <int N> __device__ __forceinline__ void put_bf16(__nv_bfloat16* p, const float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
@@ -846,21 +858,22 @@ constexpr int kJoinThreads = 128;
 
 template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_columns_kernel(const __grid_constant__ JoinArgs j) {
     dep_launch_dependents();
-    dep_wait();
+    constexpr bool kPair = JOIN == kJoinGated || JOIN == kJoinGatedFp8;
     const Args& a = j.a;
     const uint32_t rows = uint32_t(j.rows), lines = JOIN == kJoinGatedFp8 ? (rows + kBlock - 1) / kBlock * kBlock : rows;
     const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x, col = i / (lines / 4), row = (i - col * (lines / 4)) * 4;
     const bool in = col < uint32_t(j.cols) && row < rows;
+    const uint32_t tn = col / uint32_t(a.bn), up_row = rows + row;
+    const int64_t at = int64_t(col - tn * a.bn) * kTileM;
+    const Sums s(a, in ? tn * a.tiles_m + row / kTileM : 0, (at + row % kTileM) / 4);
+    const Sums su(a, in && kPair ? tn * a.tiles_m + up_row / kTileM : 0, (at + up_row % kTileM) / 4);
+    dep_wait();
     if (JOIN != kJoinGatedFp8 && !in) return;
-    const uint32_t tn = col / uint32_t(a.bn);
-    auto sum = [&](uint32_t r, float (&v)[4]) {
-        joined<1>(a, tn * a.tiles_m + r / kTileM, (int64_t(col - tn * a.bn) * kTileM + r % kTileM) / 4, v);
-    };
     float v[4] = {}, up[4];
-    if (in) sum(row, v);
-    if constexpr (JOIN == kJoinGated || JOIN == kJoinGatedFp8) {
+    if (in) s.add<1>(v);
+    if constexpr (kPair) {
         if (in) {
-            sum(rows + row, up);
+            su.add<1>(up);
             finish_gated(j, col, row, v, up);
         }
     }
@@ -872,7 +885,6 @@ template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_columns
 // After the other modes: the tiles behind the whole ones, C as the output. A thread has eight columns of a row.
 template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const __grid_constant__ JoinArgs j) {
     dep_launch_dependents();
-    dep_wait();
     constexpr bool kPair = JOIN == kJoinGated || JOIN == kJoinGatedFp8;
     constexpr uint32_t kCols = kPair ? 128 : 256, kPer = kCols / 8, kBlocks = kTileM * kPer / kJoinThreads;
     const Args& a = j.a;
@@ -882,12 +894,15 @@ template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_tiles_k
     a.place(a.whole + t, m, n);
     const int64_t row = int64_t(m) * kTileM + r, col = int64_t(n) * kCols + c;
     const bool in = row < a.rows && col < a.cols;
+    const Sums s(a, t, (int64_t(c >> 3) * kTileM + r) * 2);
+    dep_wait();
     if (JOIN != kJoinGatedFp8 && !in) return;
     float v[8] = {}, up[8];
-    if (in) joined<2>(a, t, (int64_t(c >> 3) * kTileM + r) * 2, v);
+    if (in) s.add<2>(v);
     if constexpr (kPair) {
         if (in) {
-            joined<2>(a, t, (int64_t((c + 128) >> 3) * kTileM + r) * 2, up);
+            const Sums su(a, t, (int64_t((c + 128) >> 3) * kTileM + r) * 2);
+            su.add<2>(up);
             finish_gated(j, row, col, v, up);
         }
     }
