@@ -531,7 +531,7 @@ int gr_feed_forward_backward(const gr_feed* f, const void* dy, const void* x, co
  * block that holds a value that is not finite gets the scale 255 and codes 0x7F: NaN throughout. Activations
  * have blocks of one row, weights of 128 (the last ones of either direction may be part-full). */
 typedef struct gr_blocks {
-    int64_t n_rows;      /* of a matrix, >= 0                                            */
+    int64_t n_rows;      /* of a matrix, >= 0; n_matrix · n_rows · ceil(n_cols / 128) < 2^31 */
     int64_t n_cols;      /* a multiple of 16, 16 .. GR_MAX_FF                            */
     int32_t n_matrix;    /* matrices [n_rows][n_cols] one after another, each with blocks
                             of its own; >= 1                                             */

@@ -24,7 +24,7 @@ int check_blocks(const gr_blocks* b) {
     if (!real_dtype(b->dtype)) return GR_E_DTYPE;
     if (b->n_rows < 0 || b->n_matrix < 1 || b->n_rows > (int64_t(1) << 40) / b->n_matrix || b->n_cols < 16 ||
         b->n_cols % 16 != 0 || b->n_cols > GR_MAX_FF || (b->block_rows != 1 && b->block_rows != kBlock) ||
-        b->n_rows * b->n_matrix * b->n_cols > (int64_t(1) << 38))
+        b->n_rows * b->n_matrix > 0x7fffffffLL / ceil_div(b->n_cols, kBlock))
         return GR_E_SHAPE;
     return GR_OK;
 }
