@@ -35,16 +35,6 @@ struct ScaleRows {
 cudaError_t launch_fp8_operands(const void* x, int64_t n, int64_t cols, uint8_t* codes, uint8_t* token_scales,
                                 const ScaleRows& a, const ScaleRows& b, cudaStream_t st);
 
-// Products on CUDA cores (gr_feed_simt.cu). dtype: GR_F32, GR_BF16.
-// h = act(x Wgᵀ) ⊙ (x Wuᵀ), pre [N][2][F] unless null.
-cudaError_t simt_gated(int64_t N, int D, int F, int dtype, int act, const void* x, const void* w_in, void* h,
-                       void* pre, cudaStream_t st);
-// dh = dy W_out, then dpre [N][2][F] and h from it and pre.
-cudaError_t simt_gated_grad(int64_t N, int D, int F, int dtype, int act, const void* dy, const void* w_out,
-                            const void* pre, void* dpre, void* h, cudaStream_t st);
-// out [M][N] = A Bᵀ over K. a_k, b_k: whether A is [M][K] (else [K][M]) and B [N][K] (else [K][N]).
-cudaError_t simt_product(int64_t M, int64_t N, int64_t K, int dtype, const void* a, bool a_k, const void* b,
-                         bool b_k, void* out, cudaStream_t st);
 // Products on the tcgen05 tensor cores, bf16 (gr_feed_tc.cu); `ws` as tc_feed_workspace says. `tokens`: of a
 // product whose other dimensions are the weights' (few of them go in parts over k), else INT64_MAX. Each
 // tc_product is a programmatic dependent of the launch before it on `st`, which must be this file's.
@@ -63,6 +53,13 @@ cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, const Fp8Product& in
 size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K);
 size_t tc_feed_fp8_workspace(int64_t N, int D, int F);
 size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient);
+// fp32: both passes, every operand as three bf16 terms.
+size_t f32_feed_workspace(int64_t N, int D, int F, bool gradient);
+cudaError_t f32_feed_forward(int64_t N, int64_t D, int64_t F, int act, const float* x, const float* w_in,
+                             const float* w_out, float* y, float* pre, void* ws, cudaStream_t st);
+cudaError_t f32_feed_backward(int64_t N, int64_t D, int64_t F, int act, const float* dy, const float* x,
+                              const float* w_in, const float* w_out, const float* pre, float* dx, float* dw_in,
+                              float* dw_out, void* ws, cudaStream_t st);
 // Status bits of the bounded waits of gr_feed_tc.cu (0 = none; -1 = could not be read).
 int feed_status(bool clear);
 

@@ -80,7 +80,8 @@ struct Parts {
 
 struct FeedParts {
     void *h = nullptr, *dpre = nullptr;              // gr_feed_forward and its gradient
-    float* parts = nullptr;                          // tensor cores: sums over ranges of k
+    float* parts = nullptr;                          // bf16 and FP8: sums over ranges of k
+    void* terms = nullptr;                           // fp32: operands as bf16 terms, and such sums
     uint8_t *xc = nullptr, *xs = nullptr;            // FP8: x in blocks
     uint8_t *hc = nullptr, *hs = nullptr;            // and h
     uint8_t *w_in = nullptr, *w_out = nullptr;       // and the weights' scales
@@ -96,10 +97,12 @@ struct FeedParts {
             w_in = w.take<uint8_t>(2 * ceil_div(F, kBlock) * scale_pitch(D));
             w_out = w.take<uint8_t>(ceil_div(D, kBlock) * scale_pitch(F));
             if (N > 0) parts = w.take<float>(tc_feed_fp8_workspace(f->n_tokens, f->d_model, f->d_ff));
+        } else if (f->dtype == GR_F32) {
+            if (N > 0) terms = w.take(f32_feed_workspace(f->n_tokens, f->d_model, f->d_ff, gradient));
         } else {
-            h = w.take(N * F * width(f->dtype));
-            if (gradient) dpre = w.take(2 * N * F * width(f->dtype));
-            if (f->dtype == GR_BF16 && N > 0)
+            h = w.take(N * F * 2);
+            if (gradient) dpre = w.take(2 * N * F * 2);
+            if (N > 0)
                 parts = w.take<float>(tc_feed_workspace(f->n_tokens, f->d_model, f->d_ff, gradient));
         }
         bytes = w.used;
@@ -150,13 +153,12 @@ int gr_feed_forward(const gr_feed* f, const void* x, const void* w_in, const voi
         return st;
     if ((st = usable_device())) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (f->dtype == GR_BF16) {
-        cudaError_t e = tc_gated(N, D, F, f->activation, x, w_in, p.h, pre, p.parts, s);
-        if (e == cudaSuccess) e = tc_product(N, D, F, N, p.h, true, w_out, true, y, p.parts, s);
-        return as_status(e);
-    }
-    cudaError_t e = simt_gated(N, D, F, f->dtype, f->activation, x, w_in, p.h, pre, s);
-    if (e == cudaSuccess) e = simt_product(N, D, F, f->dtype, p.h, true, w_out, true, y, s);
+    if (f->dtype == GR_F32)
+        return as_status(f32_feed_forward(N, D, F, f->activation, static_cast<const float*>(x),
+                                          static_cast<const float*>(w_in), static_cast<const float*>(w_out),
+                                          static_cast<float*>(y), static_cast<float*>(pre), p.terms, s));
+    cudaError_t e = tc_gated(N, D, F, f->activation, x, w_in, p.h, pre, p.parts, s);
+    if (e == cudaSuccess) e = tc_product(N, D, F, N, p.h, true, w_out, true, y, p.parts, s);
     return as_status(e);
 }
 
@@ -179,18 +181,16 @@ int gr_feed_forward_backward(const gr_feed* f, const void* dy, const void* x, co
         if (e == cudaSuccess) e = cudaMemsetAsync(dw_out, 0, fd, s);
         return as_status(e);
     }
-    if (f->dtype == GR_BF16) {
-        cudaError_t e = tc_gated_grad(N, D, F, f->activation, dy, w_out, pre, p.dpre, p.h, p.parts, s);
-        if (e == cudaSuccess) e = tc_product(N, D, 2 * F, N, p.dpre, true, w_in, false, dx, p.parts, s);
-        if (e == cudaSuccess)
-            e = tc_product(2 * F, D, N, INT64_MAX, p.dpre, false, x, false, dw_in, p.parts, s);
-        if (e == cudaSuccess) e = tc_product(D, F, N, INT64_MAX, dy, false, p.h, false, dw_out, p.parts, s);
-        return as_status(e);
-    }
-    cudaError_t e = simt_gated_grad(N, D, F, f->dtype, f->activation, dy, w_out, pre, p.dpre, p.h, s);
-    if (e == cudaSuccess) e = simt_product(N, D, 2 * F, f->dtype, p.dpre, true, w_in, false, dx, s);
-    if (e == cudaSuccess) e = simt_product(2 * F, D, N, f->dtype, p.dpre, false, x, false, dw_in, s);
-    if (e == cudaSuccess) e = simt_product(D, F, N, f->dtype, dy, false, p.h, false, dw_out, s);
+    if (f->dtype == GR_F32)
+        return as_status(f32_feed_backward(N, D, F, f->activation, static_cast<const float*>(dy),
+                                           static_cast<const float*>(x), static_cast<const float*>(w_in),
+                                           static_cast<const float*>(w_out), static_cast<const float*>(pre),
+                                           static_cast<float*>(dx), static_cast<float*>(dw_in),
+                                           static_cast<float*>(dw_out), p.terms, s));
+    cudaError_t e = tc_gated_grad(N, D, F, f->activation, dy, w_out, pre, p.dpre, p.h, p.parts, s);
+    if (e == cudaSuccess) e = tc_product(N, D, 2 * F, N, p.dpre, true, w_in, false, dx, p.parts, s);
+    if (e == cudaSuccess) e = tc_product(2 * F, D, N, INT64_MAX, p.dpre, false, x, false, dw_in, p.parts, s);
+    if (e == cudaSuccess) e = tc_product(D, F, N, INT64_MAX, dy, false, p.h, false, dw_out, p.parts, s);
     return as_status(e);
 }
 

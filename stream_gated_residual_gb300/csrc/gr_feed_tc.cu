@@ -282,15 +282,16 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
 // channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre; tmC2: dpre.
+// TERMS 3 (kPart): each operand as three bf16 matrices one after another, {.., matrix} boxes.
 // FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes. kGrad: no tmC0.
-template <int MODE, bool FP8, bool A_MN, bool B_MN>
+template <int MODE, bool FP8, bool A_MN, bool B_MN, int TERMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
             const __grid_constant__ CUtensorMap tmC2, const __grid_constant__ Args args) {
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = kBoxA + box_b, stages = args.stages;
+    const int rows_b = args.bn / 2, box_b = rows_b * 128, stage = TERMS * (kBoxA + box_b), stages = args.stages;
     uint8_t* out = sm + stages * stage;
     Aux& x = *reinterpret_cast<Aux*>(out + 8 * stage_out(MODE, FP8));
     uint32_t* const tops = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&x) + kAuxBytes);
@@ -298,6 +299,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr int kK = FP8 ? 128 : 64;
     // The scales take columns behind 256: one accumulator of up to 256 columns, or two of 128.
     const int accs = FP8 && args.bn > 128 ? 1 : 2, acc_cols = FP8 ? 128 : 256;
+    // A tensor core cuts off what an addition to its accumulator shifts out: 2.7e-8 of the sum on average, 8.6e-6 after
+    // the 212 of 54 blocks. That is nothing beside a rounding to bf16, but not for fp32, so there an accumulator
+    // takes four blocks at most (16 additions, 2.8e-7), and those sums are added up with rounding.
+    constexpr int kRun = TERMS > 1 ? 4 : 1 << 30;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool first = rank == 0;
@@ -333,7 +338,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         auto load_a = [&](uint32_t s, int m0, int kb) {
             if (first) mbar_expect_tx(&x.full[s], bytes);
             uint8_t* pa = sm + s * stage;
-            if constexpr (A_MN) {
+            if constexpr (TERMS > 1) {
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t, pa += kBoxA) {
+                    tma_pair_3d(pa, &tmA, A_MN ? m0 : kb * kK, A_MN ? kb * kK : m0, t, bar0 + s * 8);
+                    if (A_MN) tma_pair_3d(pa + 8192, &tmA, m0 + 64, kb * kK, t, bar0 + s * 8);
+                }
+            } else if constexpr (A_MN) {
                 tma_pair_2d(pa, &tmA, m0, kb * kK, bar0 + s * 8);
                 tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar0 + s * 8);
             } else {
@@ -341,8 +352,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         };
         auto load_b = [&](uint32_t s, int n0, int kb) {
-            uint8_t* pb = sm + s * stage + kBoxA;
-            if constexpr (MODE == kGated) {
+            uint8_t* pb = sm + s * stage + TERMS * kBoxA;
+            if constexpr (TERMS > 1) {
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t, pb += box_b)
+                    tma_pair_3d(pb, &tmB, B_MN ? n0 : kb * kK, B_MN ? kb * kK : n0, t, bar0 + s * 8);
+            } else if constexpr (MODE == kGated) {
                 tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar0 + s * 8);
             } else if constexpr (B_MN) {
                 for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar0 + s * 8);
@@ -387,13 +402,18 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                        : idesc_bf16_f32(256, args.bn) | (A_MN ? 1u << 15 : 0) | (B_MN ? 1u << 16 : 0);
             const uint32_t base = smem_u32(sm), sf0 = smem_u32(sf), copies = 1 + (args.bn + 127) / 128;
             const uint64_t da0 = A_MN ? sdesc_mn(base, 8192) : sdesc_sw128(base);
-            const uint64_t db0 = B_MN ? sdesc_mn(base + kBoxA, 8192) : sdesc_sw128(base + kBoxA);
+            const uint64_t db0 = B_MN ? sdesc_mn(base + TERMS * kBoxA, 8192) : sdesc_sw128(base + TERMS * kBoxA);
             const uint32_t hop = uint32_t(stage) >> 4;   // from a stage to the next, in a descriptor
             uint32_t s = 0, lap = 0, q = 0;              // stage, laps, steps of scales
             bool ok = true;
-            for (int j = 0; ok && units.next(u); ++j) {
-                const int b = j % accs, blocks = uniform(u.k1 - u.k0);
-                if (j >= accs && !wait_warp(&x.acc_empty[b], (j / accs - 1) & 1)) break;
+            for (int j = 0; ok && units.next(u);) {
+              const int all = uniform(u.k1 - u.k0);
+              for (int from = 0; ok && from < all; from += kRun, ++j) {
+                const int b = j % accs, blocks = min(kRun, all - from);
+                if (j >= accs && !wait_warp(&x.acc_empty[b], (j / accs - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t d = tmem + b * acc_cols;
                 for (int kb = 0; kb < blocks; ++kb) {
@@ -421,7 +441,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t a = da + k * (A_MN ? 128 : 2), bb = db + k * (B_MN ? 128 : 2);
-                            if constexpr (FP8) {
+                            if constexpr (TERMS > 1) {
+                                // the product of the first terms, and beside it the five that are smaller
+#pragma unroll
+                                for (int ta = 0; ta < TERMS; ++ta)
+#pragma unroll
+                                    for (int tb = 0; ta + tb < TERMS; ++tb)
+                                        tc_mma2(d + (ta + tb > 0 ? 128 : 0), a + ta * (kBoxA >> 4),
+                                                bb + tb * (uint32_t(box_b) >> 4), idesc,
+                                                kb > 0 || k > 0 || ta + tb > 1 || ta > 0);
+                            } else if constexpr (FP8) {
                                 const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
                                 tc_mma2_fp8(d, a, bb, idesc | (step << 4) | (step << 29), sfa, sfa + 4, kb > 0 || k > 0);
                             } else {
@@ -434,6 +463,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (++s == uint32_t(stages)) s = 0, ++lap;
                 }
                 if (ok && leader) tc_commit2(&x.acc_full[b]);
+              }
             }
             if (leader) tc_commit2(&x.done);
             wait_warp(&x.done, 0);
@@ -725,6 +755,43 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                 }
                 if (!ok) break;
+            } else if constexpr (TERMS > 1) {
+                // sums of runs, added up in registers: every other 16 columns of up to 128
+                float sum[4][16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[c][k] = 0.0f;
+                bool ok = true;
+                for (int from = now.k0;; ++j) {
+                    const uint32_t at = tmem + (j % accs) * acc_cols + lanes;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (half * 16 + c * 32 >= args.bn) continue;
+                        float lead[16], rest[16];
+                        tmem_ld16(at + half * 16 + c * 32, lead);
+                        tmem_ld16(at + 128 + half * 16 + c * 32, rest);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) sum[c][k] += lead[k] + rest[k];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(map_rank(smem_u32(&x.acc_empty[j % accs]), 0));
+                    from += kRun;
+                    if (from >= now.k1) break;
+                    ok = wait_on(&x.acc_full[(j + 1) % accs], ((j + 1) / accs) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (!ok) break;
+                float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
+                           int(rank) * kRowsA + quad * 32 + lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (half * 16 + c * 32 >= args.bn) continue;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) p[int64_t(half * 16 + c * 32 + k) * kTileM] = sum[c][k];
+                }
             } else {
                 float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
                            int(rank) * kRowsA + quad * 32 + lane;
@@ -756,7 +823,8 @@ struct JoinArgs {
     int64_t rows, cols;          // of the output (h's channels)
     __nv_bfloat16 *out, *pre_out;
     const __nv_bfloat16* pre;
-    __nv_bfloat16* dpre;
+    __nv_bfloat16* dpre;         // fp32: out (but kJoinStore's) and dpre as three terms
+    float *out_f32, *pre_f32;    // fp32: C, and pre
     uint8_t *codes, *scales;     // h in FP8 blocks
     int scale_steps;
 };
@@ -851,12 +919,92 @@ __device__ __forceinline__ void finish_fp8(const JoinArgs& j, int64_t token, int
     if ((ch & (kBlock - 1)) == 0) j.scales[scale_at(token, uint32_t(ch / kBlock), j.scale_steps)] = e;
 }
 
+// fp32: an operand of a product as three bf16 terms, each the rounding of what the ones before leave (the first
+// towards zero where it would become infinite): 24 bits and more. What is not finite is the first term alone.
+__device__ __forceinline__ void terms_of(float v, __nv_bfloat16 (&t)[3]) {
+    t[0] = __float2bfloat16_rn(v);
+    if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) {
+        t[1] = t[2] = __float2bfloat16_rn(0.0f);
+        return;
+    }
+    if ((__bfloat16_as_ushort(t[0]) & 0x7f80) == 0x7f80) t[0] = __float2bfloat16_rz(v);
+    const float r = v - __bfloat162float(t[0]);
+    t[1] = __float2bfloat16_rn(r);
+    t[2] = __float2bfloat16_rn(r - __bfloat162float(t[1]));
+}
+__device__ __forceinline__ void put_terms(__nv_bfloat16* p, int64_t hop, const float (&v)[4]) {
+    __nv_bfloat16 t[4][3];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) terms_of(v[k], t[k]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 a(t[0][i], t[1][i]), b(t[2][i], t[3][i]);
+        *reinterpret_cast<uint2*>(p + i * hop) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                            *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+struct Cut {
+    const float* from;
+    __nv_bfloat16* to;
+    int64_t n;   // a multiple of 8
+};
+struct Cuts {
+    Cut c[3];
+};
+__global__ void __launch_bounds__(256) terms_kernel(const Cuts cuts) {
+    dep_launch_dependents();
+    int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const Cut& c = cuts.c[k];
+        if (i >= 0 && i < c.n) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(c.from + i));
+            const float v[4] = {f.x, f.y, f.z, f.w};
+            put_terms(c.to + i, c.n, v);
+        }
+        i -= c.n;
+    }
+}
+__device__ __forceinline__ void put_f32(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void finish_gated_f32(const JoinArgs& j, int64_t token, int64_t ch, float (&g)[4],
+                                                 const float (&up)[4]) {
+    if (j.pre_f32) {
+        put_f32(j.pre_f32 + 2 * token * j.rows + ch, g);
+        put_f32(j.pre_f32 + (2 * token + 1) * j.rows + ch, up);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        g[k] = (j.a.act == GR_SILU ? activate<GR_SILU>(g[k]) : activate<GR_GELU>(g[k])) * up[k];
+    put_terms(j.out + token * j.rows + ch, j.rows * j.cols, g);
+}
+__device__ __forceinline__ void finish_grad_f32(const JoinArgs& j, int64_t token, int64_t ch, float (&dh)[4]) {
+    const float* q = j.pre_f32 + 2 * token * j.rows + ch;
+    const float4 g4 = *reinterpret_cast<const float4*>(q), p4 = *reinterpret_cast<const float4*>(q + j.rows);
+    const float g[4] = {g4.x, g4.y, g4.z, g4.w}, p[4] = {p4.x, p4.y, p4.z, p4.w};
+    float s[4], h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool silu = j.a.act == GR_SILU;
+        const float a = silu ? activate<GR_SILU>(g[k]) : activate<GR_GELU>(g[k]);
+        s[k] = dh[k] * p[k] * (silu ? activate_slope<GR_SILU>(g[k]) : activate_slope<GR_GELU>(g[k]));
+        h[k] = a * p[k];
+        dh[k] *= a;
+    }
+    const int64_t hop = 2 * j.rows * j.cols;
+    put_terms(j.dpre + 2 * token * j.rows + ch, hop, s);
+    put_terms(j.dpre + (2 * token + 1) * j.rows + ch, hop, dh);
+    put_terms(j.out + token * j.rows + ch, j.rows * j.cols, h);
+}
+
 // After kPart: C's rows are the output's channels, contiguous, its columns the tokens. A thread has four rows of a
 // column; in FP8 a warp has a block.
 enum Join { kJoinStore, kJoinGated, kJoinGrad, kJoinGatedFp8 };
 constexpr int kJoinThreads = 128;
 
-template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_columns_kernel(const __grid_constant__ JoinArgs j) {
+template <int JOIN, bool F32>
+__global__ void __launch_bounds__(kJoinThreads) join_columns_kernel(const __grid_constant__ JoinArgs j) {
     dep_launch_dependents();
     constexpr bool kPair = JOIN == kJoinGated || JOIN == kJoinGatedFp8;
     const Args& a = j.a;
@@ -874,11 +1022,15 @@ template <int JOIN> __global__ void __launch_bounds__(kJoinThreads) join_columns
     if constexpr (kPair) {
         if (in) {
             su.add<1>(up);
-            finish_gated(j, col, row, v, up);
+            if constexpr (F32) finish_gated_f32(j, col, row, v, up);
+            else finish_gated(j, col, row, v, up);
         }
     }
     if constexpr (JOIN == kJoinGatedFp8) finish_fp8<4, 32>(j, col, row, v, in);
+    else if constexpr (JOIN == kJoinGrad && F32) finish_grad_f32(j, col, row, v);
     else if constexpr (JOIN == kJoinGrad) finish_grad(j, col, row, v);
+    else if constexpr (JOIN == kJoinGated && F32) return;
+    else if constexpr (F32) put_f32(j.out_f32 + int64_t(col) * rows + row, v);
     else put_bf16(j.out + int64_t(col) * rows + row, v);
 }
 
@@ -982,9 +1134,9 @@ struct Operand {
     int64_t rows;
 };
 
-template <int MODE, bool FP8>
+template <int MODE, bool FP8, int TERMS>
 int stages_for(int bn) {
-    const int stage = kBoxA + bn / 2 * 128;
+    const int stage = TERMS * (kBoxA + bn / 2 * 128);
     const int room = (kSmemMax - 1024 - (FP8 ? kAuxFp8 : kAuxBytes) - 8 * stage_out(MODE, FP8)) / stage;
     return room > kMaxStages ? kMaxStages : room;
 }
@@ -998,7 +1150,7 @@ struct Plan {
     size_t bytes = 0;       // of the parts
 };
 
-template <int MODE, bool FP8, bool A_MN, bool B_MN>
+template <int MODE, bool FP8, bool A_MN, bool B_MN, int TERMS = 1>
 cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Plan& p, const CUtensorMap& c0,
                          const CUtensorMap& c1, const CUtensorMap& c2, cudaStream_t st, bool programmatic) {
     CUtensorMap ma, mb;
@@ -1008,6 +1160,11 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
     if constexpr (FP8) {
         ok = map_codes(&ma, a.p, a.rows, K, kRowsA, 128) &&
              (MODE == kGated ? map_codes_pair(&mb, b.p, b.rows, K) : map_codes(&mb, b.p, b.rows, K, rows_b, 128));
+    } else if constexpr (TERMS > 1) {
+        ok = (A_MN ? map_bf16_3d(&ma, a.p, TERMS, K, a.rows, 1, 64, 64)
+                   : map_bf16_3d(&ma, a.p, TERMS, a.rows, K, 1, kRowsA, 64)) &&
+             (B_MN ? map_bf16_3d(&mb, b.p, TERMS, K, b.rows, 1, 64, 64)
+                   : map_bf16_3d(&mb, b.p, TERMS, b.rows, K, 1, rows_b, 64));
     } else {
         ok = A_MN ? map_bf16(&ma, a.p, K, a.rows, 64, 64) : map_bf16(&ma, a.p, a.rows, K, kRowsA, 64);
         if (MODE == kGated)
@@ -1016,10 +1173,10 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
             ok = ok && (B_MN ? map_bf16(&mb, b.p, K, b.rows, 64, 64) : map_bf16(&mb, b.p, b.rows, K, rows_b, 64));
     }
     if (!ok) return cudaErrorInvalidValue;
-    args.stages = stages_for<MODE, FP8>(args.bn);
-    const size_t smem = 1024 + size_t(args.stages) * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
+    args.stages = stages_for<MODE, FP8, TERMS>(args.bn);
+    const size_t smem = 1024 + size_t(args.stages) * TERMS * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
-    return launch(pair_kernel<MODE, FP8, A_MN, B_MN>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
+    return launch(pair_kernel<MODE, FP8, A_MN, B_MN, TERMS>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
                   programmatic, ma, mb, c0, c1, c2, args);
 }
 
@@ -1059,13 +1216,13 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t K, int per_tile, bool fp8) {
 
 // Few tokens: C's rows are the weights' and its columns the tokens, in tiles of as few columns as the steps of 16 (FP8:
 // 32; 128 where the tokens' operand is not K-major) allow; all of them in parts.
-Plan plan_columns(int64_t rows, int64_t tokens, int64_t K, int step, bool fp8) {
+Plan plan_columns(int64_t rows, int64_t tokens, int64_t K, int step, bool fp8, int most = 256) {
     Plan p;
     p.columns = true;
     p.a.nk = int(ceil_div(K, fp8 ? 128 : 64));
     p.a.steps = fp8 ? uint32_t(ceil_div(p.a.nk, 4)) : uint32_t(p.a.nk);
     p.a.tiles_m = int(ceil_div(rows, kTileM));
-    p.a.tiles_n = int(ceil_div(tokens, 256));
+    p.a.tiles_n = int(ceil_div(tokens, most));
     p.a.bn = int(ceil_div(ceil_div(tokens, p.a.tiles_n), step) * step);
     p.a.tiles_n = int(ceil_div(tokens, p.a.bn));
     p.a.group = p.a.tiles_m;   // tile t: row tile t % tiles_m
@@ -1076,11 +1233,12 @@ Plan plan_columns(int64_t rows, int64_t tokens, int64_t K, int step, bool fp8) {
 
 const CUtensorMap kNone = {};
 
-template <int JOIN> cudaError_t join(const Plan& p, JoinArgs j, cudaStream_t st) {
+template <int JOIN, bool F32 = false> cudaError_t join(const Plan& p, JoinArgs j, cudaStream_t st) {
     j.a = p.a;
-    if (p.columns) {
+    if (F32 || p.columns) {
         const int64_t lines = JOIN == kJoinGatedFp8 ? ceil_div(j.rows, kBlock) * kBlock : j.rows;
-        return launch(join_columns_kernel<JOIN>, unsigned(ceil_div(lines / 4 * j.cols, kJoinThreads)), kJoinThreads, 0,
+        if (lines / 4 * j.cols > 0xffffffffLL - kJoinThreads) return cudaErrorInvalidValue;
+        return launch(join_columns_kernel<JOIN, F32>, unsigned(ceil_div(lines / 4 * j.cols, kJoinThreads)), kJoinThreads, 0,
                       st, true, j);
     }
     const int blocks = kTileM * (JOIN == kJoinGated || JOIN == kJoinGatedFp8 ? 16 : 32) / kJoinThreads;
@@ -1183,6 +1341,95 @@ size_t tc_feed_workspace(int64_t N, int D, int F, bool gradient) {
         cover(plan_product(N, D, F, N, false));
     }
     return need;
+}
+
+namespace {
+
+// ---- fp32 ----
+// The same steps with every operand as three bf16 terms and all of C in parts, whatever its size: fp32 stands for small
+// models and checks.
+template <bool A_K, bool B_K> Plan plan_f32(int64_t rows, int64_t cols, int64_t K) {
+    Plan p = plan_columns(rows, cols, K, B_K ? 16 : 128, false, 128);
+    p.a.early = 0;   // the operands' terms are of launches before
+    return p;
+}
+// C [N][M] (C's rows along M, contiguous) = B Aᵀ.
+template <int JOIN, bool A_K, bool B_K>
+cudaError_t product_f32(const __nv_bfloat16* a, const __nv_bfloat16* b, int64_t M, int64_t N, int64_t K, int act,
+                        JoinArgs j, float* ws, cudaStream_t st) {
+    Plan p = plan_f32<A_K, B_K>(M, N, K);
+    p.a.part = ws, p.a.act = act;
+    const cudaError_t e = launch_pairs<kPart, false, !A_K, !B_K, 3>({a, M}, {b, N}, K, p, kNone, kNone, kNone, st, true);
+    return e != cudaSuccess ? e : join<JOIN, true>(p, j, st);
+}
+cudaError_t cut_terms(const Cuts& c, cudaStream_t st) {
+    const int64_t n = c.c[0].n + c.c[1].n + c.c[2].n, grid = ceil_div(n / 4, 256);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch(terms_kernel, unsigned(grid), 256, 0, st, false, c);
+}
+
+// The terms of a call's operands in its workspace, and the parts.
+struct TermParts {
+    __nv_bfloat16 *x, *w_in, *w_out, *h, *dy = nullptr, *dpre = nullptr;
+    float* parts;
+    size_t bytes = 0;
+    TermParts(int64_t N, int64_t D, int64_t F, bool gradient, void* ws) {
+        char* base = static_cast<char*>(ws);
+        auto take = [&](int64_t n, size_t width) {
+            char* p = base ? base + bytes : nullptr;
+            bytes += align256(size_t(n) * width);
+            return p;
+        };
+        auto terms = [&](int64_t n) { return reinterpret_cast<__nv_bfloat16*>(take(n, 6)); };
+        x = terms(N * D), w_in = terms(2 * F * D), w_out = terms(D * F), h = terms(N * F);
+        if (gradient) dy = terms(N * D), dpre = terms(2 * N * F);
+        size_t need = 0;
+        auto cover = [&](const Plan& p) { need = p.bytes > need ? p.bytes : need; };
+        if (gradient) {
+            cover(plan_f32<false, true>(F, N, D));
+            cover(plan_f32<false, true>(D, N, 2 * F));
+            cover(plan_f32<false, false>(D, 2 * F, N));
+            cover(plan_f32<false, false>(F, D, N));
+        } else {
+            cover(plan_f32<true, true>(2 * F, N, D));
+            cover(plan_f32<true, true>(D, N, F));
+        }
+        parts = reinterpret_cast<float*>(take(int64_t(need), 1));
+    }
+};
+
+}  // namespace
+
+size_t f32_feed_workspace(int64_t N, int D, int F, bool gradient) { return TermParts(N, D, F, gradient, nullptr).bytes; }
+
+cudaError_t f32_feed_forward(int64_t N, int64_t D, int64_t F, int act, const float* x, const float* w_in,
+                             const float* w_out, float* y, float* pre, void* ws, cudaStream_t st) {
+    const TermParts t(N, D, F, false, ws);
+    cudaError_t e = cut_terms({{{x, t.x, N * D}, {w_in, t.w_in, 2 * F * D}, {w_out, t.w_out, D * F}}}, st);
+    JoinArgs j{};
+    j.out = t.h, j.pre_f32 = pre, j.rows = F, j.cols = N;
+    if (e == cudaSuccess) e = product_f32<kJoinGated, true, true>(t.w_in, t.x, 2 * F, N, D, act, j, t.parts, st);
+    j.out_f32 = y, j.rows = D, j.cols = N;
+    if (e == cudaSuccess) e = product_f32<kJoinStore, true, true>(t.w_out, t.h, D, N, F, act, j, t.parts, st);
+    return e;
+}
+
+cudaError_t f32_feed_backward(int64_t N, int64_t D, int64_t F, int act, const float* dy, const float* x,
+                              const float* w_in, const float* w_out, const float* pre, float* dx, float* dw_in,
+                              float* dw_out, void* ws, cudaStream_t st) {
+    const TermParts t(N, D, F, true, ws);
+    cudaError_t e = cut_terms({{{dy, t.dy, N * D}, {w_out, t.w_out, D * F}, {x, t.x, N * D}}}, st);
+    if (e == cudaSuccess) e = cut_terms({{{w_in, t.w_in, 2 * F * D}, {}, {}}}, st);
+    JoinArgs j{};
+    j.out = t.h, j.dpre = t.dpre, j.pre_f32 = const_cast<float*>(pre), j.rows = F, j.cols = N;
+    if (e == cudaSuccess) e = product_f32<kJoinGrad, false, true>(t.w_out, t.dy, F, N, D, act, j, t.parts, st);
+    j.out_f32 = dx, j.rows = D, j.cols = N;
+    if (e == cudaSuccess) e = product_f32<kJoinStore, false, true>(t.w_in, t.dpre, D, N, 2 * F, act, j, t.parts, st);
+    j.out_f32 = dw_in, j.rows = D, j.cols = 2 * F;
+    if (e == cudaSuccess) e = product_f32<kJoinStore, false, false>(t.x, t.dpre, D, 2 * F, N, act, j, t.parts, st);
+    j.out_f32 = dw_out, j.rows = F, j.cols = D;
+    if (e == cudaSuccess) e = product_f32<kJoinStore, false, false>(t.h, t.dy, F, D, N, act, j, t.parts, st);
+    return e;
 }
 
 // ---- FP8 ----
