@@ -8,7 +8,7 @@
 // KB for 512 cycles of MMAs. A persistent grid of pairs; in each CTA one warp feeds a ring of stages by TMA, one
 // (of the pair's first CTA) issues the MMAs, eight drain the accumulator: two accumulators in tensor memory, so
 // the MMAs of the next tile run meanwhile.
-#include <string.h>
+#include <atomic>
 
 #include "gr_feed.h"
 #include "gr_ptx.cuh"
@@ -1106,10 +1106,6 @@ bool map_codes_pair(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t st,
                    bool programmatic, Args... args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
@@ -1123,7 +1119,11 @@ cudaError_t launch(void (*kern)(KArgs...), unsigned grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-int pairs_of() { return sm_count() / 2; }
+// SM pairs of the current device; where there is none (workspace sizes asked on a host without a GPU), a GB300's.
+int pairs_of() {
+    const int n = sm_count() / 2;
+    return n > 0 ? n : 76;
+}
 
 constexpr int kFewTokens = 512;    // up to which the tokens are C's columns
 constexpr int kDivideBlocks = 48;  // blocks of k a pair has to save by dividing the last tiles
@@ -1176,6 +1176,18 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
     args.stages = stages_for<MODE, FP8, TERMS>(args.bn);
     const size_t smem = 1024 + size_t(args.stages) * TERMS * (kBoxA + rows_b * 128) + 8 * stage_out(MODE, FP8) +
                         (FP8 ? kAuxFp8 : kAuxBytes);
+    // The shared memory's limit is raised once a device.
+    static std::atomic<uint64_t> raised{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(pair_kernel<MODE, FP8, A_MN, B_MN, TERMS>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess) return e;
+        if (device <= 63) raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch(pair_kernel<MODE, FP8, A_MN, B_MN, TERMS>, unsigned(2 * p.pairs), FP8 ? kThreads + 32 : kThreads, smem, st,
                   programmatic, ma, mb, c0, c1, c2, args);
 }

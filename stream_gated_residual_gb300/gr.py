@@ -625,9 +625,6 @@ _PRODUCT = struct.Struct("=qii")       # gr_product
 _embed_desc = functools.lru_cache(1024)(_EMBED.pack)
 _norm_desc = functools.lru_cache(1024)(_NORM.pack)
 _mixer_desc = functools.lru_cache(1024)(_MIXER.pack)
-_feed_desc = functools.lru_cache(1024)(_FEED.pack)
-_blocks_desc = functools.lru_cache(1024)(_BLOCKS.pack)
-_product_desc = functools.lru_cache(1024)(_PRODUCT.pack)
 
 
 _current_device = torch._C._cuda_getDevice
@@ -940,43 +937,52 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
 
 
 # ---- the gated feed-forward sublayer, and FP8 blocks ----------------------------------------------
+#
+# What follows from shapes and dtypes alone (checks, descriptor, workspace) is kept by them.
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1}
 BLOCK = 128    # channels of an FP8 block
 
 
-def _like(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> None:
-    if not t.is_cuda or not t.is_contiguous():
+def _given(t: torch.Tensor, name: str) -> None:
+    if not (t.is_cuda and t.is_contiguous()):
         _dev(t, name)
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
 
 
 def _out(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, like: torch.Tensor,
          stream) -> torch.Tensor:
+    """The output given, checked, or a new one."""
     if t is None:
         return _new(stream, shape, dtype, like.device)
-    _like(t, name, shape, dtype)
+    _given(t, name)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
     return t
 
 
-def _feed(x: torch.Tensor, F: int, dtype: int, activation: str) -> bytes:
-    if activation not in _ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
-    return _feed_desc(x.shape[0], x.shape[1], F, dtype, _ACTIVATIONS[activation])
+def _same(name: str, shape, dtype, want, want_dtype) -> None:
+    if tuple(shape) != tuple(want) or dtype != want_dtype:
+        raise ValueError(f"{name} must be {want_dtype} of shape {list(want)}, got {dtype} of {list(shape)}")
 
 
-def _feed_args(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activation: str):
-    """(N, D, F, descriptor) of a call on bf16 or fp32 tensors."""
-    if x.dim() != 2 or x.dtype not in _DTYPES:
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+@functools.lru_cache(1024)
+def _feed_plan(xs, xt, ws, wt, os, ot, activation: str, gradient: int):
+    """(shape of pre, descriptor, workspace bytes) of a call on bf16 or fp32 tensors."""
+    if len(xs) != 2 or xt not in _DTYPES:
         raise ValueError("x must be a float32 or bfloat16 tensor [N, D]")
-    if w_in.dim() != 3 or w_in.shape[0] != 2:
+    if len(ws) != 3 or ws[0] != 2:
         raise ValueError("w_in must be [2, F, D]: the gate's weights, then the up projection's")
-    (N, D), F = x.shape, w_in.shape[1]
-    _like(x, "x", (N, D), x.dtype)
-    _like(w_in, "w_in", (2, F, D), x.dtype)
-    _like(w_out, "w_out", (D, F), x.dtype)
-    return N, D, F, _feed(x, F, _DTYPES[x.dtype], activation)
+    (N, D), F = xs, ws[1]
+    _same("w_in", ws, wt, (2, F, D), xt)
+    _same("w_out", os, ot, (D, F), xt)
+    f = _FEED.pack(N, D, F, _DTYPES[xt], _activation(activation))
+    return torch.Size((N, 2, F)), f, _need("gr_feed_workspace_size", f, gradient)
 
 
 def feed_forward(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activation: str = "silu",
@@ -985,11 +991,15 @@ def feed_forward(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activ
     """gr_feed_forward: y = (f(x W_gᵀ) * (x W_uᵀ)) W_oᵀ of x [N, D], w_in [2, F, D] (W_g, W_u) and w_out
     [D, F], all bf16 or all fp32; f is "silu" or "gelu" (erf). Returns y [N, D]; with keep=True (or a pre to
     write) (y, pre), pre [N, 2, F] the gate and up values that the gradient needs."""
-    N, D, F, f = _feed_args(x, w_in, w_out, activation)
-    y = _out(y, "y", (N, D), x.dtype, x, stream)
+    shape, dtype = x.shape, x.dtype
+    pre_shape, f, need = _feed_plan(shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 0)
+    _given(x, "x")
+    _given(w_in, "w_in")
+    _given(w_out, "w_out")
+    y = _out(y, "y", shape, dtype, x, stream)
     if keep or pre is not None:
-        pre = _out(pre, "pre", (N, 2, F), x.dtype, x, stream)
-    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 0), workspace, x, stream)
+        pre = _out(pre, "pre", pre_shape, dtype, x, stream)
+    wp, wn, _keep = _ws(need, workspace, x, stream)
     _call("gr_feed_forward", f, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), y.data_ptr(), _opt(pre), wp,
           wn, _raw_stream(stream, x, w_in, w_out, y, pre, workspace))
     return y if pre is None else (y, pre)
@@ -1001,21 +1011,35 @@ def feed_forward_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor,
                           workspace: torch.Tensor | None = None, stream=None):
     """gr_feed_forward_backward: (dx, dw_in, dw_out) in x's dtype from dy [N, D] and the pre that
     feed_forward(keep=True) returned."""
-    N, D, F, f = _feed_args(x, w_in, w_out, activation)
-    _like(dy, "dy", (N, D), x.dtype)
-    _like(pre, "pre", (N, 2, F), x.dtype)
-    dx = _out(dx, "dx", (N, D), x.dtype, x, stream)
-    dw_in = _out(dw_in, "dw_in", (2, F, D), x.dtype, x, stream)
-    dw_out = _out(dw_out, "dw_out", (D, F), x.dtype, x, stream)
-    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 1), workspace, x, stream)
+    shape, dtype = x.shape, x.dtype
+    pre_shape, f, need = _feed_plan(shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 1)
+    for t, name in ((dy, "dy"), (x, "x"), (w_in, "w_in"), (w_out, "w_out"), (pre, "pre")):
+        _given(t, name)
+    _same("dy", dy.shape, dy.dtype, shape, dtype)
+    _same("pre", pre.shape, pre.dtype, pre_shape, dtype)
+    dx = _out(dx, "dx", shape, dtype, x, stream)
+    dw_in = _out(dw_in, "dw_in", w_in.shape, dtype, x, stream)
+    dw_out = _out(dw_out, "dw_out", w_out.shape, dtype, x, stream)
+    wp, wn, _keep = _ws(need, workspace, x, stream)
     _call("gr_feed_forward_backward", f, dy.data_ptr(), x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(),
           pre.data_ptr(), dx.data_ptr(), dw_in.data_ptr(), dw_out.data_ptr(), wp, wn,
           _raw_stream(stream, x, dy, w_in, w_out, pre, dx, dw_in, dw_out, workspace))
     return dx, dw_in, dw_out
 
 
-def _up(n: int, step: int) -> int:
-    return -(-n // step)
+def _blocks_shape(shape, block_rows: int):
+    return torch.Size((*shape[:-2], -(-shape[-2] // block_rows), -(-shape[-1] // BLOCK)))
+
+
+@functools.lru_cache(1024)
+def _blocks_plan(shape, dtype, block_rows: int):
+    """(shape of the scales, descriptor)"""
+    if len(shape) not in (2, 3) or dtype not in _DTYPES:
+        raise ValueError("m must be a float32 or bfloat16 tensor [R, K] or [M, R, K]")
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
+    return _blocks_shape(shape, block_rows), _BLOCKS.pack(shape[-2], shape[-1], 1 if len(shape) == 2 else shape[0],
+                                                          block_rows, _DTYPES[dtype])
 
 
 def fp8_encode_blocks(m: torch.Tensor, block_rows: int = 1, codes: torch.Tensor | None = None,
@@ -1023,46 +1047,68 @@ def fp8_encode_blocks(m: torch.Tensor, block_rows: int = 1, codes: torch.Tensor 
     """gr_fp8_encode_blocks: m [R, K] or [M, R, K] (bf16 or fp32) -> (codes, like m, scales
     [.., ceil(R / block_rows), ceil(K / 128)]), both uint8: e4m3 codes with a power-of-two scale for each 128
     channels of a row (block_rows=1, activations) or of 128 rows (block_rows=128, weights)."""
-    if m.dim() not in (2, 3) or m.dtype not in _DTYPES:
-        raise ValueError("m must be a float32 or bfloat16 tensor [R, K] or [M, R, K]")
-    if block_rows not in (1, BLOCK):
-        raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows}")
-    _dev(m, "m")
     shape = m.shape
+    scales_shape, b = _blocks_plan(shape, m.dtype, int(block_rows))
+    _given(m, "m")
     codes = _out(codes, "codes", shape, torch.uint8, m, stream)
-    scales = _out(scales, "scales", (*shape[:-2], _up(shape[-2], block_rows), _up(shape[-1], BLOCK)),
-                  torch.uint8, m, stream)
-    b = _blocks_desc(shape[-2], shape[-1], 1 if m.dim() == 2 else shape[0], int(block_rows), _DTYPES[m.dtype])
+    scales = _out(scales, "scales", scales_shape, torch.uint8, m, stream)
     _call("gr_fp8_encode_blocks", b, m.data_ptr(), codes.data_ptr(), scales.data_ptr(),
           _raw_stream(stream, m, codes, scales))
     return codes, scales
 
 
-def _fp8_pair(pair, name: str, lead: tuple, block_rows: int):
-    """(codes, scales, rows, channels) of a matrix in blocks, with `lead` dimensions before its own two."""
+def _fp8_pair(pair, name: str):
     codes, scales = pair
-    if codes.dim() != len(lead) + 2 or codes.shape[:len(lead)] != lead:
-        raise ValueError(f"the codes of {name} must be [{', '.join([*map(str, lead), 'rows', 'channels'])}]")
-    R, K = codes.shape[-2:]
-    _like(codes, f"the codes of {name}", (*lead, R, K), torch.uint8)
-    _like(scales, f"the scales of {name}", (*lead, _up(R, block_rows), _up(K, BLOCK)), torch.uint8)
-    return codes, scales, R, K
+    _given(codes, f"the codes of {name}")
+    _given(scales, f"the scales of {name}")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"the codes and scales of {name} must be uint8")
+    return codes, scales
+
+
+def _same_scales(name: str, codes, scales, block_rows: int) -> None:
+    want = _blocks_shape(codes, block_rows)
+    if tuple(scales) != tuple(want):
+        raise ValueError(f"the scales of {name} must have shape {list(want)}, got {list(scales)}")
+
+
+@functools.lru_cache(1024)
+def _product_plan(a, asc, b, bsc):
+    """(shape of out, descriptor, workspace bytes)"""
+    if len(a) != 2 or len(b) != 2 or a[1] != b[1]:
+        raise ValueError(f"the codes must be [N, K] and [O, K], got {list(a)} and {list(b)}")
+    _same_scales("a", a, asc, 1)
+    _same_scales("b", b, bsc, BLOCK)
+    p = _PRODUCT.pack(a[0], a[1], b[0])
+    return torch.Size((a[0], b[0])), p, _need("gr_fp8_matmul_workspace_size", p)
 
 
 def fp8_matmul(a, b, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """gr_fp8_matmul: out [N, O] bf16 = A Bᵀ of a = (codes [N, K], scales [N, K/128]) in blocks of one row and
     b = (codes [O, K], scales [O/128, K/128]) in blocks of 128 rows, as fp8_encode_blocks gives them."""
-    ac, asc, N, K = _fp8_pair(a, "a", (), 1)
-    bc, bsc, O, Kb = _fp8_pair(b, "b", (), BLOCK)
-    if K != Kb:
-        raise ValueError(f"a has {K} channels, b {Kb}")
-    out = _out(out, "out", (N, O), torch.bfloat16, ac, stream)
-    p = _product_desc(N, K, O)
-    wp, wn, _keep = _ws(_need("gr_fp8_matmul_workspace_size", p), workspace, ac, stream)
+    ac, asc = _fp8_pair(a, "a")
+    bc, bsc = _fp8_pair(b, "b")
+    shape, p, need = _product_plan(ac.shape, asc.shape, bc.shape, bsc.shape)
+    out = _out(out, "out", shape, torch.bfloat16, ac, stream)
+    wp, wn, _keep = _ws(need, workspace, ac, stream)
     _call("gr_fp8_matmul", p, ac.data_ptr(), asc.data_ptr(), bc.data_ptr(), bsc.data_ptr(), out.data_ptr(),
           wp, wn, _raw_stream(stream, ac, asc, bc, bsc, out, workspace))
     return out
+
+
+@functools.lru_cache(1024)
+def _feed_fp8_plan(xs, xt, ic, isc, oc, osc, activation: str):
+    """(descriptor, workspace bytes)"""
+    if len(ic) != 3 or ic[0] != 2 or len(oc) != 2:
+        raise ValueError("the codes of w_in must be [2, F, D], those of w_out [D, F]")
+    _, F, D = ic
+    if len(xs) != 2 or xs[1] != D or tuple(oc) != (D, F) or xt != torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 [N, {D}] and the codes of w_out [{D}, {F}]")
+    _same_scales("w_in", ic, isc, BLOCK)
+    _same_scales("w_out", oc, osc, BLOCK)
+    f = _FEED.pack(xs[0], D, F, GR_FP8, _activation(activation))
+    return f, _need("gr_feed_workspace_size", f, 0)
 
 
 def feed_forward_fp8(x: torch.Tensor, w_in, w_out, activation: str = "silu", y: torch.Tensor | None = None,
@@ -1070,14 +1116,13 @@ def feed_forward_fp8(x: torch.Tensor, w_in, w_out, activation: str = "silu", y: 
     """gr_feed_forward_fp8: feed_forward of x [N, D] bf16 on FP8 weights, w_in the (codes, scales) of
     [2, F, D] and w_out those of [D, F] from fp8_encode_blocks(.., 128); x and the hidden values are encoded in
     blocks of one row on the way. Returns y [N, D] bf16."""
-    ic, isc, F, D = _fp8_pair(w_in, "w_in", (2,), BLOCK)
-    oc, osc, Do, Fo = _fp8_pair(w_out, "w_out", (), BLOCK)
-    if x.dim() != 2 or (Do, Fo) != (D, F):
-        raise ValueError(f"x must be [N, {D}] and w_out [{D}, {F}]")
-    _like(x, "x", (x.shape[0], D), torch.bfloat16)
-    y = _out(y, "y", x.shape, torch.bfloat16, x, stream)
-    f = _feed(x, F, GR_FP8, activation)
-    wp, wn, _keep = _ws(_need("gr_feed_workspace_size", f, 0), workspace, x, stream)
+    ic, isc = _fp8_pair(w_in, "w_in")
+    oc, osc = _fp8_pair(w_out, "w_out")
+    shape = x.shape
+    f, need = _feed_fp8_plan(shape, x.dtype, ic.shape, isc.shape, oc.shape, osc.shape, activation)
+    _given(x, "x")
+    y = _out(y, "y", shape, torch.bfloat16, x, stream)
+    wp, wn, _keep = _ws(need, workspace, x, stream)
     _call("gr_feed_forward_fp8", f, x.data_ptr(), ic.data_ptr(), isc.data_ptr(), oc.data_ptr(), osc.data_ptr(),
           y.data_ptr(), wp, wn, _raw_stream(stream, x, ic, isc, oc, osc, y, workspace))
     return y

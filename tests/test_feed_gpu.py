@@ -267,7 +267,7 @@ def test_nothing_is_written_behind_the_outputs(N):
 
     made = [framed(N, D), framed(N, 2, F), framed(N, D), framed(2, F, D), framed(D, F)]
     y, p, dx, dwi, dwo = (t for _, t in made)
-    feed = gr._feed(x, F, gr.GR_BF16, "silu")
+    feed = gr._FEED.pack(N, D, F, gr.GR_BF16, 0)
     for gradient in (0, 1):
         need = gr._need("gr_feed_workspace_size", feed, gradient)
         ws = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
