@@ -3,18 +3,22 @@ linear-attention mixer and a write per layer, the branches' layer norm, and tied
 
     R = embed(E, ids)                        [N, 4, D]
     for each layer:  x, s = read(R);  y = W_o · linear_attention(W_qkv · x);  R += s_i y
+                     x, s = read(R);  y = feed_forward(x);  R += s_i y          (with d_ff)
     logits = E · mean_i layer_norm(R)_i
 
 ``prompt`` runs packed sequences and leaves each one's mixer states in a slot, ``step`` goes on one token a
-request, ``gradients`` is a training step's forward and backward pass. The projections are plain
+request, ``gradients`` is a training step's forward and backward pass. The mixer's projections are plain
 torch products; everything else is the library's. ``python -m stream_gated_residual_gb300.decoder``
-trains one for a moment and lets it continue a prompt.
+trains one for a moment and lets it continue a prompt (``--d-ff N`` for one with feed-forward sublayers,
+``--fp8`` to continue on FP8 weights of those).
 
-One read a layer, no MLP sublayer: the read, write and mixer are those of "【论文解读】 Qwen3.8 Flash Next"
+With d_ff a layer has two reads, one around the mixer and one around the gated feed-forward block; without, the
+first alone. The read, write and mixer are those of "【论文解读】 Qwen3.8 Flash Next"
 (wkq9411.github.io), §二.4, with a plain linear attention in the place of its token mixer.
 """
 from __future__ import annotations
 
+import argparse
 import dataclasses
 import math
 
@@ -33,6 +37,9 @@ class Config:
     rank: int = 16
     dtype: torch.dtype = torch.bfloat16
     eps: float = 1e-6
+    d_ff: int = 0              # 0: no feed-forward sublayers
+    activation: str = "silu"
+    fp8: bool = False          # prompt and step on FP8 blocks of the feed-forward weights
 
 
 class Decoder:
@@ -54,6 +61,16 @@ class Decoder:
                 f"{i}.w_down": normal(r, K, std=0.02), f"{i}.w_up": normal(K, r, std=0.02),
                 f"{i}.w_write": normal(4, K, std=0.02),
                 f"{i}.qkv": normal(3 * H, D, std=D ** -0.5), f"{i}.out": normal(D, H, std=H ** -0.5)})
+            if cfg.d_ff:
+                self.params.update({
+                    f"{i}.ff.gamma": torch.ones(4, D, device=device),
+                    f"{i}.ff.w_down": normal(r, K, std=0.02), f"{i}.ff.w_up": normal(K, r, std=0.02),
+                    f"{i}.ff.w_write": normal(4, K, std=0.02),
+                    f"{i}.ff.w_in": normal(2, cfg.d_ff, D, std=D ** -0.5),
+                    f"{i}.ff.w_out": normal(D, cfg.d_ff, std=cfg.d_ff ** -0.5)})
+        # the sublayers in order: (layer, where its parameters are, whether it is the feed-forward block)
+        self.sublayers = [(i, f"{i}{part}", bool(part)) for i in range(cfg.layers)
+                          for part in (("", ".ff") if cfg.d_ff else ("",))]
         # memories from a few tokens to a few hundred; constants of the model
         self.log_decay = -torch.exp2(-torch.linspace(1, 8, cfg.heads, device=device))
         # the requests' mixer states, a slot each: [layer][slot, head, d, d] fp32
@@ -64,9 +81,12 @@ class Decoder:
     def pack(self) -> None:
         """The parameters in the forms the forward pass takes (after every update of ``params``)."""
         p, c = self.params, self.cfg
-        self.packed = [gr.pack_params(p[f"{i}.gamma"], p[f"{i}.w_down"], p[f"{i}.w_up"], p[f"{i}.w_write"],
-                                      c.dtype, c.eps) for i in range(c.layers)]
-        self.cast = {k: p[k].to(c.dtype) for k in p if k == "embedding" or k.endswith((".qkv", ".out"))}
+        self.packed = [gr.pack_params(p[f"{at}.gamma"], p[f"{at}.w_down"], p[f"{at}.w_up"], p[f"{at}.w_write"],
+                                      c.dtype, c.eps) for _, at, _ in self.sublayers]
+        self.cast = {k: p[k].to(c.dtype) for k in p
+                     if k == "embedding" or k.endswith((".qkv", ".out", ".w_in", ".w_out"))}
+        self.fp8 = {k: gr.fp8_encode_blocks(p[k], gr.BLOCK) for k in p if k.endswith((".w_in", ".w_out"))} \
+            if c.fp8 else {}
 
     def _embed(self, ids):
         return gr.embed(self.params["embedding"], ids, math.sqrt(self.cfg.d_model), dtype=self.cfg.dtype)
@@ -75,17 +95,29 @@ class Decoder:
         c = self.cfg
         return (x @ self.cast[f"{i}.qkv"].T).view(-1, 3, c.heads, c.d_head).unbind(1)
 
+    def _feed(self, at, x, keep):
+        """(the feed-forward block's output, what its gradient needs)"""
+        w_in, w_out, act = f"{at}.w_in", f"{at}.w_out", self.cfg.activation
+        if keep:
+            return gr.feed_forward(x, self.cast[w_in], self.cast[w_out], act, keep=True)
+        if self.fp8:
+            return gr.feed_forward_fp8(x, self.fp8[w_in], self.fp8[w_out], act), None
+        return gr.feed_forward(x, self.cast[w_in], self.cast[w_out], act), None
+
     def _layers(self, R, mix, keep=None):
-        """All layers on R in place; mix(i, q, k, v) -> o. `keep` collects what the gradients need."""
+        """All sublayers on R in place; mix(i, q, k, v) -> o. `keep` collects what the gradients need."""
         x, s = gr.read(R, self.packed[0])
-        for i in range(self.cfg.layers):
-            q, k, v = self._qkv(i, x)
-            o = mix(i, q, k, v)
-            y = o.flatten(1) @ self.cast[f"{i}.out"].T
+        for n, (i, at, feed) in enumerate(self.sublayers):
+            if feed:
+                y, kept = self._feed(at, x, keep is not None)
+            else:
+                q, k, v = self._qkv(i, x)
+                o = mix(i, q, k, v)
+                y, kept = o.flatten(1) @ self.cast[f"{i}.out"].T, (q, k, v, o)
             if keep is not None:
-                keep.append((R.clone(), x, s, q, k, v, o, y))
-            if i + 1 < self.cfg.layers:
-                x, s = gr.write_then_read(R, y, s, self.packed[i + 1])
+                keep.append((R.clone(), x, s, kept, y))
+            if n + 1 < len(self.sublayers):
+                x, s = gr.write_then_read(R, y, s, self.packed[n + 1])
             else:
                 gr.write(R, y, s)
         return R
@@ -127,29 +159,39 @@ class Decoder:
         g = {}
         dz = (dlogits @ p["embedding"] / 4)[:, None].expand(-1, 4, -1).contiguous()
         dR, g["norm.weight"], g["norm.bias"] = gr.layer_norm_backward(dz, R, p["norm.weight"], mean, rstd)
-        for i in reversed(range(c.layers)):
-            Ri, x, s, q, k, v, o, y = kept[i]
+        for (i, at, feed), (Ri, x, s, saved, y) in zip(reversed(self.sublayers), reversed(kept)):
             dR, dy, ds = gr.write_backward(dR, y, s)
-            g[f"{i}.out"] = dy.T @ o.flatten(1).float()
-            do = (dy @ p[f"{i}.out"]).view(N, c.heads, c.d_head).to(c.dtype)
-            dqkv = torch.empty(N, 3, c.heads, c.d_head, dtype=c.dtype, device=ids.device)
-            gr.linear_attention_backward(do, q, k, v, self.log_decay, seq_starts=seq_starts,
-                                         out=dqkv.unbind(1))
-            dqkv = dqkv.flatten(1).float()
-            g[f"{i}.qkv"] = dqkv.T @ x.float()
-            dread, gi = gr.read_backward(Ri, p[f"{i}.gamma"], p[f"{i}.w_down"], p[f"{i}.w_up"],
-                                         p[f"{i}.w_write"], dqkv @ p[f"{i}.qkv"], ds, c.eps)
+            if feed:
+                dx, dw_in, dw_out = gr.feed_forward_backward(
+                    dy.to(c.dtype), x, self.cast[f"{at}.w_in"], self.cast[f"{at}.w_out"], saved, c.activation)
+                dx, g[f"{at}.w_in"], g[f"{at}.w_out"] = dx.float(), dw_in.float(), dw_out.float()
+            else:
+                q, k, v, o = saved
+                g[f"{i}.out"] = dy.T @ o.flatten(1).float()
+                do = (dy @ p[f"{i}.out"]).view(N, c.heads, c.d_head).to(c.dtype)
+                dqkv = torch.empty(N, 3, c.heads, c.d_head, dtype=c.dtype, device=ids.device)
+                gr.linear_attention_backward(do, q, k, v, self.log_decay, seq_starts=seq_starts,
+                                             out=dqkv.unbind(1))
+                dqkv = dqkv.flatten(1).float()
+                g[f"{i}.qkv"] = dqkv.T @ x.float()
+                dx = dqkv @ p[f"{i}.qkv"]
+            dread, gi = gr.read_backward(Ri, p[f"{at}.gamma"], p[f"{at}.w_down"], p[f"{at}.w_up"],
+                                         p[f"{at}.w_write"], dx, ds, c.eps)
             dR += dread
-            g.update({f"{i}.{name}": t for name, t in gi.items()})
+            g.update({f"{at}.{name}": t for name, t in gi.items()})
         # the table is tied: its rows' gradient on top of the logits'
         g["embedding"] = gr.embed_backward(dR, ids, c.vocab, scale, dtable=(dlogits.T @ top).contiguous(),
                                            accumulate=True)
         return loss, g
 
 
-def main() -> None:
+def main(argv=None) -> None:
     """Learns to continue a repeated phrase, then continues it token by token."""
-    cfg = Config()
+    parser = argparse.ArgumentParser(description=main.__doc__)
+    parser.add_argument("--d-ff", type=int, default=0, help="width of the feed-forward sublayers (0: none)")
+    parser.add_argument("--fp8", action="store_true", help="continue on FP8 weights of the feed-forward sublayers")
+    args = parser.parse_args(argv)
+    cfg = Config(d_ff=args.d_ff, fp8=args.fp8)
     model = Decoder(cfg, slots=4)
     phrase = torch.randint(0, cfg.vocab, (12,), generator=torch.Generator().manual_seed(1)).cuda()
     text = phrase.repeat(40)
