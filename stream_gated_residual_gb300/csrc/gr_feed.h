@@ -35,7 +35,8 @@ struct ScaleRows {
 cudaError_t launch_fp8_operands(const void* x, int64_t n, int64_t cols, uint8_t* codes, uint8_t* token_scales,
                                 const ScaleRows& a, const ScaleRows& b, cudaStream_t st);
 
-// Products on the tcgen05 tensor cores, bf16 (gr_feed_tc.cu); `ws` as tc_feed_workspace says. `tokens`: of a
+// Products on the tcgen05 tensor cores, bf16 (gr_feed_tc.cu); `ws` as tc_feed_workspace says (this and the other
+// workspace functions: SIZE_MAX for calls that are too large to be planned). `tokens`: of a
 // product whose other dimensions are the weights' (few of them go in parts over k), else INT64_MAX. Each
 // tc_product is a programmatic dependent of the launch before it on `st`, which must be this file's.
 cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void* w_in, void* h, void* pre,

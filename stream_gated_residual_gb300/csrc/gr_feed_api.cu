@@ -71,7 +71,12 @@ int check_buffers(std::initializer_list<Span> aligned_in, std::initializer_list<
 struct Parts {
     char* base;
     size_t used = 0;
+    bool ok = true;
     template <typename T = void> T* take(size_t bytes) {
+        if (bytes == SIZE_MAX) {   // a call that cannot be planned
+            ok = false;
+            return nullptr;
+        }
         char* p = base ? base + used : nullptr;
         used += align256(bytes);
         return reinterpret_cast<T*>(p);
@@ -86,6 +91,7 @@ struct FeedParts {
     uint8_t *hc = nullptr, *hs = nullptr;            // and h
     uint8_t *w_in = nullptr, *w_out = nullptr;       // and the weights' scales
     size_t bytes = 0;
+    bool ok;
     FeedParts(const gr_feed* f, bool gradient, void* base) {
         Parts w{static_cast<char*>(base)};
         const size_t N = size_t(f->n_tokens), D = size_t(f->d_model), F = size_t(f->d_ff);
@@ -106,6 +112,7 @@ struct FeedParts {
                 parts = w.take<float>(tc_feed_workspace(f->n_tokens, f->d_model, f->d_ff, gradient));
         }
         bytes = w.used;
+        ok = w.ok;
     }
 };
 
@@ -114,12 +121,14 @@ struct ProductParts {
     uint8_t *a, *b;
     float* parts;
     size_t bytes;
+    bool ok;
     ProductParts(const gr_product* p, void* base) {
         Parts w{static_cast<char*>(base)};
         a = w.take<uint8_t>(token_scale_bytes(p->n_tokens, p->d_in));
         b = w.take<uint8_t>(ceil_div(p->d_out, kBlock) * scale_pitch(p->d_in));
         parts = w.take<float>(tc_product_fp8_workspace(p->n_tokens, p->d_out, p->d_in));
         bytes = w.used;
+        ok = w.ok;
     }
 };
 
@@ -134,7 +143,9 @@ int gr_feed_workspace_size(const gr_feed* f, int gradient, size_t* bytes) {
     const int st = check_feed(f, f && f->dtype == GR_FP8 && !gradient);
     if (st) return st;
     if (!bytes) return GR_E_NULL;
-    *bytes = FeedParts(f, gradient != 0, nullptr).bytes;
+    const FeedParts p(f, gradient != 0, nullptr);
+    if (!p.ok) return GR_E_SHAPE;
+    *bytes = p.bytes;
     return GR_OK;
 }
 
@@ -147,6 +158,7 @@ int gr_feed_forward(const gr_feed* f, const void* x, const void* w_in, const voi
     const int D = f->d_model, F = f->d_ff;
     const size_t w = width(f->dtype), nd = size_t(N) * D * w, fd = size_t(F) * D * w;
     const FeedParts p(f, false, workspace);
+    if (!p.ok) return GR_E_SHAPE;
     if ((st = check_buffers({{x, nd}, {w_in, 2 * fd}, {w_out, fd}}, {},
                             {{y, nd}, {pre, pre ? 2 * size_t(N) * F * w : 0}}, {workspace, p.bytes},
                             workspace_bytes)))
@@ -171,7 +183,10 @@ int gr_feed_forward_backward(const gr_feed* f, const void* dy, const void* x, co
     const int D = f->d_model, F = f->d_ff;
     const size_t w = width(f->dtype), nd = size_t(N) * D * w, fd = size_t(F) * D * w;
     const FeedParts p(f, true, workspace);
-    if ((st = check_buffers({{dy, nd}, {x, nd}, {w_in, 2 * fd}, {w_out, fd}, {pre, 2 * size_t(N) * F * w}}, {},
+    if (!p.ok) return GR_E_SHAPE;
+    const size_t weights = N > 0 ? fd : 0;   // without tokens only the weights' gradients are touched
+    if ((st = check_buffers({{dy, nd}, {x, nd}, {w_in, 2 * weights}, {w_out, weights},
+                             {pre, 2 * size_t(N) * F * w}}, {},
                             {{dx, nd}, {dw_in, 2 * fd}, {dw_out, fd}}, {workspace, p.bytes}, workspace_bytes)))
         return st;
     if ((st = usable_device())) return st;
@@ -213,7 +228,11 @@ int gr_fp8_matmul_workspace_size(const gr_product* p, size_t* bytes) {
     const int st = check_product(p);
     if (st) return st;
     if (!bytes) return GR_E_NULL;
-    *bytes = p->n_tokens == 0 ? 0 : ProductParts(p, nullptr).bytes;
+    *bytes = 0;
+    if (p->n_tokens == 0) return GR_OK;
+    const ProductParts w(p, nullptr);
+    if (!w.ok) return GR_E_SHAPE;
+    *bytes = w.bytes;
     return GR_OK;
 }
 
@@ -224,6 +243,7 @@ int gr_fp8_matmul(const gr_product* p, const uint8_t* a, const uint8_t* a_scales
     if (p->n_tokens == 0) return GR_OK;
     const size_t N = size_t(p->n_tokens), K = size_t(p->d_in), O = size_t(p->d_out), nb = ceil_div(K, kBlock);
     const ProductParts w(p, workspace);
+    if (!w.ok) return GR_E_SHAPE;
     if ((st = check_buffers({{a, N * K}, {b, O * K}}, {{a_scales, N * nb}, {b_scales, ceil_div(O, kBlock) * nb}},
                             {{out, N * O * 2}}, {workspace, w.bytes}, workspace_bytes)))
         return st;
@@ -245,6 +265,7 @@ int gr_feed_forward_fp8(const gr_feed* f, const void* x, const uint8_t* w_in, co
     const int D = f->d_model, F = f->d_ff;
     const size_t nd = size_t(N) * D * 2, fd = size_t(F) * D, db = ceil_div(D, kBlock), fb = ceil_div(F, kBlock);
     const FeedParts p(f, false, workspace);
+    if (!p.ok) return GR_E_SHAPE;
     if ((st = check_buffers({{x, nd}, {w_in, 2 * fd}, {w_out, fd}},
                             {{w_in_scales, 2 * fb * db}, {w_out_scales, fb * db}}, {{y, nd}},
                             {workspace, p.bytes}, workspace_bytes)))

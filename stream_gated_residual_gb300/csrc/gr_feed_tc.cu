@@ -1147,8 +1147,9 @@ struct Plan {
     bool columns = false;   // kPart
     int pairs = 0;
     uint32_t rest = 0;      // tiles in parts
-    size_t bytes = 0;       // of the parts
+    size_t bytes = 0;       // of the parts; kTooLarge where tiles or steps pass 32 bits (no memory holds such a call)
 };
+constexpr size_t kTooLarge = SIZE_MAX;
 
 template <int MODE, bool FP8, bool A_MN, bool B_MN, int TERMS = 1>
 cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Plan& p, const CUtensorMap& c0,
@@ -1195,6 +1196,11 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
 // ---- plans ----
 // The tiles behind `whole` in ranges of at least `least` steps.
 void spread(Plan& p, int64_t tiles, int64_t whole, int least) {
+    if (tiles > 0xffffffffLL || (tiles - whole) * p.a.steps > 0xffffffffLL) {
+        p.pairs = 1;
+        p.bytes = kTooLarge;
+        return;
+    }
     p.a.whole = uint32_t(whole);
     p.rest = uint32_t(tiles - whole);
     p.pairs = pairs_of();
@@ -1383,7 +1389,7 @@ cudaError_t cut_terms(const Cuts& c, cudaStream_t st) {
 // The terms of a call's operands in its workspace, and the parts.
 struct TermParts {
     __nv_bfloat16 *x, *w_in, *w_out, *h, *dy = nullptr, *dpre = nullptr;
-    float* parts;
+    float* parts = nullptr;
     size_t bytes = 0;
     TermParts(int64_t N, int64_t D, int64_t F, bool gradient, void* ws) {
         char* base = static_cast<char*>(ws);
@@ -1406,7 +1412,8 @@ struct TermParts {
             cover(plan_f32<true, true>(2 * F, N, D));
             cover(plan_f32<true, true>(D, N, F));
         }
-        parts = reinterpret_cast<float*>(take(int64_t(need), 1));
+        if (need == kTooLarge) bytes = kTooLarge;
+        else parts = reinterpret_cast<float*>(take(int64_t(need), 1));
     }
 };
 
