@@ -604,6 +604,18 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int k = 0; k < 16; ++k) v[i * 16 + k] = __uint_as_float(r[i][k]);
                 }
             };
+            // twice 64 columns, all on their way at once
+            auto get128 = [&](uint32_t col, uint32_t col2, float (&v)[64], float (&v2)[64]) {
+                uint32_t r[8][16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tmem_ld16_nowait(acc + (i < 4 ? col : col2) + (i & 3) * 16, r[i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    tmem_wait_ld(r[i]);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) (i < 4 ? v : v2)[(i & 3) * 16 + k] = __uint_as_float(r[i][k]);
+                }
+            };
             // a partial tile's sums: [256 / 8 columns][256 rows][8]
             auto put_part = [&](uint32_t col, const float (&v)[64]) {
                 float4* p = reinterpret_cast<float4*>(args.part) +
@@ -624,20 +636,30 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
             } else if constexpr (MODE == kStore) {
                 const int col = now.n * 256 + half * 128;
-                float v[64];
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    get64(half * 128 + i * 64, v);
-                    if (i == 1) drained();
+                auto put = [&](const float (&v)[64], int i) {
                     put_box(v, [&] {
                         if (col + i * 64 < args.cols) tma_store_2d(&tmC0, minep, col + i * 64, row);
                     });
+                };
+                float v[64];
+                if constexpr (FP8) {   // one accumulator: the next tile waits for it
+                    float v2[64];
+                    get128(half * 128, half * 128 + 64, v, v2);
+                    drained();
+                    put(v, 0);
+                    put(v2, 1);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        get64(half * 128 + i * 64, v);
+                        if (i == 1) drained();
+                        put(v, i);
+                    }
                 }
             } else if constexpr (MODE == kGated) {
                 const int col = now.n * 128 + half * 64;
                 float ga[64], up[64];
-                get64(half * 64, ga);
-                get64(128 + half * 64, up);
+                get128(half * 64, 128 + half * 64, ga, up);
                 drained();
                 const bool in = col < args.cols;
                 if (args.keep && in) {
