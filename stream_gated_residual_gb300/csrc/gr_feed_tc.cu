@@ -469,8 +469,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             wait_warp(&x.done, 0);
         }
     } else if (FP8 && warp == 10) {
-        // Scales: a word (four blocks) for each of 128 rows of A and bn of B into shared memory, copies of several steps
-        // under way at once. Rows behind the last have any scales: their rows or columns of C may
+        // Scales: a word (four blocks) for each of 128 rows of A and bn of B into shared memory. Rows behind the last have any scales: their rows or columns of C may
         // come out NaN, and are not stored.
         constexpr bool kTokensB = MODE == kPart;   // else A's rows are the tokens
         const Scales& sc = args.scales;
@@ -512,35 +511,33 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                              : "memory");
             }
         };
-        constexpr uint32_t kAhead = kScaleSlots - 2;
-        uint32_t issued = 0;
+        // Half of the slots at a time: the fence that hands copied words to the tensor cores waits for every copy under
+        // way, so copies of a step at a time would each take a trip to the L2 (8191 x 7168 x 4096: 158 us).
+        constexpr uint32_t kBatch = kScaleSlots / 2;
+        uint32_t q = 0;
         bool more = units.next(u), ok = true;
         int kb = u.k0;
         if (more) find(u);
-        auto issue = [&]() {
-            const uint32_t slot = issued % kScaleSlots;
-            if (issued >= kScaleSlots) ok = wait_on(&x.scales_empty[slot], ((issued / kScaleSlots) - 1) & 1);
-            if (ok) copy_step(smem_u32(sf) + slot * kScaleSlot + lane * 16, kb);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++issued;
-            kb += 4;
-            if (kb >= u.k1) {
-                more = units.next(u);
-                kb = u.k0;
-                if (more) find(u);
+        while (ok && more) {
+            const uint32_t begin = q;
+            for (uint32_t i = 0; ok && more && i < kBatch; ++i, ++q) {
+                const uint32_t slot = q % kScaleSlots;
+                if (q >= kScaleSlots) ok = wait_on(&x.scales_empty[slot], ((q / kScaleSlots) - 1) & 1);
+                if (ok) copy_step(smem_u32(sf) + slot * kScaleSlot + lane * 16, kb);
+                kb += 4;
+                if (kb >= u.k1) {
+                    more = units.next(u);
+                    kb = u.k0;
+                    if (more) find(u);
+                }
             }
-        };
-        for (uint32_t q = 0; ok; ++q) {
-            while (ok && more && issued < q + kAhead) issue();
-            if (!ok || q >= issued) break;
-            // the groups behind step q's may stay under way: kAhead - 1 of them, none once there are no more steps
-            if (issued == q + kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) arrive_remote(map_rank(smem_u32(&x.scales_full[q % kScaleSlots]), 0));
+            if (lane == 0 && ok)
+                for (uint32_t i = begin; i < q; ++i)
+                    arrive_remote(map_rank(smem_u32(&x.scales_full[i % kScaleSlots]), 0));
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         const int w = warp - 2, half = w >> 2, quad = warp & 3;
         const uint32_t mine = smem_u32(out) + w * stage_out(MODE, FP8);
