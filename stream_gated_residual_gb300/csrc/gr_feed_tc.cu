@@ -171,7 +171,6 @@ struct Args {
     Scales scales;          // FP8
     uint8_t* hs;            // FP8 kGated: h's scales, as a product's tokens
     int hs_steps;
-    __nv_bfloat16* h;       // kGrad
     __host__ __device__ uint32_t begin(uint32_t pair) const { return pair * range + (pair < longer ? pair : longer); }
     // The pair whose range holds a step.
     __device__ uint32_t owner(uint32_t step) const {
@@ -195,15 +194,15 @@ constexpr int kScaleSlots = 8;
 constexpr int kAuxBytes = 640, kAuxFp8 = kAuxBytes + 2048 + kScaleSlots * kScaleSlot;
 constexpr int kSmemMax = 232448;
 
-// Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad two
-// pairs of boxes of 32 rows x 32 columns.
+// Staging for the outputs of a warp: kStore and kGated a box of 32 rows x 64 columns (FP8 h: of bytes), kGrad two of
+// them.
 __host__ __device__ constexpr int stage_out(int mode, bool fp8) {
-    return mode == kPart ? 0 : mode == kGrad ? 2 * 2 * 2048 : mode == kGated && fp8 ? 2048 : 4096;
+    return mode == kPart ? 0 : mode == kGrad ? 2 * 4096 : mode == kGated && fp8 ? 2048 : 4096;
 }
 
 struct Aux {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2], done, loaded[8][2];
+    uint64_t acc_full[2], acc_empty[2], done, loaded[8];
     uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots], top_full[4];
     uint32_t tmem;
 };
@@ -283,7 +282,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
 // tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
 // channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre; tmC2: dpre.
 // TERMS 3 (kPart): each operand as three bf16 matrices one after another, {.., matrix} boxes.
-// FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes. kGrad: no tmC0.
+// FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
 template <int MODE, bool FP8, bool A_MN, bool B_MN, int TERMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP8 ? kThreads + 32 : kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -312,7 +311,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int b = 0; b < 2; ++b) mbar_init(&x.acc_full[b], 1), mbar_init(&x.acc_empty[b], 16);
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&x.scales_full[i], 2), mbar_init(&x.scales_empty[i], 1);
         for (int q = 0; q < 4; ++q) mbar_init(&x.top_full[q], 2);
-        for (int w = 0; w < 8; ++w) mbar_init(&x.loaded[w][0], 1), mbar_init(&x.loaded[w][1], 1);
+        for (int w = 0; w < 8; ++w) mbar_init(&x.loaded[w], 1);
         mbar_init(&x.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -544,22 +543,19 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint8_t* const minep = out + w * stage_out(MODE, FP8);
         const uint32_t lanes = uint32_t(quad) << 21;   // lane field of a tensor-memory address: quad * 32 << 16
         auto row_of = [&](const Unit& t) { return t.m * kTileM + int(rank) * kRowsA + quad * 32; };
-        // kGrad: gate and up of 32 channels of the warp's rows into one of two sets of boxes, which dgate and dup leave
-        // from. The set's last stores have read it by then.
+        // kGrad: gate and up of 64 channels of the warp's rows into its two boxes, which dgate and dup leave from, then h
         uint32_t reads = 0, used = 0;
-        auto read_pre = [&](int row, int ch) {
-            uint8_t* to = minep + (reads & 1) * 4096;
+        auto read_pre = [&](int row, int ch, int which) {
             if (lane == 0) {
-                mbar_expect_tx(&x.loaded[w][reads & 1], 4096);
-                tma_load_3d(to, &tmC1, ch, 0, row, &x.loaded[w][reads & 1]);
-                tma_load_3d(to + 2048, &tmC1, ch, 1, row, &x.loaded[w][reads & 1]);
+                if (which) mbar_expect_tx(&x.loaded[w], 8192);
+                tma_load_3d(minep + which * 4096, &tmC1, ch, which, row, &x.loaded[w]);
             }
-            ++reads;
+            reads += which;
         };
         bool more = units.next(u);
         if (MODE == kGrad && more && u.slot < 0) {
-            read_pre(row_of(u), u.n * 256 + half * 128);
-            read_pre(row_of(u), u.n * 256 + half * 128 + 32);
+            read_pre(row_of(u), u.n * 256 + half * 128, 1);
+            read_pre(row_of(u), u.n * 256 + half * 128, 0);
         }
         for (int j = 0; more; ++j) {
             const int b = j % accs;
@@ -712,29 +708,18 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const bool follows = peek.next(after) && after.slot < 0;
                 bool ok = true;
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    float dh[32];
-                    {
-                        uint32_t r[2][16];
-                        tmem_ld16_nowait(acc + half * 128 + i * 32, r[0]);
-                        tmem_ld16_nowait(acc + half * 128 + i * 32 + 16, r[1]);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            tmem_wait_ld(r[q]);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) dh[q * 16 + k] = __uint_as_float(r[q][k]);
-                        }
-                    }
-                    if (i == 3) drained();
-                    const uint32_t set = used & 1, box = mine + set * 4096;
-                    uint8_t* const boxp = minep + set * 4096;
-                    ok = ok && wait_on(&x.loaded[w][set], (used >> 1) & 1);
+                for (int i = 0; i < 2; ++i) {
+                    float dh[64];
+                    get64(half * 128 + i * 64, dh);
+                    if (i == 1) drained();
+                    ok = ok && wait_on(&x.loaded[w], used & 1);
                     ++used;
+                    uint4 h[8];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         float g[8], p[8], a[8], s[8];
-                        unpack8(ld_shared16(box + swz64(lane, c)), g);
-                        unpack8(ld_shared16(box + 2048 + swz64(lane, c)), p);
+                        unpack8(ld_shared16(mine + swz(lane, c)), g);
+                        unpack8(ld_shared16(mine + 4096 + swz(lane, c)), p);
                         if (args.act == GR_SILU) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) act_both(GR_SILU, g[k], a[k], s[k]);
@@ -750,28 +735,41 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                         uint4 v;
                         pack8(v, s);
-                        st_shared16(box + swz64(lane, c), v);
+                        st_shared16(mine + swz(lane, c), v);
                         pack8(v, a);
-                        st_shared16(box + 2048 + swz64(lane, c), v);
-                        // h straight from the registers: a third box would cost the ring a stage
-                        pack8(v, p);
-                        const int ch = col + i * 32 + c * 8;
-                        if (row + lane < args.rows && ch < args.cols)
-                            __stcs(reinterpret_cast<uint4*>(args.h + int64_t(row + lane) * args.cols + ch), v);
+                        st_shared16(mine + 4096 + swz(lane, c), v);
+                        pack8(h[c], p);
                     }
+                    const int ch = col + i * 64;
+                    const bool in = ok && row < args.rows && ch < args.cols;
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0 && ok && row < args.rows && col + i * 32 < args.cols) {
-                        tma_store_3d(&tmC2, boxp, col + i * 32, 0, row);
-                        tma_store_3d(&tmC2, boxp + 2048, col + i * 32, 1, row);
-                        bulk_commit();
+                    if (lane == 0) {
+                        if (in) {
+                            tma_store_3d(&tmC2, minep, ch, 0, row);
+                            tma_store_3d(&tmC2, minep + 4096, ch, 1, row);
+                            bulk_commit();
+                        }
+                        bulk_wait_read<0>();
                     }
-                    // two chunks on, in this tile or the next whole one
-                    if (i < 2 || follows) {
-                        if (lane == 0) bulk_wait_read<0>();
-                        if (i < 2) read_pre(row, col + (i + 2) * 32);
-                        else read_pre(row_of(after), after.n * 256 + half * 128 + (i - 2) * 32);
+                    __syncwarp();
+                    // h after them, from the gate's box; the next 64 channels, of this tile or of the next whole one
+                    const bool next = i == 0 || follows;
+                    const int next_row = i == 0 ? row : row_of(after);
+                    const int next_ch = i == 0 ? col + 64 : after.n * 256 + half * 128;
+                    if (next) read_pre(next_row, next_ch, 1);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) st_shared16(mine + swz(lane, c), h[c]);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (in) {
+                            tma_store_2d(&tmC0, minep, ch, row);
+                            bulk_commit();
+                        }
+                        if (next) bulk_wait_read<0>();
                     }
+                    if (next) read_pre(next_row, next_ch, 0);
                 }
                 if (!ok) break;
             } else if constexpr (TERMS > 1) {
@@ -824,7 +822,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             more = units.next(u);
         }
-        for (; used < reads; ++used) wait_on(&x.loaded[w][used & 1], (used >> 1) & 1);   // after a wait that ran out
+        for (; used < reads; ++used) wait_on(&x.loaded[w], used & 1);   // after a wait that ran out
         if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
@@ -1096,7 +1094,7 @@ bool map_bf16(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(cols) * 2};
     const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
     return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 2, dims, strides, box,
-                   box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // [a][b][cols] with boxes over one of a or b.
 bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t cols, int box_a, int box_b,
@@ -1105,7 +1103,7 @@ bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t co
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols * b) * 2};
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_b), cuuint32_t(box_a)};
     return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, strides, box,
-                   box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Codes [rows][cols] in boxes of 128 (64: h's) columns.
@@ -1341,7 +1339,7 @@ cudaError_t tc_gated(int64_t N, int D, int F, int act, const void* x, const void
 cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, const void* w_out, const void* pre,
                           void* dpre, void* h, float* ws, cudaStream_t st) {
     Plan p = plan_grad(N, D, F);
-    p.a.part = ws, p.a.act = act, p.a.h = static_cast<__nv_bfloat16*>(h);
+    p.a.part = ws, p.a.act = act;
     JoinArgs j{};
     j.out = static_cast<__nv_bfloat16*>(h), j.dpre = static_cast<__nv_bfloat16*>(dpre), j.pre = static_cast<const __nv_bfloat16*>(pre);
     j.rows = F, j.cols = N;
@@ -1349,10 +1347,10 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
     if (p.columns) {
         e = launch_pairs<kPart, false, true, false>({w_out, F}, {dy, N}, D, p, kNone, kNone, kNone, st, false);
     } else {
-        CUtensorMap cp, cd;
-        if (!map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 32) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 32))
+        CUtensorMap c, cp, cd;
+        if (!map_bf16(&c, h, N, F, 32, 64) || !map_bf16_3d(&cp, pre, N, 2, F, 32, 1, 64) || !map_bf16_3d(&cd, dpre, N, 2, F, 32, 1, 64))
             return cudaErrorInvalidValue;
-        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, kNone, cp, cd, st, false);
+        e = launch_pairs<kGrad, false, false, true>({dy, N}, {w_out, F}, D, p, c, cp, cd, st, false);
     }
     return e != cudaSuccess ? e : join<kJoinGrad>(p, j, st);
 }
