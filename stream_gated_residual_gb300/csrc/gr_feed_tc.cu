@@ -1142,8 +1142,9 @@ int pairs_of() {
     return n > 0 ? n : 76;
 }
 
-constexpr int kFewTokens = 512;    // up to which the tokens are C's columns
-constexpr int kDivideBlocks = 48;  // blocks of k a pair has to save by dividing the last tiles
+// Up to so many tokens they are C's columns: the block of 4096 x 11008 on 512 tokens takes 112 us (by tiles 122), on
+// 640 173 (131).
+constexpr int kFewTokens = 512;
 
 // An operand's memory and its rows along M or N.
 struct Operand {
@@ -1231,8 +1232,11 @@ void spread(Plan& p, int64_t tiles, int64_t whole, int least) {
     p.bytes = p.rest ? size_t(p.pairs) * p.a.slots * kTileM * p.a.bn * 4 : 0;
 }
 
-// Whole tiles of 256 x 256 (kGated: 128 channels), a pair each, as long as there are as many as pairs. The last
-// ones, fewer than that, are divided along k among all the pairs where that saves more than the parts cost.
+// Whole tiles of 256 x 256 (kGated: 128 channels), a pair each, as long as there are as many as pairs. The last ones,
+// fewer than that, are a pair's each too, or divided along k among all the pairs where that is expected to be shorter:
+// the parts and their sums cost about as much as 80 blocks of k (25 us), and pairs that are at different k share no
+// reads of the L2, so that operands beyond it are read from memory more than once. Divided and not, us: dx of 8192 x
+// 2560 x 10240 446 + 9 and 480, of 1536 tokens 136 + 13 and 95.
 Plan plan_tiles(int64_t rows, int64_t cols, int64_t K, int per_tile, bool fp8) {
     Plan p;
     p.a.nk = int(ceil_div(K, fp8 ? 128 : 64));
@@ -1243,7 +1247,9 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t K, int per_tile, bool fp8) {
     p.a.group = 8;
     p.a.rows = rows, p.a.cols = cols;
     const int64_t tiles = int64_t(p.a.tiles_m) * p.a.tiles_n, pairs = pairs_of(), rest = tiles % pairs;
-    const bool divide = rest && (pairs - rest) * p.a.nk > kDivideBlocks * pairs && rest * p.a.nk >= 2 * pairs;
+    const double range = double(rest) * p.a.nk / double(pairs);
+    const bool resident = (rows + cols * (256 / per_tile)) * K * (fp8 ? 1 : 2) <= (60 << 20);
+    const bool divide = range >= 2 && range * (resident ? 1.0 : 1.4) + 80 < p.a.nk;
     spread(p, tiles, divide ? tiles - rest : tiles, fp8 ? 1 : 4);
     if (tiles < p.pairs && !divide) p.pairs = int(tiles);
     return p;

@@ -42,7 +42,9 @@ def weights(D, F, dtype, seed=0):
 SIZES = [(1, 8, 8), (1, 256, 1024), (2, 2560, 1288), (5, 72, 4104), (16, 64, 128), (17, 136, 520), (33, 1000, 2728),
          (64, 512, 256), (127, 128, 640), (128, 264, 264), (129, 256, 2048), (200, 1032, 136), (256, 4096, 256),
          (257, 256, 512), (300, 2560, 1288), (511, 136, 3336), (700, 384, 1024), (1025, 512, 1160), (2305, 520, 776),
-         (4099, 264, 1032), (3400, 1160, 1160), (301, 1800, 2056)]
+         (4099, 264, 1032), (3400, 1160, 1160), (301, 1800, 2056),
+         # long sums: few tiles, and the tiles behind whole waves of them, divided along k
+         (600, 7168, 256), (600, 256, 7168), (7000, 264, 520), (5000, 7168, 512)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -174,7 +176,8 @@ def test_encode_of_what_is_not_finite(value, rows, dtype):
 @pytest.mark.parametrize("N,K,O", [(1, 16, 8), (1, 4096, 512), (3, 144, 136), (16, 128, 128), (17, 1040, 264),
                                    (64, 512, 1024), (100, 272, 2056), (128, 4096, 256), (129, 528, 520), (255, 2560, 128),
                                    (256, 640, 1032), (257, 1168, 384), (600, 512, 2560), (1111, 1040, 1288),
-                                   (3000, 656, 776), (3400, 400, 1160), (3400, 1040, 1096)])
+                                   (3000, 656, 776), (3400, 400, 1160), (3400, 1040, 1096), (600, 16384, 264),
+                                   (5000, 12288, 1032)])
 def test_fp8_matmul(N, K, O):
     a = gr.fp8_encode_blocks(randn(N, N, K) * torch.exp2(3 * randn(K, N, 1)))
     b = gr.fp8_encode_blocks(randn(O, O, K) * torch.exp2(2 * randn(1, -(-O // 128), 1)).repeat_interleave(128, 0)[:O],
@@ -199,7 +202,8 @@ def test_fp8_matmul_of_nan_blocks():
 
 @pytest.mark.parametrize("i,size", list(enumerate([
     (1, 16, 16), (1, 256, 1024), (3, 2560, 1296), (16, 64, 128), (33, 144, 400), (64, 1024, 512), (127, 272, 640),
-    (128, 512, 272), (200, 1040, 2064), (257, 256, 512), (500, 528, 784), (1030, 384, 1168), (2300, 272, 656), (4400, 1168, 1040)])))
+    (128, 512, 272), (200, 1040, 2064), (257, 256, 512), (500, 528, 784), (1030, 384, 1168), (2300, 272, 656), (4400, 1168, 1040), (600, 12288, 272),
+    (600, 272, 12288)])))
 def test_feed_forward_fp8(i, size):
     N, D, F = size
     name = ("silu", "gelu")[i % 2]
