@@ -83,7 +83,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
         }
     }
 }
-// The same by a whole warp, with one answer.
+// The same by a whole warp, with one answer: its lanes leave their loops together.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(~0u, wait_on(bar, parity)); }
 // One lane of a warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
@@ -521,7 +521,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const uint32_t begin = q;
             for (uint32_t i = 0; ok && more && i < kBatch; ++i, ++q) {
                 const uint32_t slot = q % kScaleSlots;
-                if (q >= kScaleSlots) ok = wait_on(&x.scales_empty[slot], ((q / kScaleSlots) - 1) & 1);
+                if (q >= kScaleSlots) ok = wait_warp(&x.scales_empty[slot], ((q / kScaleSlots) - 1) & 1);
                 if (ok) copy_step(smem_u32(sf) + slot * kScaleSlot + lane * 16, kb);
                 kb += 4;
                 if (kb >= u.k1) {
@@ -560,7 +560,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int j = 0; more; ++j) {
             const int b = j % accs;
             const Unit now = u;
-            if (!wait_on(&x.acc_full[b], (j / accs) & 1)) break;
+            if (!wait_warp(&x.acc_full[b], (j / accs) & 1)) break;
             tc_fence_after();
             const uint32_t acc = tmem + b * acc_cols + lanes;
             const int row = row_of(now);   // the warp's first
@@ -679,7 +679,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     t[half * 128] = top;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&x.top_full[quad]);
-                    if (!wait_on(&x.top_full[quad], j & 1)) break;
+                    if (!wait_warp(&x.top_full[quad], j & 1)) break;
                     top = max(top, *const_cast<volatile uint32_t*>(t + (half ^ 1) * 128));
                     float inv;
                     const uint8_t e = block_scale(top, inv);
@@ -712,7 +712,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     float dh[64];
                     get64(half * 128 + i * 64, dh);
                     if (i == 1) drained();
-                    ok = ok && wait_on(&x.loaded[w], used & 1);
+                    ok = ok && wait_warp(&x.loaded[w], used & 1);
                     ++used;
                     uint4 h[8];
 #pragma unroll
@@ -796,7 +796,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (lane == 0) arrive_remote(map_rank(smem_u32(&x.acc_empty[j % accs]), 0));
                     from += kRun;
                     if (from >= now.k1) break;
-                    ok = wait_on(&x.acc_full[(j + 1) % accs], ((j + 1) / accs) & 1);
+                    ok = wait_warp(&x.acc_full[(j + 1) % accs], ((j + 1) / accs) & 1);
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -822,7 +822,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             more = units.next(u);
         }
-        for (; used < reads; ++used) wait_on(&x.loaded[w], used & 1);   // after a wait that ran out
+        for (; used < reads; ++used) wait_warp(&x.loaded[w], used & 1);   // after a wait that ran out
         if (lane == 0) bulk_wait_all();
     }
     __syncwarp();

@@ -215,6 +215,45 @@ def test_feed_forward_fp8(i, size):
     within(y, want, bound, "y")
 
 
+@pytest.mark.parametrize("N", [3, 700])
+def test_feed_forward_fp8_keeps_what_is_not_finite_in_its_rows(N):
+    D, F = 272, 656
+    x, (w_in, w_out) = randn(1, N, D, dtype=BF), weights(D, F, F32)
+    w_in, w_out = gr.fp8_encode_blocks(w_in, 128), gr.fp8_encode_blocks(w_out, 128)
+    clean = gr.feed_forward_fp8(x, w_in, w_out)
+    x[1, 77] = float("inf")
+    y = gr.feed_forward_fp8(x, w_in, w_out)
+    assert torch.isnan(y[1]).all()
+    keep = torch.arange(N, device="cuda") != 1
+    assert torch.equal(y[keep], clean[keep])
+
+
+def test_rows_past_32_bits():
+    """pre, h and their gradients pass 2^31 elements: the last rows against the definition, and the weights'
+    gradients of rows that are zero but for those."""
+    N, D, F = 70_001, 64, 16_384
+    w_in, w_out = weights(D, F, BF)
+    x = torch.zeros(N, D, dtype=BF, device="cuda")
+    x[-300:] = randn(1, 300, D, dtype=BF)
+    y, pre = gr.feed_forward(x, w_in, w_out, keep=True)
+    wy, wp, by, bp = ref.forward(x[-300:], w_in, w_out, "silu", BF)
+    within(y[-300:], wy, by, "y")
+    within(pre[-300:], wp, bp, "pre")
+    assert not y[:-300].any() and not pre[:-300].any()
+    dx, dw_in, dw_out = gr.feed_forward_backward(x, x, w_in, w_out, pre)
+    want = ref.backward(x[-300:], x[-300:], w_in, w_out, pre[-300:], "silu", BF)
+    within(dx[-300:], *want[0], "dx")
+    assert not dx[:-300].any()
+    # the other rows add zeros, which leave every partial sum as it is
+    within(dw_in, *want[1], "dw_in")
+    within(dw_out, *want[2], "dw_out")
+    eight = gr.fp8_encode_blocks(w_in, 128), gr.fp8_encode_blocks(w_out, 128)
+    y = gr.feed_forward_fp8(x, *eight)
+    wy, by = ref.forward_fp8(x[-300:], *eight, "silu")
+    within(y[-300:], wy, by, "y")
+    assert not y[:-300].any()
+
+
 # ---- how calls are made -------------------------------------------------------------------------
 
 def every_call(N, D=256, F=640):
