@@ -22,7 +22,10 @@ inline int scale_pitch(int64_t k) { return 4 * scale_steps(k); }
 inline size_t token_scale_bytes(int64_t rows, int64_t k) { return size_t(ceil_div(rows, kBlock)) * scale_steps(k) * 512; }
 struct Fp8Product {
     const uint8_t *tokens, *token_scales, *weights, *weight_scales;
+    bool token_rows = false;   // token_scales in plain rows (tc_takes_rows): no launch before laid anything out
 };
+// Whether a product takes both operands' scales as the encoder left them: few tokens, rows of whole words.
+bool tc_takes_rows(int64_t N, int64_t K, const uint8_t* a_scales, const uint8_t* b_scales);
 // Rows of scales [rows][blocks] to be laid out: as tokens, or with the weights' pitch.
 struct ScaleRows {
     const uint8_t* from;
@@ -45,7 +48,7 @@ cudaError_t tc_gated_grad(int64_t N, int D, int F, int act, const void* dy, cons
                           void* dpre, void* h, float* ws, cudaStream_t st);
 cudaError_t tc_product(int64_t M, int64_t N, int64_t K, int64_t tokens, const void* a, bool a_k, const void* b,
                        bool b_k, void* out, float* ws, cudaStream_t st);
-// On FP8 blocks, programmatic dependents of the launch that laid out their scales; h in blocks of one row, its
+// On FP8 blocks, programmatic dependents of the launch that laid out their scales (if one did); h in blocks of one row, its
 // scales laid out as the tokens of the next product; out bf16.
 cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, const Fp8Product& in, uint8_t* h, uint8_t* hs, float* ws,
                          cudaStream_t st);

@@ -249,6 +249,8 @@ int gr_fp8_matmul(const gr_product* p, const uint8_t* a, const uint8_t* a_scales
         return st;
     if ((st = usable_device())) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tc_takes_rows(N, K, a_scales, b_scales))
+        return as_status(tc_product_fp8(N, O, K, {a, a_scales, b, b_scales, true}, out, w.parts, s));
     cudaError_t e = launch_fp8_operands(nullptr, 0, 0, nullptr, nullptr, {a_scales, w.a, int64_t(N), int(nb), true},
                                         {b_scales, w.b, int64_t(ceil_div(O, kBlock)), int(nb), false}, s);
     if (e == cudaSuccess) e = tc_product_fp8(N, O, K, {a, w.a, b, w.b}, out, w.parts, s);

@@ -141,11 +141,11 @@ enum Mode {
 
 // The scales of a product's operands. The tokens' as the tensor cores take them: for each 128 rows and four blocks of
 // k 512 bytes, row r's word at 16 (r % 32) + 4 (r / 32). The weights' in rows of whole words, one for each `per` rows'
-// (a matrix') 128.
+// (a matrix') 128. token_pitch: few tokens may also come in rows of whole words.
 struct Scales {
     const uint8_t *tokens, *weights;
     int64_t n_tokens, n_weights, per;
-    int pitch;
+    int pitch, token_pitch;
     __device__ const uint8_t* weight_row(uint32_t row) const {
         const uint32_t m = uint32_t(per), which = row / m;
         return weights + int64_t(which * ((m + kBlock - 1) / kBlock) + (row - which * m) / kBlock) * pitch;
@@ -500,7 +500,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int64_t row = t0 + i * 32;   // 32 rows from a multiple of 32 on
-                    if (i * 32 < args.bn && row < sc.n_tokens)
+                    if (sc.token_pitch) {
+                        if (i * 32 < args.bn && row + lane < sc.n_tokens)
+                            copy4(to + (i >> 2) * 512 + (i & 3) * 4, sc.tokens + (row + lane) * sc.token_pitch + kb);
+                    } else if (i * 32 < args.bn && row < sc.n_tokens)
                         copy4(to + (i >> 2) * 512 + (i & 3) * 4,
                               sc.tokens + ((row >> 7) * steps + st) * 512 + lane * 16 + ((row >> 5) & 3) * 4);
                 }
@@ -1479,7 +1482,7 @@ cudaError_t tc_gated_fp8(int64_t N, int D, int F, int act, const Fp8Product& in,
                          cudaStream_t st) {
     Plan p = plan_gated(N, D, F, true);
     p.a.part = ws, p.a.act = act;
-    p.a.scales = {in.token_scales, in.weight_scales, N, 2 * int64_t(F), F, scale_pitch(D)};
+    p.a.scales = {in.token_scales, in.weight_scales, N, 2 * int64_t(F), F, scale_pitch(D), 0};
     JoinArgs j{};
     j.codes = h, j.scales = hs, j.scale_steps = scale_steps(F);
     j.rows = F, j.cols = N;
@@ -1500,21 +1503,27 @@ cudaError_t tc_product_fp8(int64_t N, int64_t O, int64_t K, const Fp8Product& in
                            cudaStream_t st) {
     Plan p = plan_product(N, O, K, N, true);
     p.a.part = ws;
-    p.a.scales = {in.token_scales, in.weight_scales, N, O, O, scale_pitch(K)};
+    p.a.scales = {in.token_scales, in.weight_scales, N, O, O, scale_pitch(K), in.token_rows ? scale_pitch(K) : 0};
     JoinArgs j{};
     j.out = static_cast<__nv_bfloat16*>(out);
     j.rows = O, j.cols = N;
     cudaError_t e;
     if (p.columns) {
-        e = launch_pairs<kPart, true, false, false>({in.weights, O}, {in.tokens, N}, K, p, kNone, kNone, kNone, st, true);
+        e = launch_pairs<kPart, true, false, false>({in.weights, O}, {in.tokens, N}, K, p, kNone, kNone, kNone, st,
+                                                    !in.token_rows);
     } else {
         CUtensorMap c;
         if (!map_bf16(&c, out, N, O, 32, 64)) return cudaErrorInvalidValue;
-        e = launch_pairs<kStore, true, false, false>({in.tokens, N}, {in.weights, O}, K, p, c, kNone, kNone, st, true);
+        e = launch_pairs<kStore, true, false, false>({in.tokens, N}, {in.weights, O}, K, p, c, kNone, kNone, st,
+                                                    !in.token_rows);
     }
     return e != cudaSuccess ? e : join<kJoinStore>(p, j, st);
 }
 
+bool tc_takes_rows(int64_t N, int64_t K, const uint8_t* a_scales, const uint8_t* b_scales) {
+    return few(N) && ceil_div(K, kBlock) % 4 == 0 &&
+           ((reinterpret_cast<uintptr_t>(a_scales) | reinterpret_cast<uintptr_t>(b_scales)) & 3) == 0;
+}
 size_t tc_product_fp8_workspace(int64_t N, int64_t O, int64_t K) { return plan_product(N, O, K, N, true).bytes; }
 size_t tc_feed_fp8_workspace(int64_t N, int D, int F) {
     const size_t in = plan_gated(N, D, F, true).bytes, down = plan_product(N, D, F, N, true).bytes;

@@ -187,6 +187,21 @@ def test_fp8_matmul(N, K, O):
     within(out, want, bound, "out")
 
 
+@pytest.mark.parametrize("N", [1, 40, 300, 512, 900])
+def test_fp8_matmul_of_scales_at_any_address(N):
+    """The same bits whether the scales' rows are read as they lie or laid out first."""
+    K, O = 1024, 264
+    a = gr.fp8_encode_blocks(randn(1, N, K) * torch.exp2(3 * randn(2, N, 1)))
+    b = gr.fp8_encode_blocks(randn(3, O, K), 128)
+    want = gr.fp8_matmul(a, b)
+
+    def moved(t):
+        return torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
+
+    for pa, pb in ((a, (b[0], moved(b[1]))), ((a[0], moved(a[1])), b)):
+        assert torch.equal(gr.fp8_matmul(pa, pb), want)
+
+
 def test_fp8_matmul_of_nan_blocks():
     """A NaN exponent reaches the outputs of its rows and no others, in either operand."""
     for N in (5, 300):
