@@ -473,8 +473,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         constexpr bool kTokensB = MODE == kPart;   // else A's rows are the tokens
         const Scales& sc = args.scales;
         const uint32_t steps = args.steps;
-        const uint8_t* pw[8];   // the lane's rows of weights in the tile
-        int64_t t0 = 0;         // the tile's first token
+        const uint8_t *pw[8], *pt[8];   // the lane's rows of weights in the tile, and (kPart) of tokens
+        const uint32_t hop = sc.token_pitch ? 4 : 512;   // from a step's words of the tokens to the next's
+        int64_t t0 = 0;                 // the tile's first token
         auto find = [&](const Unit& t) {
             t0 = kTokensB ? int64_t(t.n) * args.bn : int64_t(t.m) * kTileM + rank * kRowsA;
             const int64_t w0 = kTokensB ? int64_t(t.m) * kTileM + rank * kRowsA : int64_t(t.n) * args.bn;
@@ -488,6 +489,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
                 pw[i] = row < sc.n_weights ? sc.weight_row(uint32_t(row)) : sc.weights;
             }
+            if constexpr (kTokensB) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t row = t0 + i * 32;   // 32 rows from a multiple of 32 on
+                    pt[i] = row + lane >= sc.n_tokens ? sc.tokens
+                            : sc.token_pitch          ? sc.tokens + (row + lane) * sc.token_pitch
+                                                      : sc.tokens + (row >> 7) * steps * 512 + lane * 16 + ((row >> 5) & 3) * 4;
+                }
+            }
         };
         auto copy4 = [](uint32_t to, const uint8_t* p) {
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
@@ -498,15 +508,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int i = 0; i < (kTokensB ? 4 : 8); ++i) copy4(w + (i >> 2) * 512 + (i & 3) * 4, pw[i] + kb);
             if constexpr (kTokensB) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t row = t0 + i * 32;   // 32 rows from a multiple of 32 on
-                    if (sc.token_pitch) {
-                        if (i * 32 < args.bn && row + lane < sc.n_tokens)
-                            copy4(to + (i >> 2) * 512 + (i & 3) * 4, sc.tokens + (row + lane) * sc.token_pitch + kb);
-                    } else if (i * 32 < args.bn && row < sc.n_tokens)
-                        copy4(to + (i >> 2) * 512 + (i & 3) * 4,
-                              sc.tokens + ((row >> 7) * steps + st) * 512 + lane * 16 + ((row >> 5) & 3) * 4);
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (i * 32 < args.bn) copy4(to + (i >> 2) * 512 + (i & 3) * 4, pt[i] + st * hop);
             } else if (t0 < sc.n_tokens) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
                              "l"(sc.tokens + ((t0 >> 7) * steps + st) * 512 + lane * 16)
