@@ -1,13 +1,18 @@
 // The feed-forward sublayer's products on the 5th-generation tensor cores (tcgen05, operands staged by TMA,
-// accumulators in tensor memory), bf16 and FP8 blocks:
+// accumulators in tensor memory): bf16, FP8 blocks, and fp32 as three bf16 terms.
 //
 //     C[m][n] = Σ_k A[m][k] B[n][k]
 //
-// Two CTAs on neighbouring SMs form one tile of 256 x 256 (cta_group::2): each holds 128 rows of A and half of
-// B's rows, so an operand byte that reaches an SM is used for 256 rows of the other operand, and an SM loads 32
-// KB for 512 cycles of MMAs. A persistent grid of pairs; in each CTA one warp feeds a ring of stages by TMA, one
-// (of the pair's first CTA) issues the MMAs, eight drain the accumulator: two accumulators in tensor memory, so
-// the MMAs of the next tile run meanwhile.
+// Two CTAs on neighbouring SMs form one tile of 256 x 256 (cta_group::2): each holds 128 rows of A and half of B's
+// rows, so an operand byte that reaches an SM is used for 256 rows of the other operand, and an SM loads 32 KB for
+// 512 cycles of MMAs. A persistent grid of pairs; in each CTA one warp feeds a ring of stages by TMA, one (of the
+// pair's first CTA) issues the MMAs, eight drain the accumulator: two accumulators in tensor memory, so the MMAs of
+// the next tile run meanwhile.
+//
+// Bound by the tensor pipe with many tokens: 16384 x 4096 x 22016 in bf16 takes 1.52 ms (1.94 PFLOP/s, the pipe 95%
+// active at 1.64 GHz), the same in FP8 0.88 ms (3.4 PFLOP/s, 77% active at 1.75 GHz). With few tokens they become C's
+// columns and the weights' bytes bound it: 268 MB for 64 tokens in 43.5 us from the first load to the last sum, the
+// partial sums of ranges of k joined by a second launch (2 us when it follows at once).
 #include <atomic>
 
 #include "gr_feed.h"
