@@ -362,3 +362,60 @@ def test_wrong_arguments_are_refused():
             gr.fp8_encode_blocks(*bad)
     with pytest.raises(gr.GRError):
         gr.fp8_encode_blocks(torch.zeros(4, 24, device="cuda"))
+
+
+@pytest.mark.parametrize("N", [5, 900])
+@pytest.mark.parametrize("i", range(5))
+def test_two_streams_at_once(i, N):
+    """Calls under way on two streams at the same time, each with memory of its own."""
+    name, call = every_call(N, 512, 1280)[i]
+    want = call()
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(12):
+        for side in sides:
+            with torch.cuda.stream(side):
+                got.append(call())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for outs in got for a, b in zip(outs, want)), name
+
+
+@pytest.mark.parametrize("N", [1, 60, 700])
+def test_weights_written_just_before_a_call(N):
+    """Weights are read ahead of the products' own predecessors, but not of what wrote them."""
+    D, F = 1024, 4096
+    x = randn(1, N, D, dtype=BF)
+    sets = [weights(D, F, BF, seed) for seed in (3, 9)]
+    eights = [tuple(gr.fp8_encode_blocks(w, 128) for w in s) for s in sets]
+    want = [gr.feed_forward(x, *s) for s in sets]
+    want8 = [gr.feed_forward_fp8(x, *e) for e in eights]
+    w = [t.clone() for t in sets[0]]
+    e = [tuple(t.clone() for t in pair) for pair in eights[0]]
+    got, got8 = [], []
+    for k in range(10):
+        for to, new in zip(w, sets[k % 2]):
+            to.copy_(new)
+        got.append(gr.feed_forward(x, *w))
+        for pair, new in zip(e, eights[k % 2]):
+            for to, t in zip(pair, new):
+                to.copy_(t)
+        got8.append(gr.feed_forward_fp8(x, *e))
+    for k in range(10):
+        assert torch.equal(got[k], want[k % 2]) and torch.equal(got8[k], want8[k % 2]), k
+
+
+def test_results_do_not_depend_on_what_the_workspace_holds():
+    """Workspaces and outputs full of NaN bytes before the call, for every way a call can be divided."""
+    for N in (3, 300, 700, 2305):
+        for name, call in every_call(N, 1032 - 8, 2064):
+            want = call()
+            torch.cuda.synchronize()
+            kept = torch.empty
+            try:
+                torch.empty = lambda *a, **k: kept(*a, **k).view(torch.uint8).fill_(255).view(k["dtype"]) \
+                    if k.get("dtype") != torch.uint8 else kept(*a, **k).fill_(255)
+                again = call()
+            finally:
+                torch.empty = kept
+            assert all(torch.equal(a, b) for a, b in zip(want, again)), (name, N)
