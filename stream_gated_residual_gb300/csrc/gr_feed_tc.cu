@@ -165,6 +165,7 @@ struct Args {
     int stages;
     int act;
     int keep;               // kGated: write pre
+    int whole_a, whole_b;   // MN-major operands of whole groups of 64 rows: a box of both groups at once
     int early;              // A is not the launch before's: its first stages are read ahead of it
     int trigger;            // the next launch may start beside this one
     // Tiles 0 .. whole - 1 are done by a pair each; the others' steps of k, one after another, in even ranges
@@ -350,8 +351,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (A_MN) tma_pair_3d(pa + 8192, &tmA, m0 + 64, kb * kK, t, bar0 + s * 8);
                 }
             } else if constexpr (A_MN) {
-                tma_pair_2d(pa, &tmA, m0, kb * kK, bar0 + s * 8);
-                tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar0 + s * 8);
+                if (args.whole_a) {
+                    tma_pair_3d(pa, &tmA, 0, kb * kK, m0 >> 6, bar0 + s * 8);
+                } else {
+                    tma_pair_2d(pa, &tmA, m0, kb * kK, bar0 + s * 8);
+                    tma_pair_2d(pa + 8192, &tmA, m0 + 64, kb * kK, bar0 + s * 8);
+                }
             } else {
                 tma_pair_2d(pa, &tmA, kb * kK, m0, bar0 + s * 8);
             }
@@ -365,7 +370,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             } else if constexpr (MODE == kGated) {
                 tma_pair_3d(pb, &tmB, kb * kK, n0, int(rank), bar0 + s * 8);
             } else if constexpr (B_MN) {
-                for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar0 + s * 8);
+                if (args.whole_b)
+                    tma_pair_3d(pb, &tmB, 0, kb * kK, n0 >> 6, bar0 + s * 8);
+                else
+                    for (int i = 0; i < rows_b; i += 64) tma_pair_2d(pb + i * 128, &tmB, n0 + i, kb * kK, bar0 + s * 8);
             } else {
                 tma_pair_2d(pb, &tmB, kb * kK, n0, bar0 + s * 8);
             }
@@ -1118,6 +1126,14 @@ bool map_bf16_3d(CUtensorMap* m, const void* p, int64_t a, int64_t b, int64_t co
                    CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// A bf16 matrix [k][rows], rows a multiple of 64, as [rows / 64][k][64]: boxes of `groups` x 64 k x 64 rows, each group
+// where a box of its own would lie.
+bool map_groups(CUtensorMap* m, const void* p, int64_t k, int64_t rows, int groups) {
+    const cuuint64_t dims[3] = {64, cuuint64_t(k), cuuint64_t(rows / 64)};
+    const cuuint64_t strides[2] = {cuuint64_t(rows) * 2, 128};
+    const cuuint32_t box[3] = {64, 64, cuuint32_t(groups)};
+    return map_box(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 // Codes [rows][cols] in boxes of 128 (64: h's) columns.
 bool map_codes(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows, int box_cols) {
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(cols)};
@@ -1197,11 +1213,17 @@ cudaError_t launch_pairs(const Operand& a, const Operand& b, int64_t K, const Pl
              (B_MN ? map_bf16_3d(&mb, b.p, TERMS, K, b.rows, 1, 64, 64)
                    : map_bf16_3d(&mb, b.p, TERMS, b.rows, K, 1, rows_b, 64));
     } else {
-        ok = A_MN ? map_bf16(&ma, a.p, K, a.rows, 64, 64) : map_bf16(&ma, a.p, a.rows, K, kRowsA, 64);
+        args.whole_a = A_MN && a.rows % 64 == 0;
+        args.whole_b = B_MN && b.rows % 64 == 0 && rows_b % 64 == 0;
+        ok = args.whole_a ? map_groups(&ma, a.p, K, a.rows, kRowsA / 64)
+             : A_MN       ? map_bf16(&ma, a.p, K, a.rows, 64, 64)
+                          : map_bf16(&ma, a.p, a.rows, K, kRowsA, 64);
         if (MODE == kGated)
             ok = ok && map_bf16_3d(&mb, b.p, 2, b.rows, K, 1, 128, 64);
         else
-            ok = ok && (B_MN ? map_bf16(&mb, b.p, K, b.rows, 64, 64) : map_bf16(&mb, b.p, b.rows, K, rows_b, 64));
+            ok = ok && (args.whole_b ? map_groups(&mb, b.p, K, b.rows, rows_b / 64)
+                        : B_MN       ? map_bf16(&mb, b.p, K, b.rows, 64, 64)
+                                     : map_bf16(&mb, b.p, b.rows, K, rows_b, 64));
     }
     if (!ok) return cudaErrorInvalidValue;
     args.stages = stages_for<MODE, FP8, TERMS>(args.bn);
