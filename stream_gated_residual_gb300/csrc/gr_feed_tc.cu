@@ -286,7 +286,8 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     }
 }
 
-// tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64}. tmB: the same over bn / 2 rows (kGated: {k,
+// tmA: K-major {k, row} box {64, 128}, MN-major {row, k} box {64, 64} or, of whole groups of 64 rows, {row % 64, k,
+// row / 64} box {64, 64, 2}. tmB: the same over bn / 2 rows (kGated: {k,
 // channel, matrix} box {64, 128, 1}). tmC0: C, or h; tmC1: pre; tmC2: dpre.
 // TERMS 3 (kPart): each operand as three bf16 matrices one after another, {.., matrix} boxes.
 // FP8: codes, both operands K-major, boxes of 128 k; tmC0 of kGated: h's codes.
