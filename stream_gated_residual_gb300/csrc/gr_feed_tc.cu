@@ -170,9 +170,12 @@ struct Args {
     int trigger;            // the next launch may start beside this one
     // Tiles 0 .. whole - 1 are done by a pair each; the others' steps of k, one after another, in even ranges
     uint32_t whole;
+    // chunk > 0: no tile is whole; a pair's in turn are chunks of so many blocks, of all tiles their first, then their next
+    uint32_t chunk, tiles;
+    uint32_t turns;         // whole tiles, or chunks
     uint32_t steps;         // of a tile: nk in steps of one block (FP8: four, what a word of scales covers)
     uint32_t range, longer; // steps of a range; the first `longer` have one more
-    int slots;              // partial tiles a pair may write
+    int slots;              // partial tiles a pair's range may have
     float* part;
     int64_t rows, cols;     // of C (kGated: channels of h): boxes that start behind them are not stored
     Scales scales;          // FP8
@@ -219,18 +222,24 @@ static_assert(sizeof(Aux) <= kAuxBytes, "aux");
 // A pair's pieces of work, in the order all its roles go through them.
 struct Unit {
     int m, n, k0, k1;
-    int slot;   // of the pair's partial tiles; -1: a whole tile
+    int slot;   // of the partial tiles; -1: a whole tile
 };
 template <int STEP> struct Units {
     const Args& a;
     uint32_t tile, pairs, at, end;
-    int slot = 0;
+    int slot;
     __device__ Units(const Args& a, uint32_t pair, uint32_t pairs)
-        : a(a), tile(pair), pairs(pairs), at(a.begin(pair)), end(a.begin(pair + 1)) {}
+        : a(a), tile(pair), pairs(pairs), at(a.begin(pair)), end(a.begin(pair + 1)), slot(int(pair) * a.slots) {}
     __device__ bool next(Unit& u) {
-        if (tile < a.whole) {
-            a.place(tile, u.m, u.n);
+        if (tile < a.turns) {
+            uint32_t t = tile;
             u.k0 = 0, u.k1 = a.nk, u.slot = -1;
+            if (a.chunk) {
+                const uint32_t c = tile / a.tiles;
+                t -= c * a.tiles;
+                u.k0 = int(c * a.chunk), u.k1 = min(u.k0 + int(a.chunk), a.nk), u.slot = int(tile);
+            }
+            a.place(t, u.m, u.n);
             tile += pairs;
             return true;
         }
@@ -330,9 +339,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr int kK = FP8 ? 128 : 64;
     // The scales take columns behind 256: one accumulator of up to 256 columns, or two of 128.
     const int accs = FP8 && args.bn > 128 ? 1 : 2, acc_cols = FP8 ? 128 : 256;
-    // A tensor core cuts off what an addition to its accumulator shifts out: 2.7e-8 of the sum on average, 8.6e-6 after
-    // the 212 of 54 blocks. That is nothing beside a rounding to bf16, but not for fp32, so there an accumulator
-    // takes four blocks at most (16 additions, 2.8e-7), and those sums are added up with rounding.
+    // A tensor core cuts off what an addition to its accumulator shifts out, up to a unit in its last place. Few enough of
+    // them (kLongest) are nothing beside a rounding to bf16, but not for fp32, so there an accumulator takes four blocks at
+    // most (16 additions, 2.8e-7), and those sums are added up with rounding.
     constexpr int kRun = TERMS > 1 ? 4 : 1 << 30;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -657,7 +666,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // a partial tile's sums: [256 / 8 columns][256 rows][8]
             auto put_part = [&](uint32_t col, const float (&v)[64]) {
                 float4* p = reinterpret_cast<float4*>(args.part) +
-                            (int64_t(cluster_id_x()) * args.slots + now.slot) * (kTileM * 64) +
+                            int64_t(now.slot) * (kTileM * 64) +
                             (int64_t(col >> 3) * kTileM + int(rank) * kRowsA + quad * 32 + lane) * 2;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -854,7 +863,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc_fence_after();
                 }
                 if (!ok) break;
-                float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
+                float* p = args.part + int64_t(now.slot) * (int64_t(kTileM) * args.bn) +
                            int(rank) * kRowsA + quad * 32 + lane;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -863,7 +872,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int k = 0; k < 16; ++k) p[int64_t(half * 16 + c * 32 + k) * kTileM] = sum[c][k];
                 }
             } else {
-                float* p = args.part + (int64_t(cluster_id_x()) * args.slots + now.slot) * (int64_t(kTileM) * args.bn) +
+                float* p = args.part + int64_t(now.slot) * (int64_t(kTileM) * args.bn) +
                            int(rank) * kRowsA + quad * 32 + lane;
                 for (int c = half * 16; c < args.bn; c += 32) {
                     float v[16];
@@ -906,10 +915,17 @@ struct Sums {
     int64_t hop;
     uint32_t more;
     __device__ Sums(const Args& a, uint32_t t, int64_t at) {
-        const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
         const int64_t tile = int64_t(kTileM) * a.bn / 4;
-        hop = a.slots * tile;
         const float4* p = reinterpret_cast<const float4*>(a.part) + at;
+        if (a.chunk) {
+            hop = a.tiles * tile;
+            from = p + t * tile;
+            rest = from + hop;
+            more = (uint32_t(a.nk) - 1) / a.chunk;
+            return;
+        }
+        const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
+        hop = a.slots * tile;
         from = p + first * hop + (t - a.begin(first) / a.steps) * tile;
         rest = p + (first + 1) * hop;
         more = last - first;
@@ -1286,7 +1302,8 @@ void spread(Plan& p, int64_t tiles, int64_t whole, int least) {
         p.bytes = kTooLarge;
         return;
     }
-    p.a.whole = uint32_t(whole);
+    p.a.whole = p.a.turns = uint32_t(whole);
+    p.a.tiles = uint32_t(tiles);
     p.rest = uint32_t(tiles - whole);
     p.pairs = pairs_of();
     const int64_t total = int64_t(p.rest) * p.a.steps;
@@ -1297,6 +1314,36 @@ void spread(Plan& p, int64_t tiles, int64_t whole, int least) {
     p.a.range = uint32_t(total / p.pairs), p.a.longer = uint32_t(total % p.pairs);
     p.a.slots = int(ceil_div(ceil_div(total, p.pairs), p.a.steps)) + 1;
     p.bytes = p.rest ? size_t(p.pairs) * p.a.slots * kTileM * p.a.bn * 4 : 0;
+}
+
+// How many blocks of k an accumulator takes in bf16 and FP8. Each addition of 16 products (FP8: 32) is cut to its last
+// place: on sums of one sign that took 1.1 to 1.7 units of the sum so far, so that in one accumulator the weights'
+// gradients of a million tokens came out 4.0e-3 to 6.6e-3 short, more than half a unit of bf16, and of this many blocks at a
+// time up to 3.8e-4.
+constexpr int kLongest = 1024;
+static_assert(GR_MAX_FF / 128 <= kLongest, "FP8 needs no chunks");
+
+// A product whose accumulators would take more goes in chunks of k whose sums are added up like other parts. All tiles
+// are at the same chunk, so that they share their operands' reads in the L2; chunks as long as keeps the pairs busy. The
+// gradient of 131072 tokens of 2560 x 10240 takes 27.0 ms (26.8 in one accumulator a tile), of 65536 13.3 either way.
+void bound(Plan& p) {
+    const int64_t tiles = p.a.tiles, pairs = pairs_of(), nk = p.a.nk;
+    if (p.bytes == kTooLarge || nk <= kLongest || (p.a.whole == 0 && p.a.range < uint32_t(kLongest))) return;
+    int64_t best = INT64_MAX;
+    const int64_t fewest = ceil_div(nk, kLongest);
+    for (int64_t c = fewest; c == fewest || (c < fewest + 64 && c <= nk / 256); ++c) {
+        const int64_t chunk = ceil_div(nk, c), turns = tiles * ceil_div(nk, chunk);
+        const int64_t time = ceil_div(turns, pairs) * (chunk + 16);   // the parts' stores: about 16 blocks
+        if (time >= best - best / 32) continue;                      // more parts only where they save some time
+        best = time;
+        p.a.chunk = uint32_t(chunk);
+        p.a.turns = uint32_t(turns);
+        p.bytes = size_t(turns) * kTileM * p.a.bn * 4;
+        if (turns > 0x7fffffffLL) p.bytes = kTooLarge;
+    }
+    p.a.whole = p.a.range = p.a.longer = 0;
+    p.rest = uint32_t(tiles);
+    p.pairs = int(p.a.turns < uint32_t(pairs) ? p.a.turns : pairs);
 }
 
 // Whole tiles of 256 x 256 (kGated: 128 channels), a pair each, as long as there are as many as pairs. The last ones,
@@ -1319,6 +1366,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t K, int per_tile, bool fp8) {
     const bool divide = range >= 2 && range * (resident ? 1.0 : 1.4) + 80 < p.a.nk;
     spread(p, tiles, divide ? tiles - rest : tiles, fp8 ? 1 : 4);
     if (tiles < p.pairs && !divide) p.pairs = int(tiles);
+    bound(p);
     // Not where the sums of parts come next: their CTAs, waiting beside the products, make them slower (the gradient of
     // 16384 tokens of 256 x 1024: 205 us instead of 126).
     p.a.trigger = p.rest == 0;
@@ -1362,7 +1410,10 @@ bool few(int64_t tokens) { return tokens <= kFewTokens; }
 
 // C [M][N] = A Bᵀ.
 Plan plan_product(int64_t M, int64_t N, int64_t K, int64_t tokens, bool fp8) {
-    return few(tokens) ? plan_columns(N, M, K, fp8 ? 32 : 16, fp8) : plan_tiles(M, N, K, 256, fp8);
+    if (!few(tokens)) return plan_tiles(M, N, K, 256, fp8);
+    Plan p = plan_columns(N, M, K, fp8 ? 32 : 16, fp8);
+    bound(p);
+    return p;
 }
 template <bool A_K, bool B_K>
 cudaError_t product(const void* a, const void* b, void* out, int64_t M, int64_t N, int64_t K, int64_t tokens,

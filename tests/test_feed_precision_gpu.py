@@ -107,3 +107,44 @@ def test_gelu_far_below_zero_in_fp8(N):
                             "gelu")
     bound = (g.double() ** 2 + 8) * ULP
     relative(y, gelu(g)[0][:, None].expand(N, D), (2.0 ** -4 * (1 + bound) + bound)[:, None], "y")
+
+
+# ---- sums over very many tokens -------------------------------------------------------------------
+
+def test_one_signed_sums_over_a_million_tokens():
+    """The weights' gradients of 2^20 tokens, all terms of one sign. h = 16 u (GELU of 16 is 16, u a power of two),
+    dh = dy's first channel, dgate = dh u and dup = 16 dh are exact in bf16, so
+        dW_o[d][f] = 16 u_f Σ dy[n][d],   dW_u[f][d] = 16 Σ dy[n][0] x[n][d],   dW_g[f][d] = u_f Σ dy[n][0] x[n][d].
+    The result's rounding is off by 2^-8. An accumulator takes up to 1024 blocks of 64 k, 2^12 additions of 16 products each,
+    which are cut to its last place with three guard bits at least: up to two units, 2^-22, of the sum so far, which is
+    half of the last one on average: 2^-11. The parts' sums add a few units. The 2304 sums of each kind are spread evenly
+    over an octave, so their roundings, of deviation 2^-8 / sqrt(3), average to zero within four times 2^-8 /
+    sqrt(3 · 2304) < 2^-12. (One accumulator for all of k would add 2^16 cuts.)"""
+    N, D, F = 1 << 20, 2304, 1792
+
+    def some(seed):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed)
+        v = torch.rand(N, D, generator=gen, device="cuda", dtype=F32).add_(0.5)
+        return v.mul_(torch.linspace(1, 2, D, device="cuda")).to(BF)
+
+    x, dy = some(1), some(2)
+    u = torch.exp2((torch.arange(F, device="cuda") % 4 - 1).float())
+    pre = torch.empty(N, 2, F, dtype=BF, device="cuda")
+    pre[:, 0], pre[:, 1] = 16, u.to(BF)
+    w_in = torch.zeros(2, F, D, dtype=BF, device="cuda")
+    w_out = torch.zeros(D, F, dtype=BF, device="cuda")
+    w_out[0] = 1
+    dx, dw_in, dw_out = gr.feed_forward_backward(dy, x, w_in, w_out, pre, "gelu")
+    assert not dx.any()
+    del dx, pre
+    each = [torch.stack([(x[at:at + 65536].double() * dy[at:at + 65536, :1].double()).sum(0),
+                         dy[at:at + 65536].double().sum(0)]) for at in range(0, N, 65536)]
+    xy, total = torch.stack(each).sum(0)
+    for got, want, what in ((dw_out, 16 * total[:, None] * u.double(), "dw_out"),
+                            (dw_in[0], u.double()[:, None] * xy, "dw_in, gate"),
+                            (dw_in[1], (16 * xy)[None].expand(F, D), "dw_in, up")):
+        off = (got.double() - want) / want
+        print(f"{what}: {off.mean().item():.3e} on average, {off.abs().max().item():.3e} at most")
+        assert off.abs().max().item() <= 2.0 ** -8 + 2.0 ** -11, what
+        assert off.mean().abs().item() <= 2.0 ** -11 + 2.0 ** -12, what
