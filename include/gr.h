@@ -494,7 +494,7 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
  * of a sum of one sign), two runs on the same inputs give the same bits. fp32 products are formed from three bf16 terms of each
  * operand, with errors as small as fp32 sums' own. A value that is not finite makes the outputs that it enters not
  * finite (not always the infinity or NaN that a sum in order would give) and no others. Calls whose tiles or steps
- * of k pass 32 bits, beyond any memory, are refused (GR_E_SHAPE). */
+ * of k pass 32 bits, beyond any memory, are refused (GR_E_SHAPE), in fp32 those with N · max(D, F) above 2^34 − 1024. */
 typedef struct gr_feed {
     int64_t n_tokens;    /* N: 0 .. 2^31 − 1                                             */
     int32_t d_model;     /* D: a multiple of 8 (FP8: 16) in [8, GR_MAX_D]                */

@@ -1558,7 +1558,8 @@ struct TermParts {
             cover(plan_f32<true, true>(2 * F, N, D));
             cover(plan_f32<true, true>(D, N, F));
         }
-        if (need == kTooLarge) bytes = kTooLarge;
+        // the joins count their threads, four rows of a column each, in 32 bits
+        if (need == kTooLarge || N * (D > F ? D : F) > (int64_t(1) << 34) - 1024) bytes = kTooLarge;
         else parts = reinterpret_cast<float*>(take(int64_t(need), 1));
     }
 };
