@@ -612,7 +612,7 @@ def write_then_read_fp8(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tens
 #
 # These calls are also made for a few tokens at a time, where the binding itself is what a call costs.
 # Descriptors are packed bytes, kept by their values (numbers of Python: a tensor would be kept by its
-# identity); workspace sizes are kept by the descriptor (both are pure functions of the arguments), and
+# identity); workspace sizes are kept by the descriptor and the device (they depend on its number of SMs), and
 # pointers go as plain integers.
 
 _EMBED = struct.Struct("=qqiiiiif")    # gr_embedding
@@ -658,12 +658,21 @@ def _call(name: str, *args) -> None:
         raise GRError(status, name)
 
 
+def _here() -> int:
+    """The device that the library sizes workspaces for: the current one (asked where the process sees several)."""
+    return _current_device() if _several_devices() else 0
+
+
 @functools.lru_cache(1024)
-def _need(name: str, desc: bytes, *args) -> int:
-    """Bytes of a workspace-size entry (a function of the descriptor alone)."""
+def _need_on(device: int, name: str, desc: bytes, *args) -> int:
+    """Bytes of a workspace-size entry on `device`, which is the current one."""
     n = ctypes.c_size_t(0)
     _call(name, desc, *args, ctypes.byref(n))
     return n.value
+
+
+def _need(name: str, desc: bytes, *args) -> int:
+    return _need_on(_here(), name, desc, *args)
 
 
 def _ws(need: int, workspace: torch.Tensor | None, like: torch.Tensor, stream):
@@ -938,7 +947,7 @@ def linear_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor
 
 # ---- the gated feed-forward sublayer, and FP8 blocks ----------------------------------------------
 #
-# What follows from shapes and dtypes alone (checks, descriptor, workspace) is kept by them.
+# What follows from shapes and dtypes (checks, descriptor) and the device (workspace) is kept by them.
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1}
 BLOCK = 128    # channels of an FP8 block
@@ -972,7 +981,7 @@ def _activation(name: str) -> int:
 
 
 @functools.lru_cache(1024)
-def _feed_plan(xs, xt, ws, wt, os, ot, activation: str, gradient: int):
+def _feed_plan(device: int, xs, xt, ws, wt, os, ot, activation: str, gradient: int):
     """(shape of pre, descriptor, workspace bytes) of a call on bf16 or fp32 tensors."""
     if len(xs) != 2 or xt not in _DTYPES:
         raise ValueError("x must be a float32 or bfloat16 tensor [N, D]")
@@ -982,7 +991,7 @@ def _feed_plan(xs, xt, ws, wt, os, ot, activation: str, gradient: int):
     _same("w_in", ws, wt, (2, F, D), xt)
     _same("w_out", os, ot, (D, F), xt)
     f = _FEED.pack(N, D, F, _DTYPES[xt], _activation(activation))
-    return torch.Size((N, 2, F)), f, _need("gr_feed_workspace_size", f, gradient)
+    return torch.Size((N, 2, F)), f, _need_on(device, "gr_feed_workspace_size", f, gradient)
 
 
 def feed_forward(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activation: str = "silu",
@@ -992,7 +1001,7 @@ def feed_forward(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, activ
     [D, F], all bf16 or all fp32; f is "silu" or "gelu" (erf). Returns y [N, D]; with keep=True (or a pre to
     write) (y, pre), pre [N, 2, F] the gate and up values that the gradient needs."""
     shape, dtype = x.shape, x.dtype
-    pre_shape, f, need = _feed_plan(shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 0)
+    pre_shape, f, need = _feed_plan(_here(), shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 0)
     _given(x, "x")
     _given(w_in, "w_in")
     _given(w_out, "w_out")
@@ -1012,7 +1021,7 @@ def feed_forward_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor,
     """gr_feed_forward_backward: (dx, dw_in, dw_out) in x's dtype from dy [N, D] and the pre that
     feed_forward(keep=True) returned."""
     shape, dtype = x.shape, x.dtype
-    pre_shape, f, need = _feed_plan(shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 1)
+    pre_shape, f, need = _feed_plan(_here(), shape, dtype, w_in.shape, w_in.dtype, w_out.shape, w_out.dtype, activation, 1)
     for t, name in ((dy, "dy"), (x, "x"), (w_in, "w_in"), (w_out, "w_out"), (pre, "pre")):
         _given(t, name)
     _same("dy", dy.shape, dy.dtype, shape, dtype)
@@ -1073,14 +1082,14 @@ def _same_scales(name: str, codes, scales, block_rows: int) -> None:
 
 
 @functools.lru_cache(1024)
-def _product_plan(a, asc, b, bsc):
+def _product_plan(device: int, a, asc, b, bsc):
     """(shape of out, descriptor, workspace bytes)"""
     if len(a) != 2 or len(b) != 2 or a[1] != b[1]:
         raise ValueError(f"the codes must be [N, K] and [O, K], got {list(a)} and {list(b)}")
     _same_scales("a", a, asc, 1)
     _same_scales("b", b, bsc, BLOCK)
     p = _PRODUCT.pack(a[0], a[1], b[0])
-    return torch.Size((a[0], b[0])), p, _need("gr_fp8_matmul_workspace_size", p)
+    return torch.Size((a[0], b[0])), p, _need_on(device, "gr_fp8_matmul_workspace_size", p)
 
 
 def fp8_matmul(a, b, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -1089,7 +1098,7 @@ def fp8_matmul(a, b, out: torch.Tensor | None = None, workspace: torch.Tensor | 
     b = (codes [O, K], scales [O/128, K/128]) in blocks of 128 rows, as fp8_encode_blocks gives them."""
     ac, asc = _fp8_pair(a, "a")
     bc, bsc = _fp8_pair(b, "b")
-    shape, p, need = _product_plan(ac.shape, asc.shape, bc.shape, bsc.shape)
+    shape, p, need = _product_plan(_here(), ac.shape, asc.shape, bc.shape, bsc.shape)
     out = _out(out, "out", shape, torch.bfloat16, ac, stream)
     wp, wn, _keep = _ws(need, workspace, ac, stream)
     _call("gr_fp8_matmul", p, ac.data_ptr(), asc.data_ptr(), bc.data_ptr(), bsc.data_ptr(), out.data_ptr(),
@@ -1098,7 +1107,7 @@ def fp8_matmul(a, b, out: torch.Tensor | None = None, workspace: torch.Tensor | 
 
 
 @functools.lru_cache(1024)
-def _feed_fp8_plan(xs, xt, ic, isc, oc, osc, activation: str):
+def _feed_fp8_plan(device: int, xs, xt, ic, isc, oc, osc, activation: str):
     """(descriptor, workspace bytes)"""
     if len(ic) != 3 or ic[0] != 2 or len(oc) != 2:
         raise ValueError("the codes of w_in must be [2, F, D], those of w_out [D, F]")
@@ -1108,7 +1117,7 @@ def _feed_fp8_plan(xs, xt, ic, isc, oc, osc, activation: str):
     _same_scales("w_in", ic, isc, BLOCK)
     _same_scales("w_out", oc, osc, BLOCK)
     f = _FEED.pack(xs[0], D, F, GR_FP8, _activation(activation))
-    return f, _need("gr_feed_workspace_size", f, 0)
+    return f, _need_on(device, "gr_feed_workspace_size", f, 0)
 
 
 def feed_forward_fp8(x: torch.Tensor, w_in, w_out, activation: str = "silu", y: torch.Tensor | None = None,
@@ -1119,7 +1128,7 @@ def feed_forward_fp8(x: torch.Tensor, w_in, w_out, activation: str = "silu", y: 
     ic, isc = _fp8_pair(w_in, "w_in")
     oc, osc = _fp8_pair(w_out, "w_out")
     shape = x.shape
-    f, need = _feed_fp8_plan(shape, x.dtype, ic.shape, isc.shape, oc.shape, osc.shape, activation)
+    f, need = _feed_fp8_plan(_here(), shape, x.dtype, ic.shape, isc.shape, oc.shape, osc.shape, activation)
     _given(x, "x")
     y = _out(y, "y", shape, torch.bfloat16, x, stream)
     wp, wn, _keep = _ws(need, workspace, x, stream)
