@@ -21,6 +21,7 @@ from __future__ import annotations
 import argparse
 import dataclasses
 import math
+import sys
 
 import torch
 
@@ -185,7 +186,7 @@ class Decoder:
         return loss, g
 
 
-def main(argv=None) -> None:
+def main(argv=()) -> None:
     """Learns to continue a repeated phrase, then continues it token by token."""
     parser = argparse.ArgumentParser(description=main.__doc__)
     parser.add_argument("--d-ff", type=int, default=0, help="width of the feed-forward sublayers (0: none)")
@@ -216,4 +217,4 @@ def main(argv=None) -> None:
 
 
 if __name__ == "__main__":
-    main()
+    main(sys.argv[1:])
