@@ -42,6 +42,17 @@ class Config:
     activation: str = "silu"
     fp8: bool = False          # prompt and step on FP8 blocks of the feed-forward weights
 
+    def __post_init__(self):
+        step = 16 if self.fp8 else 8
+        if self.d_ff < 0 or self.d_ff % step:
+            raise ValueError(f"d_ff must be 0 or a multiple of {step}, got {self.d_ff}")
+        if self.activation not in ("silu", "gelu"):
+            raise ValueError(f"activation must be 'silu' or 'gelu', got {self.activation!r}")
+        if self.fp8 and not self.d_ff:
+            raise ValueError("fp8 is for the feed-forward sublayers' weights: it needs d_ff")
+        if self.fp8 and (self.dtype != torch.bfloat16 or self.d_model % step):
+            raise ValueError(f"fp8 takes bfloat16 rows of a multiple of {step} channels, got {self.dtype}, {self.d_model}")
+
 
 class Decoder:
     def __init__(self, cfg: Config, slots: int = 0, seed: int = 0, device="cuda"):
@@ -192,6 +203,8 @@ def main(argv=()) -> None:
     parser.add_argument("--d-ff", type=int, default=0, help="width of the feed-forward sublayers (0: none)")
     parser.add_argument("--fp8", action="store_true", help="continue on FP8 weights of the feed-forward sublayers")
     args = parser.parse_args(argv)
+    if args.fp8 and not args.d_ff:
+        parser.error("--fp8 needs --d-ff")
     cfg = Config(d_ff=args.d_ff, fp8=args.fp8)
     model = Decoder(cfg, slots=4)
     phrase = torch.randint(0, cfg.vocab, (12,), generator=torch.Generator().manual_seed(1)).cuda()
