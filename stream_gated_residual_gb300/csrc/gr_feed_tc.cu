@@ -1006,7 +1006,8 @@ __device__ __forceinline__ void finish_fp8(const JoinArgs& j, int64_t token, int
 }
 
 // fp32: an operand of a product as three bf16 terms, each the rounding of what the ones before leave (the first
-// towards zero where it would become infinite): 24 bits and more. What is not finite is the first term alone.
+// towards zero where it would become infinite): 24 bits and more, below 2^-110 to half of bf16's last place, 2^-134. What
+// is not finite is the first term alone.
 __device__ __forceinline__ void terms_of(float v, __nv_bfloat16 (&t)[3]) {
     t[0] = __float2bfloat16_rn(v);
     if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) {

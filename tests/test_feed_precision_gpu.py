@@ -109,6 +109,27 @@ def test_gelu_far_below_zero_in_fp8(N):
     relative(y, gelu(g)[0][:, None].expand(N, D), (2.0 ** -4 * (1 + bound) + bound)[:, None], "y")
 
 
+# ---- fp32 operands of any size --------------------------------------------------------------------
+
+@pytest.mark.parametrize("power", [0, -60, -100, -110, -120, -126, 60, 90])
+def test_fp32_products_of_small_and_large_operands(power):
+    """An operand is held as three bf16 terms: to 2^-24 of it, but to no less than 2^-134, half of bf16's last place. dy
+    of size 2^power against h of size 1: dW_o = dyᵀ h within the bound of sums of N products, (N + 4) units of the sum of
+    magnitudes, which covers h's own error beside it (16 units), and 2^-134 Σ |h|."""
+    N, D, F = 300, 64, 136
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(power + 200)
+    dy, x, w_in, w_out, pre = (torch.randn(*shape, generator=gen, device="cuda")
+                               for shape in ((N, D), (N, D), (2, F, D), (D, F), (N, 2, F)))
+    dy *= 2.0 ** power
+    dw_out = gr.feed_forward_backward(dy, x, w_in, w_out, pre)[2]
+    gate, up = pre.double().unbind(1)
+    h = gate * torch.sigmoid(gate) * up
+    size = dy.double().abs().T @ h.abs()
+    bound = (N + 20) * ULP * size + 2.0 ** -134 * h.abs().sum(0)
+    assert ((dw_out.double() - dy.double().T @ h).abs() <= bound).all()
+
+
 # ---- sums over very many tokens -------------------------------------------------------------------
 
 def test_one_signed_sums_over_a_million_tokens():
