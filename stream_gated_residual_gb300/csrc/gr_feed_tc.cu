@@ -171,7 +171,7 @@ struct Args {
     // Tiles 0 .. whole - 1 are done by a pair each; the others' steps of k, one after another, in even ranges
     uint32_t whole;
     // chunk > 0: no tile is whole; a pair's in turn are chunks of so many blocks, of all tiles their first, then their next
-    uint32_t chunk, tiles;
+    uint32_t chunk, chunks, tiles;
     uint32_t turns;         // whole tiles, or chunks
     uint32_t steps;         // of a tile: nk in steps of one block (FP8: four, what a word of scales covers)
     uint32_t range, longer; // steps of a range; the first `longer` have one more
@@ -237,7 +237,7 @@ template <int STEP> struct Units {
             if (a.chunk) {
                 const uint32_t c = tile / a.tiles;
                 t -= c * a.tiles;
-                u.k0 = int(c * a.chunk), u.k1 = min(u.k0 + int(a.chunk), a.nk), u.slot = int(tile);
+                u.k0 = int(c * a.chunk), u.k1 = min(u.k0 + int(a.chunk), a.nk), u.slot = int(t * a.chunks + c);
             }
             a.place(t, u.m, u.n);
             tile += pairs;
@@ -915,17 +915,10 @@ struct Sums {
     int64_t hop;
     uint32_t more;
     __device__ Sums(const Args& a, uint32_t t, int64_t at) {
-        const int64_t tile = int64_t(kTileM) * a.bn / 4;
-        const float4* p = reinterpret_cast<const float4*>(a.part) + at;
-        if (a.chunk) {
-            hop = a.tiles * tile;
-            from = p + t * tile;
-            rest = from + hop;
-            more = (uint32_t(a.nk) - 1) / a.chunk;
-            return;
-        }
         const uint32_t first = a.owner(t * a.steps), last = a.owner(t * a.steps + a.steps - 1);
+        const int64_t tile = int64_t(kTileM) * a.bn / 4;
         hop = a.slots * tile;
+        const float4* p = reinterpret_cast<const float4*>(a.part) + at;
         from = p + first * hop + (t - a.begin(first) / a.steps) * tile;
         rest = p + (first + 1) * hop;
         more = last - first;
@@ -1333,11 +1326,11 @@ void bound(Plan& p) {
     int64_t best = INT64_MAX;
     const int64_t fewest = ceil_div(nk, kLongest);
     for (int64_t c = fewest; c == fewest || (c < fewest + 64 && c <= nk / 256); ++c) {
-        const int64_t chunk = ceil_div(nk, c), turns = tiles * ceil_div(nk, chunk);
+        const int64_t chunk = ceil_div(nk, c), chunks = ceil_div(nk, chunk), turns = tiles * chunks;
         const int64_t time = ceil_div(turns, pairs) * (chunk + 16);   // the parts' stores: about 16 blocks
         if (time >= best - best / 32) continue;                      // more parts only where they save some time
         best = time;
-        p.a.chunk = uint32_t(chunk);
+        p.a.chunk = uint32_t(chunk), p.a.chunks = uint32_t(chunks);
         p.a.turns = uint32_t(turns);
         p.bytes = size_t(turns) * kTileM * p.a.bn * 4;
         if (turns > 0x7fffffffLL) p.bytes = kTooLarge;
@@ -1397,6 +1390,11 @@ const CUtensorMap kNone = {};
 
 template <int JOIN, bool F32 = false> cudaError_t join(const Plan& p, JoinArgs j, cudaStream_t st) {
     j.a = p.a;
+    if (p.a.chunk) {   // a tile's chunks as ranges of one step each
+        j.a.steps = p.a.chunks;
+        j.a.range = 1;
+        j.a.slots = 1;
+    }
     if (F32 || p.columns) {
         const int64_t lines = JOIN == kJoinGatedFp8 ? ceil_div(j.rows, kBlock) * kBlock : j.rows;
         if (lines / 4 * j.cols > 0xffffffffLL - kJoinThreads) return cudaErrorInvalidValue;
