@@ -454,63 +454,63 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t s = 0, lap = 0, q = 0;              // stage, laps, steps of scales
             bool ok = true;
             for (int j = 0; ok && units.next(u);) {
-              const int all = uniform(u.k1 - u.k0);
-              for (int from = 0; ok && from < all; from += kRun, ++j) {
-                const int b = j % accs, blocks = min(kRun, all - from);
-                if (j >= accs && !wait_warp(&x.acc_empty[b], (j / accs - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + b * acc_cols;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    const uint32_t step = uint32_t(kb) & 3;
-                    if (FP8 && step == 0) {
-                        // the scales of this and the next three blocks; the copies run in order with the MMAs
-                        if (!wait_warp(&x.scales_full[q % kScaleSlots], (q / kScaleSlots) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (leader)
-                            for (uint32_t i = 0; i < copies; ++i)
-                                tc_copy_scales(tmem + kColScales + (q & 1) * 16 + i * 4,
-                                               sf0 + (q % kScaleSlots) * kScaleSlot + i * 512);
-                        ++q;
-                    }
-                    if (!wait_warp(&x.full[s], lap & 1)) {
+                const int all = uniform(u.k1 - u.k0);
+                for (int from = 0; ok && from < all; from += kRun, ++j) {
+                    const int b = j % accs, blocks = min(kRun, all - from);
+                    if (j >= accs && !wait_warp(&x.acc_empty[b], (j / accs - 1) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    if (leader) {
-                        const uint64_t da = da0 + s * hop, db = db0 + s * hop;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t a = da + k * (A_MN ? 128 : 2), bb = db + k * (B_MN ? 128 : 2);
-                            if constexpr (TERMS > 1) {
-                                // the product of the first terms, and beside it the five that are smaller
-#pragma unroll
-                                for (int ta = 0; ta < TERMS; ++ta)
-#pragma unroll
-                                    for (int tb = 0; ta + tb < TERMS; ++tb)
-                                        tc_mma2(d + (ta + tb > 0 ? 128 : 0), a + ta * (kBoxA >> 4),
-                                                bb + tb * (uint32_t(box_b) >> 4), idesc,
-                                                kb > 0 || k > 0 || ta + tb > 1 || ta > 0);
-                            } else if constexpr (FP8) {
-                                const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
-                                tc_mma2_fp8(d, a, bb, idesc | (step << 4) | (step << 29), sfa, sfa + 4, kb > 0 || k > 0);
-                            } else {
-                                tc_mma2(d, a, bb, idesc, kb > 0 || k > 0);
+                    const uint32_t d = tmem + b * acc_cols;
+                    for (int kb = 0; kb < blocks; ++kb) {
+                        const uint32_t step = uint32_t(kb) & 3;
+                        if (FP8 && step == 0) {
+                            // the scales of this and the next three blocks; the copies run in order with the MMAs
+                            if (!wait_warp(&x.scales_full[q % kScaleSlots], (q / kScaleSlots) & 1)) {
+                                ok = false;
+                                break;
                             }
+                            tc_fence_after();
+                            if (leader)
+                                for (uint32_t i = 0; i < copies; ++i)
+                                    tc_copy_scales(tmem + kColScales + (q & 1) * 16 + i * 4,
+                                                   sf0 + (q % kScaleSlots) * kScaleSlot + i * 512);
+                            ++q;
                         }
-                        tc_commit2(&x.empty[s]);
-                        if (FP8 && (step == 3 || kb + 1 == blocks)) tc_commit2(&x.scales_empty[(q - 1) % kScaleSlots]);
+                        if (!wait_warp(&x.full[s], lap & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t da = da0 + s * hop, db = db0 + s * hop;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t a = da + k * (A_MN ? 128 : 2), bb = db + k * (B_MN ? 128 : 2);
+                                if constexpr (TERMS > 1) {
+                                    // the product of the first terms, and beside it the five that are smaller
+#pragma unroll
+                                    for (int ta = 0; ta < TERMS; ++ta)
+#pragma unroll
+                                        for (int tb = 0; ta + tb < TERMS; ++tb)
+                                            tc_mma2(d + (ta + tb > 0 ? 128 : 0), a + ta * (kBoxA >> 4),
+                                                    bb + tb * (uint32_t(box_b) >> 4), idesc,
+                                                    kb > 0 || k > 0 || ta + tb > 1 || ta > 0);
+                                } else if constexpr (FP8) {
+                                    const uint32_t sfa = tmem + kColScales + ((q - 1) & 1) * 16;
+                                    tc_mma2_fp8(d, a, bb, idesc | (step << 4) | (step << 29), sfa, sfa + 4, kb > 0 || k > 0);
+                                } else {
+                                    tc_mma2(d, a, bb, idesc, kb > 0 || k > 0);
+                                }
+                            }
+                            tc_commit2(&x.empty[s]);
+                            if (FP8 && (step == 3 || kb + 1 == blocks)) tc_commit2(&x.scales_empty[(q - 1) % kScaleSlots]);
+                        }
+                        if (++s == uint32_t(stages)) s = 0, ++lap;
                     }
-                    if (++s == uint32_t(stages)) s = 0, ++lap;
+                    if (ok && leader) tc_commit2(&x.acc_full[b]);
                 }
-                if (ok && leader) tc_commit2(&x.acc_full[b]);
-              }
             }
             if (leader) tc_commit2(&x.done);
             wait_warp(&x.done, 0);
@@ -565,7 +565,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         };
         // Half of the slots at a time: the fence that hands copied words to the tensor cores waits for every copy under
-        // way, so copies of a step at a time would each take a trip to the L2 (8191 x 7168 x 4096: 158 us).
+        // way, so copies of a step at a time would each take a trip to the L2 (16384 tokens of 4096 x 11008: 1.59 ms, so 1.55).
         constexpr uint32_t kBatch = kScaleSlots / 2;
         uint32_t q = 0;
         bool more = units.next(u), ok = true;
