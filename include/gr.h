@@ -490,8 +490,8 @@ int gr_linear_attention_backward(const gr_mixer* m, const gr_rows* dO, const gr_
  * module around the token mixer, one around the MLP). Per token, with f the activation:
  *     gate = W_g x,  up = W_u x,     h = f(gate) ⊙ up,     y = W_o h
  * in bf16 or fp32, with its gradient, and on FP8 weights. Conventions as above; sums and activations are
- * fp32, two runs on the same inputs give the same bits. A sum of more than 65536 terms is formed in parts, so
- * that what a tensor core's additions cut off stays below 2^-11 of a sum of one sign. fp32 products are formed
+ * fp32, two runs on the same inputs give the same bits. A bf16 sum of more than 65536 terms is formed in parts,
+ * so that what a tensor core's additions cut off stays below 2^-11 of a sum of one sign. fp32 products are formed
  * from three bf16 terms of each operand, with errors as small as fp32 sums' own; operands below 2^-110 are held
  * to 2^-134 instead of 24 bits. A value that is not finite makes the outputs that it enters not finite (not
  * always the infinity or NaN that a sum in order would give) and no others. Calls whose tiles or steps of k pass

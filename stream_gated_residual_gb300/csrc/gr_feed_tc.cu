@@ -339,7 +339,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr int kK = FP8 ? 128 : 64;
     // The scales take columns behind 256: one accumulator of up to 256 columns, or two of 128.
     const int accs = FP8 && args.bn > 128 ? 1 : 2, acc_cols = FP8 ? 128 : 256;
-    // A tensor core cuts off what an addition to its accumulator shifts out, up to a unit in its last place. Few enough of
+    // A tensor core cuts off what an addition to its accumulator shifts out, up to two units in its last place. Few enough of
     // them (kLongest) are nothing beside a rounding to bf16, but not for fp32, so there an accumulator takes four blocks at
     // most (16 additions, 2.8e-7), and those sums are added up with rounding.
     constexpr int kRun = TERMS > 1 ? 4 : 1 << 30;

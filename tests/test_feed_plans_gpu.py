@@ -143,6 +143,23 @@ def test_sums_over_tokens_in_chunks():
     gradients_close(call(), *t)
 
 
+def test_sums_over_hidden_channels_in_chunks():
+    """65544 hidden channels are 1025 blocks of 64 of the down product, 2049 of dx: y of 520 tokens in chunks of whole
+    tiles, dx of 40 tokens, which are the product's columns, in chunks of theirs."""
+    F = 65_544
+    call, (x, w_in, w_out) = inputs("feed_forward", 520, 8192, F)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        made = parts("feed_forward", 520, 8192, F) // (256 * 256 * 4)
+        assert made % 96 == 0 and 2 <= made // 96 <= 4
+    got, wp = call()[0], ref.forward(x, w_in, w_out, "silu", BF)
+    h = ref.act(wp[1][:, 0], "silu")[0] * wp[1][:, 1]
+    within(got, wp[0], wp[2], "y")
+    close(got, wp[0], (h.square() @ w_out.double().square().T).sum().sqrt().item(), "y")
+    del call, x, w_in, w_out, wp, h, got
+    call, t = inputs("feed_forward_backward", 40, 12288, F)
+    gradients_close(call(), *t)
+
+
 @pytest.mark.parametrize("N,K,O", [(64, 7168, 2048), (600, 16384, 264), (8191, 7168, 520)])
 def test_long_fp8_sums_lose_nothing(N, K, O):
     call, t = inputs("fp8_matmul", N, K, O)
